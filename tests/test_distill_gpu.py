@@ -1,0 +1,348 @@
+"""The distillation loss and its gradient on the GPU (two calls, one pass, autograd) against the fp64
+oracle, within the tolerances derived in tests/_logits_grading.py."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import logits_oracle as L
+from tests import _logits_grading as G
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def vce():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need CUDA")
+    import vocab_cross_entropy_gb300 as v
+    return v
+
+
+class Case:
+    """Student logits (a matrix inside a wider one), teacher entries and labels; near: the teacher is
+    the student plus noise of that size."""
+
+    def __init__(self, T, V, K, dtype=BF16, tau=1.0, tail=True, near=1.0, tdtype=F32, pad=0, left=0, seed=0):
+        g = torch.Generator().manual_seed(seed + T + V + K)
+        full = (2.0 * torch.randn(T, V + pad, generator=g)).to(dtype)
+        self.z = full.cuda()[:, left:left + V]
+        t = full[:, left:left + V].double() + near * torch.randn(T, V, generator=g).double()
+        tv, ids, _, rest = L.topk(t.numpy(), K, tau)
+        self.values = torch.from_numpy(tv).to(tdtype).cuda()
+        self.ids = torch.from_numpy(ids).cuda()
+        self.tail = torch.from_numpy(rest).to(F32).cuda() if tail else None
+        self.labels = None
+        self.tau = tau
+
+    def teacher(self):
+        return self.ids, self.values, self.tail, self.tau, self.labels
+
+    def oracle(self, reduction, go=1.0):
+        host = lambda x: None if x is None else x.detach().double().cpu().numpy()
+        v = host(self.values)
+        v = np.where(self.ids.cpu().numpy() >= 0, v, -np.inf)
+        return L.distill(host(self.z), self.ids.cpu().numpy(), v, host(self.tail), self.tau,
+                         None if self.labels is None else self.labels.cpu().numpy(), reduction, go)
+
+    def sizes(self):
+        z, t = self.z.float(), self.values.float()
+        fin = lambda x: float(x[torch.isfinite(x)].abs().max()) if torch.isfinite(x).any() else 0.0
+        tmax = fin(t)
+        if self.tail is not None:
+            tmax = max(tmax, fin(self.tail) * self.tau)
+        return fin(z), tmax, self.tau
+
+
+def check(vce, c, reduction="mean", gdtype=None, go=None):
+    """Both calls and the one pass against the oracle.  go: an upstream gradient per row or a number."""
+    T = c.z.shape[0]
+    per_row = reduction == "none"
+    if go is None:
+        go = np.linspace(0.5, 1.5, T) if per_row else 1.0
+    up = torch.as_tensor(np.atleast_1d(go), dtype=F32, device="cuda")
+    ref = c.oracle(reduction, up.cpu().double().numpy())
+    gdtype = gdtype or c.z.dtype
+    eps = torch.finfo(gdtype).eps if gdtype is BF16 else 2.0 ** -23
+    loss, rows, stats, tops, status = vce.ce_distill_forward(c.z, *c.teacher(), reduction=reduction)
+    assert vce.vce_get_status(status) == 0
+    G.check_distill_loss(rows.cpu(), ref, *c.sizes())
+    grad = vce.ce_distill_backward(c.z, c.ids, stats, tops, up, c.tau, reduction, grad_dtype=gdtype)
+    G.check_distill_grad(grad.double().cpu(), ref, *c.sizes(), eps)
+    l1, r1, g1, s1 = vce.ce_distill_forward_backward(c.z, *c.teacher(), reduction=reduction, grad_output=up,
+                                                    grad_dtype=gdtype)
+    assert vce.vce_get_status(s1) == 0
+    G.check_distill_loss(r1.cpu(), ref, *c.sizes())
+    G.check_distill_grad(g1.double().cpu(), ref, *c.sizes(), eps)
+    if per_row:
+        assert loss is None and l1 is None
+        return
+    for got, r in ((loss, rows), (l1, r1)):   # the sum of the rows it wrote: compensated, one rounding
+        total = r.double().sum().item() / (max(ref["n"], 1) if reduction == "mean" else 1)
+        if ref["n"] == 0 and reduction == "mean":
+            assert np.isnan(got.item())
+        else:
+            assert abs(got.item() - total) <= 2.0 ** -23 * abs(total)
+
+
+@pytest.mark.parametrize("tail", [True, False])
+@pytest.mark.parametrize("T,V,K,dtype,tau", [
+    (1, 1, 1, F32, 1.0), (3, 2, 2, BF16, 1.0), (5, 9, 1, BF16, 2.0), (64, 1000, 8, F32, 1.0), (33, 1003, 256, BF16, 2.0),
+    (6, 8192, 64, BF16, 4.0), (20, 32001, 100, BF16, 1.0), (2, 128256, 64, BF16, 2.0), (3, 70000, 32, F32, 1.0),
+    (1, 300001, 20, F32, 1.0), (700, 600, 33, BF16, 1.0)])
+def test_distill(vce, T, V, K, dtype, tau, tail):
+    check(vce, Case(T, V, K, dtype, tau, tail))
+
+
+@pytest.mark.parametrize("reduction", ["mean", "sum", "none"])
+@pytest.mark.parametrize("dtype,gdtype", [(BF16, BF16), (BF16, F32), (F32, BF16), (F32, F32)])
+def test_distill_types_and_reductions(vce, dtype, gdtype, reduction):
+    check(vce, Case(17, 5000, 12, dtype, 1.5, True, tdtype=BF16), reduction, gdtype)
+
+
+@pytest.mark.parametrize("dtype,gdtype", [(BF16, BF16), (BF16, F32), (F32, BF16)])
+@pytest.mark.parametrize("V,pad,left", [(4001, 0, 0), (4001, 6, 3), (4096, 1, 1), (4100, 4, 4), (33000, 5, 2)])
+def test_distill_layouts(vce, V, pad, left, dtype, gdtype):
+    check(vce, Case(7, V, 20, dtype, 1.0, True, pad=pad, left=left), "sum", gdtype, go=0.75)
+
+
+@pytest.mark.parametrize("gdtype,pad,left", [(BF16, 3, 1), (F32, 2, 2), (BF16, 8, 0)])
+def test_distill_gradient_layouts(vce, gdtype, pad, left):
+    """A gradient inside a wider matrix, aligned unlike the logits: the columns around it stay."""
+    T, V = 6, 9001
+    c = Case(T, V, 10, BF16, 2.0, True)
+    full = torch.full((T, V + pad), 7.0, dtype=gdtype, device="cuda")
+    grad = full[:, left:left + V]
+    up = torch.ones(1, device="cuda")
+    ref = c.oracle("mean")
+    eps = torch.finfo(gdtype).eps
+    for one_pass in (False, True):
+        full.fill_(7.0)
+        if one_pass:
+            vce.ce_distill_forward_backward(c.z, *c.teacher(), grad_output=up, grad_logits=grad)
+        else:
+            _, _, stats, tops, _ = vce.ce_distill_forward(c.z, *c.teacher())
+            vce.ce_distill_backward(c.z, c.ids, stats, tops, up, c.tau, grad_logits=grad)
+        G.check_distill_grad(grad.double().cpu(), ref, *c.sizes(), eps)
+        assert torch.all(full[:, :left] == 7.0) and torch.all(full[:, left + V:] == 7.0)
+
+
+@pytest.mark.parametrize("near", [0.0, 1e-3, 30.0])
+@pytest.mark.parametrize("tail", [True, False])
+def test_distill_near_and_far_teachers(vce, near, tail):
+    """A student that matches its teacher (losses far below the rounding of its log-probabilities), and
+    one that is far off."""
+    check(vce, Case(9, 3000, 16, F32, 1.0, tail, near=near))
+
+
+def test_distill_confident_student(vce):
+    """One column with margins of 17 to 90: the tail's mass is far below fp32's resolution at 1, and the
+    losses 1e-8 to 1e-39 keep their relative accuracy (K = 1: the cross-entropy's collapse regime)."""
+    c = Case(8, 4000, 1, F32, 1.0, False)
+    rows = torch.arange(8, device="cuda")
+    margins = torch.linspace(17, 80, 8, device="cuda")
+    c.z[rows, c.ids[:, 0]] = c.z.amax(1) + margins
+    ref = c.oracle("none")
+    loss = vce.ce_distill_forward(c.z, *c.teacher(), reduction="none")[1].double().cpu().numpy()
+    assert np.all(np.abs(loss - ref["loss_rows"]) <= 1e-4 * ref["loss_rows"]) and np.all(loss > 0)
+    ce = vce.ce_forward(c.z.contiguous(), c.ids[:, 0].contiguous(), reduction="none")[1].double().cpu().numpy()
+    assert np.all(np.abs(loss - ce) <= 1e-4 * ce)
+    g = vce.ce_distill_forward_backward(c.z, *c.teacher(), reduction="none")[2]
+    top = g.gather(1, c.ids)[:, 0].double().cpu().numpy()
+    assert np.all(np.abs(top + ref["loss_rows"]) <= 1e-4 * ref["loss_rows"])   # -(1 - p), p near 1
+    check(vce, c, "sum")
+
+
+def test_distill_ragged_and_ignored_rows(vce):
+    c = Case(12, 2500, 9, BF16, 2.0, True)
+    c.ids[1, 4:] = -1            # fewer entries
+    c.ids[2, 1] = -1             # a gap
+    c.ids[3] = -1                # no teacher
+    c.ids[4, 1:] = -1            # one entry
+    c.labels = torch.arange(12, device="cuda") % 50
+    c.labels[[0, 7]] = -100
+    c.z[3] = float("nan")        # an ignored row's logits do not matter
+    c.z[7] = float("inf")
+    keep = c.z.clone()
+    c.z[3], c.z[7] = 0.0, 0.0
+    refs = {r: c.oracle(r) for r in ("mean", "sum")}
+    c.z.copy_(keep)
+    size = (float(keep[0].float().abs().max()) + 8.0, 30.0, 2.0)
+    for r, ref in refs.items():
+        up = torch.ones(1, device="cuda")
+        loss, rows, stats, tops, status = vce.ce_distill_forward(c.z, *c.teacher(), reduction=r)
+        assert vce.vce_get_status(status) == 0
+        G.check_distill_loss(rows.cpu(), ref, *size)
+        assert abs(loss.item() - ref["loss_out"]) <= 1e-4 * ref["loss_out"]
+        assert torch.all(tops[3] == 0) and torch.all(stats[3] == 0) and torch.all(stats[7] == 0)
+        g = vce.ce_distill_backward(c.z, c.ids, stats, tops, up, c.tau, r)
+        G.check_distill_grad(g.double().cpu(), ref, *size, 2.0 ** -7)
+        g = vce.ce_distill_forward_backward(c.z, *c.teacher(), reduction=r)[2]
+        G.check_distill_grad(g.double().cpu(), ref, *size, 2.0 ** -7)
+
+
+@pytest.mark.parametrize("reduction", ["mean", "sum"])
+def test_distill_with_every_row_ignored(vce, reduction):
+    c = Case(4, 300, 3)
+    c.ids[:, 0] = -1
+    check(vce, c, reduction)
+
+
+def test_distill_masked_students(vce):
+    """-inf logits: among the tail, on entries (infinite loss where q > 0), all of the tail, all of the
+    entries, and a row of nothing else."""
+    inf = float("inf")
+    c = Case(7, 600, 4, F32, 1.0, True)
+    cols = torch.arange(600, device="cuda")
+    c.z[0, ::3] = -inf
+    c.z[0, c.ids[0]] = 1.0
+    c.z[1, c.ids[1, 2]] = -inf
+    c.values[2, 1:] = -inf                          # a teacher entry without mass on a masked logit
+    c.z[2, c.ids[2, 1]] = -inf
+    is_top = torch.zeros(600, dtype=torch.bool, device="cuda")
+    is_top[c.ids[3]] = True
+    c.z[3][~is_top] = -inf                          # nothing left in the tail, which has mass
+    c.z[4, c.ids[4]] = -inf                         # nothing left among the entries
+    c.tail[5] = -inf
+    is_top = torch.zeros(600, dtype=torch.bool, device="cuda")
+    is_top[c.ids[5]] = True
+    c.z[5][~is_top] = -inf                          # nothing left in a tail without mass: finite
+    assert cols.numel() == 600
+    rows = [0, 1, 2, 3, 4, 5]
+    live = Case.__new__(Case)
+    live.z, live.ids, live.values, live.tail = c.z[rows], c.ids[rows], c.values[rows], c.tail[rows]
+    live.labels, live.tau = None, 1.0
+    ref = live.oracle("sum")
+    loss, r, stats, tops, status = vce.ce_distill_forward(live.z, *live.teacher(), reduction="sum")
+    assert vce.vce_get_status(status) == 0 and loss.item() == inf
+    G.check_distill_loss(r.cpu(), ref, *live.sizes())
+    assert [bool(np.isinf(x)) for x in ref["loss_rows"]] == [False, True, False, True, True, False]
+    up = torch.ones(1, device="cuda")
+    g2 = vce.ce_distill_backward(live.z, live.ids, stats, tops, up, 1.0, "sum")
+    g1 = vce.ce_distill_forward_backward(live.z, *live.teacher(), reduction="sum")[2]
+    for g in (g1, g2):
+        G.check_distill_grad(g.double().cpu(), ref, *live.sizes(), 2.0 ** -23)
+    c.z[6] = -inf                                   # no student at all: NaN, and no gradient
+    loss, r, g, status = vce.ce_distill_forward_backward(c.z, *c.teacher(), reduction="sum")
+    assert vce.vce_get_status(status) == 0
+    assert torch.isnan(r[6]) and torch.all(g[6] == 0)
+
+
+def test_distill_bad_teachers(vce):
+    """Ids out of range or twice in a row, and teachers without finite mass: a status, a NaN loss, no
+    gradient; the other rows are not touched by it."""
+    good = Case(8, 20000, 6, BF16, 1.0, True)
+    ref = good.oracle("sum")
+    for what in range(6):
+        c = Case(8, 20000, 6, BF16, 1.0, True)
+        if what == 0:
+            c.ids[3, 2] = 20000
+        elif what == 1:
+            c.ids[3, 0] = -2
+        elif what == 2:
+            c.ids[3, 5] = c.ids[3, 1]
+        elif what == 3:
+            c.values[3] = -float("inf")
+            c.tail[3] = -float("inf")
+        elif what == 4:
+            c.values[3, 1] = float("nan")
+        else:
+            c.tail[3] = float("inf")
+        loss, rows, stats, tops, status = vce.ce_distill_forward(c.z, *c.teacher(), reduction="sum")
+        assert vce.vce_get_status(status) == 2 and torch.isnan(loss).all(), what
+        assert torch.isnan(rows).nonzero().flatten().tolist() == [3]
+        up = torch.ones(1, device="cuda")
+        g2 = vce.ce_distill_backward(c.z, c.ids, stats, tops, up, 1.0, "sum")
+        l1, r1, g1, s1 = vce.ce_distill_forward_backward(c.z, *c.teacher(), reduction="sum")
+        assert vce.vce_get_status(s1) == 2 and torch.isnan(r1).nonzero().flatten().tolist() == [3]
+        others = [0, 1, 2, 4, 5, 6, 7]
+        part = {k: (v[others] if isinstance(v, np.ndarray) else v) for k, v in ref.items()}
+        for g in (g1, g2):
+            assert torch.all(g[3] == 0), what
+            G.check_distill_grad(g[others].double().cpu(), part, *good.sizes(), 2.0 ** -7)
+
+
+@pytest.mark.parametrize("V,dtype", [(900001, BF16), (450000, F32)])
+def test_distill_rows_longer_than_shared_memory(vce, V, dtype):
+    check(vce, Case(3, V, 40, dtype, 1.0, True))
+    c = Case(2, V, 3, dtype, 1.0, True)
+    c.ids[0, 2] = c.ids[0, 1]               # a refused row of that length ends cleanly too
+    _, rows, g, status = vce.ce_distill_forward_backward(c.z, *c.teacher())
+    assert vce.vce_get_status(status) == 2 and torch.isnan(rows[0]) and torch.all(g[0] == 0)
+
+
+def test_distill_same_bits_every_time(vce):
+    c = Case(200, 40001, 64, BF16, 2.0, True)
+    up = torch.ones(1, device="cuda")
+    def both():
+        loss, rows, stats, tops, _ = vce.ce_distill_forward(c.z, *c.teacher())
+        return (loss, rows, stats, tops, vce.ce_distill_backward(c.z, c.ids, stats, tops, up, c.tau),
+                *vce.ce_distill_forward_backward(c.z, *c.teacher(), grad_output=up)[:3])
+    first = both()
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(both(), first))
+
+
+def test_distill_autograd(vce):
+    for reduction in ("mean", "sum", "none"):
+        c = Case(10, 3001, 7, F32, 2.0, True)
+        z = c.z.clone().requires_grad_(True)
+        loss = vce.distill_cross_entropy(z, *c.teacher(), reduction=reduction)
+        up = torch.linspace(0.5, 2, 10, device="cuda") if reduction == "none" else torch.tensor(0.7, device="cuda")
+        loss.backward(up.expand(loss.shape))
+        ref = c.oracle(reduction, up.double().cpu().numpy())
+        G.check_distill_grad(z.grad.double().cpu(), ref, *c.sizes(), 2.0 ** -23)
+    # against differences of the fp64 loss
+    want = c.z.double().cpu().numpy()
+    i, j, h = 3, int(c.ids[3, 2]), 1e-4
+    f = lambda d: (lambda zz: (zz.__setitem__((i, j), zz[i, j] + d), L.distill(
+        zz, c.ids.cpu().numpy(), c.values.double().cpu().numpy(), c.tail.double().cpu().numpy(), 2.0)["loss_rows"][i])[1])(want.copy())
+    diff = (f(h) - f(-h)) / (2 * h) * float(up[i])
+    assert abs(z.grad[i, j].item() - diff) <= 1e-4 * abs(diff) + 1e-7
+
+
+def test_distill_streams_and_graphs(vce):
+    c, d = Case(30, 30001, 16, BF16, 1.0, True), Case(30, 30001, 16, BF16, 1.0, True, seed=9)
+    up = torch.ones(1, device="cuda")
+    want = {id(x): vce.ce_distill_forward_backward(x.z, *x.teacher(), grad_output=up) for x in (c, d)}
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    got = [(x, vce.ce_distill_forward_backward(x.z, *x.teacher(), grad_output=up, stream=s))
+           for x, s in zip((c, d, c, d), streams)]
+    torch.cuda.synchronize()
+    for x, g in got:
+        assert all(torch.equal(a, b) for a, b in zip(g[:3], want[id(x)][:3]))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        loss, rows, stats, tops, status = vce.ce_distill_forward(c.z, *c.teacher())
+        grad = vce.ce_distill_backward(c.z, c.ids, stats, tops, up)
+    for name in ("ids", "values", "tail"):
+        getattr(c, name).copy_(getattr(d, name))
+    c.z.copy_(d.z)
+    graph.replay()
+    fresh = vce.ce_distill_forward(d.z, *d.teacher())
+    assert torch.equal(loss, fresh[0]) and torch.equal(rows, fresh[1])
+    assert torch.equal(grad, vce.ce_distill_backward(d.z, d.ids, fresh[2], fresh[3], up))
+
+
+def test_distill_refusals(vce):
+    c = Case(4, 100, 5)
+    go = torch.ones(1, device="cuda")
+    with pytest.raises(vce.VceError):
+        vce.ce_distill_forward(c.z, c.ids, c.values, temperature=0.0)
+    with pytest.raises(TypeError):
+        vce.ce_distill_forward(c.z, c.ids.int(), c.values)
+    with pytest.raises(ValueError):
+        vce.ce_distill_forward(c.z, c.ids, c.values[:, :4])
+    with pytest.raises(ValueError):
+        vce.ce_distill_forward(c.z, c.ids, c.values, c.tail[:3])
+    with pytest.raises(TypeError):
+        vce.ce_distill_forward(c.z, c.ids, c.values.half())
+    with pytest.raises(ValueError):
+        vce.ce_distill_forward_backward(c.z, c.ids, c.values, grad_output=torch.ones(4, device="cuda"))
+    with pytest.raises(vce.VceError):
+        vce.ce_distill_forward_backward(c.z, c.ids, c.values, grad_output=go, grad_logits=c.z)
+    with pytest.raises(ValueError):
+        vce.ce_distill_forward(c.z, c.ids.cpu(), c.values)
+    out = vce.ce_distill_forward_backward(c.z[:0], c.ids[:0], c.values[:0], reduction="sum")
+    assert out[0].item() == 0 and out[2].shape == (0, 100) and vce.vce_get_status(out[3]) == 0

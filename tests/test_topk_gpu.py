@@ -1,0 +1,149 @@
+"""ce_topk on the GPU against the fp64 oracle: ids and values exactly, log-sum-exps within the
+tolerance derived in tests/_logits_grading.py."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import logits_oracle as L
+from tests import _logits_grading as G
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def vce():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need CUDA")
+    import vocab_cross_entropy_gb300 as v
+    return v
+
+
+def logits_of(T, V, dtype, seed, pad=0, left=0, std=2.0):
+    """[T, V] logits on the GPU inside a matrix of pad more columns, left of them before the first."""
+    g = torch.Generator().manual_seed(seed)
+    full = (std * torch.randn(T, V + pad, generator=g)).to(dtype).cuda()
+    return full[:, left:left + V]
+
+
+def check(vce, z, k, tau=1.0):
+    values, ids, lse, tail = [x.cpu().numpy() for x in vce.ce_topk(z, k, tau)]
+    host = z.double().cpu().numpy()
+    rv, ri, rl, rt = L.topk(host, k, tau)
+    assert np.array_equal(ids, ri)
+    assert np.array_equal(values.astype(np.float64), rv)
+    zmax = np.abs(host[np.isfinite(host)]).max(initial=0.0)
+    G.check_lse(lse, rl, zmax, tau)
+    G.check_lse(tail, rt, zmax, tau, "tail")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,V,k", [(1, 1, 1), (3, 7, 7), (5, 33, 4), (64, 1000, 8), (2, 1000, 256), (1, 8192, 256),
+                                   (7, 8193, 1), (1, 128256, 20), (19, 32001, 64), (400, 5003, 50), (2, 300001, 100)])
+def test_topk(vce, T, V, k, dtype):
+    check(vce, logits_of(T, V, dtype, T + V + k), k, 0.7 if V % 2 else 1.0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("pad,left", [(1, 0), (1, 1), (13, 5), (8, 0), (7, 7)])
+def test_topk_layouts(vce, pad, left, dtype):
+    check(vce, logits_of(9, 4001, dtype, pad + left, pad, left), 40, 2.0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_topk_ties(vce, dtype):
+    """Constant rows, rows of few distinct values, sorted rows: equal logits in column order."""
+    V = 20011
+    z = torch.zeros(6, V, dtype=dtype)
+    z[1] = (torch.arange(V) % 3).to(dtype)
+    z[2] = torch.linspace(-4, 4, V).to(dtype)
+    z[3] = torch.linspace(4, -4, V).to(dtype)
+    z[4, ::2] = -0.0
+    z[5] = torch.where(torch.arange(V) % 977 == 5, 1.0, -1.0).to(dtype)
+    for k in (1, 17, 256):
+        check(vce, z.cuda(), k)
+
+
+@pytest.mark.parametrize("V", [77, 5000, 128256])
+def test_topk_masked_rows(vce, V):
+    """-inf entries are never among the K: rows with nothing, one logit, and fewer than K."""
+    z = logits_of(5, V, torch.float32, V)
+    z[0] = -float("inf")
+    z[1] = -float("inf")
+    z[1, V // 2] = 1.5
+    z[2, 9:] = -float("inf")
+    z[3, ::2] = -float("inf")
+    z[4] = torch.finfo(torch.float32).min
+    z[4, 3] = 2.0
+    check(vce, z, 30)
+
+
+def test_topk_one_value_far_above(vce):
+    """The tail is summed without the K: with a margin of 60 it would cancel to nothing as a difference,
+    and as part of a group whose maximum is the large logit it would underflow at a margin of 150."""
+    z = logits_of(3, 40000, torch.float32, 5)
+    z[0, 17] = 60.0
+    z[1, 39999] = 150.0
+    z[2] -= 120.0
+    z[2, 20000] = 30.0
+    check(vce, z, 1)
+    check(vce, z, 5)
+
+
+def test_topk_many_rows_and_wide(vce):
+    z = logits_of(2000, 1500, torch.bfloat16, 8)
+    check(vce, z, 33)
+    check(vce, logits_of(2, 2000003, torch.bfloat16, 9), 256, 4.0)
+
+
+def test_topk_same_bits_every_time(vce):
+    z = logits_of(300, 128256, torch.bfloat16, 10)
+    first = [x.clone() for x in vce.ce_topk(z, 64, 2.0)]
+    for _ in range(5):
+        for a, b in zip(vce.ce_topk(z, 64, 2.0), first):
+            assert torch.equal(a, b)
+
+
+def test_topk_streams_and_graphs(vce):
+    z = logits_of(40, 50001, torch.bfloat16, 11)
+    want = vce.ce_topk(z, 20)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = [vce.ce_topk(z, 20, stream=s) for s in streams]       # at once, on three streams
+    torch.cuda.synchronize()
+    for g in got:
+        assert all(torch.equal(a, b) for a, b in zip(g, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = vce.ce_topk(z, 20)
+    other = logits_of(40, 50001, torch.bfloat16, 12)
+    want = [x.clone() for x in vce.ce_topk(other, 20)]
+    z.copy_(other)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(held, want))
+
+
+def test_topk_leaves_what_is_behind_its_outputs(vce):
+    T, k = 5, 9
+    z = logits_of(T, 999, torch.bfloat16, 13)
+    bufs = [torch.full((T * k + 8,), -7.0, device="cuda"), torch.full((T * k + 8,), -7, dtype=torch.int64, device="cuda"),
+            torch.full((T + 8,), -7.0, device="cuda"), torch.full((T + 8,), -7.0, device="cuda")]
+    vce.ce_topk(z, k, values=bufs[0][:T * k].view(T, k), ids=bufs[1][:T * k].view(T, k), lse=bufs[2][:T],
+                tail_lse=bufs[3][:T])
+    for b, n in zip(bufs, (T * k, T * k, T, T)):
+        assert torch.all(b[n:] == -7)
+
+
+def test_topk_refusals(vce):
+    z = logits_of(4, 100, torch.float32, 1)
+    with pytest.raises(ValueError):
+        vce.ce_topk(z, 0)
+    for kw in (dict(k=101), dict(k=257), dict(k=5, temperature=0.0), dict(k=5, temperature=float("nan"))):
+        with pytest.raises(vce.VceError):
+            vce.ce_topk(z, **kw)
+    with pytest.raises(TypeError):
+        vce.ce_topk(z, 5, ids=torch.empty(4, 5, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError):
+        vce.ce_topk(z, 5, values=torch.empty(4, 6, device="cuda"))
+    out = vce.ce_topk(z[:0], 5)
+    assert [tuple(x.shape) for x in out] == [(0, 5), (0, 5), (0,), (0,)]

@@ -19,7 +19,9 @@ __all__ = ["VceError", "lib", "library_path", "ce_forward", "ce_backward", "ce_f
            "linear_ce_workspace_bytes", "linear_ce_fwd_bwd", "linear_ce_fwd_bwd_filtered", "linear_ce_fwd_bwd_timed",
            "vce_get_status", "vce_status_string", "vce_debug_checks", "vce_debug_status", "use_library",
            "restore_library",
-           "vce_abi_version", "cross_entropy", "IGNORE_INDEX", "F32", "BF16", "RED"]
+           "vce_abi_version", "cross_entropy", "IGNORE_INDEX", "F32", "BF16", "RED",
+           "ce_topk", "ce_distill_forward", "ce_distill_backward", "ce_distill_forward_backward",
+           "distill_cross_entropy", "logits_process", "logits_process_backward", "process_logits", "MAX_TOPK"]
 
 IGNORE_INDEX = -100
 F32, BF16 = 0, 1
@@ -95,7 +97,17 @@ def _load(path=None):
         L.vce_test_ce_fused_stall.restype = i32
         L.vce_test_ce_fwd_stall.argtypes = [p, i64, i64, p, p, p, p, ctypes.c_uint64, p, p]
         L.vce_test_ce_fwd_stall.restype = i32
-    for name in ("ce_forward", "ce_backward", "ce_forward_ls", "ce_backward_ls", "ce_forward_backward",
+    L.ce_topk.argtypes = [p, i32, i64, i64, i64, i32, f32, p, p, p, p, p]
+    L.ce_distill_forward.argtypes = [p, i32, i64, i64, i64, p, p, i32, p, i32, f32, p, i64, i32, p, p, p, p, p, p]
+    L.ce_distill_backward.argtypes = [p, i32, i64, i64, i64, p, i32, f32, i32, p, p, p, p, i32, i64, p]
+    L.ce_distill_forward_backward.argtypes = [p, i32, i64, i64, i64, p, p, i32, p, i32, f32, p, i64, i32, p, p, p, p,
+                                              p, i32, i64, p, p]
+    L.logits_process.argtypes = [p, i32, i64, i64, i64, p, p, p, p, p, i64, p, p, p, p, i64, p, p, i64, p, i32, i64, p,
+                                 p]
+    L.logits_process_backward.argtypes = [p, i32, i64, i64, i64, p, i32, i64, p, p, p, i64, p, p, i64, p, i32, i64, p,
+                                          p]
+    for name in ("ce_topk", "ce_distill_forward", "ce_distill_backward", "ce_distill_forward_backward",
+                 "logits_process", "logits_process_backward", "ce_forward", "ce_backward", "ce_forward_ls", "ce_backward_ls", "ce_forward_backward",
                  "ce_forward_backward_ls", "ce_merge_chunks_ls",
                  "ce_merge_chunks", "ce_merge_chunks_noalloc",
                  "linear_ce_fwd_bwd", "linear_ce_fwd_bwd_filtered", "linear_ce_fwd_bwd_timed",
@@ -548,3 +560,7 @@ class _CrossEntropy(torch.autograd.Function):
 def cross_entropy(logits, labels, ignore_index=IGNORE_INDEX, reduction="mean", label_smoothing=0.0):
     """Collapse-safe softmax cross-entropy of [T, V] float32/bfloat16 CUDA logits with autograd."""
     return _CrossEntropy.apply(logits, labels, ignore_index, reduction, float(label_smoothing))
+
+
+from .logits_ops import (MAX_TOPK, ce_distill_backward, ce_distill_forward, ce_distill_forward_backward,  # noqa: E402
+                         ce_topk, distill_cross_entropy, logits_process, logits_process_backward, process_logits)

@@ -1,0 +1,713 @@
+// Distillation loss against a teacher's top K logits, its gradient, and both in one pass.
+//
+// Mathematics (one row, scale s = 1 / temperature; "top" the K columns of the teacher's entries,
+// "tail" the other columns).  With log-sum-exps Lq, R of the teacher's top and tail, and Lr, L' of
+// the student's (L' summed without the top columns, as the cross-entropy's forward leaves out its
+// target), the masses are logistic functions of two numbers,
+//     Q = sigma(a), q_T = sigma(-a), a = Lq - R;    P = sigma(b), p_T = sigma(-b), b = Lr - L',
+// and with qh_k = e^{s t_k - Lq}, r_k = e^{s z_k - Lr}, phi(x) = e^x - 1 - x >= 0:
+//     KL = Q phi(log P/Q) + q_T phi(log p_T/q_T) + Q sum_k qh_k phi(log r_k/qh_k)
+// (the linear terms add up to 0, since p and q sum to 1), a sum of terms >= 0: nothing cancels
+// when the student matches its teacher, nor when one column holds all the mass.  The gradient of
+// tau^2 KL is tau (p - q):
+//     tail:  tau (p_T - q_T) e^{s z_j - L'}        top:  tau [Q (r_k - qh_k) + (q_T - p_T) r_k]
+// with p_T - q_T a difference of logistic functions taken as a product (sigmoid_diff).
+//
+// Kernels.  k_distill: one thread-block cluster per row, each block a slice of the columns,
+// streamed through shared memory (row_stream.cuh).  One extra warp reads the K entries, marks
+// their columns in a bitmap (a word per consumer thread and stage, so a thread learns from one
+// word whether any of its 32 values is left out) and does all arithmetic on the K entries while
+// the columns stream.  The blocks then exchange (max, sum-exp) pairs through distributed shared
+// memory.  With the gradient (kGrad) the stages are kept and turned into gradient entries once
+// the pairs are merged.  k_distill_bwd: the gradient alone, from the saved statistics.
+// k_distill_reduce sums the losses in a fixed order; k_distill_count counts N before a one-pass
+// call with MEAN.  Nothing is shared between launches.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "ce_fold.cuh"
+#include "row_launch.h"
+#include "row_stream.cuh"
+#include "vce_logits.h"
+
+namespace vce {
+namespace distill {
+
+using namespace rs;
+
+constexpr int kProducerWarp = kConsumerWarps, kTopWarp = kConsumerWarps + 1;
+constexpr int kThreads = kConsumers + 64;
+constexpr int kPerLane = VCE_MAX_TOPK / 32;   // entries per lane of the top warp
+
+struct Args {
+    const void* logits;
+    int64_t T, V, ld;
+    const int64_t* ids;
+    const void* tvals;
+    const float* tail;
+    int K, tbf16;
+    float tau, scale, k2;        // temperature, 1 / temperature, log2(e) / temperature
+    const int64_t* labels;
+    int64_t ignore_index;
+    int red;
+    const float* go;             // kGrad
+    const float* inv_n;          // kGrad, MEAN
+    float* loss_rows;
+    float4* row_stats;
+    float* top_grads;            // forward alone
+    void* grad;                  // kGrad
+    int64_t ld_g;
+    int cluster, nbuf, max_stages;
+};
+
+struct alignas(16) Ctl {
+    float4 slot[kMaxCluster];    // (max, sum-exp, error code, -) of the cluster's blocks
+    Barriers bar;
+    float red_m[kConsumerWarps], red_s[kConsumerWarps];
+    float zmax, lnr, lq, kl_top; // of the entries: max z, log sum e^{s (z - max)}, Lq, sum qh phi
+    int code;                    // error found among the entries
+};
+
+struct alignas(8) Entry {        // of each teacher entry
+    float r, diff;               // r_k, r_k - qh_k
+    int col;                     // column, -1: none
+    int pad;
+};
+
+__host__ __device__ constexpr int smem_bytes(int nbuf, int max_stages, int K) {
+    return nbuf * kStageBytes + max_stages * kConsumers * 4 + (K * (int)sizeof(Entry) + 15) / 16 * 16 +
+           (int)sizeof(Ctl);
+}
+
+// ---- scalar functions --------------------------------------------------------------------------
+
+__device__ __forceinline__ float sigmoid(float x) {
+    const float e = expf(-fabsf(x));
+    return (x >= 0.f ? 1.f : e) / (1.f + e);
+}
+
+// sigma(u) - sigma(v), without cancellation: sigma(u) sigma(-v) (1 - e^{v-u}).
+__device__ __forceinline__ float sigmoid_diff(float u, float v) {
+    if (u == v) return 0.f;
+    const float d = v - u;
+    return d < 0.f ? -sigmoid(u) * sigmoid(-v) * expm1f(d) : sigmoid(-u) * sigmoid(v) * expm1f(-d);
+}
+
+// q phi(x), phi(x) = e^x - 1 - x, where p = q e^x: the power series of phi near 0 (to x^9 / 9!,
+// 2e-9 relative at 0.5), else p - q - q x, which loses at most two bits there.
+__device__ __forceinline__ float q_phi(float q, float p, float x) {
+    if (!(q > 0.f)) return p;
+    if (fabsf(x) < 0.5f) {
+        float c = 1.f / 362880.f;
+        c = fmaf(c, x, 1.f / 40320.f);
+        c = fmaf(c, x, 1.f / 5040.f);
+        c = fmaf(c, x, 1.f / 720.f);
+        c = fmaf(c, x, 1.f / 120.f);
+        c = fmaf(c, x, 1.f / 24.f);
+        c = fmaf(c, x, 1.f / 6.f);
+        c = fmaf(c, x, 0.5f);
+        return q * (x * x * c);
+    }
+    return (p - q) - q * x;
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, off));
+    return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
+    return v;
+}
+
+// ---- gradient entries ---------------------------------------------------------------------------
+
+// Writes the gradient coef 2^(z k2 - bias) of a thread's vectors of a stage.  vec: the row's
+// gradient vectors are aligned for GroupStore.
+template <typename S, typename O>
+__device__ __forceinline__ void write_grads(const uint4 (&x)[kU], const Row& r, const Slice& s, int j, int tid,
+                                            O* grow, bool vec, float coef, float k2, float bias) {
+    constexpr int G = Elt<S>::kGroup;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+        const int v = s.v0 + j * kStageVecs + tid + u * kConsumers;
+        if (v >= s.v0 + s.n) continue;
+        float g[G];
+        Elt<S>::unpack(x[u], g);
+#pragma unroll
+        for (int k = 0; k < G; ++k) g[k] = coef * ex2(fmaf(g[k], k2, -bias));
+        const int64_t c0 = (int64_t)v * G - r.shift;
+        if (vec && v >= r.iv0 && v < r.iv1) {
+            GroupStore<O, G>::run(grow + c0, g);
+        } else {
+#pragma unroll
+            for (int k = 0; k < G; ++k)
+                if (c0 + k >= 0 && c0 + k < r.V) Elt<O>::store1(grow + c0 + k, g[k]);
+        }
+    }
+}
+
+// +0.0 over the slice's columns, by NT threads.
+template <typename S, typename O>
+__device__ __forceinline__ void zero_grads(const Row& r, const Slice& s, O* grow, bool vec, int tid, int NT) {
+    constexpr int G = Elt<S>::kGroup;
+    const float zero[G] = {};
+    for (int v = s.v0 + tid; v < s.v0 + s.n; v += NT) {
+        const int64_t c0 = (int64_t)v * G - r.shift;
+        if (vec && v >= r.iv0 && v < r.iv1) {
+            GroupStore<O, G>::run(grow + c0, zero);
+        } else {
+            for (int k = 0; k < G; ++k)
+                if (c0 + k >= 0 && c0 + k < r.V) Elt<O>::store1(grow + c0 + k, 0.f);
+        }
+    }
+}
+
+template <typename S, typename O>
+__device__ __forceinline__ bool grads_aligned(const Row& r, const O* grow) {
+    constexpr int G = Elt<S>::kGroup;
+    return (reinterpret_cast<uintptr_t>(grow - r.shift) % (GroupStore<O, G>::kAlign)) == 0;
+}
+
+// ---- the row kernel -------------------------------------------------------------------------------
+
+template <typename S, typename O, bool kGrad>
+__global__ void __launch_bounds__(kThreads, 3) k_distill(const __grid_constant__ Args a) {
+    constexpr int G = Elt<S>::kGroup;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint8_t* bufs = smem;
+    uint32_t* marks = reinterpret_cast<uint32_t*>(smem + a.nbuf * kStageBytes);
+    Entry* entry = reinterpret_cast<Entry*>(marks + a.max_stages * kConsumers);
+    Ctl& ctl = *reinterpret_cast<Ctl*>(reinterpret_cast<uint8_t*>(entry) + (a.K * (int)sizeof(Entry) + 15) / 16 * 16);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int C = a.cluster;
+    const int rank = C > 1 ? (int)cluster_rank() : 0;
+    const int64_t row = blockIdx.x / C;
+    const Row r = make_row<S>(a.logits, row, a.ld, a.V);
+    const Slice sl = make_slice(r, C, rank);
+    const int64_t* ids = a.ids + row * a.K;
+    O* grow = kGrad ? static_cast<O*>(a.grad) + row * a.ld_g : nullptr;
+    const bool vec = kGrad && grads_aligned<S, O>(r, grow);
+
+    // a row without a teacher or with the ignored label: nothing of it is read (all blocks alike)
+    if (ids[0] == -1 || (a.labels && a.labels[row] == a.ignore_index)) {
+        if (rank == 0) {
+            if (tid == 0) {
+                a.loss_rows[row] = 0.f;
+                a.row_stats[row] = make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            if (!kGrad)
+                for (int k = tid; k < a.K; k += kThreads) a.top_grads[row * a.K + k] = 0.f;
+        }
+        if (kGrad) zero_grads<S, O>(r, sl, grow, vec, tid, kThreads);
+        return;
+    }
+
+    const bool held = sl.nst <= a.nbuf;              // the slice stays in shared memory
+    // a slice that is not held is copied twice; of its second round, the ring's first fill goes out
+    // before the statistics are done (later stages wait for the gradient to release theirs)
+    const int total = kGrad && !held ? 2 * sl.nst : sl.nst;
+    const int early = min(total, sl.nst + a.nbuf);
+    int issued = 0;
+    if (tid == kProducerWarp * 32) {
+        init_barriers(ctl.bar, a.nbuf);
+        ctl.code = 0;
+        for (; issued < min(sl.nst, a.nbuf); ++issued) issue_stage(bufs, ctl.bar, a.nbuf, r, sl, issued, issued);
+    }
+    if (C > 1) cluster_arrive();                     // this block runs: peers may write into it
+    for (int i = tid; i < sl.nst * kConsumers; i += kThreads) marks[i] = 0;
+    __syncthreads();
+
+    // the entries: columns, marks
+    int col[kPerLane];
+    if (warp == kTopWarp) {
+        int bad = 0;
+        int64_t id[kPerLane];
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) id[i] = lane + 32 * i < a.K ? ids[lane + 32 * i] : -1;
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) {
+            col[i] = id[i] >= 0 && id[i] < a.V ? (int)id[i] : -1;
+            bad |= id[i] != -1 && col[i] < 0;
+            if (col[i] >= 0) {
+                const int at = col[i] + r.shift, v = at / G - sl.v0;
+                if (v >= 0 && v < sl.n) {
+                    const int j = v / kStageVecs, w = v % kStageVecs;
+                    const uint32_t bit = 1u << ((w / kConsumers) * G + at % G);
+                    bad |= (atomicOr(&marks[j * kConsumers + w % kConsumers], bit) & bit) != 0;
+                }
+            }
+        }
+        if (__any_sync(0xFFFFFFFFu, bad) && lane == 0) ctl.code = VCE_ERR_TEACHER;
+    }
+    __syncthreads();
+
+    if (warp == kProducerWarp) {
+        if (lane == 0) {
+            for (; issued < early; ++issued) {
+                const int j = issued < sl.nst ? issued : issued - sl.nst;
+                if (!issue_stage(bufs, ctl.bar, a.nbuf, r, sl, j, issued)) break;
+            }
+        }
+    } else if (warp == kTopWarp) {
+        // all arithmetic on the K entries, while the columns stream
+        float z[kPerLane], t[kPerLane];
+        const S* zrow = static_cast<const S*>(a.logits) + row * a.ld;
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) {
+            const int k = lane + 32 * i;
+            z[i] = t[i] = -kInf;
+            if (col[i] >= 0) {
+                z[i] = Elt<S>::load1(zrow + col[i]);
+                t[i] = a.tbf16 ? Elt<uint16_t>::load1(static_cast<const uint16_t*>(a.tvals) + row * a.K + k)
+                               : Elt<float>::load1(static_cast<const float*>(a.tvals) + row * a.K + k);
+            }
+        }
+        float zm = -kInf, tm = -kInf;
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) {
+            zm = fmaxf(zm, z[i]);
+            tm = fmaxf(tm, t[i]);
+        }
+        zm = warp_max(zm);
+        tm = warp_max(tm);
+        float rs_ = 0.f, qs = 0.f;
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) {
+            if (z[i] > -kInf) rs_ += expf((z[i] - zm) * a.scale);
+            if (col[i] >= 0 && t[i] != -kInf) qs += expf((t[i] - tm) * a.scale);   // NaN: the row is refused below
+        }
+        rs_ = warp_sum(rs_);
+        qs = warp_sum(qs);
+        const float lnr = logf(rs_), lnq = logf(qs), inv_r = 1.f / rs_, inv_q = 1.f / qs;
+        float kl = 0.f;
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) {
+            const int k = lane + 32 * i;
+            if (k >= a.K) continue;
+            float rk = 0.f, diff = 0.f;
+            if (col[i] >= 0) {
+                float qk = 0.f, y = -kInf;
+                if (z[i] > -kInf) rk = expf((z[i] - zm) * a.scale) * inv_r;
+                if (t[i] > -kInf) qk = expf((t[i] - tm) * a.scale) * inv_q;
+                if (z[i] > -kInf && t[i] > -kInf) {
+                    // log(r_k / qh_k): differences of logits first, which are exact or nearly so
+                    y = ((z[i] - zm) - (t[i] - tm)) * a.scale - (lnr - lnq);
+                    diff = y < 0.5f ? qk * expm1f(y) : rk - qk;
+                } else {
+                    diff = rk - qk;
+                }
+                kl += q_phi(qk, rk, y);
+            }
+            entry[k] = Entry{rk, diff, col[i], 0};
+        }
+        kl = warp_sum(kl);
+        if (lane == 0) {
+            ctl.zmax = zm;
+            ctl.lnr = lnr;
+            ctl.lq = tm > -kInf ? tm * a.scale + lnq : tm;   // -inf: no mass among the entries; NaN stays
+            ctl.kl_top = kl;
+        }
+    } else {
+        float m = -kInf, s = 0.f, mb = 0.f;
+        for (int j = 0; j < sl.nst; ++j) {
+            const uint32_t word = marks[j * kConsumers + tid];
+            wait_stage(ctl.bar, a.nbuf, j);
+            uint4 x[kU];
+            load_stage<S>(bufs, a.nbuf, r, sl, j, j, tid, x);
+            if (!(kGrad && held)) release_stage(ctl.bar, a.nbuf, j);
+            float v[kU][G];
+#pragma unroll
+            for (int u = 0; u < kU; ++u) Elt<S>::unpack(x[u], v[u]);
+            if (word) {   // the entries' columns are left out
+#pragma unroll
+                for (int u = 0; u < kU; ++u)
+#pragma unroll
+                    for (int k = 0; k < G; ++k)
+                        if ((word >> (u * G + k)) & 1u) v[u][k] = -kInf;
+            }
+            pair_push<G>(v, m, s, mb, a.k2);
+        }
+        pair_warp_reduce(m, s, a.k2);
+        if (lane == 0) {
+            ctl.red_m[warp] = m;
+            ctl.red_s[warp] = s;
+        }
+    }
+    __syncthreads();
+
+    // ---- the row's statistics, by every thread alike ----
+    float M = -kInf, S0 = 0.f;
+    for (int w = 0; w < kConsumerWarps; ++w) pair_merge(M, S0, ctl.red_m[w], ctl.red_s[w], a.k2);
+    int code = ctl.bar.err ? ctl.bar.err : ctl.code;
+    if (C > 1) {
+        cluster_wait();                              // every peer runs
+        if (tid < C) st_peer(peer_addr(&ctl.slot[rank], tid), make_float4(M, S0, __int_as_float(code), 0.f));
+        cluster_arrive();
+        cluster_wait();
+        M = -kInf;
+        S0 = 0.f;
+        code = 0;
+        for (int p = 0; p < C; ++p) {                // the same order in every block
+            const float4 o = ctl.slot[p];
+            pair_merge(M, S0, o.x, o.y, a.k2);
+            code = max(code, __float_as_int(o.z));
+        }
+    }
+    const float R = a.tail ? a.tail[row] : -kInf, Lq = ctl.lq;
+    if (!code && !((Lq > -kInf || R > -kInf) && Lq < kInf && R < kInf)) code = VCE_ERR_TEACHER;   // no finite mass
+    const bool has_tail = S0 > 0.f, has_top = ctl.zmax > -kInf;
+    float b;
+    if (has_tail && has_top) b = (ctl.zmax - M) * a.scale + (ctl.lnr - logf(S0));
+    else b = has_top ? kInf : -kInf;
+    const float at = Lq == -kInf ? -kInf : Lq - R;   // R = -inf: +inf
+    const float P = sigmoid(b), pT = sigmoid(-b), Q = sigmoid(at), qT = sigmoid(-at);
+    const float D = sigmoid_diff(-b, -at);           // p_T - q_T
+    const bool dead = code || !(has_tail || has_top);
+    const float Lt = has_tail ? M * a.scale + logf(S0) : -kInf;
+    if (rank == 0 && tid == 0) {
+        float kl = q_phi(Q, P, softplus_f(-at) - softplus_f(-b)) + q_phi(qT, pT, softplus_f(at) - softplus_f(b));
+        if (Q > 0.f) kl += Q * ctl.kl_top;
+        a.loss_rows[row] = dead ? __int_as_float(0x7FC00000) : a.tau * a.tau * kl;
+        // weight: 1, negative for a row with an error, until the reduction writes it
+        a.row_stats[row] = make_float4(Lt, dead ? 0.f : D, 0.f, code ? -(float)code : 1.f);
+    }
+    if (!kGrad) {
+        if (rank == 0)
+            for (int k = tid; k < a.K; k += kThreads) {
+                const Entry e = entry[k];
+                a.top_grads[row * a.K + k] = dead || e.col < 0 ? 0.f : a.tau * (Q * e.diff - D * e.r);
+            }
+    } else if (dead) {
+        zero_grads<S, O>(r, sl, grow, vec, tid, kThreads);
+    } else {
+        const float c = a.go[a.red == VCE_RED_NONE ? row : 0] * (a.red == VCE_RED_MEAN ? *a.inv_n : 1.f) * a.tau;
+        if (warp < kConsumerWarps) {
+            const float coef = c * D, bias = has_tail ? Lt * kLog2e : 0.f;
+            for (int j = 0; j < sl.nst; ++j) {
+                const int q = held ? j : sl.nst + j;
+                if (!held) wait_stage(ctl.bar, a.nbuf, q);
+                uint4 x[kU];
+                load_stage<S>(bufs, a.nbuf, r, sl, j, q, tid, x);
+                if (!held) release_stage(ctl.bar, a.nbuf, q);
+                write_grads<S, O>(x, r, sl, j, tid, grow, vec, coef, a.k2, bias);
+            }
+        } else if (tid == kProducerWarp * 32) {
+            for (; issued < total; ++issued)
+                if (!issue_stage(bufs, ctl.bar, a.nbuf, r, sl, issued - sl.nst, issued)) break;
+        }
+        __syncthreads();                             // the entries' gradients go over the tail's
+        for (int k = tid; k < a.K; k += kThreads) {
+            const Entry e = entry[k];
+            const int v = e.col >= 0 ? (e.col + r.shift) / G - sl.v0 : -1;
+            if (v >= 0 && v < sl.n && dbg::ok(e.col < a.V, dbg::kCols))
+                Elt<O>::store1(grow + e.col, c * (Q * e.diff - D * e.r));
+        }
+    }
+    // copies that nothing waited for (after an abort, or of a row without a gradient) land first
+    if ((ctl.bar.abort || (kGrad && dead)) && tid == kProducerWarp * 32) drain(ctl.bar, a.nbuf, issued);
+}
+
+// ---- the gradient from saved statistics --------------------------------------------------------------
+
+struct BwdArgs {
+    const void* logits;
+    int64_t T, V, ld;
+    const int64_t* ids;
+    int K;
+    float tau, k2;
+    int red;
+    const float4* row_stats;
+    const float* top_grads;
+    const float* go;
+    void* grad;
+    int64_t ld_g;
+    int parts, nbuf;
+};
+
+template <typename S, typename O>
+__global__ void __launch_bounds__(kConsumers + 32, 3) k_distill_bwd(const __grid_constant__ BwdArgs a) {
+    constexpr int G = Elt<S>::kGroup;
+    extern __shared__ __align__(128) uint8_t smem[];
+    Barriers& bar = *reinterpret_cast<Barriers*>(smem + a.nbuf * kStageBytes);
+    const int tid = threadIdx.x, warp = tid >> 5;
+    const int64_t row = blockIdx.x / a.parts;
+    const Row r = make_row<S>(a.logits, row, a.ld, a.V);
+    const Slice sl = make_slice(r, a.parts, (int)(blockIdx.x - row * a.parts));
+    O* grow = static_cast<O*>(a.grad) + row * a.ld_g;
+    const bool vec = grads_aligned<S, O>(r, grow);
+    const float4 st = a.row_stats[row];
+    if (st.w == 0.f) {
+        zero_grads<S, O>(r, sl, grow, vec, tid, kConsumers + 32);
+        return;
+    }
+    int issued = 0;
+    if (tid == kConsumers) {
+        init_barriers(bar, a.nbuf);
+        for (; issued < min(sl.nst, a.nbuf); ++issued) issue_stage(smem, bar, a.nbuf, r, sl, issued, issued);
+    }
+    const float cw = a.go[a.red == VCE_RED_NONE ? row : 0] * st.w;
+    __syncthreads();
+    if (warp == kConsumerWarps) {
+        if (tid == kConsumers)
+            for (; issued < sl.nst; ++issued)
+                if (!issue_stage(smem, bar, a.nbuf, r, sl, issued, issued)) break;
+    } else {
+        const float coef = cw * a.tau * st.y, bias = st.x == -kInf ? 0.f : st.x * kLog2e;
+        for (int j = 0; j < sl.nst; ++j) {
+            wait_stage(bar, a.nbuf, j);
+            uint4 x[kU];
+            load_stage<S>(smem, a.nbuf, r, sl, j, j, tid, x);
+            release_stage(bar, a.nbuf, j);
+            write_grads<S, O>(x, r, sl, j, tid, grow, vec, coef, a.k2, bias);
+        }
+    }
+    __syncthreads();
+    for (int k = tid; k < a.K; k += kConsumers + 32) {
+        const int64_t id = a.ids[row * a.K + k];
+        if (id < 0 || id >= a.V) continue;
+        const int v = (int)(id + r.shift) / G - sl.v0;
+        if (v >= 0 && v < sl.n) Elt<O>::store1(grow + id, cw * a.top_grads[row * a.K + k]);
+    }
+    if (bar.abort && tid == kConsumers) drain(bar, a.nbuf, issued);
+}
+
+// ---- N before a one-pass MEAN, and the losses' sum ----------------------------------------------------
+
+constexpr int kReduceThreads = 1024;
+
+// block sum of one integer per thread
+__device__ __forceinline__ long long block_count(long long n, long long* sm) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, off);
+    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = n;
+    __syncthreads();
+    long long t = 0;
+    for (int w = 0; w < kReduceThreads / 32; ++w) t += sm[w];
+    return t;
+}
+
+__global__ void __launch_bounds__(kReduceThreads) k_distill_count(const int64_t* ids, int K, const int64_t* labels,
+                                                                  int64_t ignore_index, int64_t T, float* inv_n) {
+    __shared__ long long sm[kReduceThreads / 32];
+    long long n = 0;
+#pragma unroll 8
+    for (int64_t i = threadIdx.x; i < T; i += kReduceThreads)
+        n += ids[i * K] != -1 && !(labels && labels[i] == ignore_index);
+    n = block_count(n, sm);
+    if (threadIdx.x == 0) *inv_n = n > 0 ? (float)(1.0 / (double)n) : 0.f;
+}
+
+// loss_out, status, and the rows' weights (1, a negative error code or 0 on entry; read only where
+// MEAN needs N, the codes always).
+__global__ void __launch_bounds__(kReduceThreads) k_distill_reduce(const float* loss_rows, float4* row_stats, int64_t T,
+                                                                   int red, float* loss_out, int32_t* status) {
+    __shared__ long long sm[kReduceThreads / 32];
+    __shared__ float sum[kReduceThreads / 32], comp[kReduceThreads / 32];
+    __shared__ int code;
+    if (threadIdx.x == 0) code = 0;
+    __syncthreads();
+    long long n = 0;
+    int mine = 0;
+#pragma unroll 8
+    for (int64_t i = threadIdx.x; i < T; i += kReduceThreads) {
+        const float w = row_stats[i].w;
+        n += w != 0.f;
+        if (w < 0.f) mine = max(mine, (int)-w);
+    }
+    if (mine) atomicMax(&code, mine);
+    n = block_count(n, sm);
+    const float weight = red == VCE_RED_MEAN ? (n > 0 ? (float)(1.0 / (double)n) : 0.f) : 1.f;
+#pragma unroll 8
+    for (int64_t i = threadIdx.x; i < T; i += kReduceThreads) {
+        const float w = row_stats[i].w;
+        row_stats[i].w = w > 0.f ? weight : 0.f;
+    }
+    if (red != VCE_RED_NONE) fold::sum_losses<kReduceThreads>(loss_rows, T, n, red, loss_out, sum, comp);
+    if (threadIdx.x == 0) *status = code;
+}
+
+// ---- host ----------------------------------------------------------------------------------------------
+
+// Blocks of a row: enough that a slice's stages (and, in one pass, the whole slice) leave room for
+// three blocks an SM, and, for few rows, enough blocks for the SMs.
+void shape(int64_t T, int64_t V, int G, bool hold, int K, int sms, int* cluster, int* nbuf, int* stages) {
+    const int64_t nv = (V + 2 * G - 2) / G;   // vectors of a row, at most
+    int C = 1;
+    auto st = [&](int c) { return (int)(((nv + c - 1) / c + kStageVecs - 1) / kStageVecs); };
+    const int fit = 4;                         // stages of 16 KB beside the marks: three blocks an SM
+    while (C < kMaxCluster && ((hold && st(C) > fit) || (T * C < 2 * sms && st(C) > 1))) C *= 2;
+    int nb = std::min(st(C), fit);
+    if (hold && st(C) > fit) {                 // long rows: as much of the slice as fits one block an SM
+        nb = std::min(st(C), kMaxBufs);
+        while (nb > fit && smem_bytes(nb, st(C), K) > 232448) --nb;
+    }
+    while (C < kMaxCluster && smem_bytes(nb, st(C), K) > 232448) C *= 2;
+    *cluster = C;
+    *stages = st(C);
+    *nbuf = std::max(1, std::min(nb, st(C)));
+}
+
+template <typename S, typename O, bool kGrad>
+cudaError_t run(Args& a, int sms, cudaStream_t s) {
+    shape(a.T, a.V, Elt<S>::kGroup, kGrad, a.K, sms, &a.cluster, &a.nbuf, &a.max_stages);
+    const int bytes = smem_bytes(a.nbuf, a.max_stages, a.K);
+    return launch_clusters(k_distill<S, O, kGrad>, a.T * a.cluster, a.cluster, kThreads, bytes, s, a);
+}
+
+template <typename S, typename O>
+cudaError_t run_bwd(BwdArgs& a, cudaStream_t s) {
+    constexpr int G = Elt<S>::kGroup;
+    const int64_t nv = (a.V + 2 * G - 2) / G;
+    a.parts = (int)((nv + 4 * kStageVecs - 1) / (4 * kStageVecs));   // four stages a block
+    a.nbuf = (int)std::min<int64_t>(4, (nv + kStageVecs - 1) / kStageVecs);
+    const int bytes = a.nbuf * kStageBytes + (int)sizeof(Barriers);
+    return launch_clusters(k_distill_bwd<S, O>, a.T * a.parts, 1, kConsumers + 32, bytes, s, a);
+}
+
+int check_shape(int dt, int64_t T, int64_t V, int64_t ld, int K, float tau, int red) {
+    if (dt != VCE_F32 && dt != VCE_BF16) return VCE_ERR_DTYPE;
+    if (red != VCE_RED_NONE && red != VCE_RED_SUM && red != VCE_RED_MEAN) return VCE_ERR_DTYPE;
+    // blocks of a launch stay within the grid's 2^31
+    if (T < 0 || T > VCE_MAX_TOPK_T || V < 1 || V > VCE_MAX_TOPK_V) return VCE_ERR_SHAPE;
+    if (K < 1 || K > VCE_MAX_TOPK || K > V || !temperature_ok(tau)) return VCE_ERR_ARG;
+    if (ld < V) return VCE_ERR_LD;
+    if (!fits_bytes(T, ld, dt == VCE_BF16 ? 2 : 4)) return VCE_ERR_SHAPE;
+    return VCE_OK;
+}
+
+}  // namespace distill
+
+VCE_DEBUG_READER(debug_word_distill)
+
+namespace {
+
+using namespace distill;
+
+int forward_checks(const Args& a, vce_dtype dt, vce_dtype tdt, float tau, const int32_t* status) {
+    int rc = check_shape(dt, a.T, a.V, a.ld, a.K, tau, a.red);
+    if (rc) return rc;
+    if (tdt != VCE_F32 && tdt != VCE_BF16) return VCE_ERR_DTYPE;
+    if (!status || (a.T && (!a.logits || !a.ids || !a.tvals || !a.loss_rows || !a.row_stats)))
+        return VCE_ERR_NULL;
+    if (!aligned(a.logits, dt == VCE_BF16 ? 2 : 4) || !aligned(a.ids, 8) || !aligned(a.tvals, tdt == VCE_BF16 ? 2 : 4) ||
+        !aligned(a.tail, 4) || !aligned(a.labels, 8) || !aligned(a.loss_rows, 4) || !aligned(a.row_stats, 16) ||
+        !aligned(status, 4))
+        return VCE_ERR_ALIGN;
+    return VCE_OK;
+}
+
+cudaError_t reduce(const Args& a, float* loss_out, int32_t* status, cudaStream_t s) {
+    k_distill_reduce<<<1, kReduceThreads, 0, s>>>(a.loss_rows, a.row_stats, a.T, a.red, loss_out, status);
+    return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace vce
+
+using namespace vce;
+
+extern "C" int ce_distill_forward(const void* logits, vce_dtype dt, int64_t T, int64_t V, int64_t ld,
+                                  const int64_t* teacher_ids, const void* teacher_values, vce_dtype tdt,
+                                  const float* teacher_tail, int K, float temperature, const int64_t* labels,
+                                  int64_t ignore_index, vce_reduction red, float* loss_rows, float* loss_out,
+                                  float* row_stats, float* top_grads, int32_t* status, vce_stream_t s) {
+    distill::Args a{};
+    a.logits = logits, a.T = T, a.V = V, a.ld = ld;
+    a.ids = teacher_ids, a.tvals = teacher_values, a.tail = teacher_tail, a.K = K, a.tbf16 = tdt == VCE_BF16;
+    a.tau = temperature, a.scale = 1.f / temperature, a.k2 = kLog2e / temperature;
+    a.labels = labels, a.ignore_index = ignore_index, a.red = red;
+    a.loss_rows = loss_rows, a.row_stats = reinterpret_cast<float4*>(row_stats), a.top_grads = top_grads;
+    int rc = forward_checks(a, dt, tdt, temperature, status);
+    if (rc) return rc;
+    if (red != VCE_RED_NONE && !loss_out) return VCE_ERR_NULL;
+    if (T && !top_grads) return VCE_ERR_NULL;
+    if (!aligned(top_grads, 4) || !aligned(loss_out, 4)) return VCE_ERR_ALIGN;
+    if ((rc = require_sm100())) return rc;
+    cudaError_t e = cudaSuccess;
+    if (T) {
+        const int sms = device_sm_count();
+        e = dt == VCE_BF16 ? distill::run<uint16_t, float, false>(a, sms, s) : distill::run<float, float, false>(a, sms, s);
+    }
+    if (e == cudaSuccess) e = reduce(a, loss_out, status, s);
+    return record_cuda(e) == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
+}
+
+extern "C" int ce_distill_backward(const void* logits, vce_dtype dt, int64_t T, int64_t V, int64_t ld,
+                                   const int64_t* teacher_ids, int K, float temperature, vce_reduction red,
+                                   const float* row_stats, const float* top_grads, const float* grad_output,
+                                   void* grad_logits, vce_dtype grad_dt, int64_t ld_grad, vce_stream_t s) {
+    int rc = distill::check_shape(dt, T, V, ld, K, temperature, red);
+    if (rc) return rc;
+    if (grad_dt != VCE_F32 && grad_dt != VCE_BF16) return VCE_ERR_DTYPE;
+    if (ld_grad < V) return VCE_ERR_LD;
+    const size_t es = dt == VCE_BF16 ? 2 : 4, gs = grad_dt == VCE_BF16 ? 2 : 4;
+    if (!fits_bytes(T, ld_grad, gs)) return VCE_ERR_SHAPE;
+    if (T == 0) return VCE_OK;
+    if (!logits || !teacher_ids || !row_stats || !top_grads || !grad_output || !grad_logits) return VCE_ERR_NULL;
+    if (!aligned(logits, es) || !aligned(grad_logits, gs) || !aligned(teacher_ids, 8) || !aligned(row_stats, 16) ||
+        !aligned(top_grads, 4) || !aligned(grad_output, 4))
+        return VCE_ERR_ALIGN;
+    if (rs::overlap(logits, T, V, ld, es, grad_logits, ld_grad, gs)) return VCE_ERR_ARG;
+    if ((rc = require_sm100())) return rc;
+    distill::BwdArgs a{};
+    a.logits = logits, a.T = T, a.V = V, a.ld = ld, a.ids = teacher_ids, a.K = K;
+    a.tau = temperature, a.k2 = kLog2e / temperature, a.red = red;
+    a.row_stats = reinterpret_cast<const float4*>(row_stats), a.top_grads = top_grads, a.go = grad_output;
+    a.grad = grad_logits, a.ld_g = ld_grad;
+    cudaError_t e;
+    if (dt == VCE_BF16)
+        e = grad_dt == VCE_BF16 ? distill::run_bwd<uint16_t, uint16_t>(a, s) : distill::run_bwd<uint16_t, float>(a, s);
+    else
+        e = grad_dt == VCE_BF16 ? distill::run_bwd<float, uint16_t>(a, s) : distill::run_bwd<float, float>(a, s);
+    return record_cuda(e) == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
+}
+
+extern "C" int ce_distill_forward_backward(const void* logits, vce_dtype dt, int64_t T, int64_t V, int64_t ld,
+                                           const int64_t* teacher_ids, const void* teacher_values, vce_dtype tdt,
+                                           const float* teacher_tail, int K, float temperature,
+                                           const int64_t* labels, int64_t ignore_index, vce_reduction red,
+                                           const float* grad_output, float* loss_rows, float* loss_out,
+                                           float* row_stats, void* grad_logits, vce_dtype grad_dt, int64_t ld_grad,
+                                           int32_t* status, vce_stream_t s) {
+    distill::Args a{};
+    a.logits = logits, a.T = T, a.V = V, a.ld = ld;
+    a.ids = teacher_ids, a.tvals = teacher_values, a.tail = teacher_tail, a.K = K, a.tbf16 = tdt == VCE_BF16;
+    a.tau = temperature, a.scale = 1.f / temperature, a.k2 = kLog2e / temperature;
+    a.labels = labels, a.ignore_index = ignore_index, a.red = red, a.go = grad_output, a.inv_n = loss_out;
+    a.loss_rows = loss_rows, a.row_stats = reinterpret_cast<float4*>(row_stats);
+    a.grad = grad_logits, a.ld_g = ld_grad;
+    int rc = forward_checks(a, dt, tdt, temperature, status);
+    if (rc) return rc;
+    if (grad_dt != VCE_F32 && grad_dt != VCE_BF16) return VCE_ERR_DTYPE;
+    if (ld_grad < V) return VCE_ERR_LD;
+    const size_t gs = grad_dt == VCE_BF16 ? 2 : 4;
+    if (!fits_bytes(T, ld_grad, gs)) return VCE_ERR_SHAPE;
+    if (red != VCE_RED_NONE && !loss_out) return VCE_ERR_NULL;
+    if (T && (!grad_output || !grad_logits)) return VCE_ERR_NULL;
+    if (!aligned(grad_output, 4) || !aligned(grad_logits, gs) || !aligned(loss_out, 4)) return VCE_ERR_ALIGN;
+    if (T && rs::overlap(logits, T, V, ld, dt == VCE_BF16 ? 2 : 4, grad_logits, ld_grad, gs)) return VCE_ERR_ARG;
+    if ((rc = require_sm100())) return rc;
+    cudaError_t e = cudaSuccess;
+    if (T) {
+        if (red == VCE_RED_MEAN) {
+            distill::k_distill_count<<<1, distill::kReduceThreads, 0, s>>>(teacher_ids, K, labels, ignore_index, T,
+                                                                           loss_out);
+            e = cudaGetLastError();
+        }
+        const int sms = device_sm_count();
+        if (e != cudaSuccess) ;
+        else if (dt == VCE_BF16)
+            e = grad_dt == VCE_BF16 ? distill::run<uint16_t, uint16_t, true>(a, sms, s)
+                                    : distill::run<uint16_t, float, true>(a, sms, s);
+        else
+            e = grad_dt == VCE_BF16 ? distill::run<float, uint16_t, true>(a, sms, s)
+                                    : distill::run<float, float, true>(a, sms, s);
+    }
+    if (e == cudaSuccess) e = reduce(a, loss_out, status, s);
+    return record_cuda(e) == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
+}

@@ -7,6 +7,7 @@
 #include "vce.h"
 #include "vce_check.cuh"
 #include "vce_host.h"
+#include "vce_logits.h"
 
 namespace vce {
 
@@ -60,6 +61,9 @@ extern "C" const char* vce_status_string(int status) {
     switch (status) {
         case VCE_OK: return "ok";
         case VCE_ERR_LABEL: return "a label is neither ignore_index nor in [0, V)";
+        case VCE_ERR_TEACHER: return "a teacher id outside [0, V), one twice in a row, or a teacher without mass";
+        case VCE_ERR_PARAM: return "a temperature or repetition penalty is not finite and > 0";
+        case VCE_ERR_OFFSETS: return "row offsets descend or leave their list";
         case VCE_ERR_NULL: return "a required pointer is NULL";
         case VCE_ERR_DTYPE: return "unknown or unsupported dtype or reduction";
         case VCE_ERR_SHAPE: return "invalid or overflowing size";
@@ -109,7 +113,8 @@ extern "C" int vce_debug_status(int32_t* host_out) {
     if (cudaDeviceSynchronize() != cudaSuccess) return VCE_ERR_CUDA;
     int (*const readers[])(int32_t*) = {vce::debug_word_ce_fwd,   vce::debug_word_ce_bwd, vce::debug_word_ce_fwd_ring,
                                         vce::debug_word_ce_bwd_ring, vce::debug_word_ce_ring, vce::debug_word_ce_fused,
-                                        vce::debug_word_lce,      vce::debug_word_gemm_hooks};
+                                        vce::debug_word_lce,      vce::debug_word_gemm_hooks, vce::debug_word_topk,
+                                        vce::debug_word_distill,  vce::debug_word_process};
     for (auto rd : readers) {
         int32_t w = 0;
         if (rd(&w) != 0) return VCE_ERR_CUDA;

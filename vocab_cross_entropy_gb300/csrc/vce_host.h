@@ -45,6 +45,9 @@ int debug_word_ce_bwd_ring(int32_t* out);
 int debug_word_ce_ring(int32_t* out);
 int debug_word_ce_fused(int32_t* out);
 int debug_word_lce(int32_t* out);
+int debug_word_topk(int32_t* out);
+int debug_word_distill(int32_t* out);
+int debug_word_process(int32_t* out);
 int debug_word_gemm_hooks(int32_t* out);
 
 }  // namespace vce
