@@ -142,8 +142,7 @@ VCE_API int ce_distill_forward_backward(const void* logits, vce_dtype dt, int64_
  *                                column once), [n_bias] fp32, [T + 1] int64
  *   mask, mask_ld                [T, mask_ld] 32-bit words, bit j % 32 of word j / 32 allows column j;
  *                                mask_ld >= ceil(V / 32) words
- *   out, out_dt, ld_out          [T, ld_out]; may be the logits themselves (same dtype and leading
- *                                dimension); VCE_ERR_ARG if it overlaps them otherwise
+ *   out, out_dt, ld_out          [T, ld_out]; VCE_ERR_ARG if it overlaps the logits
  *   row_status                   [T] int32, written for every row: 0; VCE_ERR_LABEL (a history or
  *                                bias id outside [0, V), skipped, or bias ids not ascending);
  *                                VCE_ERR_PARAM (a temperature or repetition penalty that is not
@@ -166,8 +165,7 @@ VCE_API int logits_process(const void* logits, vce_dtype dt, int64_t T, int64_t 
  * The penalties n f, p and the biases do not enter.
  *   grad_out, gdt, ld_gout   [T, ld_gout];  logits, dt, ld: the unprocessed ones (read at the
  *                            columns of the history only; may be NULL without a history)
- *   grad_logits, grad_dt, ld_grad   [T, ld_grad]; may be grad_out itself (same dtype and leading
- *                            dimension); VCE_ERR_ARG if it overlaps it otherwise, or the logits
+ *   grad_logits, grad_dt, ld_grad   [T, ld_grad]; VCE_ERR_ARG if it overlaps grad_out or the logits
  */
 VCE_API int logits_process_backward(const void* grad_out, vce_dtype gdt, int64_t T, int64_t V, int64_t ld_gout,
                                     const void* logits, vce_dtype dt, int64_t ld,

@@ -124,13 +124,13 @@ def test_refusals_of_the_library(vce):
     assert proc(dt=9) == -2 and proc(odt=9) == -2 and proc(V=0) == -3 and proc(ld=63) == -4 and proc(old=63) == -4
     assert proc(mask=x, mld=1) == -4 and proc(hist=x) == -1 and proc(bias=x, boff=x) == -1 and proc(off=x) == -1
     assert proc(rep=x) == -1                                     # a penalty without a history
-    assert proc(out=x, odt=0) == -8 and proc(out=x + 2) == -8 and proc(out=x, old=65) == -8
+    assert proc(out=x) == -8 and proc(out=x, odt=0) == -8 and proc(out=x + 2) == -8 and proc(out=x, old=65) == -8
     assert proc(rs=None) == -1 and proc(temp=x + 2) == -5 and proc(n=-1) == -3 and proc(T=0) == 0
 
     def procb(z=0x900000, grad=0x1900000, hist=x, off=x, ld=64):
         return lib.logits_process_backward(x, 1, 4, 64, 64, z, 1, ld, None, None, hist, 0, off, None, 0, grad, 1, 64, x,
                                            None)
-    assert procb(z=None) == -1 and procb(ld=60) == -4 and procb(grad=0x900000) == -8
+    assert procb(z=None) == -1 and procb(ld=60) == -4 and procb(grad=0x900000) == -8 and procb(grad=x) == -8
 
 
 def test_refusals_of_the_wrappers(vce):

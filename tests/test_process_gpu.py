@@ -79,15 +79,10 @@ class Case:
 EPS = {BF16: 2.0 ** -7, F32: 2.0 ** -23}
 
 
-def check(vce, c, odtype=None, in_place=False):
+def check(vce, c, odtype=None):
     odtype = odtype or c.z.dtype
     want, size = c.oracle()
-    if in_place:
-        z = c.z.clone(memory_format=torch.preserve_format) if c.z.is_contiguous() else c.z
-        out, status = vce.logits_process(z, out=z, **c.kwargs())
-        assert out.data_ptr() == z.data_ptr()
-    else:
-        out, status = vce.logits_process(c.z, out_dtype=odtype, **c.kwargs())
+    out, status = vce.logits_process(c.z, out_dtype=odtype, **c.kwargs())
     assert out.dtype is odtype and torch.all(status == 0)
     G.check_processed(out.double().cpu().numpy(), want, size, EPS[odtype])
 
@@ -107,10 +102,21 @@ def test_process_layouts(vce, V, pad, left, dtype, odtype):
     check(vce, Case(7, V, dtype, 100, 10, True, pad=pad, left=left), odtype)
 
 
-@pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("V,pad,left", [(5001, 0, 0), (5001, 3, 2), (40000, 0, 0)])
-def test_process_in_place(vce, V, pad, left, dtype):
-    check(vce, Case(6, V, dtype, 200, 30, True, pad=pad, left=left), in_place=True)
+def test_process_history_lengths(vce):
+    """Rows of no token to many in one call: hash tables of every size, and windows of columns for the
+    rows that are too long for them."""
+    for V, lens in ((40000, [0, 1, 47, 48, 49, 383, 384, 385, 3000, 12288, 12289, 60000]), (70001, [0] * 40 + [9000]),
+                    (33, [0, 500, 2000]), (9000, [5000, 30000])):
+        c = Case(len(lens), V, BF16, 8, 3, True)
+        rng = np.random.default_rng(V)
+        c.hist = [rng.integers(0, V, n) if i % 2 else rng.integers(0, min(V, 700), n) for i, n in enumerate(lens)]
+        c.prompt = np.array([n // 3 for n in lens])
+        check(vce, c, F32)
+        up = torch.randn(c.T, V, device="cuda").to(BF16)
+        want, size = c.oracle(up)
+        g, status = vce.logits_process_backward(up, c.z, grad_dtype=F32, **c.kwargs(backward=True))
+        assert torch.all(status == 0)
+        G.check_processed(g.double().cpu().numpy(), want, size, EPS[F32])
 
 
 @pytest.mark.parametrize("dtype,odtype", [(BF16, F32), (F32, BF16), (F32, F32)])
@@ -149,9 +155,6 @@ def test_process_backward(vce, T, V, history, mask, dtype, gdtype):
     g, status = vce.logits_process_backward(up, c.z, **c.kwargs(backward=True))
     assert g.dtype is dtype and torch.all(status == 0)
     G.check_processed(g.double().cpu().numpy(), want, size, EPS[dtype])
-    if gdtype is dtype:
-        same, _ = vce.logits_process_backward(up, c.z, grad_logits=up, **c.kwargs(backward=True))
-        assert torch.equal(same, g)
 
 
 def test_process_autograd(vce):
@@ -238,6 +241,11 @@ def test_process_refusals(vce):
         vce.logits_process(c.z, **bad(temperature=kw["temperature"][:2]))
     with pytest.raises(vce.VceError):
         vce.logits_process(c.z, repetition_penalty=kw["repetition_penalty"])
+    for over in (c.z, torch.cat([c.z, c.z])[2:6]):
+        with pytest.raises(vce.VceError):
+            vce.logits_process(over, out=over)
+    with pytest.raises(vce.VceError):
+        vce.logits_process_backward(c.z, c.z.clone(), grad_logits=c.z)
     with pytest.raises(vce.VceError):
         vce.logits_process(c.z, out=c.z.view(-1).view(BF16)[:400].view(4, 100))
     with pytest.raises(vce.VceError):
@@ -273,7 +281,7 @@ def test_a_teachers_masked_top_k_into_a_student(vce):
 
 
 def test_a_decoded_token(vce):
-    """One token of a batch: in-place processing, then the best tokens with their log-probabilities."""
+    """One token of a batch: its processed logits, then the best tokens with their log-probabilities."""
     c = Case(6, 128256, BF16, 500, 10, True, seed=5)
     out, status = vce.logits_process(c.z, out_dtype=F32, **c.kwargs())
     values, ids, lse, _ = vce.ce_topk(out, 5)
@@ -284,4 +292,5 @@ def test_a_decoded_token(vce):
     assert (~open_).sum() == 1 and torch.all(status == 0)          # the row with nothing allowed
     logp = (values - lse[:, None]).double().cpu().numpy()[open_]
     tol = G.lse_tol(np.abs(host[np.isfinite(host)]).max(), 1.0) + 2.0 ** -23 * 16
-    assert np.all(np.abs(logp - (rv - rl[:, None])[open_])[np.isfinite(rv[open_])] <= tol)
+    there = np.isfinite(rv[open_])
+    assert np.all(np.abs(logp[there] - (rv - rl[:, None])[open_][there]) <= tol)

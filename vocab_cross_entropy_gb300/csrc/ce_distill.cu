@@ -96,7 +96,9 @@ __device__ __forceinline__ float sigmoid_diff(float u, float v) {
 }
 
 // q phi(x), phi(x) = e^x - 1 - x, where p = q e^x: the power series of phi near 0 (to x^9 / 9!,
-// 2e-9 relative at 0.5), else p - q - q x, which loses at most two bits there.
+// 2e-9 relative at 0.5), else e^x - 1 - x, which loses at most two bits there.  Everything comes from
+// x, not from p: an error common to all x_k (a log-sum-exp's) then leaves the sum of the terms as it
+// is to first order, since both sides sum to 1.
 __device__ __forceinline__ float q_phi(float q, float p, float x) {
     if (!(q > 0.f)) return p;
     if (fabsf(x) < 0.5f) {
@@ -110,7 +112,7 @@ __device__ __forceinline__ float q_phi(float q, float p, float x) {
         c = fmaf(c, x, 0.5f);
         return q * (x * x * c);
     }
-    return (p - q) - q * x;
+    return x < 80.f ? q * (expm1f(x) - x) : (p - q) - q * x;   // e^x would overflow
 }
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -544,9 +546,9 @@ void shape(int64_t T, int64_t V, int G, bool hold, int K, int sms, int* cluster,
     int nb = std::min(st(C), fit);
     if (hold && st(C) > fit) {                 // long rows: as much of the slice as fits one block an SM
         nb = std::min(st(C), kMaxBufs);
-        while (nb > fit && smem_bytes(nb, st(C), K) > 232448) --nb;
+        while (nb > fit && smem_bytes(nb, st(C), K) > kMaxSmem) --nb;
     }
-    while (C < kMaxCluster && smem_bytes(nb, st(C), K) > 232448) C *= 2;
+    while (C < kMaxCluster && smem_bytes(nb, st(C), K) > kMaxSmem) C *= 2;
     *cluster = C;
     *stages = st(C);
     *nbuf = std::max(1, std::min(nb, st(C)));
@@ -556,7 +558,7 @@ template <typename S, typename O, bool kGrad>
 cudaError_t run(Args& a, int sms, cudaStream_t s) {
     shape(a.T, a.V, Elt<S>::kGroup, kGrad, a.K, sms, &a.cluster, &a.nbuf, &a.max_stages);
     const int bytes = smem_bytes(a.nbuf, a.max_stages, a.K);
-    return launch_clusters(k_distill<S, O, kGrad>, a.T * a.cluster, a.cluster, kThreads, bytes, s, a);
+    return launch_clusters<k_distill<S, O, kGrad>>(a.T * a.cluster, a.cluster, kThreads, bytes, s, a);
 }
 
 template <typename S, typename O>
@@ -566,7 +568,7 @@ cudaError_t run_bwd(BwdArgs& a, cudaStream_t s) {
     a.parts = (int)((nv + 4 * kStageVecs - 1) / (4 * kStageVecs));   // four stages a block
     a.nbuf = (int)std::min<int64_t>(4, (nv + kStageVecs - 1) / kStageVecs);
     const int bytes = a.nbuf * kStageBytes + (int)sizeof(Barriers);
-    return launch_clusters(k_distill_bwd<S, O>, a.T * a.parts, 1, kConsumers + 32, bytes, s, a);
+    return launch_clusters<k_distill_bwd<S, O>>(a.T * a.parts, 1, kConsumers + 32, bytes, s, a);
 }
 
 int check_shape(int dt, int64_t T, int64_t V, int64_t ld, int K, float tau, int red) {

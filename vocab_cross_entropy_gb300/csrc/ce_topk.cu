@@ -424,7 +424,7 @@ cudaError_t run(Args& a, int sms, cudaStream_t s) {
     a.cluster = C;
     a.max_stages = st(C);
     a.nbuf = std::min(3, st(C));
-    return launch_clusters(k_topk<S>, a.T * C, C, kThreads, smem_bytes(a.nbuf, a.max_stages), s, a);
+    return launch_clusters<k_topk<S>>(a.T * C, C, kThreads, smem_bytes(a.nbuf, a.max_stages), s, a);
 }
 
 }  // namespace topk

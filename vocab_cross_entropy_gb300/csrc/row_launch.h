@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <cmath>
 
 #include "vce.h"
@@ -13,25 +14,45 @@
 namespace vce {
 namespace rs {
 
-// blocks in clusters of `cluster` along x.
-template <typename Kern, typename Args>
-cudaError_t launch_clusters(Kern kern, int64_t blocks, int cluster, int threads, int smem, cudaStream_t s,
-                            const Args& args) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+constexpr int kMaxSmem = 232448;   // shared memory of a block, at most
+
+// Launches `blocks` blocks of kKernel in clusters of `cluster` along x.  A kernel is allowed all of
+// an SM's shared memory once per device (the attribute costs a launch about 2 us on the host); a
+// launch that fails is tried once more with the attribute set again, since a device reset drops it.
+template <auto kKernel, typename Args>
+cudaError_t launch_clusters(int64_t blocks, int cluster, int threads, int smem, cudaStream_t s, const Args& args) {
+    static std::atomic<uint64_t> allowed{0};   // bit d: device d (kMaxDevices = 64)
+    int d = 0;
+    cudaError_t e = cudaGetDevice(&d);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = d >= 0 && d < kMaxDevices ? 1ull << d : 0;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)cluster;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    int n = 0;
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = (unsigned)cluster;
+        attr[n].val.clusterDim.y = 1;
+        attr[n++].val.clusterDim.z = 1;
+    }
     cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, args);
+    cfg.numAttrs = (unsigned)n;
+    const bool known = (allowed.load(std::memory_order_acquire) & bit) != 0;
+    for (int tries = known ? 0 : 1; tries < 2; ++tries) {
+        if (tries) {
+            e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+            if (e != cudaSuccess) return e;
+            allowed.fetch_or(bit, std::memory_order_release);
+        }
+        e = cudaLaunchKernelEx(&cfg, kKernel, args);
+        if (e == cudaSuccess) return e;
+        if (!tries) (void)cudaGetLastError();
+    }
+    return e;
 }
 
 // Whether a [T, V] matrix of es-byte elements and another (same T and V) share any byte of their
