@@ -88,11 +88,12 @@ __device__ __forceinline__ float sigmoid(float x) {
     return (x >= 0.f ? 1.f : e) / (1.f + e);
 }
 
-// sigma(u) - sigma(v), without cancellation: sigma(u) sigma(-v) (1 - e^{v-u}).
+// sigma(u) - sigma(v), without cancellation: for u > v, sigma(u) sigma(-v) (1 - e^{v-u}).
 __device__ __forceinline__ float sigmoid_diff(float u, float v) {
     if (u == v) return 0.f;
-    const float d = v - u;
-    return d < 0.f ? -sigmoid(u) * sigmoid(-v) * expm1f(d) : sigmoid(-u) * sigmoid(v) * expm1f(-d);
+    const float hi = fmaxf(u, v), lo = fminf(u, v);
+    const float d = sigmoid(hi) * sigmoid(-lo) * -expm1f(lo - hi);
+    return u > v ? d : -d;
 }
 
 // q phi(x), phi(x) = e^x - 1 - x, where p = q e^x: the power series of phi near 0 (to x^9 / 9!,
@@ -128,22 +129,33 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 // ---- gradient entries ---------------------------------------------------------------------------
 
-// Writes the gradient coef 2^(z k2 - bias) of a thread's vectors of a stage.  vec: the row's
-// gradient vectors are aligned for GroupStore.
-template <typename S, typename O>
-__device__ __forceinline__ void write_grads(const uint4 (&x)[kU], const Row& r, const Slice& s, int j, int tid,
-                                            O* grow, bool vec, float coef, float k2, float bias) {
+// Writes the gradient coef 2^(z k2 - bias) of a thread's U vectors of a stage (zero: +0.0 whatever
+// they hold).  vec: the row's gradient vectors are aligned for GroupStore.
+template <typename S, typename O, int U, int NT>
+__device__ __forceinline__ void write_grads(const uint4 (&x)[U], const Row& r, const Slice& s, int j, int tid,
+                                            O* grow, bool vec, float coef, float k2, float bias, bool zero = false) {
     constexpr int G = Elt<S>::kGroup;
+    constexpr int B = U * NT;                        // vectors of a stage
+    const int v0 = s.v0 + j * B + tid;
+    const bool inside = vec && s.v0 + j * B >= r.iv0 && s.v0 + (j + 1) * B <= min(s.v0 + s.n, r.iv1);
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-        const int v = s.v0 + j * kStageVecs + tid + u * kConsumers;
-        if (v >= s.v0 + s.n) continue;
+    for (int u = 0; u < U; ++u) {
+        const int v = v0 + u * NT;
+        if (!inside && v >= s.v0 + s.n) continue;
         float g[G];
         Elt<S>::unpack(x[u], g);
 #pragma unroll
-        for (int k = 0; k < G; ++k) g[k] = coef * ex2(fmaf(g[k], k2, -bias));
+        for (int k = 0; k < G; k += 2) {
+            float a0, a1;
+            ffma2(g[k], g[k + 1], k2, -bias, a0, a1);
+            fmul2(ex2(a0), ex2(a1), coef, g[k], g[k + 1]);
+        }
+        if (zero) {
+#pragma unroll
+            for (int k = 0; k < G; ++k) g[k] = 0.f;
+        }
         const int64_t c0 = (int64_t)v * G - r.shift;
-        if (vec && v >= r.iv0 && v < r.iv1) {
+        if (inside || (vec && v >= r.iv0 && v < r.iv1)) {
             GroupStore<O, G>::run(grow + c0, g);
         } else {
 #pragma unroll
@@ -173,6 +185,94 @@ template <typename S, typename O>
 __device__ __forceinline__ bool grads_aligned(const Row& r, const O* grow) {
     constexpr int G = Elt<S>::kGroup;
     return (reinterpret_cast<uintptr_t>(grow - r.shift) % (GroupStore<O, G>::kAlign)) == 0;
+}
+
+// ---- a row's scalars -------------------------------------------------------------------------------
+
+// All arithmetic on the K entries, by one warp (lane + 32 i: entry k; col -1: none, z, t -inf there):
+// each entry's (r_k, r_k - qh_k), the largest z, log sum e^{s (z - max)}, Lq and sum qh phi.
+__device__ __forceinline__ void top_arithmetic(const Args& a, int K, int lane, const int (&col)[kPerLane],
+                                               const float (&z)[kPerLane], const float (&t)[kPerLane], Entry* entry,
+                                               float& zm, float& lnr, float& lq, float& kl) {
+    float tm = -kInf;
+    zm = -kInf;
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) {
+        zm = fmaxf(zm, z[i]);
+        tm = fmaxf(tm, t[i]);
+    }
+    zm = warp_max(zm);
+    tm = warp_max(tm);
+    float rs_ = 0.f, qs = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) {
+        if (32 * i >= K) break;
+        if (z[i] > -kInf) rs_ += expf((z[i] - zm) * a.scale);
+        if (col[i] >= 0 && t[i] != -kInf) qs += expf((t[i] - tm) * a.scale);   // NaN: the row is refused
+    }
+    rs_ = warp_sum(rs_);
+    qs = warp_sum(qs);
+    const float lnq = logf(qs), inv_r = 1.f / rs_, inv_q = 1.f / qs;
+    lnr = logf(rs_);
+    kl = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) {
+        const int k = lane + 32 * i;
+        if (32 * i >= K) break;
+        if (k >= K) continue;
+        float rk = 0.f, diff = 0.f;
+        if (col[i] >= 0) {
+            float qk = 0.f, y = -kInf;
+            if (z[i] > -kInf) rk = expf((z[i] - zm) * a.scale) * inv_r;
+            if (t[i] > -kInf) qk = expf((t[i] - tm) * a.scale) * inv_q;
+            if (z[i] > -kInf && t[i] > -kInf) {
+                // log(r_k / qh_k): differences of logits first, which are exact or nearly so
+                y = ((z[i] - zm) - (t[i] - tm)) * a.scale - (lnr - lnq);
+                diff = y < 0.5f ? qk * expm1f(y) : rk - qk;
+            } else {
+                diff = rk - qk;
+            }
+            kl += q_phi(qk, rk, y);
+        }
+        entry[k] = Entry{rk, diff, col[i], 0};
+    }
+    kl = warp_sum(kl);
+    lq = tm > -kInf ? tm * a.scale + lnq : tm;   // -inf: no mass among the entries; NaN stays
+}
+
+// What the gradient needs of a row's masses, in few dependent steps (consumers wait for it), and what
+// the loss needs besides.
+struct Finish {
+    float lt, d, q;              // L', p_T - q_T, Q
+    float at, b;                 // Q = sigma(at), P = sigma(b)
+    int code;                    // the row's error
+    bool dead;                   // no gradient (an error, or a student row of -inf only)
+};
+
+// From the tail's pair (M, S0), the entries' scalars and the teacher's tail R.
+__device__ __forceinline__ Finish finish_row(const Args& a, float M, float S0, float zmax, float lnr, float Lq,
+                                             float R, int code) {
+    Finish f;
+    f.code = code;
+    if (!code && !((Lq > -kInf || R > -kInf) && Lq < kInf && R < kInf)) f.code = VCE_ERR_TEACHER;   // no finite mass
+    const bool has_tail = S0 > 0.f, has_top = zmax > -kInf;
+    const float ln_s = has_tail ? logf(S0) : 0.f;
+    if (has_tail && has_top) f.b = (zmax - M) * a.scale + (lnr - ln_s);
+    else f.b = has_top ? kInf : -kInf;
+    f.at = Lq == -kInf ? -kInf : Lq - R;             // R = -inf: +inf
+    f.q = sigmoid(f.at);
+    f.d = sigmoid_diff(-f.b, -f.at);                 // p_T - q_T
+    f.dead = f.code || !(has_tail || has_top);
+    f.lt = has_tail ? M * a.scale + ln_s : -kInf;
+    return f;
+}
+
+// tau^2 KL from the row's masses and the entries' sum of qh phi; NaN where there is no loss.
+__device__ __forceinline__ float loss_of(const Args& a, const Finish& f, float kl_top) {
+    float kl = q_phi(f.q, sigmoid(f.b), softplus_f(-f.at) - softplus_f(-f.b)) +
+               q_phi(sigmoid(-f.at), sigmoid(-f.b), softplus_f(f.at) - softplus_f(f.b));
+    if (f.q > 0.f) kl += f.q * kl_top;
+    return f.dead ? __int_as_float(0x7FC00000) : a.tau * a.tau * kl;
 }
 
 // ---- the row kernel -------------------------------------------------------------------------------
@@ -269,49 +369,12 @@ __global__ void __launch_bounds__(kThreads, 3) k_distill(const __grid_constant__
                                : Elt<float>::load1(static_cast<const float*>(a.tvals) + row * a.K + k);
             }
         }
-        float zm = -kInf, tm = -kInf;
-#pragma unroll
-        for (int i = 0; i < kPerLane; ++i) {
-            zm = fmaxf(zm, z[i]);
-            tm = fmaxf(tm, t[i]);
-        }
-        zm = warp_max(zm);
-        tm = warp_max(tm);
-        float rs_ = 0.f, qs = 0.f;
-#pragma unroll
-        for (int i = 0; i < kPerLane; ++i) {
-            if (z[i] > -kInf) rs_ += expf((z[i] - zm) * a.scale);
-            if (col[i] >= 0 && t[i] != -kInf) qs += expf((t[i] - tm) * a.scale);   // NaN: the row is refused below
-        }
-        rs_ = warp_sum(rs_);
-        qs = warp_sum(qs);
-        const float lnr = logf(rs_), lnq = logf(qs), inv_r = 1.f / rs_, inv_q = 1.f / qs;
-        float kl = 0.f;
-#pragma unroll
-        for (int i = 0; i < kPerLane; ++i) {
-            const int k = lane + 32 * i;
-            if (k >= a.K) continue;
-            float rk = 0.f, diff = 0.f;
-            if (col[i] >= 0) {
-                float qk = 0.f, y = -kInf;
-                if (z[i] > -kInf) rk = expf((z[i] - zm) * a.scale) * inv_r;
-                if (t[i] > -kInf) qk = expf((t[i] - tm) * a.scale) * inv_q;
-                if (z[i] > -kInf && t[i] > -kInf) {
-                    // log(r_k / qh_k): differences of logits first, which are exact or nearly so
-                    y = ((z[i] - zm) - (t[i] - tm)) * a.scale - (lnr - lnq);
-                    diff = y < 0.5f ? qk * expm1f(y) : rk - qk;
-                } else {
-                    diff = rk - qk;
-                }
-                kl += q_phi(qk, rk, y);
-            }
-            entry[k] = Entry{rk, diff, col[i], 0};
-        }
-        kl = warp_sum(kl);
+        float zm, lnr, lq, kl;
+        top_arithmetic(a, a.K, lane, col, z, t, entry, zm, lnr, lq, kl);
         if (lane == 0) {
             ctl.zmax = zm;
             ctl.lnr = lnr;
-            ctl.lq = tm > -kInf ? tm * a.scale + lnq : tm;   // -inf: no mass among the entries; NaN stays
+            ctl.lq = lq;
             ctl.kl_top = kl;
         }
     } else {
@@ -360,43 +423,32 @@ __global__ void __launch_bounds__(kThreads, 3) k_distill(const __grid_constant__
             code = max(code, __float_as_int(o.z));
         }
     }
-    const float R = a.tail ? a.tail[row] : -kInf, Lq = ctl.lq;
-    if (!code && !((Lq > -kInf || R > -kInf) && Lq < kInf && R < kInf)) code = VCE_ERR_TEACHER;   // no finite mass
-    const bool has_tail = S0 > 0.f, has_top = ctl.zmax > -kInf;
-    float b;
-    if (has_tail && has_top) b = (ctl.zmax - M) * a.scale + (ctl.lnr - logf(S0));
-    else b = has_top ? kInf : -kInf;
-    const float at = Lq == -kInf ? -kInf : Lq - R;   // R = -inf: +inf
-    const float P = sigmoid(b), pT = sigmoid(-b), Q = sigmoid(at), qT = sigmoid(-at);
-    const float D = sigmoid_diff(-b, -at);           // p_T - q_T
-    const bool dead = code || !(has_tail || has_top);
-    const float Lt = has_tail ? M * a.scale + logf(S0) : -kInf;
-    if (rank == 0 && tid == 0) {
-        float kl = q_phi(Q, P, softplus_f(-at) - softplus_f(-b)) + q_phi(qT, pT, softplus_f(at) - softplus_f(b));
-        if (Q > 0.f) kl += Q * ctl.kl_top;
-        a.loss_rows[row] = dead ? __int_as_float(0x7FC00000) : a.tau * a.tau * kl;
+    const Finish f = finish_row(a, M, S0, ctl.zmax, ctl.lnr, ctl.lq, a.tail ? a.tail[row] : -kInf, code);
+    const bool dead = f.dead;
+    if (rank == 0 && tid == kProducerWarp * 32) {
+        a.loss_rows[row] = loss_of(a, f, ctl.kl_top);
         // weight: 1, negative for a row with an error, until the reduction writes it
-        a.row_stats[row] = make_float4(Lt, dead ? 0.f : D, 0.f, code ? -(float)code : 1.f);
+        a.row_stats[row] = make_float4(f.lt, dead ? 0.f : f.d, 0.f, f.code ? -(float)f.code : 1.f);
     }
     if (!kGrad) {
         if (rank == 0)
             for (int k = tid; k < a.K; k += kThreads) {
                 const Entry e = entry[k];
-                a.top_grads[row * a.K + k] = dead || e.col < 0 ? 0.f : a.tau * (Q * e.diff - D * e.r);
+                a.top_grads[row * a.K + k] = dead || e.col < 0 ? 0.f : a.tau * (f.q * e.diff - f.d * e.r);
             }
     } else if (dead) {
         zero_grads<S, O>(r, sl, grow, vec, tid, kThreads);
     } else {
         const float c = a.go[a.red == VCE_RED_NONE ? row : 0] * (a.red == VCE_RED_MEAN ? *a.inv_n : 1.f) * a.tau;
         if (warp < kConsumerWarps) {
-            const float coef = c * D, bias = has_tail ? Lt * kLog2e : 0.f;
+            const float coef = c * f.d, bias = f.lt > -kInf ? f.lt * kLog2e : 0.f;
             for (int j = 0; j < sl.nst; ++j) {
                 const int q = held ? j : sl.nst + j;
                 if (!held) wait_stage(ctl.bar, a.nbuf, q);
                 uint4 x[kU];
                 load_stage<S>(bufs, a.nbuf, r, sl, j, q, tid, x);
                 if (!held) release_stage(ctl.bar, a.nbuf, q);
-                write_grads<S, O>(x, r, sl, j, tid, grow, vec, coef, a.k2, bias);
+                write_grads<S, O, kU, kConsumers>(x, r, sl, j, tid, grow, vec, coef, a.k2, bias);
             }
         } else if (tid == kProducerWarp * 32) {
             for (; issued < total; ++issued)
@@ -407,12 +459,520 @@ __global__ void __launch_bounds__(kThreads, 3) k_distill(const __grid_constant__
             const Entry e = entry[k];
             const int v = e.col >= 0 ? (e.col + r.shift) / G - sl.v0 : -1;
             if (v >= 0 && v < sl.n && dbg::ok(e.col < a.V, dbg::kCols))
-                Elt<O>::store1(grow + e.col, c * (Q * e.diff - D * e.r));
+                Elt<O>::store1(grow + e.col, c * (f.q * e.diff - f.d * e.r));
         }
     }
     // copies that nothing waited for (after an abort, or of a row without a gradient) land first
     if ((ctl.bar.abort || (kGrad && dead)) && tid == kProducerWarp * 32) drain(ctl.bar, a.nbuf, issued);
 }
+
+// ---- many rows: a persistent kernel -----------------------------------------------------------------
+//
+// One block per SM (a cluster of C blocks per row) walks the rows cid, cid + ncl, ... with the copies
+// of the next rows always in flight.  Its warps have roles, which hand rows on through mbarriers,
+// everything that belongs to a row doubled by the parity of its number in the block's sequence:
+//   producer        copies the rows' slices into the stage ring, running ahead as stages are released
+//   patch           overwrites the entries' columns in the loaded stages with -inf, and writes the row's
+//                   partial first and last vectors there, so the consumers' sums need not know of either
+//   top 0, top 1    (even and odd rows) the arithmetic on the K entries
+//   consumers       the tail's pair of a row; in one pass then the first stages of the next row, while
+//                   this row's statistics are exchanged, this row's gradient from the held stages,
+//                   releasing each, and the rest of the next row
+//   stats           merges the warps' pairs and the cluster's, finishes the row, and writes the
+//                   entries' gradients (in one pass once the consumers have written the row)
+// Every role walks the same rows by itself (a lane looks at each of the next 32 rows' label and first
+// id), so nothing has to be handed on about rows that are skipped.
+
+namespace ring {
+
+constexpr int kWarps = 16, kNT = kWarps * 32;       // consumers
+constexpr int kProducer = kWarps, kPatch = kWarps + 1, kTop = kWarps + 2, kStats = kWarps + 4;
+constexpr int kRingThreads = (kWarps + 5) * 32;
+constexpr int kSeen = 512;                          // slots of a top warp's table of columns (for ids given twice)
+// Stages: in one pass 16 KB, so that a held row gives them back in small steps; 32 KB in the forward
+// alone, whose stages are given back at once (less to do per stage).
+template <bool kGrad>
+struct Geom {
+    static constexpr int kU = kGrad ? 2 : 4;        // vectors of a stage per consumer thread
+    static constexpr int kVecs = kU * kNT, kBytes = kVecs * 16;
+    static constexpr int kBufs = kGrad ? 13 : 6;
+    static constexpr int kHeld = 8;                 // stages of a slice that is held, at most
+};
+enum { kErrRow = 107, kErrPartials = 108, kErrCoefs = 109 };
+
+struct TopStats {
+    float zmax, lnr, lq, kl;
+    int code;
+};
+struct Coefs {                   // of the tail's gradient
+    float coef, bias;            // coef 2^(z k2 - bias)
+    int dead;
+};
+
+struct alignas(16) RingCtl {
+    float4 slot[2][kMaxCluster];
+    uint64_t full[13], ready[13], empty[13];   // of the stages: copied, patched, released
+    uint64_t topped[2];          // their arithmetic (the top warp)
+    uint64_t paired[2];          // the consumer warps' pairs
+    uint64_t exchanged[2];       // the cluster's pairs
+    uint64_t finished[2];        // the row's coefficients (stats)
+    uint64_t written[2];         // the tail's gradient (consumer warps)
+    uint64_t freed[2];           // the stats warp is done with the entries
+    TopStats top[2];
+    uint32_t seen[2][kSeen];
+    Coefs coefs[2];
+    float red_m[2][kWarps], red_s[2][kWarps];
+    int abort, err;
+};
+
+__host__ __device__ constexpr int ring_smem(int stages_bytes, int K) {
+    return stages_bytes + 2 * K * (int)sizeof(Entry) + (int)sizeof(RingCtl) + 16;
+}
+
+// make_slice in stages of the ring.
+template <bool kGrad>
+__device__ __forceinline__ Slice ring_slice(const Row& r, int parts, int part) {
+    Slice s;
+    const int per = parts == 1 ? r.nv : (r.nv + parts - 1) / parts;
+    s.v0 = min(r.nv, part * per);
+    s.n = min(r.nv - s.v0, per);
+    s.nst = (s.n + Geom<kGrad>::kVecs - 1) / Geom<kGrad>::kVecs;
+    return s;
+}
+
+// A position of the ring, moved on stage by stage (a division by the number of stages, twice a stage in
+// every consumer thread, took a fifth of the issue slots).
+template <int N>
+struct Cursor {
+    int st;
+    uint32_t phase;
+    __device__ __forceinline__ void step() {
+        if (++st == N) {
+            st = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+// The rows cid, cid + ncl, ... that have a teacher and are not ignored (a warp, in step); of the others,
+// skipped(row).  The labels and first ids of the next 32 rows are on their way while a batch is in use.
+struct Walk {
+    int64_t base, step;
+    uint32_t left;
+    int64_t id, label;           // of this lane's row of the next batch
+};
+
+__device__ __forceinline__ void walk_load(Walk& w, const Args& a, int64_t row) {
+    w.id = row < a.T ? a.ids[row * a.K] : -1;
+    w.label = row < a.T && a.labels ? a.labels[row] : 0;
+}
+__device__ __forceinline__ void walk_start(Walk& w, const Args& a, int64_t cid, int64_t ncl) {
+    w.step = ncl;
+    w.base = cid - 32 * ncl;
+    w.left = 0;
+    walk_load(w, a, cid + (int64_t)(threadIdx.x & 31) * ncl);
+}
+// The next row, or -1 behind the last.
+template <typename F>
+__device__ __forceinline__ int64_t walk_next(Walk& w, const Args& a, F skipped) {
+    while (!w.left) {
+        w.base += 32 * w.step;
+        if (w.base >= a.T) return -1;
+        w.left = __ballot_sync(0xFFFFFFFFu, w.id != -1 && !(a.labels && w.label == a.ignore_index));
+        const uint32_t there = __ballot_sync(0xFFFFFFFFu, w.base + (int64_t)(threadIdx.x & 31) * w.step < a.T);
+        for (uint32_t no = there & ~w.left; no; no &= no - 1) skipped(w.base + (int64_t)(__ffs(no) - 1) * w.step);
+        walk_load(w, a, w.base + (int64_t)(32 + (threadIdx.x & 31)) * w.step);
+    }
+    const int b = __ffs(w.left) - 1;
+    w.left &= w.left - 1;
+    return w.base + (int64_t)b * w.step;
+}
+__device__ __forceinline__ int64_t walk_next(Walk& w, const Args& a) {
+    return walk_next(w, a, [](int64_t) {});
+}
+
+__device__ __forceinline__ void arrive_peer(uint32_t bar_addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_addr) : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(tc::smem_u32(bar)), "r"(parity), "r"(10000)
+        : "memory");
+    return ok != 0;
+}
+
+// This thread's vectors of stage j of the slice; -inf beyond its end.
+template <typename S, int U>
+__device__ __forceinline__ void ring_load(const uint8_t* buf8, const Slice& s, int j, int tid, uint4 (&x)[U]) {
+    const uint4* buf = reinterpret_cast<const uint4*>(buf8) + tid;
+    const int left = s.n - j * (U * kNT);
+    if (left >= U * kNT) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) x[u] = tc::lds16(buf + u * kNT);
+    } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) x[u] = tid + u * kNT < left ? tc::lds16(buf + u * kNT) : stage::neg_inf16<S>();
+    }
+}
+
+template <typename S, typename O, bool kGrad>
+__global__ void __launch_bounds__(kRingThreads, 1) k_distill_ring(const __grid_constant__ Args a) {
+    constexpr int G = Elt<S>::kGroup;
+    extern __shared__ __align__(128) uint8_t smem[];
+    using Ge = Geom<kGrad>;
+    constexpr int nbuf = Ge::kBufs, U = Ge::kU, kRingVecs = Ge::kVecs, kRingBytes = Ge::kBytes;
+    const int K = a.K, C = a.cluster;
+    Entry* entries = reinterpret_cast<Entry*>(smem + nbuf * kRingBytes);   // [2][K]
+    RingCtl& ctl = *reinterpret_cast<RingCtl*>((reinterpret_cast<uintptr_t>(entries + 2 * K) + 15) / 16 * 16);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = C > 1 ? (int)cluster_rank() : 0;
+    const int64_t cid = blockIdx.x / C, ncl = gridDim.x / C;
+    auto wait = [&](uint64_t* bar, int64_t e, int code) {   // the phase of row e of a barrier doubled by parity
+        return tc::mbar_wait(bar, (uint32_t)(e >> 1) & 1, &ctl.abort, &ctl.err, code);
+    };
+
+    if (tid == 0) {
+        for (int i = 0; i < nbuf; ++i) {
+            tc::mbar_init(&ctl.full[i], 1);
+            tc::mbar_init(&ctl.ready[i], 1);
+            tc::mbar_init(&ctl.empty[i], kWarps);
+        }
+        for (int p = 0; p < 2; ++p) {
+            tc::mbar_init(&ctl.topped[p], 1);
+            tc::mbar_init(&ctl.paired[p], kWarps);
+            tc::mbar_init(&ctl.exchanged[p], C);
+            tc::mbar_init(&ctl.finished[p], 1);
+            tc::mbar_init(&ctl.written[p], kWarps);
+            tc::mbar_init(&ctl.freed[p], 1);
+        }
+        ctl.abort = ctl.err = 0;
+        tc::fence_mbar_init();
+    }
+    if (C > 1) cluster_arrive(), cluster_wait();
+    else __syncthreads();
+
+    Walk walk;
+    walk_start(walk, a, cid, ncl);
+
+    if (warp == kProducer) {
+        Cursor<nbuf> at{0, 1};                         // waits for "released" start a phase back
+        int q = 0;
+        for (;;) {
+            const int64_t row = walk_next(walk, a);
+            if (row < 0 || *reinterpret_cast<volatile int*>(&ctl.abort)) break;
+            if (lane == 0) {
+                const Row r = make_row<S>(a.logits, row, a.ld, a.V);
+                const Slice sl = ring_slice<kGrad>(r, C, rank);
+                for (int j = 0; j < sl.nst; ++j, ++q, at.step()) {
+                    const int st = at.st;
+                    if (!tc::mbar_wait(&ctl.empty[st], at.phase, &ctl.abort, &ctl.err, kErrEmpty)) break;
+                    const int v = sl.v0 + j * kRingVecs;
+                    const int lo = max(v, r.iv0), hi = min(min(v + kRingVecs, sl.v0 + sl.n), r.iv1);
+                    if (hi > lo && dbg::ok(lo >= 0 && hi <= r.nv, dbg::kCols)) {
+                        tc::mbar_arrive_expect_tx(&ctl.full[st], (uint32_t)(hi - lo) * 16);
+                        tc::bulk_load(smem + st * kRingBytes + (lo - v) * 16, r.base + (int64_t)lo * 16,
+                                      (uint32_t)(hi - lo) * 16, &ctl.full[st]);
+                    } else {
+                        tc::mbar_arrive(&ctl.full[st]);
+                    }
+                }
+            }
+            __syncwarp();
+        }
+        // after an abort, copies in flight land before the block may leave
+        if (lane == 0 && *reinterpret_cast<volatile int*>(&ctl.abort)) {
+            int never = 0;
+            for (int p = max(0, q - nbuf); p < q; ++p)
+                tc::mbar_wait(&ctl.full[p % nbuf], (p / nbuf) & 1, &never, nullptr, 0);
+        }
+        __syncwarp();
+    } else if (warp == kPatch) {
+        Cursor<nbuf> at{0, 0};
+        const S neg = sizeof(S) == 2 ? (S)0xFF80u : (S)-kInf;
+        for (bool ok = true; ok;) {
+            const int64_t row = walk_next(walk, a);
+            if (row < 0) break;
+            const Row r = make_row<S>(a.logits, row, a.ld, a.V);
+            const Slice sl = ring_slice<kGrad>(r, C, rank);
+            // the entries' places among the slice's elements; anything else is in no stage
+            uint32_t place[kPerLane];
+#pragma unroll
+            for (int i = 0; i < kPerLane; ++i) {
+                place[i] = 0xFFFFFFFFu;
+                if (32 * i >= K) continue;
+                const int64_t id = lane + 32 * i < K ? a.ids[row * K + lane + 32 * i] : -1;
+                if (id >= 0 && id < a.V) place[i] = (uint32_t)((int)id + r.shift - sl.v0 * G);
+            }
+            // lanes 0 .. G - 1: the first vector, if it is partial and the slice's; G .. 2 G - 1: the last
+            const int edge = lane < G ? (r.shift ? 0 : -1) : (r.iv1 < r.nv && (r.nv > 1 || !r.shift) ? r.nv - 1 : -1);
+            const int64_t ecol = (int64_t)edge * G - r.shift + lane % G;
+            const bool mine = lane < 2 * G && edge >= sl.v0 && edge < sl.v0 + sl.n;
+            S evalue = neg;
+            if (mine && ecol >= 0 && ecol < a.V) evalue = static_cast<const S*>(a.logits)[row * a.ld + ecol];
+            const uint32_t eplace = mine ? (uint32_t)((edge - sl.v0) * G + lane % G) : 0xFFFFFFFFu;
+            for (int j = 0; j < sl.nst; ++j, at.step()) {
+                ok = tc::mbar_wait(&ctl.full[at.st], at.phase, &ctl.abort, &ctl.err, kErrFull);
+                if (!__all_sync(0xFFFFFFFFu, ok)) {
+                    ok = false;
+                    break;
+                }
+                S* buf = reinterpret_cast<S*>(smem + at.st * kRingBytes);
+                const uint32_t first = (uint32_t)(j * kRingVecs * G);
+                if (eplace - first < (uint32_t)(kRingVecs * G)) buf[eplace - first] = evalue;
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < kPerLane; ++i) {
+                    if (32 * i >= K) break;
+                    if (place[i] - first < (uint32_t)(kRingVecs * G)) buf[place[i] - first] = neg;
+                }
+                // these writes before the next copy into the stage, which goes through another proxy
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&ctl.ready[at.st]);
+            }
+        }
+    } else if (warp == kTop || warp == kTop + 1) {
+        const int par = warp - kTop;
+        Entry* en = entries + par * K;
+        uint32_t* seen = ctl.seen[par];
+        int64_t last = -1;
+        for (int64_t e = 0;; ++e) {
+            const int64_t row = walk_next(walk, a);
+            if (row < 0) break;
+            if ((e & 1) != par) continue;
+            const int64_t* ids = a.ids + row * K;
+            const S* zrow = static_cast<const S*>(a.logits) + row * a.ld;
+            int64_t id[kPerLane];
+#pragma unroll
+            for (int i = 0; i < kPerLane; ++i) {
+                if (32 * i >= K) break;
+                id[i] = lane + 32 * i < K ? ids[lane + 32 * i] : -1;
+            }
+            for (int i = lane; i < kSeen; i += 32) seen[i] = 0xFFFFFFFFu;
+            __syncwarp();
+            int bad = 0;
+            int col[kPerLane];
+            float z[kPerLane], t[kPerLane];
+#pragma unroll
+            for (int i = 0; i < kPerLane; ++i) {
+                const int k = lane + 32 * i;
+                col[i] = -1;
+                z[i] = t[i] = -kInf;
+                if (32 * i >= K) continue;
+                if (id[i] >= 0 && id[i] < a.V) {
+                    col[i] = (int)id[i];
+                    z[i] = Elt<S>::load1(zrow + col[i]);
+                    t[i] = a.tbf16 ? Elt<uint16_t>::load1(static_cast<const uint16_t*>(a.tvals) + row * K + k)
+                                   : Elt<float>::load1(static_cast<const float*>(a.tvals) + row * K + k);
+                } else {
+                    bad |= id[i] != -1;
+                }
+            }
+            // a column twice: the table (at most half full) already holds it
+#pragma unroll
+            for (int i = 0; i < kPerLane; ++i) {
+                if (32 * i >= K) break;
+                if (col[i] < 0) continue;
+                uint32_t at = ((uint32_t)col[i] * 2654435761u) >> 8 & (kSeen - 1);
+                uint32_t was;
+                while ((was = atomicCAS(seen + at, 0xFFFFFFFFu, (uint32_t)col[i])) != 0xFFFFFFFFu && was != (uint32_t)col[i])
+                    at = (at + 1) & (kSeen - 1);
+                bad |= was == (uint32_t)col[i];
+            }
+            bad = __any_sync(0xFFFFFFFFu, bad);
+            if (last >= 0 && !wait(&ctl.freed[par], last, kErrRow)) break;
+            last = e;
+            float zm, lnr, lq, kl;
+            top_arithmetic(a, K, lane, col, z, t, en, zm, lnr, lq, kl);
+            __syncwarp();
+            if (lane == 0) {
+                ctl.top[par] = TopStats{zm, lnr, lq, kl, bad ? VCE_ERR_TEACHER : 0};
+                tc::mbar_arrive(&ctl.topped[par]);
+            }
+        }
+    } else if (warp == kStats) {
+        const float inv_n = kGrad && a.red == VCE_RED_MEAN ? *a.inv_n : 1.f;
+        for (int64_t e = 0;; ++e) {
+            const int par = (int)(e & 1);
+            const int64_t row = walk_next(walk, a, [&](int64_t no) {   // an ignored row
+                if (rank != 0) return;
+                if (lane == 0) {
+                    a.loss_rows[no] = 0.f;
+                    a.row_stats[no] = make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+                if (!kGrad)
+                    for (int k = lane; k < K; k += 32) a.top_grads[no * K + k] = 0.f;
+            });
+            if (row < 0) break;
+            const float go = kGrad ? a.go[a.red == VCE_RED_NONE ? row : 0] * inv_n * a.tau : 0.f;
+            const float R = a.tail ? a.tail[row] : -kInf;
+            if (!wait(&ctl.paired[par], e, kErrPartials)) break;
+            float M = lane < kWarps ? ctl.red_m[par][lane] : -kInf;
+            float S0 = lane < kWarps ? ctl.red_s[par][lane] : 0.f;
+#pragma unroll
+            for (int off = kWarps / 2; off > 0; off >>= 1) {   // lanes 0 .. kWarps - 1 into lane 0
+                const float m2 = __shfl_xor_sync(0xFFFFFFFFu, M, off);
+                const float s2 = __shfl_xor_sync(0xFFFFFFFFu, S0, off);
+                pair_merge(M, S0, m2, s2, a.k2);
+            }
+            M = __shfl_sync(0xFFFFFFFFu, M, 0);
+            S0 = __shfl_sync(0xFFFFFFFFu, S0, 0);
+            if (!wait(&ctl.topped[par], e, kErrRow)) break;
+            const TopStats ts = ctl.top[par];
+            int code = ts.code;
+            if (C > 1) {
+                if (lane < C) {
+                    st_peer(peer_addr(&ctl.slot[par][rank], lane), make_float4(M, S0, __int_as_float(code), 0.f));
+                    arrive_peer(peer_addr(&ctl.exchanged[par], lane));
+                }
+                __syncwarp();
+                const uint64_t t0 = tc::globaltimer();
+                bool ok = true;
+                while (!try_wait_cluster(&ctl.exchanged[par], (uint32_t)(e >> 1) & 1)) {
+                    ok = !*reinterpret_cast<volatile int*>(&ctl.abort);
+                    if (ok && tc::globaltimer() - t0 > tc::kWaitNs) {
+                        ctl.abort = 1;
+                        atomicCAS(&ctl.err, 0, (int)kErrRow);
+                        ok = false;
+                    }
+                    if (!ok) break;
+                }
+                if (!__all_sync(0xFFFFFFFFu, ok)) break;
+                M = -kInf;
+                S0 = 0.f;
+                code = 0;
+                for (int p = 0; p < C; ++p) {   // the same order in every block
+                    const float4 o = ctl.slot[par][p];
+                    pair_merge(M, S0, o.x, o.y, a.k2);
+                    code = max(code, __float_as_int(o.z));
+                }
+            }
+            const Finish f = finish_row(a, M, S0, ts.zmax, ts.lnr, ts.lq, R, code);
+            if (lane == 0) {
+                ctl.coefs[par] = Coefs{go * f.d, f.lt > -kInf ? f.lt * kLog2e : 0.f, f.dead};
+                tc::mbar_arrive(&ctl.finished[par]);
+                if (rank == 0) {
+                    a.loss_rows[row] = loss_of(a, f, ts.kl);
+                    a.row_stats[row] = make_float4(f.lt, f.dead ? 0.f : f.d, 0.f, f.code ? -(float)f.code : 1.f);
+                }
+            }
+            __syncwarp();
+            if (kGrad && !wait(&ctl.written[par], e, kErrCoefs)) break;
+            const Row r = make_row<S>(a.logits, row, a.ld, a.V);
+            const Slice sl = ring_slice<kGrad>(r, C, rank);
+            const float c = kGrad ? go : a.tau;
+            for (int k = lane; k < K; k += 32) {
+                const Entry en = entries[par * K + k];
+                const float g = f.dead || en.col < 0 ? 0.f : c * (f.q * en.diff - f.d * en.r);
+                if (!kGrad) {
+                    if (rank == 0) a.top_grads[row * K + k] = g;
+                } else if (en.col >= 0 && !f.dead) {
+                    const int v = (en.col + r.shift) / G - sl.v0;
+                    if (v >= 0 && v < sl.n) Elt<O>::store1(static_cast<O*>(a.grad) + row * a.ld_g + en.col, g);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&ctl.freed[par]);
+        }
+    } else {
+        // ---------------- consumers ----------------
+        struct Pair {
+            float m, s, mb;
+        };
+        // stages [j0, j1) of a row, at ring positions from `at` on
+        auto forward = [&](Cursor<nbuf>& at, int j0, int j1, const Slice& sl, Pair& p) {
+            for (int j = j0; j < j1; ++j, at.step()) {
+                tc::mbar_wait(&ctl.ready[at.st], at.phase, &ctl.abort, &ctl.err, kErrFull);
+                uint4 x[U];
+                ring_load<S, U>(smem + at.st * kRingBytes, sl, j, tid, x);
+                if (!kGrad) {
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&ctl.empty[at.st]);
+                }
+                float v[U][G];
+#pragma unroll
+                for (int u = 0; u < U; ++u) Elt<S>::unpack(x[u], v[u]);
+                pair_push<G>(v, p.m, p.s, p.mb, a.k2);
+            }
+        };
+        auto publish = [&](int64_t e, Pair p) {
+            const int par = (int)(e & 1);
+            pair_warp_reduce(p.m, p.s, a.k2);
+            // row e - 2's pairs have been read (in one pass that follows from its gradient)
+            if (!kGrad && e >= 2) wait(&ctl.finished[par], e - 2, kErrCoefs);
+            if (lane == 0) {
+                ctl.red_m[par][warp] = p.m;
+                ctl.red_s[par][warp] = p.s;
+                tc::mbar_arrive(&ctl.paired[par]);
+            }
+            __syncwarp();
+        };
+        Cursor<nbuf> at{0, 0}, back{0, 0};             // the next stage to sum, and to turn into gradients
+        auto next = [&]() {
+            return walk_next(walk, a, [&](int64_t no) {    // an ignored row
+                if (!kGrad) return;
+                const Row r = make_row<S>(a.logits, no, a.ld, a.V);
+                O* g = static_cast<O*>(a.grad) + no * a.ld_g;
+                zero_grads<S, O>(r, ring_slice<kGrad>(r, C, rank), g, grads_aligned<S, O>(r, g), tid, kNT);
+            });
+        };
+        int64_t row = -1, row2 = next();                   // the row held, and the next one
+        Row r{};
+        Slice sl{};
+        sl.nst = 0;
+        for (int64_t e = -1; (row >= 0 || row2 >= 0) && !*reinterpret_cast<volatile int*>(&ctl.abort); ++e) {
+            Row r2{};
+            Slice sl2{};
+            Pair p{-kInf, 0.f, 0.f};
+            int pre = 0;
+            if (row2 >= 0) {
+                r2 = make_row<S>(a.logits, row2, a.ld, a.V);
+                sl2 = ring_slice<kGrad>(r2, C, rank);
+                // the next row's stages that fit beside this one's (forward alone: all of them)
+                pre = kGrad ? min(sl2.nst, nbuf - sl.nst) : sl2.nst;
+            }
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {         // the next row's first stages, this row, the rest
+                if (row2 >= 0) forward(at, half ? pre : 0, half ? sl2.nst : pre, sl2, p);
+                if (!kGrad || half || row < 0) continue;
+                const int par = (int)(e & 1);
+                if (!wait(&ctl.finished[par], e, kErrCoefs)) break;
+                const Coefs cf = ctl.coefs[par];
+                O* grow = static_cast<O*>(a.grad) + row * a.ld_g;
+                const bool vec = grads_aligned<S, O>(r, grow);
+                for (int j = 0; j < sl.nst; ++j, back.step()) {
+                    uint4 x[U];
+                    ring_load<S, U>(smem + back.st * kRingBytes, sl, j, tid, x);
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&ctl.empty[back.st]);
+                    write_grads<S, O, U, kNT>(x, r, sl, j, tid, grow, vec, cf.coef, a.k2, cf.bias, cf.dead);
+                }
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&ctl.written[par]);
+            }
+            if (row2 >= 0) publish(e + 1, p);
+            row = row2;
+            r = r2;
+            sl = sl2;
+            if (row2 >= 0) row2 = next();
+        }
+    }
+    // after an abort: no row of this block is known to be right
+    __syncthreads();
+    if (ctl.abort && rank == 0)
+        for (int64_t row = cid + (int64_t)tid * ncl; row < a.T; row += (int64_t)kRingThreads * ncl) {
+            a.loss_rows[row] = __int_as_float(0x7FC00000);
+            a.row_stats[row].w = -(float)(ctl.err ? ctl.err : kErrRow);
+        }
+    if (C > 1) cluster_arrive(), cluster_wait();       // no block leaves while a peer may write into it
+}
+
+}  // namespace ring
 
 // ---- the gradient from saved statistics --------------------------------------------------------------
 
@@ -465,7 +1025,7 @@ __global__ void __launch_bounds__(kConsumers + 32, 3) k_distill_bwd(const __grid
             uint4 x[kU];
             load_stage<S>(smem, a.nbuf, r, sl, j, j, tid, x);
             release_stage(bar, a.nbuf, j);
-            write_grads<S, O>(x, r, sl, j, tid, grow, vec, coef, a.k2, bias);
+            write_grads<S, O, kU, kConsumers>(x, r, sl, j, tid, grow, vec, coef, a.k2, bias);
         }
     }
     __syncthreads();
@@ -554,8 +1114,28 @@ void shape(int64_t T, int64_t V, int G, bool hold, int K, int sms, int* cluster,
     *nbuf = std::max(1, std::min(nb, st(C)));
 }
 
+// The persistent kernel's blocks of a row; 0: rows too long to hold.
+template <bool kGrad>
+int ring_cluster(int64_t T, int64_t V, int G, int sms) {
+    using Ge = ring::Geom<kGrad>;
+    const int64_t nv = (V + 2 * G - 2) / G;
+    auto st = [&](int c) { return (int)(((nv + c - 1) / c + Ge::kVecs - 1) / Ge::kVecs); };
+    int C = 1;
+    while (C < kMaxCluster && ((kGrad && st(C) > Ge::kHeld) || (T * C < sms && st(C) > 1))) C *= 2;
+    return kGrad && st(C) > Ge::kHeld ? 0 : C;
+}
+
 template <typename S, typename O, bool kGrad>
 cudaError_t run(Args& a, int sms, cudaStream_t s) {
+    a.cluster = ring_cluster<kGrad>(a.T, a.V, Elt<S>::kGroup, sms);
+    if (a.cluster) {
+        const int bytes = ring::ring_smem(ring::Geom<kGrad>::kBufs * ring::Geom<kGrad>::kBytes, a.K);
+        const int64_t clusters = std::min<int64_t>(
+            a.T, resident_clusters<ring::k_distill_ring<S, O, kGrad>>(a.cluster, ring::kRingThreads, bytes, sms));
+        if (clusters > 0)
+            return launch_clusters<ring::k_distill_ring<S, O, kGrad>>(clusters * a.cluster, a.cluster,
+                                                                     ring::kRingThreads, bytes, s, a);
+    }
     shape(a.T, a.V, Elt<S>::kGroup, kGrad, a.K, sms, &a.cluster, &a.nbuf, &a.max_stages);
     const int bytes = smem_bytes(a.nbuf, a.max_stages, a.K);
     return launch_clusters<k_distill<S, O, kGrad>>(a.T * a.cluster, a.cluster, kThreads, bytes, s, a);

@@ -55,6 +55,37 @@ cudaError_t launch_clusters(int64_t blocks, int cluster, int threads, int smem, 
     return e;
 }
 
+// Clusters of `cluster` blocks of kKernel (one block an SM) that run at once, asked for once per device
+// and cluster size; 0 if it cannot be told.
+template <auto kKernel>
+int resident_clusters(int cluster, int threads, int smem, int sms) {
+    if (cluster == 1) return sms;
+    static std::atomic<int> known[kMaxDevices][5];
+    int d = 0, log2 = 0;
+    if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= kMaxDevices) return 0;
+    while ((1 << log2) < cluster) ++log2;
+    int n = known[d][log2].load(std::memory_order_acquire);
+    if (n) return n;
+    if (cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess) return 0;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(sms / cluster * cluster));
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kKernel, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return 0;
+    }
+    known[d][log2].store(n, std::memory_order_release);
+    return n;
+}
+
 // Whether a [T, V] matrix of es-byte elements and another (same T and V) share any byte of their
 // extents (T >= 1).
 inline bool overlap(const void* a, int64_t T, int64_t V, int64_t ld_a, size_t es_a, const void* b, int64_t ld_b,

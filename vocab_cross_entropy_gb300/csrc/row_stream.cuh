@@ -196,11 +196,11 @@ __device__ __forceinline__ void pair_warp_reduce(float& m, float& s, float k2) {
 }
 
 // sum of 2^(v k2 - mb) over a thread's vectors of a stage
-template <int G>
-__device__ __forceinline__ float sum_exp(const float (&v)[kU][G], float k2, float mb) {
-    float t[kU];
+template <int G, int U>
+__device__ __forceinline__ float sum_exp(const float (&v)[U][G], float k2, float mb) {
+    float t[U];
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
+    for (int u = 0; u < U; ++u) {
         float e[G];
 #pragma unroll
         for (int k = 0; k < G; ++k) e[k] = ex2(fmaf(v[u][k], k2, -mb));
@@ -211,17 +211,17 @@ __device__ __forceinline__ float sum_exp(const float (&v)[kU][G], float k2, floa
         t[u] = e[0];
     }
 #pragma unroll
-    for (int w = 1; w < kU; w *= 2)
+    for (int w = 1; w < U; w *= 2)
 #pragma unroll
-        for (int u = 0; u + w < kU; u += 2 * w) t[u] += t[u + w];
+        for (int u = 0; u + w < U; u += 2 * w) t[u] += t[u + w];
     return t[0];
 }
 
-template <int G>
-__device__ __forceinline__ float max_of(const float (&v)[kU][G]) {
+template <int G, int U>
+__device__ __forceinline__ float max_of(const float (&v)[U][G]) {
     float m = v[0][0];
 #pragma unroll
-    for (int u = 0; u < kU; ++u)
+    for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int k = 0; k < G; ++k) m = fmaxf(m, v[u][k]);
     return m;
@@ -229,21 +229,23 @@ __device__ __forceinline__ float max_of(const float (&v)[kU][G]) {
 
 // Adds a stage's values to a pair whose reference m moves only when a term would pass 2^32
 // (m is then one of the values, so s >= 1 and nothing overflows).
-template <int G>
-__device__ __forceinline__ void pair_push(const float (&v)[kU][G], float& m, float& s, float& mb, float k2) {
+template <int G, int U>
+__device__ __forceinline__ void pair_push(const float (&v)[U][G], float& m, float& s, float& mb, float k2) {
     if (m == -kInf) {
         const float vm = max_of<G>(v);
         if (vm == -kInf) return;
         m = vm;
         mb = m * k2;
     }
-    float t = sum_exp<G>(v, k2, mb);
-    if (!(t < 4294967296.f)) {   // a value far above the reference: take the new maximum
-        const float vm = fmaxf(m, max_of<G>(v));
+    float t;
+#pragma unroll 1
+    for (int again = 0;; again = 1) {   // one copy of the sum's code, for the instruction cache
+        t = sum_exp<G>(v, k2, mb);
+        if (again || t < 4294967296.f) break;
+        const float vm = fmaxf(m, max_of<G>(v));   // a value far above the reference: take the new maximum
         s *= ex2((m - vm) * k2);
         m = vm;
         mb = m * k2;
-        t = sum_exp<G>(v, k2, mb);
     }
     s += t;
 }
