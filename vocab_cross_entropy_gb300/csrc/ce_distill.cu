@@ -488,6 +488,7 @@ namespace ring {
 constexpr int kWarps = 16, kNT = kWarps * 32;       // consumers
 constexpr int kProducer = kWarps, kPatch = kWarps + 1, kTop = kWarps + 2, kStats = kWarps + 4;
 constexpr int kRingThreads = (kWarps + 5) * 32;
+constexpr uint32_t kSuspend = 10000;                // ns a poll may sleep: waiting warps leave the issue slots to others
 constexpr int kSeen = 512;                          // slots of a top warp's table of columns (for ids given twice)
 // Stages: in one pass 16 KB, so that a held row gives them back in small steps; 32 KB in the forward
 // alone, whose stages are given back at once (less to do per stage).
@@ -533,7 +534,7 @@ __host__ __device__ constexpr int ring_smem(int stages_bytes, int K) {
 template <bool kGrad>
 __device__ __forceinline__ Slice ring_slice(const Row& r, int parts, int part) {
     Slice s;
-    const int per = parts == 1 ? r.nv : (r.nv + parts - 1) / parts;
+    const int per = (r.nv + parts - 1) >> (31 - __clz(parts));   // parts: a power of two
     s.v0 = min(r.nv, part * per);
     s.n = min(r.nv - s.v0, per);
     s.nst = (s.n + Geom<kGrad>::kVecs - 1) / Geom<kGrad>::kVecs;
@@ -633,7 +634,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_distill_ring(const __grid_c
     const int rank = C > 1 ? (int)cluster_rank() : 0;
     const int64_t cid = blockIdx.x / C, ncl = gridDim.x / C;
     auto wait = [&](uint64_t* bar, int64_t e, int code) {   // the phase of row e of a barrier doubled by parity
-        return tc::mbar_wait(bar, (uint32_t)(e >> 1) & 1, &ctl.abort, &ctl.err, code);
+        return tc::mbar_wait(bar, (uint32_t)(e >> 1) & 1, &ctl.abort, &ctl.err, code, tc::kWaitNs, kSuspend);
     };
 
     if (tid == 0) {
@@ -716,7 +717,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_distill_ring(const __grid_c
             if (mine && ecol >= 0 && ecol < a.V) evalue = static_cast<const S*>(a.logits)[row * a.ld + ecol];
             const uint32_t eplace = mine ? (uint32_t)((edge - sl.v0) * G + lane % G) : 0xFFFFFFFFu;
             for (int j = 0; j < sl.nst; ++j, at.step()) {
-                ok = tc::mbar_wait(&ctl.full[at.st], at.phase, &ctl.abort, &ctl.err, kErrFull);
+                ok = tc::mbar_wait(&ctl.full[at.st], at.phase, &ctl.abort, &ctl.err, kErrFull, tc::kWaitNs, kSuspend);
                 if (!__all_sync(0xFFFFFFFFu, ok)) {
                     ok = false;
                     break;
@@ -887,7 +888,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_distill_ring(const __grid_c
         // stages [j0, j1) of a row, at ring positions from `at` on
         auto forward = [&](Cursor<nbuf>& at, int j0, int j1, const Slice& sl, Pair& p) {
             for (int j = j0; j < j1; ++j, at.step()) {
-                tc::mbar_wait(&ctl.ready[at.st], at.phase, &ctl.abort, &ctl.err, kErrFull);
+                tc::mbar_wait(&ctl.ready[at.st], at.phase, &ctl.abort, &ctl.err, kErrFull, tc::kWaitNs, kSuspend);
                 uint4 x[U];
                 ring_load<S, U>(smem + at.st * kRingBytes, sl, j, tid, x);
                 if (!kGrad) {
