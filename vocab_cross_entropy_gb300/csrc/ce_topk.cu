@@ -4,10 +4,10 @@
 // One pass over the logits.  The row (or its slice, in a thread-block cluster) streams through
 // shared memory (row_stream.cuh); of every group of 16 or 32 values -- a consumer thread's vectors
 // of a stage -- only the maximum and the sum of exponentials relative to it are kept.  The K-th
-// largest group maximum is a lower bound t of the K-th largest value: K groups hold a value >= t,
-// and every value >= t lies in a group whose maximum is >= t.  So
-//   1. t: a binary search over the bits of the maxima's order keys (counts of keys >= t), stopped
-//      as soon as no more than K + K/4 groups remain;
+// largest group maximum is a lower bound t of the K-th largest value (K groups hold a value >= t), and
+// every value >= t lies in a group whose maximum is >= t.  So
+//   1. t: a binary search over the bits of the maxima's order keys (counts of keys >= t), among the
+//      largest maxima of 512 sets of groups;
 //   2. the groups with a maximum >= t are read once more (from L2): their values >= t become
 //      candidates, and the group's pair is rebuilt from the other values, so the candidates are
 //      left out of the tail's sum without a subtraction;
@@ -32,13 +32,14 @@ namespace topk {
 
 using namespace rs;
 
-constexpr int kThreads = kConsumers + 32;   // the last warp: producer
-constexpr int kWarps = kThreads / 32;
+constexpr int kThreads = kConsumers + 32;   // k_topk: consumers, which also select, and the producer warp
+constexpr int kSel = 256, kSelWarps = kSel / 32;   // threads that select
+static_assert(kSel == kConsumers, "the consumers of k_topk select");
 constexpr int kMaxCand = 1024;              // candidates of a block
 constexpr int kMaxSel = 512;                // groups read again
-constexpr uint32_t kKeyMin = 0x00800000u;   // order key of the lowest finite value
+constexpr uint32_t kKeyMin = 0x00800000u;   // order key of the lowest finite value (-inf is one below)
 
-// Scratch over the stage buffers, once the columns have streamed through.
+// Scratch of the selection (in k_topk over the stage buffers, once the columns have streamed through).
 constexpr int kCandAt = 0;                                   // [kMaxCand] candidates
 constexpr int kListAt = kCandAt + kMaxCand * 8;              // [kMaxCand] candidates by rank (read by peers)
 constexpr int kSelAt = kListAt + kMaxCand * 8;               // [kMaxSel] group numbers
@@ -47,7 +48,7 @@ constexpr int kPartEnd = kPartAt + kMaxSel * kU * 8;
 constexpr int kInAt = kSelAt;                                // [cluster * K] the cluster's lists
 constexpr int kOutAt = kInAt + kMaxCluster * VCE_MAX_TOPK * 8;   // the same by rank
 constexpr int kScratch = kOutAt + kMaxCluster * VCE_MAX_TOPK * 8;
-static_assert(kScratch <= 3 * kStageBytes && kPartEnd <= 3 * kStageBytes && kMaxCand >= VCE_MAX_TOPK, "scratch");
+static_assert(kScratch <= 3 * kStageBytes && kPartEnd <= kScratch && kMaxCand >= VCE_MAX_TOPK, "scratch");
 
 struct Args {
     const void* logits;
@@ -60,18 +61,29 @@ struct Args {
     int cluster, nbuf, max_stages;
 };
 
-struct alignas(16) Ctl {
+constexpr int kRowsPerSm = 2;               // rows for each SM from which the persistent kernel runs
+
+// What the selecting threads share.
+struct alignas(16) SelCtl {
     float4 tail;                    // the block's pair of the columns left out (read by peers)
+    float red_m[kSelWarps], red_s[kSelWarps];
+    int count[2][kSelWarps];
+    int nsel, ncand;
+    float bound;
+};
+
+struct alignas(16) Ctl {
+    SelCtl sel;
     Barriers bar;
-    float red_m[kWarps], red_s[kWarps];
-    int count[2][kWarps];
-    int nsel, ncand, neq;
 };
 
 __host__ __device__ constexpr int smem_bytes(int nbuf, int max_stages) {
     const int b = nbuf * kStageBytes;
     return (b > kScratch ? b : kScratch) + max_stages * kConsumers * 8 + (int)sizeof(Ctl);
 }
+
+// Barrier of the selecting threads.
+__device__ __forceinline__ void sel_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSel) : "memory"); }
 
 // Keys in the order of the values (larger value, larger key); -0 as +0.
 __device__ __forceinline__ uint32_t key_of(float v) {
@@ -88,16 +100,29 @@ __device__ __forceinline__ uint64_t cand_of(uint32_t key, int col) {
 __device__ __forceinline__ uint32_t cand_key(uint64_t c) { return (uint32_t)(c >> 32); }
 __device__ __forceinline__ int cand_col(uint64_t c) { return (int)(0xFFFFFFFFu - (uint32_t)c); }
 
-// Sum over the block of each thread's n (call number it picks one of two buffers, so one barrier
-// a call is enough).
-__device__ __forceinline__ int block_sum(int n, Ctl& ctl, int it) {
+// Sum over the selecting threads of each one's n (call number it picks one of two buffers, so one
+// barrier a call is enough).
+__device__ __forceinline__ int block_sum(int n, SelCtl& ctl, int it) {
     n = __reduce_add_sync(0xFFFFFFFFu, n);
-    if ((threadIdx.x & 31) == 0) ctl.count[it & 1][threadIdx.x >> 5] = n;
-    __syncthreads();
+    if ((threadIdx.x & 31) == 0) ctl.count[it & 1][(threadIdx.x >> 5) % kSelWarps] = n;
+    sel_sync();
     int t = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) t += ctl.count[it & 1][w];
+    for (int w = 0; w < kSelWarps; ++w) t += ctl.count[it & 1][w];
     return t;
+}
+// Merges the selecting threads' pairs; every thread has the result.
+__device__ __forceinline__ void block_pair(float& m, float& s, SelCtl& ctl, float k2) {
+    const int warp = (threadIdx.x >> 5) % kSelWarps;
+    pair_warp_reduce(m, s, k2);
+    if ((threadIdx.x & 31) == 0) {
+        ctl.red_m[warp] = m;
+        ctl.red_s[warp] = s;
+    }
+    sel_sync();
+    m = -kInf;
+    s = 0.f;
+    for (int w = 0; w < kSelWarps; ++w) pair_merge(m, s, ctl.red_m[w], ctl.red_s[w], k2);
 }
 
 // The pair of G values, -inf left out.
@@ -118,14 +143,14 @@ __device__ __forceinline__ float2 pair_of(const float (&v)[G], float k2) {
 // as its search takes: for slices where the bound from the groups admits too many.  Candidates go
 // to cand (ctl.ncand of them), everything else into this thread's pair (tm, ts).
 template <typename S>
-__device__ __noinline__ void exact_threshold(const Args& a, const Row& r, const Slice& sl, Ctl& ctl, uint64_t* cand,
-                                             float& tm, float& ts) {
+__device__ __noinline__ void exact_threshold(const Args& a, const Row& r, const Slice& sl, SelCtl& ctl, uint64_t* cand,
+                                             int tid, float& tm, float& ts) {
     constexpr int G = Elt<S>::kGroup;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int lane = tid & 31, warp = tid >> 5;
     int it = 0;
     auto count_from = [&](uint32_t t) {
         int n = 0;
-        for (int i = tid; i < sl.n; i += kThreads) {
+        for (int i = tid; i < sl.n; i += kSel) {
             float v[G];
             Elt<S>::unpack(load_vector<S>(r, sl.v0 + i), v);
 #pragma unroll
@@ -133,6 +158,7 @@ __device__ __noinline__ void exact_threshold(const Args& a, const Row& r, const 
         }
         return block_sum(n, ctl, it++);
     };
+    sel_sync();                                // ctl.count of the caller's search has been read
     uint32_t t = kKeyMin;
     if (count_from(kKeyMin) >= a.K) {
         t = 0;
@@ -140,10 +166,10 @@ __device__ __noinline__ void exact_threshold(const Args& a, const Row& r, const 
             if (count_from(t | (1u << bit)) >= a.K) t |= 1u << bit;
     }
     if (tid == 0) ctl.ncand = 0;
-    __syncthreads();
+    sel_sync();
     // above t: candidates; equal: counted; below: the tail
     int eq = 0;
-    for (int i = tid; i < sl.n; i += kThreads) {
+    for (int i = tid; i < sl.n; i += kSel) {
         float v[G];
         Elt<S>::unpack(load_vector<S>(r, sl.v0 + i), v);
 #pragma unroll
@@ -162,10 +188,10 @@ __device__ __noinline__ void exact_threshold(const Args& a, const Row& r, const 
     const int total_eq = block_sum(eq, ctl, it++);
     const int above = min(ctl.ncand, kMaxCand);
     const int want = min(total_eq, a.K - above);
-    __syncthreads();
+    sel_sync();
     // the first `want` values equal to t, in column order: vectors i = base + tid
     int found = 0;
-    for (int base = 0; base < sl.n && found < want; base += kThreads) {
+    for (int base = 0; base < sl.n && found < want; base += kSel) {
         const int i = base + tid;
         uint32_t hits = 0;
         if (i < sl.n) {
@@ -182,23 +208,228 @@ __device__ __noinline__ void exact_threshold(const Args& a, const Row& r, const 
         }
         if (lane == 31) ctl.count[0][warp] = before;
         before += found - n;
-        __syncthreads();
+        sel_sync();
         int all = 0;
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < kSelWarps; ++w) {
             if (w < warp) before += ctl.count[0][w];
             all += ctl.count[0][w];
         }
         for (; hits && before < want; hits &= hits - 1, ++before)
             cand[above + before] = cand_of(t, (sl.v0 + i) * G - r.shift + __ffs(hits) - 1);
         found += all;
-        __syncthreads();
+        sel_sync();
     }
     if (tid == 0) {
         ctl.ncand = above + want;
         if (total_eq > want) pair_merge(tm, ts, value_of(t), (float)(total_eq - want), a.k2);
     }
-    __syncthreads();
+    sel_sync();
 }
+
+// The K largest of a slice whose groups' maxima and sums are in gm and gs ([stages][GT], group t of
+// stage j holding the vectors j GT kU + t + u GT), by the kSel selecting threads: the sorted
+// candidates, at least K places with 0 behind the last, in the scratch's list, and the pair of the
+// columns that are not among the first K (the same in every thread).
+template <typename S, int GT>
+__device__ __forceinline__ void select(const Args& a, const Row& r, const Slice& sl, int stages, SelCtl& ctl,
+                                       uint8_t* scratch, float* gm, float* gs, int tid, float& tm, float& ts) {
+    constexpr int G = Elt<S>::kGroup;
+    static_assert(GT % kSel == 0, "whole rounds of groups");
+    const int K = a.K, rounds = stages * (GT / kSel), groups = stages * GT;   // rounds <= 64
+    uint64_t* cand = reinterpret_cast<uint64_t*>(scratch + kCandAt);
+    uint64_t* list = reinterpret_cast<uint64_t*>(scratch + kListAt);
+    int* sel = reinterpret_cast<int*>(scratch + kSelAt);
+    float2* part = reinterpret_cast<float2*>(scratch + kPartAt);
+    const int lane = tid & 31, warp = tid >> 5;
+    // ---- 1. the bound t ----
+    // Each thread's groups are tid + i kSel; the largest key of its even and of its odd ones are two of
+    // 2 kSel values, each that of some column, so the K-th largest of them bounds the K-th largest value
+    // from below nearly as well as that of all groups (K = 64: 73 groups are read again instead of 64),
+    // and one warp finds it in registers, without barriers.
+    float top2[2] = {-kInf, -kInf};
+    int i = 0;
+#pragma unroll 4
+    for (; i + 1 < rounds; i += 2) {
+        top2[0] = fmaxf(top2[0], gm[i * kSel + tid]);
+        top2[1] = fmaxf(top2[1], gm[(i + 1) * kSel + tid]);
+    }
+    if (i < rounds) top2[0] = fmaxf(top2[0], gm[i * kSel + tid]);
+    uint32_t* tops = reinterpret_cast<uint32_t*>(scratch + kSelAt);   // [2 kSel]
+    tops[tid] = key_of(top2[0]);
+    tops[kSel + tid] = key_of(top2[1]);
+    sel_sync();
+    if (warp == 0) {
+        constexpr int N = 2 * kSel / 32;
+        uint32_t k[N], most = 0;
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            k[i] = tops[lane + 32 * i];
+            most = max(most, k[i]);
+            n += k[i] >= kKeyMin;
+        }
+        most = __reduce_max_sync(0xFFFFFFFFu, most);
+        uint32_t t = kKeyMin;
+        if (__reduce_add_sync(0xFFFFFFFFu, n) >= K) {
+            t = 0;
+            for (int bit = 31; bit >= (sizeof(S) == 2 ? 16 : 0); --bit) {
+                const uint32_t c = t | (1u << bit);
+                if (c > most) continue;        // none is as large
+                n = 0;
+#pragma unroll
+                for (int i = 0; i < N; ++i) n += k[i] >= c;
+                n = __reduce_add_sync(0xFFFFFFFFu, n);
+                if (n >= K) t = c;
+                if (n >= K && n <= K + K / 8) break;
+            }
+            t = max(t, kKeyMin);
+        }
+        if (lane == 0) {
+            ctl.bound = value_of(t);
+            ctl.nsel = ctl.ncand = 0;
+        }
+    }
+    sel_sync();
+    const float t = ctl.bound;
+    // ---- 2. candidates ----
+    // the groups with a value >= t: a place on the list for each lane's, one atomic a warp
+    {
+        uint64_t mine = 0;                     // bit i: group tid + i kSel
+        if (fmaxf(top2[0], top2[1]) >= t) {
+#pragma unroll 4
+            for (int i = 0; i < rounds; ++i) mine |= (uint64_t)(gm[i * kSel + tid] >= t) << i;
+        }
+        const int n = __popcll(mine);
+        int at = n;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int o = __shfl_up_sync(0xFFFFFFFFu, at, off);
+            if (lane >= off) at += o;
+        }
+        int base = 0;
+        if (lane == 31 && at) base = atomicAdd(&ctl.nsel, at);
+        at += __shfl_sync(0xFFFFFFFFu, base, 31) - n;
+        for (; mine; mine &= mine - 1, ++at)
+            if (at < kMaxSel) sel[at] = tid + (__ffsll((long long)mine) - 1) * kSel;
+    }
+    sel_sync();
+    const int nsel = ctl.nsel;
+    tm = -kInf;
+    ts = 0.f;                                  // this thread's pair of the columns left out
+    if (nsel <= kMaxSel) {
+        // vectors of the listed groups, two in flight a thread
+        const int tasks = nsel * kU;
+        for (int task0 = tid; task0 < tasks; task0 += 2 * kSel) {
+            uint4 x[2];
+            int at[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int task = task0 + h * kSel;
+                at[h] = -1;
+                if (task >= tasks) continue;
+                const int g = sel[task / kU];
+                const int i = (g / GT) * (GT * kU) + g % GT + (task % kU) * GT;
+                if (i >= sl.n) continue;
+                at[h] = i;
+                x[h] = load_vector<S>(r, sl.v0 + i);
+            }
+#pragma unroll 1
+            for (int h = 0; h < 2 && task0 + h * kSel < tasks; ++h) {
+                float2 p = make_float2(-kInf, 0.f);
+                if (at[0] >= 0) {
+                    float v[G];
+                    Elt<S>::unpack(x[0], v);
+                    uint32_t hits = 0;
+#pragma unroll
+                    for (int k = 0; k < G; ++k) hits |= (v[k] >= t ? 1u : 0u) << k;
+                    if (hits) {
+                        int n = atomicAdd(&ctl.ncand, __popc(hits));
+#pragma unroll
+                        for (int k = 0; k < G; ++k)
+                            if ((hits >> k) & 1u) {
+                                if (n < kMaxCand) cand[n] = cand_of(key_of(v[k]), (sl.v0 + at[0]) * G - r.shift + k);
+                                ++n;
+                                v[k] = -kInf;
+                            }
+                    }
+                    p = pair_of<G>(v, a.k2);
+                }
+                part[task0 + h * kSel] = p;
+                x[0] = x[1];
+                at[0] = at[1];
+            }
+        }
+        sel_sync();
+    }
+    if (nsel > kMaxSel || ctl.ncand > kMaxCand) {
+        exact_threshold<S>(a, r, sl, ctl, cand, tid, tm, ts);
+    } else {
+        for (int i = tid; i < nsel; i += kSel) {
+            float m = -kInf, s = 0.f;
+#pragma unroll
+            for (int u = 0; u < kU; ++u) pair_merge(m, s, part[i * kU + u].x, part[i * kU + u].y, a.k2);
+            gm[sel[i]] = m;
+            gs[sel[i]] = s;
+        }
+        sel_sync();
+#pragma unroll 4
+        for (int g = tid; g < groups; g += kSel) tm = fmaxf(tm, gm[g]);
+        if (tm > -kInf) {
+#pragma unroll 4
+            for (int g = tid; g < groups; g += kSel) ts += gs[g] * ex2((gm[g] - tm) * a.k2);   // 0 * 0 for -inf
+        }
+    }
+    // ---- 3. ranks ----
+    const int n = min(ctl.ncand, kMaxCand);
+    for (int i = tid; i < n; i += kSel) {
+        const uint64_t c = cand[i];
+        int rk = 0;
+#pragma unroll 8
+        for (int q = 0; q < n; ++q) rk += cand[q] > c;
+        list[rk] = c;
+    }
+    for (int i = n + tid; i < K; i += kSel) list[i] = 0;
+    sel_sync();
+    for (int i = K + tid; i < n; i += kSel) pair_merge(tm, ts, value_of(cand_key(list[i])), 1.f, a.k2);
+    block_pair(tm, ts, ctl, a.k2);
+}
+
+// The row's outputs from its sorted list and the pair of the rest, by the selecting threads.
+__device__ __forceinline__ void outputs(const Args& a, int64_t row, const uint64_t* top, bool ok, float tm, float ts,
+                                        int tid) {
+    const float bad = __int_as_float(0x7FC00000);
+    for (int k = tid; k < a.K; k += kSel) {
+        const uint64_t c = top[k];
+        a.values[row * a.K + k] = ok ? (c ? value_of(cand_key(c)) : -kInf) : bad;
+        a.ids[row * a.K + k] = ok && c ? cand_col(c) : -1;
+    }
+    if (tid < 32) {
+        float m = top[0] ? value_of(cand_key(top[0])) : -kInf, s = 0.f;
+        for (int k = tid; k < a.K; k += 32)
+            if (top[k]) s += ex2((value_of(cand_key(top[k])) - m) * a.k2);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
+        pair_merge(m, s, tm, ts, a.k2);
+        if (tid == 0) {
+            a.lse[row] = !ok ? bad : s > 0.f ? m * a.scale + logf(s) : -kInf;
+            a.tail[row] = !ok ? bad : ts > 0.f ? tm * a.scale + logf(ts) : -kInf;
+        }
+    }
+}
+
+// A group's maximum and the sum of its exponentials relative to it.
+template <typename S>
+__device__ __forceinline__ void group_of(const uint4 (&x)[kU], float k2, float& m, float& s) {
+    constexpr int G = Elt<S>::kGroup;
+    const float top = max_of_loaded<S>(x);
+    float v[kU][G];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) Elt<S>::unpack(x[u], v[u]);
+    m = top;
+    s = top == -kInf ? 0.f : sum_exp<G>(v, k2, top * k2);
+}
+
+// ---- one cluster per row -------------------------------------------------------------------------
 
 template <typename S>
 __global__ void __launch_bounds__(kThreads, 3) k_topk(const __grid_constant__ Args a) {
@@ -208,10 +439,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_topk(const __grid_constant__ Ar
     float* gm = reinterpret_cast<float*>(smem + over);
     float* gs = gm + a.max_stages * kConsumers;
     Ctl& ctl = *reinterpret_cast<Ctl*>(gs + a.max_stages * kConsumers);
-    uint64_t* cand = reinterpret_cast<uint64_t*>(smem + kCandAt);
     uint64_t* list = reinterpret_cast<uint64_t*>(smem + kListAt);
-    int* sel = reinterpret_cast<int*>(smem + kSelAt);
-    float2* part = reinterpret_cast<float2*>(smem + kPartAt);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int C = a.cluster, K = a.K;
     const int rank = C > 1 ? (int)cluster_rank() : 0;
@@ -222,7 +450,6 @@ __global__ void __launch_bounds__(kThreads, 3) k_topk(const __grid_constant__ Ar
     int issued = 0;
     if (tid == kConsumers) {
         init_barriers(ctl.bar, a.nbuf);
-        ctl.nsel = ctl.ncand = 0;
         for (; issued < min(sl.nst, a.nbuf); ++issued) issue_stage(smem, ctl.bar, a.nbuf, r, sl, issued, issued);
     }
     __syncthreads();
@@ -236,12 +463,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_topk(const __grid_constant__ Ar
             uint4 x[kU];
             load_stage<S>(smem, a.nbuf, r, sl, j, j, tid, x);
             release_stage(ctl.bar, a.nbuf, j);
-            float v[kU][G];
-#pragma unroll
-            for (int u = 0; u < kU; ++u) Elt<S>::unpack(x[u], v[u]);
-            const float m = max_of<G>(v);
-            gm[j * kConsumers + tid] = m;
-            gs[j * kConsumers + tid] = m == -kInf ? 0.f : sum_exp<G>(v, a.k2, m * a.k2);
+            group_of<S>(x, a.k2, gm[j * kConsumers + tid], gs[j * kConsumers + tid]);
         }
     }
     __syncthreads();
@@ -249,110 +471,18 @@ __global__ void __launch_bounds__(kThreads, 3) k_topk(const __grid_constant__ Ar
     if (!ok && tid == kConsumers) drain(ctl.bar, a.nbuf, issued);
     if (!ok) __syncthreads();                  // the scratch overlies the stages
 
-    // ---- 1. the bound t from the groups' maxima (a thread's own: no barrier before reading them) ----
-    const bool consumer = tid < kConsumers;
-    int it = 0;
-    auto groups_from = [&](uint32_t t) {
-        int n = 0;
-        if (consumer)
-            for (int j = 0; j < sl.nst; ++j) n += key_of(gm[j * kConsumers + tid]) >= t;
-        return block_sum(n, ctl, it++);
-    };
-    uint32_t t = kKeyMin;
-    if (groups_from(kKeyMin) >= K) {
-        t = 0;
-        for (int bit = 31; bit >= (sizeof(S) == 2 ? 16 : 0); --bit) {
-            const int n = groups_from(t | (1u << bit));
-            if (n >= K) {
-                t |= 1u << bit;
-                if (n <= K + K / 4) break;
-            }
-        }
-        t = max(t, kKeyMin);
-    }
-    // ---- 2. candidates ----
-    if (consumer)
-        for (int j = 0; j < sl.nst; ++j)
-            if (key_of(gm[j * kConsumers + tid]) >= t) {
-                const int at = atomicAdd(&ctl.nsel, 1);
-                if (at < kMaxSel) sel[at] = j * kConsumers + tid;
-            }
-    __syncthreads();
-    const int nsel = ctl.nsel;
-    float tm = -kInf, ts = 0.f;                // this thread's pair of the columns left out
-    if (nsel <= kMaxSel) {
-        for (int task = tid; task < nsel * kU; task += kThreads) {
-            const int g = sel[task / kU];
-            const int i = (g / kConsumers) * kStageVecs + g % kConsumers + (task % kU) * kConsumers;
-            float2 p = make_float2(-kInf, 0.f);
-            if (i < sl.n) {
-                float v[G];
-                Elt<S>::unpack(load_vector<S>(r, sl.v0 + i), v);
-#pragma unroll
-                for (int k = 0; k < G; ++k) {
-                    const uint32_t key = key_of(v[k]);
-                    if (key >= t) {
-                        const int at = atomicAdd(&ctl.ncand, 1);
-                        if (at < kMaxCand) cand[at] = cand_of(key, (sl.v0 + i) * G - r.shift + k);
-                        v[k] = -kInf;
-                    }
-                }
-                p = pair_of<G>(v, a.k2);
-            }
-            part[task] = p;
-        }
-        __syncthreads();
-    }
-    if (nsel > kMaxSel || ctl.ncand > kMaxCand) {
-        exact_threshold<S>(a, r, sl, ctl, cand, tm, ts);
-    } else {
-        for (int i = tid; i < nsel; i += kThreads) {
-            float m = -kInf, s = 0.f;
-#pragma unroll
-            for (int u = 0; u < kU; ++u) pair_merge(m, s, part[i * kU + u].x, part[i * kU + u].y, a.k2);
-            gm[sel[i]] = m;
-            gs[sel[i]] = s;
-        }
-        __syncthreads();
-        if (consumer)
-            for (int j = 0; j < sl.nst; ++j)
-                pair_merge(tm, ts, gm[j * kConsumers + tid], gs[j * kConsumers + tid], a.k2);
-    }
-    // ---- 3. ranks ----
-    const int n = min(ctl.ncand, kMaxCand);
-    for (int i = tid; i < n; i += kThreads) {
-        const uint64_t c = cand[i];
-        int rk = 0;
-#pragma unroll 8
-        for (int q = 0; q < n; ++q) rk += cand[q] > c;
-        list[rk] = c;
-    }
-    for (int i = n + tid; i < K; i += kThreads) list[i] = 0;
-    __syncthreads();
-    for (int i = K + tid; i < n; i += kThreads) pair_merge(tm, ts, value_of(cand_key(list[i])), 1.f, a.k2);
-    auto block_pair = [&](float& m, float& s) {
-        pair_warp_reduce(m, s, a.k2);
-        if (lane == 0) {
-            ctl.red_m[warp] = m;
-            ctl.red_s[warp] = s;
-        }
-        __syncthreads();
-        m = -kInf;
-        s = 0.f;
-        for (int w = 0; w < kWarps; ++w) pair_merge(m, s, ctl.red_m[w], ctl.red_s[w], a.k2);
-    };
-    block_pair(tm, ts);
+    float tm = -kInf, ts = 0.f;
+    if (tid < kSel) select<S, kConsumers>(a, r, sl, sl.nst, ctl.sel, smem, gm, gs, tid, tm, ts);
     bool all_ok = ok;
     const uint64_t* top = list;
-    // ---- 4. the cluster's lists ----
     if (C > 1) {
-        if (tid == 0) ctl.tail = make_float4(tm, ts, ok ? 1.f : 0.f, 0.f);
+        if (tid == 0) ctl.sel.tail = make_float4(tm, ts, ok ? 1.f : 0.f, 0.f);
         cluster_arrive();
         cluster_wait();
         uint64_t* in = reinterpret_cast<uint64_t*>(smem + kInAt);
         uint64_t* out = reinterpret_cast<uint64_t*>(smem + kOutAt);
-        if (rank == 0) {
-            for (int i = tid; i < C * K; i += kThreads) {
+        if (rank == 0 && tid < kSel) {
+            for (int i = tid; i < C * K; i += kSel) {
                 const int p = i / K;
                 in[i] = ld_peer_u64(peer_addr(list + (i - p * K), (uint32_t)p));
                 out[i] = 0;
@@ -360,16 +490,16 @@ __global__ void __launch_bounds__(kThreads, 3) k_topk(const __grid_constant__ Ar
             tm = -kInf;
             ts = 0.f;
             for (int p = 0; p < C; ++p) {
-                const float4 o = ld_peer_f4(peer_addr(&ctl.tail, (uint32_t)p));
+                const float4 o = ld_peer_f4(peer_addr(&ctl.sel.tail, (uint32_t)p));
                 if (tid == 0) pair_merge(tm, ts, o.x, o.y, a.k2);
                 all_ok = all_ok && o.z != 0.f;
             }
         }
         cluster_arrive();                      // the peers may leave
         cluster_wait();
-        if (rank != 0) return;
-        __syncthreads();
-        for (int i = tid; i < C * K; i += kThreads) {
+        if (rank != 0 || tid >= kSel) return;
+        sel_sync();
+        for (int i = tid; i < C * K; i += kSel) {
             const uint64_t c = in[i];
             if (!c) continue;
             int rk = i % K;
@@ -386,29 +516,140 @@ __global__ void __launch_bounds__(kThreads, 3) k_topk(const __grid_constant__ Ar
             }
             out[rk] = c;
         }
-        __syncthreads();
-        for (int i = K + tid; i < C * K; i += kThreads)
+        sel_sync();
+        for (int i = K + tid; i < C * K; i += kSel)
             if (out[i]) pair_merge(tm, ts, value_of(cand_key(out[i])), 1.f, a.k2);
-        block_pair(tm, ts);
+        block_pair(tm, ts, ctl.sel, a.k2);
         top = out;
     }
-    // ---- outputs ----
-    for (int k = tid; k < K; k += kThreads) {
-        const uint64_t c = top[k];
-        a.values[row * K + k] = all_ok ? (c ? value_of(cand_key(c)) : -kInf) : __int_as_float(0x7FC00000);
-        a.ids[row * K + k] = all_ok && c ? cand_col(c) : -1;
+    if (tid < kSel) outputs(a, row, top, all_ok, tm, ts, tid);
+}
+
+// ---- many rows: a persistent kernel -----------------------------------------------------------------
+//
+// One block per SM walks the rows blockIdx.x, blockIdx.x + gridDim.x, ...: consumers reduce a row's
+// groups while the selecting warps work on the row before, so the copies never stop for a selection.
+
+constexpr int kPWarps = 16, kPNT = kPWarps * 32;             // consumers
+constexpr int kPVecs = kPNT * kU, kPBytes = kPVecs * 16;     // a stage: 32 KB
+constexpr int kPBufs = 3, kPStages = 8;                      // stages of the ring and, at most, of a row
+constexpr int kPProducer = kPWarps, kPSelect = kPWarps + 1;
+constexpr int kPThreads = (kPWarps + 1) * 32 + kSel;
+constexpr uint32_t kSuspend = 10000;                         // ns a poll may sleep
+static_assert(kPSelect % kSelWarps == 1, "a selecting warp's number is its warp's, less one, mod kSelWarps");
+
+struct alignas(16) PCtl {
+    SelCtl sel;
+    uint64_t full[kPBufs], empty[kPBufs];
+    uint64_t grouped[2], taken[2];   // a row's groups are there; have been selected from
+    int abort, err;
+};
+constexpr int kPSmem = kPBufs * kPBytes + kScratch + 2 * kPStages * kPNT * 8 + (int)sizeof(PCtl);
+
+template <typename S>
+__global__ void __launch_bounds__(kPThreads, 1) k_topk_rows(const __grid_constant__ Args a) {
+    constexpr int G = Elt<S>::kGroup;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint8_t* scratch = smem + kPBufs * kPBytes;
+    float* groups = reinterpret_cast<float*>(scratch + kScratch);   // [2][maxima, sums][kPStages][kPNT]
+    PCtl& ctl = *reinterpret_cast<PCtl*>(groups + 4 * kPStages * kPNT);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    volatile int* abort = &ctl.abort;
+    if (tid == 0) {
+        for (int i = 0; i < kPBufs; ++i) {
+            tc::mbar_init(&ctl.full[i], 1);
+            tc::mbar_init(&ctl.empty[i], kPWarps);
+        }
+        for (int p = 0; p < 2; ++p) {
+            tc::mbar_init(&ctl.grouped[p], kPWarps);
+            tc::mbar_init(&ctl.taken[p], kSelWarps);
+        }
+        ctl.abort = ctl.err = 0;
+        tc::fence_mbar_init();
     }
-    if (warp == 0) {
-        float m = top[0] ? value_of(cand_key(top[0])) : -kInf, s = 0.f;
-        for (int k = lane; k < K; k += 32)
-            if (top[k]) s += ex2((value_of(cand_key(top[k])) - m) * a.k2);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
-        pair_merge(m, s, tm, ts, a.k2);
+    __syncthreads();
+    auto slice_of = [&](const Row& r) { return Slice{0, r.nv, (r.nv + kPVecs - 1) / kPVecs}; };
+    int st = 0;
+    uint32_t phase = 0;
+    auto step = [&]() {
+        if (++st == kPBufs) {
+            st = 0;
+            phase ^= 1;
+        }
+    };
+    if (warp == kPProducer) {
         if (lane == 0) {
-            const float bad = __int_as_float(0x7FC00000);
-            a.lse[row] = !all_ok ? bad : s > 0.f ? m * a.scale + logf(s) : -kInf;
-            a.tail[row] = !all_ok ? bad : ts > 0.f ? tm * a.scale + logf(ts) : -kInf;
+            int q = 0;
+            for (int64_t row = blockIdx.x; row < a.T && !*abort; row += gridDim.x) {
+                const Row r = make_row<S>(a.logits, row, a.ld, a.V);
+                const Slice sl = slice_of(r);
+                for (int j = 0; j < sl.nst; ++j, ++q, step()) {
+                    if (!tc::mbar_wait(&ctl.empty[st], phase ^ 1, &ctl.abort, &ctl.err, kErrEmpty, tc::kWaitNs, kSuspend)) break;
+                    const int lo = max(j * kPVecs, r.iv0), hi = min((j + 1) * kPVecs, r.iv1);
+                    if (hi > lo && dbg::ok(lo >= 0 && hi <= r.nv, dbg::kCols)) {
+                        tc::mbar_arrive_expect_tx(&ctl.full[st], (uint32_t)(hi - lo) * 16);
+                        tc::bulk_load(smem + st * kPBytes + (lo - j * kPVecs) * 16, r.base + (int64_t)lo * 16,
+                                      (uint32_t)(hi - lo) * 16, &ctl.full[st]);
+                    } else {
+                        tc::mbar_arrive(&ctl.full[st]);
+                    }
+                }
+            }
+            if (*abort) {                      // copies in flight land before the block may leave
+                int never = 0;
+                for (int p = max(0, q - kPBufs); p < q; ++p)
+                    tc::mbar_wait(&ctl.full[p % kPBufs], (p / kPBufs) & 1, &never, nullptr, 0);
+            }
+        }
+        __syncwarp();
+    } else if (warp < kPWarps) {
+        int64_t e = 0;
+        for (int64_t row = blockIdx.x; row < a.T && !*abort; row += gridDim.x, ++e) {
+            const int par = (int)(e & 1);
+            const Row r = make_row<S>(a.logits, row, a.ld, a.V);
+            const Slice sl = slice_of(r);
+            // row e - 2's groups have been selected from
+            if (e >= 2) tc::mbar_wait(&ctl.taken[par], (uint32_t)((e - 2) >> 1) & 1, &ctl.abort, &ctl.err, kErrEmpty,
+                                      tc::kWaitNs, kSuspend);
+            float* gm = groups + par * 2 * kPStages * kPNT + tid;
+            for (int j = 0; j < sl.nst; ++j, step()) {
+                tc::mbar_wait(&ctl.full[st], phase, &ctl.abort, &ctl.err, kErrFull, tc::kWaitNs, kSuspend);
+                const uint4* buf = reinterpret_cast<const uint4*>(smem + st * kPBytes) + tid;
+                const int at = j * kPVecs + tid;
+                uint4 x[kU];
+                if (j * kPVecs >= r.iv0 && (j + 1) * kPVecs <= r.iv1) {
+#pragma unroll
+                    for (int u = 0; u < kU; ++u) x[u] = tc::lds16(buf + u * kPNT);
+                } else {
+#pragma unroll
+                    for (int u = 0; u < kU; ++u) {
+                        const int v = at + u * kPNT;
+                        x[u] = stage::neg_inf16<S>();
+                        if (v < r.nv) x[u] = v >= r.iv0 && v < r.iv1 ? tc::lds16(buf + u * kPNT) : load_partial<S>(r, v);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&ctl.empty[st]);
+                group_of<S>(x, a.k2, gm[j * kPNT], gm[(kPStages + j) * kPNT]);
+            }
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&ctl.grouped[par]);
+        }
+    } else {
+        const int stid = tid - kPSelect * 32;
+        int64_t e = 0;
+        for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x, ++e) {
+            const int par = (int)(e & 1);
+            const Row r = make_row<S>(a.logits, row, a.ld, a.V);
+            const Slice sl = slice_of(r);
+            tc::mbar_wait(&ctl.grouped[par], (uint32_t)(e >> 1) & 1, &ctl.abort, &ctl.err, kErrFull, tc::kWaitNs, kSuspend);
+            float* gm = groups + par * 2 * kPStages * kPNT;
+            float tm, ts;
+            select<S, kPNT>(a, r, sl, sl.nst, ctl.sel, scratch, gm, gm + kPStages * kPNT, stid, tm, ts);
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&ctl.taken[par]);
+            outputs(a, row, reinterpret_cast<const uint64_t*>(scratch + kListAt), !*abort, tm, ts, stid);
+            sel_sync();                        // the list has been read
         }
     }
 }
@@ -417,6 +658,8 @@ template <typename S>
 cudaError_t run(Args& a, int sms, cudaStream_t s) {
     constexpr int G = Elt<S>::kGroup;
     const int64_t nv = (a.V + 2 * G - 2) / G;
+    if (a.T >= kRowsPerSm * sms && nv > kPVecs && nv <= kPStages * kPVecs)
+        return launch_clusters<k_topk_rows<S>>(sms, 1, kPThreads, kPSmem, s, a);
     auto st = [&](int c) { return (int)(((nv + c - 1) / c + kStageVecs - 1) / kStageVecs); };
     // few rows: blocks for the SMs; long rows: groups that leave room for two blocks an SM
     int C = 1;

@@ -195,26 +195,35 @@ __device__ __forceinline__ void pair_warp_reduce(float& m, float& s, float k2) {
     }
 }
 
-// sum of 2^(v k2 - mb) over a thread's vectors of a stage
+// (d0, d1) = (a0 + b0, a1 + b1), in one packed instruction; each sum rounds as the scalar one.
+__device__ __forceinline__ void fadd2(float a0, float a1, float b0, float b1, float& d0, float& d1) {
+    asm("{\n\t.reg .b64 pa, pb, pd;\n\t"
+        "mov.b64 pa, {%2, %3};\n\tmov.b64 pb, {%4, %5};\n\t"
+        "add.rn.f32x2 pd, pa, pb;\n\tmov.b64 {%0, %1}, pd;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
+// sum of 2^(v k2 - mb) over a thread's vectors of a stage: exponents and sums two at a time (even and
+// odd values summed apart), since the issue slots are what these kernels run short of
 template <int G, int U>
 __device__ __forceinline__ float sum_exp(const float (&v)[U][G], float k2, float mb) {
-    float t[U];
+    constexpr int N = U * G;
+    float e[N];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        float e[G];
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int k = 0; k < G; ++k) e[k] = ex2(fmaf(v[u][k], k2, -mb));
+        for (int k = 0; k < G; k += 2) {
+            float a0, a1;
+            ffma2(v[u][k], v[u][k + 1], k2, -mb, a0, a1);
+            e[u * G + k] = ex2(a0);
+            e[u * G + k + 1] = ex2(a1);
+        }
 #pragma unroll
-        for (int w = 1; w < G; w *= 2)
+    for (int w = 2; w < N; w *= 2)
 #pragma unroll
-            for (int k = 0; k + w < G; k += 2 * w) e[k] += e[k + w];
-        t[u] = e[0];
-    }
-#pragma unroll
-    for (int w = 1; w < U; w *= 2)
-#pragma unroll
-        for (int u = 0; u + w < U; u += 2 * w) t[u] += t[u + w];
-    return t[0];
+        for (int k = 0; k + w < N; k += 2 * w) fadd2(e[k], e[k + 1], e[k + w], e[k + w + 1], e[k], e[k + 1]);
+    return e[0] + e[1];
 }
 
 template <int G, int U>
@@ -248,6 +257,31 @@ __device__ __forceinline__ void pair_push(const float (&v)[U][G], float& m, floa
         mb = m * k2;
     }
     s += t;
+}
+
+// The largest of a thread's vectors of a stage as they were loaded (bf16: two at a time).
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+template <typename S, int U>
+__device__ __forceinline__ float max_of_loaded(const uint4 (&x)[U]) {
+    if (sizeof(S) == 2) {
+        uint32_t m = x[0].x;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (u) m = max_bf16x2(m, x[u].x);
+            m = max_bf16x2(max_bf16x2(m, x[u].y), max_bf16x2(x[u].z, x[u].w));
+        }
+        return fmaxf(bf16_lo(m), bf16_hi(m));
+    }
+    float m = __uint_as_float(x[0].x);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        m = fmaxf(fmaxf(fmaxf(m, __uint_as_float(x[u].x)), fmaxf(__uint_as_float(x[u].y), __uint_as_float(x[u].z))),
+                  __uint_as_float(x[u].w));
+    return m;
 }
 
 // ---- thread-block clusters -------------------------------------------------------------------
