@@ -95,8 +95,35 @@ def test_topk_many_rows_and_wide(vce):
     check(vce, logits_of(2, 2000003, torch.bfloat16, 9), 256, 4.0)
 
 
+@pytest.mark.parametrize("dtype,V,pad,left", [(torch.bfloat16, 20011, 0, 0), (torch.bfloat16, 70000, 8, 8),
+                                              (torch.float32, 16385, 3, 1), (torch.bfloat16, 131000, 0, 0)])
+@pytest.mark.parametrize("k", [1, 64, 256])
+def test_topk_rows_enough_for_every_sm(vce, dtype, V, pad, left, k):
+    """More rows than two an SM: sampled rows against the oracle, and rows of ties, of -inf and with
+    one value far above among them."""
+    T = 330
+    z = logits_of(T, V, dtype, V + k, pad, left)
+    z[5] = 0.25
+    z[17] = -float("inf")
+    z[18, 3:] = -float("inf")
+    z[170, V - 1] = 90.0
+    z[171] = (torch.arange(V, device="cuda") % 5).to(dtype)
+    values, ids, lse, tail = [x.cpu().numpy() for x in vce.ce_topk(z, k, 0.9)]
+    rows = np.array([0, 5, 17, 18, 151, 152, 153, 170, 171, 303, 304, 329])
+    host = z[torch.from_numpy(rows).cuda()].double().cpu().numpy()
+    rv, ri, rl, rt = L.topk(host, k, 0.9)
+    assert np.array_equal(ids[rows], ri) and np.array_equal(values[rows].astype(np.float64), rv)
+    zmax = np.abs(host[np.isfinite(host)]).max()
+    G.check_lse(lse[rows], rl, zmax, 0.9)
+    G.check_lse(tail[rows], rt, zmax, 0.9, "tail")
+    # every row against the few-rows path, which takes another kernel
+    for r in range(0, T, 110):
+        v2, i2, _, _ = vce.ce_topk(z[r:r + 110], k, 0.9)
+        assert np.array_equal(i2.cpu().numpy(), ids[r:r + 110]) and np.array_equal(v2.cpu().numpy(), values[r:r + 110])
+
+
 def test_topk_same_bits_every_time(vce):
-    z = logits_of(300, 128256, torch.bfloat16, 10)
+    z = logits_of(400, 128256, torch.bfloat16, 10)
     first = [x.clone() for x in vce.ce_topk(z, 64, 2.0)]
     for _ in range(5):
         for a, b in zip(vce.ce_topk(z, 64, 2.0), first):

@@ -33,22 +33,21 @@ namespace topk {
 using namespace rs;
 
 constexpr int kThreads = kConsumers + 32;   // k_topk: consumers, which also select, and the producer warp
-constexpr int kSel = 256, kSelWarps = kSel / 32;   // threads that select
-static_assert(kSel == kConsumers, "the consumers of k_topk select");
+constexpr int kSets = 512;                  // sets of groups among whose maxima the bound is searched
 constexpr int kMaxCand = 1024;              // candidates of a block
 constexpr int kMaxSel = 512;                // groups read again
 constexpr uint32_t kKeyMin = 0x00800000u;   // order key of the lowest finite value (-inf is one below)
 
-// Scratch of the selection (in k_topk over the stage buffers, once the columns have streamed through).
+// Scratch of a selection (in k_topk over the stage buffers, once the columns have streamed through).
 constexpr int kCandAt = 0;                                   // [kMaxCand] candidates
-constexpr int kListAt = kCandAt + kMaxCand * 8;              // [kMaxCand] candidates by rank (read by peers)
-constexpr int kSelAt = kListAt + kMaxCand * 8;               // [kMaxSel] group numbers
+constexpr int kSelAt = kCandAt + kMaxCand * 8;               // [kMaxSel] group numbers; before, [kSets] maxima
 constexpr int kPartAt = kSelAt + kMaxSel * 4;                // [kMaxSel * kU] pairs of the vectors read again
-constexpr int kPartEnd = kPartAt + kMaxSel * kU * 8;
-constexpr int kInAt = kSelAt;                                // [cluster * K] the cluster's lists
+constexpr int kListAt = kPartAt;                             // then [kMaxCand] candidates by rank (read by peers)
+constexpr int kScratch = kPartAt + kMaxSel * kU * 8;
+constexpr int kInAt = kListAt + kMaxCand * 8;                // [cluster * K] the cluster's lists
 constexpr int kOutAt = kInAt + kMaxCluster * VCE_MAX_TOPK * 8;   // the same by rank
-constexpr int kScratch = kOutAt + kMaxCluster * VCE_MAX_TOPK * 8;
-static_assert(kScratch <= 3 * kStageBytes && kPartEnd <= kScratch && kMaxCand >= VCE_MAX_TOPK, "scratch");
+constexpr int kClusterScratch = kOutAt + kMaxCluster * VCE_MAX_TOPK * 8;
+static_assert(kMaxCand * 8 <= kMaxSel * kU * 8 && kSets * 4 <= kMaxSel * 4 && kMaxCand >= VCE_MAX_TOPK, "scratch");
 
 struct Args {
     const void* logits;
@@ -66,8 +65,8 @@ constexpr int kRowsPerSm = 2;               // rows for each SM from which the p
 // What the selecting threads share.
 struct alignas(16) SelCtl {
     float4 tail;                    // the block's pair of the columns left out (read by peers)
-    float red_m[kSelWarps], red_s[kSelWarps];
-    int count[2][kSelWarps];
+    float red_m[8], red_s[8];       // by the selecting warp
+    int count[2][8];
     int nsel, ncand;
     float bound;
 };
@@ -79,11 +78,20 @@ struct alignas(16) Ctl {
 
 __host__ __device__ constexpr int smem_bytes(int nbuf, int max_stages) {
     const int b = nbuf * kStageBytes;
-    return (b > kScratch ? b : kScratch) + max_stages * kConsumers * 8 + (int)sizeof(Ctl);
+    return (b > kClusterScratch ? b : kClusterScratch) + max_stages * kConsumers * 8 + (int)sizeof(Ctl);
 }
 
-// Barrier of the selecting threads.
-__device__ __forceinline__ void sel_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSel) : "memory"); }
+// NS threads (whole warps of consecutive numbers, tid counted from the first) select together; a
+// barrier of theirs, number `id`.
+template <int NS>
+struct Team {
+    static_assert(NS % 32 == 0 && NS <= 256 && kSets % NS == 0, "selecting threads");
+    static constexpr int kThreads = NS, kWarps = NS / 32;
+    int tid, id;
+    __device__ __forceinline__ void sync() const { asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(NS) : "memory"); }
+    __device__ __forceinline__ int warp() const { return tid >> 5; }
+    __device__ __forceinline__ int lane() const { return tid & 31; }
+};
 
 // Keys in the order of the values (larger value, larger key); -0 as +0.
 __device__ __forceinline__ uint32_t key_of(float v) {
@@ -102,27 +110,28 @@ __device__ __forceinline__ int cand_col(uint64_t c) { return (int)(0xFFFFFFFFu -
 
 // Sum over the selecting threads of each one's n (call number it picks one of two buffers, so one
 // barrier a call is enough).
-__device__ __forceinline__ int block_sum(int n, SelCtl& ctl, int it) {
+template <int NS>
+__device__ __forceinline__ int block_sum(const Team<NS>& tm, int n, SelCtl& ctl, int it) {
     n = __reduce_add_sync(0xFFFFFFFFu, n);
-    if ((threadIdx.x & 31) == 0) ctl.count[it & 1][(threadIdx.x >> 5) % kSelWarps] = n;
-    sel_sync();
+    if (tm.lane() == 0) ctl.count[it & 1][tm.warp()] = n;
+    tm.sync();
     int t = 0;
 #pragma unroll
-    for (int w = 0; w < kSelWarps; ++w) t += ctl.count[it & 1][w];
+    for (int w = 0; w < Team<NS>::kWarps; ++w) t += ctl.count[it & 1][w];
     return t;
 }
 // Merges the selecting threads' pairs; every thread has the result.
-__device__ __forceinline__ void block_pair(float& m, float& s, SelCtl& ctl, float k2) {
-    const int warp = (threadIdx.x >> 5) % kSelWarps;
+template <int NS>
+__device__ __forceinline__ void block_pair(const Team<NS>& team, float& m, float& s, SelCtl& ctl, float k2) {
     pair_warp_reduce(m, s, k2);
-    if ((threadIdx.x & 31) == 0) {
-        ctl.red_m[warp] = m;
-        ctl.red_s[warp] = s;
+    if (team.lane() == 0) {
+        ctl.red_m[team.warp()] = m;
+        ctl.red_s[team.warp()] = s;
     }
-    sel_sync();
+    team.sync();
     m = -kInf;
     s = 0.f;
-    for (int w = 0; w < kSelWarps; ++w) pair_merge(m, s, ctl.red_m[w], ctl.red_s[w], k2);
+    for (int w = 0; w < Team<NS>::kWarps; ++w) pair_merge(m, s, ctl.red_m[w], ctl.red_s[w], k2);
 }
 
 // The pair of G values, -inf left out.
@@ -142,23 +151,23 @@ __device__ __forceinline__ float2 pair_of(const float (&v)[G], float k2) {
 // The K largest of the slice by the exact K-th value, every value read from global memory as often
 // as its search takes: for slices where the bound from the groups admits too many.  Candidates go
 // to cand (ctl.ncand of them), everything else into this thread's pair (tm, ts).
-template <typename S>
+template <typename S, int NS>
 __device__ __noinline__ void exact_threshold(const Args& a, const Row& r, const Slice& sl, SelCtl& ctl, uint64_t* cand,
-                                             int tid, float& tm, float& ts) {
+                                             Team<NS> team, float& tm, float& ts) {
     constexpr int G = Elt<S>::kGroup;
-    const int lane = tid & 31, warp = tid >> 5;
+    const int tid = team.tid, lane = team.lane(), warp = team.warp();
     int it = 0;
     auto count_from = [&](uint32_t t) {
         int n = 0;
-        for (int i = tid; i < sl.n; i += kSel) {
+        for (int i = tid; i < sl.n; i += NS) {
             float v[G];
             Elt<S>::unpack(load_vector<S>(r, sl.v0 + i), v);
 #pragma unroll
             for (int k = 0; k < G; ++k) n += key_of(v[k]) >= t;
         }
-        return block_sum(n, ctl, it++);
+        return block_sum(team, n, ctl, it++);
     };
-    sel_sync();                                // ctl.count of the caller's search has been read
+    team.sync();                                // ctl.count of the caller's search has been read
     uint32_t t = kKeyMin;
     if (count_from(kKeyMin) >= a.K) {
         t = 0;
@@ -166,10 +175,10 @@ __device__ __noinline__ void exact_threshold(const Args& a, const Row& r, const 
             if (count_from(t | (1u << bit)) >= a.K) t |= 1u << bit;
     }
     if (tid == 0) ctl.ncand = 0;
-    sel_sync();
+    team.sync();
     // above t: candidates; equal: counted; below: the tail
     int eq = 0;
-    for (int i = tid; i < sl.n; i += kSel) {
+    for (int i = tid; i < sl.n; i += NS) {
         float v[G];
         Elt<S>::unpack(load_vector<S>(r, sl.v0 + i), v);
 #pragma unroll
@@ -185,13 +194,13 @@ __device__ __noinline__ void exact_threshold(const Args& a, const Row& r, const 
         const float2 p = pair_of<G>(v, a.k2);
         pair_merge(tm, ts, p.x, p.y, a.k2);
     }
-    const int total_eq = block_sum(eq, ctl, it++);
+    const int total_eq = block_sum(team, eq, ctl, it++);
     const int above = min(ctl.ncand, kMaxCand);
     const int want = min(total_eq, a.K - above);
-    sel_sync();
+    team.sync();
     // the first `want` values equal to t, in column order: vectors i = base + tid
     int found = 0;
-    for (int base = 0; base < sl.n && found < want; base += kSel) {
+    for (int base = 0; base < sl.n && found < want; base += NS) {
         const int i = base + tid;
         uint32_t hits = 0;
         if (i < sl.n) {
@@ -208,58 +217,63 @@ __device__ __noinline__ void exact_threshold(const Args& a, const Row& r, const 
         }
         if (lane == 31) ctl.count[0][warp] = before;
         before += found - n;
-        sel_sync();
+        team.sync();
         int all = 0;
-        for (int w = 0; w < kSelWarps; ++w) {
+        for (int w = 0; w < Team<NS>::kWarps; ++w) {
             if (w < warp) before += ctl.count[0][w];
             all += ctl.count[0][w];
         }
         for (; hits && before < want; hits &= hits - 1, ++before)
             cand[above + before] = cand_of(t, (sl.v0 + i) * G - r.shift + __ffs(hits) - 1);
         found += all;
-        sel_sync();
+        team.sync();
     }
     if (tid == 0) {
         ctl.ncand = above + want;
         if (total_eq > want) pair_merge(tm, ts, value_of(t), (float)(total_eq - want), a.k2);
     }
-    sel_sync();
+    team.sync();
 }
 
 // The K largest of a slice whose groups' maxima and sums are in gm and gs ([stages][GT], group t of
-// stage j holding the vectors j GT kU + t + u GT), by the kSel selecting threads: the sorted
+// stage j holding the vectors j GT kU + t + u GT), by a team: the sorted
 // candidates, at least K places with 0 behind the last, in the scratch's list, and the pair of the
 // columns that are not among the first K (the same in every thread).
-template <typename S, int GT>
+template <typename S, int GT, int NS>
 __device__ __forceinline__ void select(const Args& a, const Row& r, const Slice& sl, int stages, SelCtl& ctl,
-                                       uint8_t* scratch, float* gm, float* gs, int tid, float& tm, float& ts) {
+                                       uint8_t* scratch, float* gm, float* gs, const Team<NS>& team, float& tm, float& ts) {
     constexpr int G = Elt<S>::kGroup;
-    static_assert(GT % kSel == 0, "whole rounds of groups");
-    const int K = a.K, rounds = stages * (GT / kSel), groups = stages * GT;   // rounds <= 64
+    static_assert(GT % NS == 0, "whole rounds of groups");
+    constexpr int SP = kSets / NS;             // sets of a thread
+    const int tid = team.tid, lane = team.lane(), warp = team.warp();
+    const int K = a.K, rounds = stages * (GT / NS), groups = stages * GT;   // rounds <= 64
     uint64_t* cand = reinterpret_cast<uint64_t*>(scratch + kCandAt);
     uint64_t* list = reinterpret_cast<uint64_t*>(scratch + kListAt);
     int* sel = reinterpret_cast<int*>(scratch + kSelAt);
     float2* part = reinterpret_cast<float2*>(scratch + kPartAt);
-    const int lane = tid & 31, warp = tid >> 5;
     // ---- 1. the bound t ----
-    // Each thread's groups are tid + i kSel; the largest key of its even and of its odd ones are two of
-    // 2 kSel values, each that of some column, so the K-th largest of them bounds the K-th largest value
-    // from below nearly as well as that of all groups (K = 64: 73 groups are read again instead of 64),
-    // and one warp finds it in registers, without barriers.
-    float top2[2] = {-kInf, -kInf};
-    int i = 0;
-#pragma unroll 4
-    for (; i + 1 < rounds; i += 2) {
-        top2[0] = fmaxf(top2[0], gm[i * kSel + tid]);
-        top2[1] = fmaxf(top2[1], gm[(i + 1) * kSel + tid]);
+    // Each thread's groups are tid + i NS, round i in its set i mod SP.  The largest values of the kSets
+    // sets are values of as many columns, so the K-th largest of them bounds the K-th largest value from
+    // below nearly as well as that of all groups (K = 64: 73 groups are read again instead of 64), and
+    // one warp finds it in registers, without barriers.
+    float most_of[SP];
+#pragma unroll
+    for (int q = 0; q < SP; ++q) most_of[q] = -kInf;
+    for (int i = 0; i < rounds; i += SP) {
+#pragma unroll
+        for (int q = 0; q < SP; ++q)
+            if (i + q < rounds) most_of[q] = fmaxf(most_of[q], gm[(i + q) * NS + tid]);
     }
-    if (i < rounds) top2[0] = fmaxf(top2[0], gm[i * kSel + tid]);
-    uint32_t* tops = reinterpret_cast<uint32_t*>(scratch + kSelAt);   // [2 kSel]
-    tops[tid] = key_of(top2[0]);
-    tops[kSel + tid] = key_of(top2[1]);
-    sel_sync();
+    uint32_t* tops = reinterpret_cast<uint32_t*>(scratch + kSelAt);   // [kSets]
+    float most_mine = -kInf;
+#pragma unroll
+    for (int q = 0; q < SP; ++q) {
+        tops[q * NS + tid] = key_of(most_of[q]);
+        most_mine = fmaxf(most_mine, most_of[q]);
+    }
+    team.sync();
     if (warp == 0) {
-        constexpr int N = 2 * kSel / 32;
+        constexpr int N = kSets / 32;
         uint32_t k[N], most = 0;
         int n = 0;
 #pragma unroll
@@ -289,15 +303,15 @@ __device__ __forceinline__ void select(const Args& a, const Row& r, const Slice&
             ctl.nsel = ctl.ncand = 0;
         }
     }
-    sel_sync();
+    team.sync();
     const float t = ctl.bound;
     // ---- 2. candidates ----
     // the groups with a value >= t: a place on the list for each lane's, one atomic a warp
     {
-        uint64_t mine = 0;                     // bit i: group tid + i kSel
-        if (fmaxf(top2[0], top2[1]) >= t) {
+        uint64_t mine = 0;                     // bit i: group tid + i NS
+        if (most_mine >= t) {
 #pragma unroll 4
-            for (int i = 0; i < rounds; ++i) mine |= (uint64_t)(gm[i * kSel + tid] >= t) << i;
+            for (int i = 0; i < rounds; ++i) mine |= (uint64_t)(gm[i * NS + tid] >= t) << i;
         }
         const int n = __popcll(mine);
         int at = n;
@@ -310,21 +324,21 @@ __device__ __forceinline__ void select(const Args& a, const Row& r, const Slice&
         if (lane == 31 && at) base = atomicAdd(&ctl.nsel, at);
         at += __shfl_sync(0xFFFFFFFFu, base, 31) - n;
         for (; mine; mine &= mine - 1, ++at)
-            if (at < kMaxSel) sel[at] = tid + (__ffsll((long long)mine) - 1) * kSel;
+            if (at < kMaxSel) sel[at] = tid + (__ffsll((long long)mine) - 1) * NS;
     }
-    sel_sync();
+    team.sync();
     const int nsel = ctl.nsel;
     tm = -kInf;
     ts = 0.f;                                  // this thread's pair of the columns left out
     if (nsel <= kMaxSel) {
         // vectors of the listed groups, two in flight a thread
         const int tasks = nsel * kU;
-        for (int task0 = tid; task0 < tasks; task0 += 2 * kSel) {
+        for (int task0 = tid; task0 < tasks; task0 += 2 * NS) {
             uint4 x[2];
             int at[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int task = task0 + h * kSel;
+                const int task = task0 + h * NS;
                 at[h] = -1;
                 if (task >= tasks) continue;
                 const int g = sel[task / kU];
@@ -334,7 +348,7 @@ __device__ __forceinline__ void select(const Args& a, const Row& r, const Slice&
                 x[h] = load_vector<S>(r, sl.v0 + i);
             }
 #pragma unroll 1
-            for (int h = 0; h < 2 && task0 + h * kSel < tasks; ++h) {
+            for (int h = 0; h < 2 && task0 + h * NS < tasks; ++h) {
                 float2 p = make_float2(-kInf, 0.f);
                 if (at[0] >= 0) {
                     float v[G];
@@ -354,51 +368,53 @@ __device__ __forceinline__ void select(const Args& a, const Row& r, const Slice&
                     }
                     p = pair_of<G>(v, a.k2);
                 }
-                part[task0 + h * kSel] = p;
+                part[task0 + h * NS] = p;
                 x[0] = x[1];
                 at[0] = at[1];
             }
         }
-        sel_sync();
+        team.sync();
     }
     if (nsel > kMaxSel || ctl.ncand > kMaxCand) {
-        exact_threshold<S>(a, r, sl, ctl, cand, tid, tm, ts);
+        exact_threshold<S, NS>(a, r, sl, ctl, cand, team, tm, ts);
     } else {
-        for (int i = tid; i < nsel; i += kSel) {
+        for (int i = tid; i < nsel; i += NS) {
             float m = -kInf, s = 0.f;
 #pragma unroll
             for (int u = 0; u < kU; ++u) pair_merge(m, s, part[i * kU + u].x, part[i * kU + u].y, a.k2);
             gm[sel[i]] = m;
             gs[sel[i]] = s;
         }
-        sel_sync();
+        team.sync();
 #pragma unroll 4
-        for (int g = tid; g < groups; g += kSel) tm = fmaxf(tm, gm[g]);
+        for (int g = tid; g < groups; g += NS) tm = fmaxf(tm, gm[g]);
         if (tm > -kInf) {
 #pragma unroll 4
-            for (int g = tid; g < groups; g += kSel) ts += gs[g] * ex2((gm[g] - tm) * a.k2);   // 0 * 0 for -inf
+            for (int g = tid; g < groups; g += NS) ts += gs[g] * ex2((gm[g] - tm) * a.k2);   // 0 * 0 for -inf
         }
     }
     // ---- 3. ranks ----
     const int n = min(ctl.ncand, kMaxCand);
-    for (int i = tid; i < n; i += kSel) {
+    for (int i = tid; i < n; i += NS) {
         const uint64_t c = cand[i];
         int rk = 0;
 #pragma unroll 8
         for (int q = 0; q < n; ++q) rk += cand[q] > c;
         list[rk] = c;
     }
-    for (int i = n + tid; i < K; i += kSel) list[i] = 0;
-    sel_sync();
-    for (int i = K + tid; i < n; i += kSel) pair_merge(tm, ts, value_of(cand_key(list[i])), 1.f, a.k2);
-    block_pair(tm, ts, ctl, a.k2);
+    for (int i = n + tid; i < K; i += NS) list[i] = 0;
+    team.sync();
+    for (int i = K + tid; i < n; i += NS) pair_merge(tm, ts, value_of(cand_key(list[i])), 1.f, a.k2);
+    block_pair(team, tm, ts, ctl, a.k2);
 }
 
 // The row's outputs from its sorted list and the pair of the rest, by the selecting threads.
+template <int NS>
 __device__ __forceinline__ void outputs(const Args& a, int64_t row, const uint64_t* top, bool ok, float tm, float ts,
-                                        int tid) {
+                                        const Team<NS>& team) {
+    const int tid = team.tid;
     const float bad = __int_as_float(0x7FC00000);
-    for (int k = tid; k < a.K; k += kSel) {
+    for (int k = tid; k < a.K; k += NS) {
         const uint64_t c = top[k];
         a.values[row * a.K + k] = ok ? (c ? value_of(cand_key(c)) : -kInf) : bad;
         a.ids[row * a.K + k] = ok && c ? cand_col(c) : -1;
@@ -433,14 +449,15 @@ __device__ __forceinline__ void group_of(const uint4 (&x)[kU], float k2, float& 
 
 template <typename S>
 __global__ void __launch_bounds__(kThreads, 3) k_topk(const __grid_constant__ Args a) {
-    constexpr int G = Elt<S>::kGroup;
     extern __shared__ __align__(128) uint8_t smem[];
-    const int over = max(a.nbuf * kStageBytes, kScratch);
+    const int over = max(a.nbuf * kStageBytes, kClusterScratch);
     float* gm = reinterpret_cast<float*>(smem + over);
     float* gs = gm + a.max_stages * kConsumers;
     Ctl& ctl = *reinterpret_cast<Ctl*>(gs + a.max_stages * kConsumers);
     uint64_t* list = reinterpret_cast<uint64_t*>(smem + kListAt);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr int NS = kConsumers;             // the consumers select
+    const Team<NS> team{tid, 1};
     const int C = a.cluster, K = a.K;
     const int rank = C > 1 ? (int)cluster_rank() : 0;
     const int64_t row = blockIdx.x / C;
@@ -472,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_topk(const __grid_constant__ Ar
     if (!ok) __syncthreads();                  // the scratch overlies the stages
 
     float tm = -kInf, ts = 0.f;
-    if (tid < kSel) select<S, kConsumers>(a, r, sl, sl.nst, ctl.sel, smem, gm, gs, tid, tm, ts);
+    if (tid < NS) select<S, kConsumers, NS>(a, r, sl, sl.nst, ctl.sel, smem, gm, gs, team, tm, ts);
     bool all_ok = ok;
     const uint64_t* top = list;
     if (C > 1) {
@@ -481,8 +498,8 @@ __global__ void __launch_bounds__(kThreads, 3) k_topk(const __grid_constant__ Ar
         cluster_wait();
         uint64_t* in = reinterpret_cast<uint64_t*>(smem + kInAt);
         uint64_t* out = reinterpret_cast<uint64_t*>(smem + kOutAt);
-        if (rank == 0 && tid < kSel) {
-            for (int i = tid; i < C * K; i += kSel) {
+        if (rank == 0 && tid < NS) {
+            for (int i = tid; i < C * K; i += NS) {
                 const int p = i / K;
                 in[i] = ld_peer_u64(peer_addr(list + (i - p * K), (uint32_t)p));
                 out[i] = 0;
@@ -497,9 +514,9 @@ __global__ void __launch_bounds__(kThreads, 3) k_topk(const __grid_constant__ Ar
         }
         cluster_arrive();                      // the peers may leave
         cluster_wait();
-        if (rank != 0 || tid >= kSel) return;
-        sel_sync();
-        for (int i = tid; i < C * K; i += kSel) {
+        if (rank != 0 || tid >= NS) return;
+        team.sync();
+        for (int i = tid; i < C * K; i += NS) {
             const uint64_t c = in[i];
             if (!c) continue;
             int rk = i % K;
@@ -516,42 +533,42 @@ __global__ void __launch_bounds__(kThreads, 3) k_topk(const __grid_constant__ Ar
             }
             out[rk] = c;
         }
-        sel_sync();
-        for (int i = K + tid; i < C * K; i += kSel)
+        team.sync();
+        for (int i = K + tid; i < C * K; i += NS)
             if (out[i]) pair_merge(tm, ts, value_of(cand_key(out[i])), 1.f, a.k2);
-        block_pair(tm, ts, ctl.sel, a.k2);
+        block_pair(team, tm, ts, ctl.sel, a.k2);
         top = out;
     }
-    if (tid < kSel) outputs(a, row, top, all_ok, tm, ts, tid);
+    if (tid < NS) outputs(a, row, top, all_ok, tm, ts, team);
 }
 
 // ---- many rows: a persistent kernel -----------------------------------------------------------------
 //
 // One block per SM walks the rows blockIdx.x, blockIdx.x + gridDim.x, ...: consumers reduce a row's
-// groups while the selecting warps work on the row before, so the copies never stop for a selection.
+// groups while two teams of selecting warps work on the rows before (even and odd ones), so the copies
+// never stop for a selection, and a selection's waits are covered by the other's.
 
 constexpr int kPWarps = 16, kPNT = kPWarps * 32;             // consumers
 constexpr int kPVecs = kPNT * kU, kPBytes = kPVecs * 16;     // a stage: 32 KB
 constexpr int kPBufs = 3, kPStages = 8;                      // stages of the ring and, at most, of a row
 constexpr int kPProducer = kPWarps, kPSelect = kPWarps + 1;
-constexpr int kPThreads = (kPWarps + 1) * 32 + kSel;
+constexpr int kPTeam = 128;                                  // selecting threads of a team
+constexpr int kPThreads = (kPWarps + 1) * 32 + 2 * kPTeam;
 constexpr uint32_t kSuspend = 10000;                         // ns a poll may sleep
-static_assert(kPSelect % kSelWarps == 1, "a selecting warp's number is its warp's, less one, mod kSelWarps");
 
 struct alignas(16) PCtl {
-    SelCtl sel;
+    SelCtl sel[2];
     uint64_t full[kPBufs], empty[kPBufs];
     uint64_t grouped[2], taken[2];   // a row's groups are there; have been selected from
     int abort, err;
 };
-constexpr int kPSmem = kPBufs * kPBytes + kScratch + 2 * kPStages * kPNT * 8 + (int)sizeof(PCtl);
+constexpr int kPSmem = kPBufs * kPBytes + 2 * kScratch + 2 * kPStages * kPNT * 8 + (int)sizeof(PCtl);
 
 template <typename S>
 __global__ void __launch_bounds__(kPThreads, 1) k_topk_rows(const __grid_constant__ Args a) {
-    constexpr int G = Elt<S>::kGroup;
     extern __shared__ __align__(128) uint8_t smem[];
-    uint8_t* scratch = smem + kPBufs * kPBytes;
-    float* groups = reinterpret_cast<float*>(scratch + kScratch);   // [2][maxima, sums][kPStages][kPNT]
+    uint8_t* scratch = smem + kPBufs * kPBytes;                     // [2]
+    float* groups = reinterpret_cast<float*>(scratch + 2 * kScratch);   // [2][maxima, sums][kPStages][kPNT]
     PCtl& ctl = *reinterpret_cast<PCtl*>(groups + 4 * kPStages * kPNT);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile int* abort = &ctl.abort;
@@ -562,7 +579,7 @@ __global__ void __launch_bounds__(kPThreads, 1) k_topk_rows(const __grid_constan
         }
         for (int p = 0; p < 2; ++p) {
             tc::mbar_init(&ctl.grouped[p], kPWarps);
-            tc::mbar_init(&ctl.taken[p], kSelWarps);
+            tc::mbar_init(&ctl.taken[p], kPTeam / 32);
         }
         ctl.abort = ctl.err = 0;
         tc::fence_mbar_init();
@@ -636,20 +653,21 @@ __global__ void __launch_bounds__(kPThreads, 1) k_topk_rows(const __grid_constan
             if (lane == 0) tc::mbar_arrive(&ctl.grouped[par]);
         }
     } else {
-        const int stid = tid - kPSelect * 32;
-        int64_t e = 0;
-        for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x, ++e) {
-            const int par = (int)(e & 1);
+        const int par = (tid - kPSelect * 32) / kPTeam;
+        const Team<kPTeam> team{(tid - kPSelect * 32) % kPTeam, 1 + par};
+        uint8_t* mine = scratch + par * kScratch;
+        float* gm = groups + par * 2 * kPStages * kPNT;
+        uint32_t phase_of = 0;
+        for (int64_t row = blockIdx.x + (int64_t)par * gridDim.x; row < a.T; row += 2 * (int64_t)gridDim.x, phase_of ^= 1) {
             const Row r = make_row<S>(a.logits, row, a.ld, a.V);
             const Slice sl = slice_of(r);
-            tc::mbar_wait(&ctl.grouped[par], (uint32_t)(e >> 1) & 1, &ctl.abort, &ctl.err, kErrFull, tc::kWaitNs, kSuspend);
-            float* gm = groups + par * 2 * kPStages * kPNT;
+            tc::mbar_wait(&ctl.grouped[par], phase_of, &ctl.abort, &ctl.err, kErrFull, tc::kWaitNs, kSuspend);
             float tm, ts;
-            select<S, kPNT>(a, r, sl, sl.nst, ctl.sel, scratch, gm, gm + kPStages * kPNT, stid, tm, ts);
+            select<S, kPNT, kPTeam>(a, r, sl, sl.nst, ctl.sel[par], mine, gm, gm + kPStages * kPNT, team, tm, ts);
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&ctl.taken[par]);
-            outputs(a, row, reinterpret_cast<const uint64_t*>(scratch + kListAt), !*abort, tm, ts, stid);
-            sel_sync();                        // the list has been read
+            outputs(a, row, reinterpret_cast<const uint64_t*>(mine + kListAt), !*abort, tm, ts, team);
+            team.sync();                       // the list has been read
         }
     }
 }
