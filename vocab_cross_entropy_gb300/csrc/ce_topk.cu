@@ -76,9 +76,17 @@ struct alignas(16) Ctl {
     Barriers bar;
 };
 
+// The scratch lies over the stage buffers, or behind them where they hold the whole slice (which is
+// then read again from there).
+__host__ __device__ constexpr int scratch_at(int nbuf, int max_stages) {
+    return max_stages <= nbuf ? nbuf * kStageBytes : 0;
+}
+__host__ __device__ constexpr int scratch_end(int nbuf, int max_stages) {
+    const int b = nbuf * kStageBytes, e = scratch_at(nbuf, max_stages) + kClusterScratch;
+    return b > e ? b : e;
+}
 __host__ __device__ constexpr int smem_bytes(int nbuf, int max_stages) {
-    const int b = nbuf * kStageBytes;
-    return (b > kClusterScratch ? b : kClusterScratch) + max_stages * kConsumers * 8 + (int)sizeof(Ctl);
+    return scratch_end(nbuf, max_stages) + max_stages * kConsumers * 8 + (int)sizeof(Ctl);
 }
 
 // NS threads (whole warps of consecutive numbers, tid counted from the first) select together; a
@@ -238,10 +246,12 @@ __device__ __noinline__ void exact_threshold(const Args& a, const Row& r, const 
 // The K largest of a slice whose groups' maxima and sums are in gm and gs ([stages][GT], group t of
 // stage j holding the vectors j GT kU + t + u GT), by a team: the sorted
 // candidates, at least K places with 0 behind the last, in the scratch's list, and the pair of the
-// columns that are not among the first K (the same in every thread).
+// columns that are not among the first K (the same in every thread).  held: the slice's vectors in
+// shared memory, if they are all there.
 template <typename S, int GT, int NS>
 __device__ __forceinline__ void select(const Args& a, const Row& r, const Slice& sl, int stages, SelCtl& ctl,
-                                       uint8_t* scratch, float* gm, float* gs, const Team<NS>& team, float& tm, float& ts) {
+                                       uint8_t* scratch, float* gm, float* gs, const Team<NS>& team, float& tm, float& ts,
+                                       const uint8_t* held = nullptr) {
     constexpr int G = Elt<S>::kGroup;
     static_assert(GT % NS == 0, "whole rounds of groups");
     constexpr int SP = kSets / NS;             // sets of a thread
@@ -345,7 +355,8 @@ __device__ __forceinline__ void select(const Args& a, const Row& r, const Slice&
                 const int i = (g / GT) * (GT * kU) + g % GT + (task % kU) * GT;
                 if (i >= sl.n) continue;
                 at[h] = i;
-                x[h] = load_vector<S>(r, sl.v0 + i);
+                const int v = sl.v0 + i;
+                x[h] = held && v >= r.iv0 && v < r.iv1 ? tc::lds16(held + (size_t)i * 16) : load_vector<S>(r, v);
             }
 #pragma unroll 1
             for (int h = 0; h < 2 && task0 + h * NS < tasks; ++h) {
@@ -450,11 +461,11 @@ __device__ __forceinline__ void group_of(const uint4 (&x)[kU], float k2, float& 
 template <typename S>
 __global__ void __launch_bounds__(kThreads, 3) k_topk(const __grid_constant__ Args a) {
     extern __shared__ __align__(128) uint8_t smem[];
-    const int over = max(a.nbuf * kStageBytes, kClusterScratch);
-    float* gm = reinterpret_cast<float*>(smem + over);
+    uint8_t* scratch = smem + scratch_at(a.nbuf, a.max_stages);
+    float* gm = reinterpret_cast<float*>(smem + scratch_end(a.nbuf, a.max_stages));
     float* gs = gm + a.max_stages * kConsumers;
     Ctl& ctl = *reinterpret_cast<Ctl*>(gs + a.max_stages * kConsumers);
-    uint64_t* list = reinterpret_cast<uint64_t*>(smem + kListAt);
+    uint64_t* list = reinterpret_cast<uint64_t*>(scratch + kListAt);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr int NS = kConsumers;             // the consumers select
     const Team<NS> team{tid, 1};
@@ -489,15 +500,16 @@ __global__ void __launch_bounds__(kThreads, 3) k_topk(const __grid_constant__ Ar
     if (!ok) __syncthreads();                  // the scratch overlies the stages
 
     float tm = -kInf, ts = 0.f;
-    if (tid < NS) select<S, kConsumers, NS>(a, r, sl, sl.nst, ctl.sel, smem, gm, gs, team, tm, ts);
+    if (tid < NS) select<S, kConsumers, NS>(a, r, sl, sl.nst, ctl.sel, scratch, gm, gs, team, tm, ts,
+                                               a.max_stages <= a.nbuf ? smem : nullptr);
     bool all_ok = ok;
     const uint64_t* top = list;
     if (C > 1) {
         if (tid == 0) ctl.sel.tail = make_float4(tm, ts, ok ? 1.f : 0.f, 0.f);
         cluster_arrive();
         cluster_wait();
-        uint64_t* in = reinterpret_cast<uint64_t*>(smem + kInAt);
-        uint64_t* out = reinterpret_cast<uint64_t*>(smem + kOutAt);
+        uint64_t* in = reinterpret_cast<uint64_t*>(scratch + kInAt);
+        uint64_t* out = reinterpret_cast<uint64_t*>(scratch + kOutAt);
         if (rank == 0 && tid < NS) {
             for (int i = tid; i < C * K; i += NS) {
                 const int p = i / K;
@@ -679,9 +691,9 @@ cudaError_t run(Args& a, int sms, cudaStream_t s) {
     if (a.T >= kRowsPerSm * sms && nv > kPVecs && nv <= kPStages * kPVecs)
         return launch_clusters<k_topk_rows<S>>(sms, 1, kPThreads, kPSmem, s, a);
     auto st = [&](int c) { return (int)(((nv + c - 1) / c + kStageVecs - 1) / kStageVecs); };
-    // few rows: blocks for the SMs; long rows: groups that leave room for two blocks an SM
+    // few rows: as many blocks as run at once, two an SM; long rows: groups that leave room for two
     int C = 1;
-    while (C < kMaxCluster && ((a.T * C < 2 * sms && st(C) > 1) || smem_bytes(3, st(C)) > 116000)) C *= 2;
+    while (C < kMaxCluster && ((2 * C * a.T <= 2 * sms && st(C) > 1) || smem_bytes(3, st(C)) > 116000)) C *= 2;
     a.cluster = C;
     a.max_stages = st(C);
     a.nbuf = std::min(3, st(C));
