@@ -44,10 +44,8 @@ constexpr int kSelAt = kCandAt + kMaxCand * 8;               // [kMaxSel] group 
 constexpr int kPartAt = kSelAt + kMaxSel * 4;                // [kMaxSel * kU] pairs of the vectors read again
 constexpr int kListAt = kPartAt;                             // then [kMaxCand] candidates by rank (read by peers)
 constexpr int kScratch = kPartAt + kMaxSel * kU * 8;
-constexpr int kInAt = kListAt + kMaxCand * 8;                // [cluster * K] the cluster's lists
-constexpr int kOutAt = kInAt + kMaxCluster * VCE_MAX_TOPK * 8;   // the same by rank
-constexpr int kClusterScratch = kOutAt + kMaxCluster * VCE_MAX_TOPK * 8;
-static_assert(kMaxCand * 8 <= kMaxSel * kU * 8 && kSets * 4 <= kMaxSel * 4 && kMaxCand >= VCE_MAX_TOPK, "scratch");
+constexpr int kOutAt = kCandAt;                              // at last, [cluster * K] the cluster's lists by rank
+static_assert(kMaxCluster * VCE_MAX_TOPK * 8 <= kScratch && kMaxCand * 8 <= kMaxSel * kU * 8 && kSets * 4 <= kMaxSel * 4 && kMaxCand >= VCE_MAX_TOPK, "scratch");
 
 struct Args {
     const void* logits;
@@ -64,7 +62,7 @@ constexpr int kRowsPerSm = 2;               // rows for each SM from which the p
 
 // What the selecting threads share.
 struct alignas(16) SelCtl {
-    float4 tail;                    // the block's pair of the columns left out (read by peers)
+    float4 tail[kMaxCluster];       // in a cluster's first block: each block's pair of the columns left out
     float red_m[8], red_s[8];       // by the selecting warp
     int count[2][8];
     int nsel, ncand;
@@ -82,11 +80,12 @@ __host__ __device__ constexpr int scratch_at(int nbuf, int max_stages) {
     return max_stages <= nbuf ? nbuf * kStageBytes : 0;
 }
 __host__ __device__ constexpr int scratch_end(int nbuf, int max_stages) {
-    const int b = nbuf * kStageBytes, e = scratch_at(nbuf, max_stages) + kClusterScratch;
+    const int b = nbuf * kStageBytes, e = scratch_at(nbuf, max_stages) + kScratch;
     return b > e ? b : e;
 }
-__host__ __device__ constexpr int smem_bytes(int nbuf, int max_stages) {
-    return scratch_end(nbuf, max_stages) + max_stages * kConsumers * 8 + (int)sizeof(Ctl);
+__host__ __device__ constexpr int smem_bytes(int nbuf, int max_stages, int cluster, int K) {
+    return scratch_end(nbuf, max_stages) + max_stages * kConsumers * 8 + (int)sizeof(Ctl) +
+           (cluster > 1 ? cluster * K * 8 : 0);
 }
 
 // NS threads (whole warps of consecutive numbers, tid counted from the first) select together; a
@@ -299,12 +298,12 @@ __device__ __forceinline__ void select(const Args& a, const Row& r, const Slice&
             for (int bit = 31; bit >= (sizeof(S) == 2 ? 16 : 0); --bit) {
                 const uint32_t c = t | (1u << bit);
                 if (c > most) continue;        // none is as large
-                n = 0;
+                int part4[4] = {};
 #pragma unroll
-                for (int i = 0; i < N; ++i) n += k[i] >= c;
-                n = __reduce_add_sync(0xFFFFFFFFu, n);
+                for (int i = 0; i < N; ++i) part4[i % 4] += k[i] >= c;
+                n = __reduce_add_sync(0xFFFFFFFFu, (part4[0] + part4[1]) + (part4[2] + part4[3]));
                 if (n >= K) t = c;
-                if (n >= K && n <= K + K / 8) break;
+                if (n >= K && n <= K + K / 2) break;   // near enough: a few more groups are read again
             }
             t = max(t, kKeyMin);
         }
@@ -419,7 +418,7 @@ __device__ __forceinline__ void select(const Args& a, const Row& r, const Slice&
     block_pair(team, tm, ts, ctl, a.k2);
 }
 
-// The row's outputs from its sorted list and the pair of the rest, by the selecting threads.
+// The row's outputs from its sorted list and the pair of the rest (of the team's first warp), by a team.
 template <int NS>
 __device__ __forceinline__ void outputs(const Args& a, int64_t row, const uint64_t* top, bool ok, float tm, float ts,
                                         const Team<NS>& team) {
@@ -465,6 +464,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_topk(const __grid_constant__ Ar
     float* gm = reinterpret_cast<float*>(smem + scratch_end(a.nbuf, a.max_stages));
     float* gs = gm + a.max_stages * kConsumers;
     Ctl& ctl = *reinterpret_cast<Ctl*>(gs + a.max_stages * kConsumers);
+    uint64_t* in = reinterpret_cast<uint64_t*>(&ctl + 1);   // [cluster][K] in the cluster's first block
     uint64_t* list = reinterpret_cast<uint64_t*>(scratch + kListAt);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr int NS = kConsumers;             // the consumers select
@@ -480,6 +480,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_topk(const __grid_constant__ Ar
         init_barriers(ctl.bar, a.nbuf);
         for (; issued < min(sl.nst, a.nbuf); ++issued) issue_stage(smem, ctl.bar, a.nbuf, r, sl, issued, issued);
     }
+    if (C > 1) cluster_arrive_relaxed();       // this block runs: peers may write into it
     __syncthreads();
     if (warp == kConsumerWarps) {
         if (lane == 0)
@@ -502,40 +503,35 @@ __global__ void __launch_bounds__(kThreads, 3) k_topk(const __grid_constant__ Ar
     float tm = -kInf, ts = 0.f;
     if (tid < NS) select<S, kConsumers, NS>(a, r, sl, sl.nst, ctl.sel, scratch, gm, gs, team, tm, ts,
                                                a.max_stages <= a.nbuf ? smem : nullptr);
-    bool all_ok = ok;
-    const uint64_t* top = list;
-    if (C > 1) {
-        if (tid == 0) ctl.sel.tail = make_float4(tm, ts, ok ? 1.f : 0.f, 0.f);
-        cluster_arrive();
-        cluster_wait();
-        uint64_t* in = reinterpret_cast<uint64_t*>(scratch + kInAt);
-        uint64_t* out = reinterpret_cast<uint64_t*>(scratch + kOutAt);
-        if (rank == 0 && tid < NS) {
-            for (int i = tid; i < C * K; i += NS) {
-                const int p = i / K;
-                in[i] = ld_peer_u64(peer_addr(list + (i - p * K), (uint32_t)p));
-                out[i] = 0;
-            }
-            tm = -kInf;
-            ts = 0.f;
+    if (C == 1) {
+        if (tid < NS) outputs(a, row, list, ok, tm, ts, team);
+        return;
+    }
+    // ---- 4. every block's list and pair into the first block, which merges them ----
+    cluster_wait();                            // the first block runs
+    if (tid < NS)
+        for (int i = tid; i < K; i += NS) st_peer_u64(peer_addr(in + rank * K + i, 0), list[i]);
+    if (tid == 0) st_peer(peer_addr(&ctl.sel.tail[rank], 0), make_float4(tm, ts, ok ? 1.f : 0.f, 0.f));
+    cluster_arrive();
+    cluster_wait();
+    if (rank != 0 || tid >= NS) return;
+    uint64_t* out = reinterpret_cast<uint64_t*>(scratch + kOutAt);
+    const int n = C * K;
+    for (int i = tid; i < n; i += NS) out[i] = 0;
+    team.sync();
+    for (int i = tid; i < n; i += NS) {
+        const uint64_t c = in[i];
+        if (!c) continue;
+        int rk = 0;
+        if (n <= 512) {
+#pragma unroll 8
+            for (int q = 0; q < n; ++q) rk += in[q] > c;
+        } else {                               // ranks in the other lists, which are sorted
+            const int own = i / K;
+            rk = i - own * K;
             for (int p = 0; p < C; ++p) {
-                const float4 o = ld_peer_f4(peer_addr(&ctl.sel.tail, (uint32_t)p));
-                if (tid == 0) pair_merge(tm, ts, o.x, o.y, a.k2);
-                all_ok = all_ok && o.z != 0.f;
-            }
-        }
-        cluster_arrive();                      // the peers may leave
-        cluster_wait();
-        if (rank != 0 || tid >= NS) return;
-        team.sync();
-        for (int i = tid; i < C * K; i += NS) {
-            const uint64_t c = in[i];
-            if (!c) continue;
-            int rk = i % K;
-            for (int p = 0; p < C; ++p) {
-                if (p == i / K) continue;
                 const uint64_t* l = in + p * K;
-                int lo = 0, hi = K;            // entries of l above c
+                int lo = 0, hi = p == own ? 0 : K;   // entries of l above c
                 while (lo < hi) {
                     const int mid = (lo + hi) / 2;
                     if (l[mid] > c) lo = mid + 1;
@@ -543,15 +539,21 @@ __global__ void __launch_bounds__(kThreads, 3) k_topk(const __grid_constant__ Ar
                 }
                 rk += lo;
             }
-            out[rk] = c;
         }
-        team.sync();
-        for (int i = K + tid; i < C * K; i += NS)
-            if (out[i]) pair_merge(tm, ts, value_of(cand_key(out[i])), 1.f, a.k2);
-        block_pair(team, tm, ts, ctl.sel, a.k2);
-        top = out;
+        out[rk] = c;
     }
-    if (tid < NS) outputs(a, row, top, all_ok, tm, ts, team);
+    team.sync();
+    // the columns left out, by the warp that writes their log-sum-exp: the blocks' and the lists' rest
+    bool all_ok = true;
+    for (int p = 0; p < C; ++p) all_ok = all_ok && ctl.sel.tail[p].z != 0.f;
+    if (tid < 32) {
+        tm = tid < C ? ctl.sel.tail[tid].x : -kInf;
+        ts = tid < C ? ctl.sel.tail[tid].y : 0.f;
+        for (int i = K + tid; i < n; i += 32)
+            if (out[i]) pair_merge(tm, ts, value_of(cand_key(out[i])), 1.f, a.k2);
+        pair_warp_reduce(tm, ts, a.k2);
+    }
+    outputs(a, row, out, all_ok, tm, ts, team);
 }
 
 // ---- many rows: a persistent kernel -----------------------------------------------------------------
@@ -693,11 +695,11 @@ cudaError_t run(Args& a, int sms, cudaStream_t s) {
     auto st = [&](int c) { return (int)(((nv + c - 1) / c + kStageVecs - 1) / kStageVecs); };
     // few rows: as many blocks as run at once, two an SM; long rows: groups that leave room for two
     int C = 1;
-    while (C < kMaxCluster && ((2 * C * a.T <= 2 * sms && st(C) > 1) || smem_bytes(3, st(C)) > 116000)) C *= 2;
+    while (C < kMaxCluster && ((2 * C * a.T <= 2 * sms && st(C) > 1) || smem_bytes(3, st(C), C, a.K) > 116000)) C *= 2;
     a.cluster = C;
     a.max_stages = st(C);
     a.nbuf = std::min(3, st(C));
-    return launch_clusters<k_topk<S>>(a.T * C, C, kThreads, smem_bytes(a.nbuf, a.max_stages), s, a);
+    return launch_clusters<k_topk<S>>(a.T * C, C, kThreads, smem_bytes(a.nbuf, a.max_stages, C, a.K), s, a);
 }
 
 }  // namespace topk
