@@ -77,6 +77,28 @@ def test_topk_masked_rows(vce, V):
     check(vce, z, 30)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,V", [(4, 90), (4, 9001), (400, 20000)])
+def test_topk_masks_of_the_lowest_value(vce, T, V, dtype):
+    """Columns masked with the type's lowest value, whose product with log2(e) / temperature passes
+    fp32: they take no part where anything else is left, and are the log-sum-exp where nothing is."""
+    low = torch.finfo(dtype).min
+    z = torch.full((T, V), low, dtype=dtype, device="cuda")
+    z[1, 7] = 2.0
+    z[2, 5:25] = 1.0
+    values, ids, lse, tail = [x.double().cpu().numpy() for x in vce.ce_topk(z, 20)]
+    want_lse, want_tail = [low, 2.0, 1.0 + np.log(20.0), low], [low, low, low, low]
+    np.testing.assert_allclose(lse[:4], want_lse, rtol=1e-6)
+    np.testing.assert_allclose(tail[:4], want_tail, rtol=1e-6)
+    assert ids[0].tolist() == list(range(20)) and ids[1].tolist() == [7] + list(range(7)) + list(range(8, 20))
+    assert ids[2].tolist() == list(range(5, 25)) and np.all(lse[4:] == lse[0])
+    # as a teacher and as a student: the masked columns carry no mass
+    student = torch.randn(T, V, device="cuda")
+    out = vce.ce_distill_forward(student, ids_ := vce.ce_topk(z, 20)[1], vce.ce_topk(z, 20)[0], vce.ce_topk(z, 20)[3])
+    want = -torch.log_softmax(student[1], 0)[7].item()
+    assert vce.vce_get_status(out[4]) == 0 and abs(out[1][1].item() - want) <= 1e-5 * want and ids_.shape == (T, 20)
+
+
 def test_topk_one_value_far_above(vce):
     """The tail is summed without the K: with a margin of 60 it would cancel to nothing as a difference,
     and as part of a group whose maximum is the large logit it would underflow at a margin of 150."""

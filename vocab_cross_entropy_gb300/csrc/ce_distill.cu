@@ -62,11 +62,17 @@ struct Args {
     int cluster, nbuf, max_stages;
 };
 
+// Of a row's entries: the largest logits z, t of the student and the teacher, the sums of e^{s (z - max)}
+// and e^{s (t - max)} (0: no mass, NaN stays), and sum qh phi(log r/qh).
+struct Top {
+    float zmax, zsum, tmax, tsum, kl;
+};
+
 struct alignas(16) Ctl {
     float4 slot[kMaxCluster];    // (max, sum-exp, error code, -) of the cluster's blocks
     Barriers bar;
     float red_m[kConsumerWarps], red_s[kConsumerWarps];
-    float zmax, lnr, lq, kl_top; // of the entries: max z, log sum e^{s (z - max)}, Lq, sum qh phi
+    Top top;                     // of the entries
     int code;                    // error found among the entries
 };
 
@@ -190,12 +196,10 @@ __device__ __forceinline__ bool grads_aligned(const Row& r, const O* grow) {
 // ---- a row's scalars -------------------------------------------------------------------------------
 
 // All arithmetic on the K entries, by one warp (lane + 32 i: entry k; col -1: none, z, t -inf there):
-// each entry's (r_k, r_k - qh_k), the largest z, log sum e^{s (z - max)}, Lq and sum qh phi.
-__device__ __forceinline__ void top_arithmetic(const Args& a, int K, int lane, const int (&col)[kPerLane],
-                                               const float (&z)[kPerLane], const float (&t)[kPerLane], Entry* entry,
-                                               float& zm, float& lnr, float& lq, float& kl) {
-    float tm = -kInf;
-    zm = -kInf;
+// each entry's (r_k, r_k - qh_k), and the scalars of Top.
+__device__ __forceinline__ Top top_arithmetic(const Args& a, int K, int lane, const int (&col)[kPerLane],
+                                               const float (&z)[kPerLane], const float (&t)[kPerLane], Entry* entry) {
+    float zm = -kInf, tm = -kInf;
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) {
         zm = fmaxf(zm, z[i]);
@@ -212,9 +216,8 @@ __device__ __forceinline__ void top_arithmetic(const Args& a, int K, int lane, c
     }
     rs_ = warp_sum(rs_);
     qs = warp_sum(qs);
-    const float lnq = logf(qs), inv_r = 1.f / rs_, inv_q = 1.f / qs;
-    lnr = logf(rs_);
-    kl = 0.f;
+    const float ln = logf(rs_) - logf(qs), inv_r = 1.f / rs_, inv_q = 1.f / qs;
+    float kl = 0.f;
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) {
         const int k = lane + 32 * i;
@@ -227,7 +230,7 @@ __device__ __forceinline__ void top_arithmetic(const Args& a, int K, int lane, c
             if (t[i] > -kInf) qk = expf((t[i] - tm) * a.scale) * inv_q;
             if (z[i] > -kInf && t[i] > -kInf) {
                 // log(r_k / qh_k): differences of logits first, which are exact or nearly so
-                y = ((z[i] - zm) - (t[i] - tm)) * a.scale - (lnr - lnq);
+                y = ((z[i] - zm) - (t[i] - tm)) * a.scale - ln;
                 diff = y < 0.5f ? qk * expm1f(y) : rk - qk;
             } else {
                 diff = rk - qk;
@@ -237,40 +240,68 @@ __device__ __forceinline__ void top_arithmetic(const Args& a, int K, int lane, c
         entry[k] = Entry{rk, diff, col[i], 0};
     }
     kl = warp_sum(kl);
-    lq = tm > -kInf ? tm * a.scale + lnq : tm;   // -inf: no mass among the entries; NaN stays
+    return Top{zm, rs_, tm, qs, kl};
 }
 
 // What the gradient needs of a row's masses, in few dependent steps (consumers wait for it), and what
-// the loss needs besides.
+// the loss needs besides.  The masses of the student and the teacher enter as the ratios
+// ws = p_T / P = e^-b and wt = q_T / Q = e^-at: a logarithm of size 8 is rounded by 5e-7, which is all
+// the loss's error where the masses are nearly alike, a ratio by 6e-8 of itself.
 struct Finish {
     float lt, d, q;              // L', p_T - q_T, Q
-    float at, b;                 // Q = sigma(at), P = sigma(b)
+    float ws, wt;
     int code;                    // the row's error
+    bool ratios;                 // ws and wt are within range: else the logarithms at and b are used
     bool dead;                   // no gradient (an error, or a student row of -inf only)
+    float at, b;
 };
 
 // From the tail's pair (M, S0), the entries' scalars and the teacher's tail R.
-__device__ __forceinline__ Finish finish_row(const Args& a, float M, float S0, float zmax, float lnr, float Lq,
-                                             float R, int code) {
+__device__ __forceinline__ Finish finish_row(const Args& a, float M, float S0, const Top& t, float R, int code) {
     Finish f;
     f.code = code;
-    if (!code && !((Lq > -kInf || R > -kInf) && Lq < kInf && R < kInf)) f.code = VCE_ERR_TEACHER;   // no finite mass
-    const bool has_tail = S0 > 0.f, has_top = zmax > -kInf;
-    const float ln_s = has_tail ? logf(S0) : 0.f;
-    if (has_tail && has_top) f.b = (zmax - M) * a.scale + (lnr - ln_s);
-    else f.b = has_top ? kInf : -kInf;
-    f.at = Lq == -kInf ? -kInf : Lq - R;             // R = -inf: +inf
-    f.q = sigmoid(f.at);
-    f.d = sigmoid_diff(-f.b, -f.at);                 // p_T - q_T
+    // no finite teacher mass (comparisons that a NaN fails)
+    if (!code && !((t.tsum > 0.f || R > -kInf) && t.tsum < kInf && R < kInf)) f.code = VCE_ERR_TEACHER;
+    const bool has_tail = S0 > 0.f, has_top = t.zmax > -kInf;
+    const float gap = fmaf(t.zmax, a.k2, -M);        // one rounding
+    f.ws = (S0 / t.zsum) * exp2f(-gap);
+    f.wt = expf(fmaf(-t.tmax, a.scale, R)) / t.tsum;
+    f.ratios = f.ws > 1e-30f && f.ws < 1e30f && (f.wt > 1e-30f || R == -kInf) && f.wt < 1e30f;
+    f.at = f.b = 0.f;
+    if (f.ratios) {
+        f.q = 1.f / (1.f + f.wt);
+        f.d = (f.ws - f.wt) * f.q / (1.f + f.ws);
+    } else {
+        if (has_tail && has_top) f.b = gap * kLn2 + (logf(t.zsum) - logf(S0));
+        else f.b = has_top ? kInf : -kInf;
+        f.at = t.tsum > 0.f ? (t.tmax * a.scale - R) + logf(t.tsum) : -kInf;   // R = -inf: +inf
+        f.q = sigmoid(f.at);
+        f.d = sigmoid_diff(-f.b, -f.at);             // p_T - q_T
+    }
     f.dead = f.code || !(has_tail || has_top);
-    f.lt = has_tail ? M * a.scale + ln_s : -kInf;
+    f.lt = has_tail ? M * kLn2 + logf(S0) : -kInf;
     return f;
 }
 
 // tau^2 KL from the row's masses and the entries' sum of qh phi; NaN where there is no loss.
 __device__ __forceinline__ float loss_of(const Args& a, const Finish& f, float kl_top) {
-    float kl = q_phi(f.q, sigmoid(f.b), softplus_f(-f.at) - softplus_f(-f.b)) +
-               q_phi(sigmoid(-f.at), sigmoid(-f.b), softplus_f(f.at) - softplus_f(f.b));
+    float x1, x2, P, pT, qT;                         // log P/Q, log p_T/q_T
+    if (f.ratios) {
+        const float d = f.ws - f.wt, r = f.ws / f.wt;
+        const float q = -d / (1.f + f.ws);
+        x1 = q > -0.5f && q < 1.f ? log1pf(q) : log1pf(f.wt) - log1pf(f.ws);
+        x2 = x1 + (r > 0.5f && r < 2.f ? log1pf(d / f.wt) : logf(r));
+        P = 1.f / (1.f + f.ws);
+        pT = f.ws * P;
+        qT = f.wt * f.q;
+    } else {
+        x1 = softplus_f(-f.at) - softplus_f(-f.b);
+        x2 = softplus_f(f.at) - softplus_f(f.b);
+        P = sigmoid(f.b);
+        pT = sigmoid(-f.b);
+        qT = sigmoid(-f.at);
+    }
+    float kl = q_phi(f.q, P, x1) + q_phi(qT, pT, x2);
     if (f.q > 0.f) kl += f.q * kl_top;
     return f.dead ? __int_as_float(0x7FC00000) : a.tau * a.tau * kl;
 }
@@ -369,16 +400,10 @@ __global__ void __launch_bounds__(kThreads, 3) k_distill(const __grid_constant__
                                : Elt<float>::load1(static_cast<const float*>(a.tvals) + row * a.K + k);
             }
         }
-        float zm, lnr, lq, kl;
-        top_arithmetic(a, a.K, lane, col, z, t, entry, zm, lnr, lq, kl);
-        if (lane == 0) {
-            ctl.zmax = zm;
-            ctl.lnr = lnr;
-            ctl.lq = lq;
-            ctl.kl_top = kl;
-        }
+        const Top top = top_arithmetic(a, a.K, lane, col, z, t, entry);
+        if (lane == 0) ctl.top = top;
     } else {
-        float m = -kInf, s = 0.f, mb = 0.f;
+        float m = -kInf, s = 0.f;
         for (int j = 0; j < sl.nst; ++j) {
             const uint32_t word = marks[j * kConsumers + tid];
             wait_stage(ctl.bar, a.nbuf, j);
@@ -395,9 +420,9 @@ __global__ void __launch_bounds__(kThreads, 3) k_distill(const __grid_constant__
                     for (int k = 0; k < G; ++k)
                         if ((word >> (u * G + k)) & 1u) v[u][k] = -kInf;
             }
-            pair_push<G>(v, m, s, mb, a.k2);
+            pair_push<G>(v, m, s, a.k2);
         }
-        pair_warp_reduce(m, s, a.k2);
+        pair_warp_reduce(m, s);
         if (lane == 0) {
             ctl.red_m[warp] = m;
             ctl.red_s[warp] = s;
@@ -407,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_distill(const __grid_constant__
 
     // ---- the row's statistics, by every thread alike ----
     float M = -kInf, S0 = 0.f;
-    for (int w = 0; w < kConsumerWarps; ++w) pair_merge(M, S0, ctl.red_m[w], ctl.red_s[w], a.k2);
+    for (int w = 0; w < kConsumerWarps; ++w) pair_merge(M, S0, ctl.red_m[w], ctl.red_s[w]);
     int code = ctl.bar.err ? ctl.bar.err : ctl.code;
     if (C > 1) {
         cluster_wait();                              // every peer runs
@@ -419,14 +444,14 @@ __global__ void __launch_bounds__(kThreads, 3) k_distill(const __grid_constant__
         code = 0;
         for (int p = 0; p < C; ++p) {                // the same order in every block
             const float4 o = ctl.slot[p];
-            pair_merge(M, S0, o.x, o.y, a.k2);
+            pair_merge(M, S0, o.x, o.y);
             code = max(code, __float_as_int(o.z));
         }
     }
-    const Finish f = finish_row(a, M, S0, ctl.zmax, ctl.lnr, ctl.lq, a.tail ? a.tail[row] : -kInf, code);
+    const Finish f = finish_row(a, M, S0, ctl.top, a.tail ? a.tail[row] : -kInf, code);
     const bool dead = f.dead;
     if (rank == 0 && tid == kProducerWarp * 32) {
-        a.loss_rows[row] = loss_of(a, f, ctl.kl_top);
+        a.loss_rows[row] = loss_of(a, f, ctl.top.kl);
         // weight: 1, negative for a row with an error, until the reduction writes it
         a.row_stats[row] = make_float4(f.lt, dead ? 0.f : f.d, 0.f, f.code ? -(float)f.code : 1.f);
     }
@@ -502,7 +527,7 @@ struct Geom {
 enum { kErrRow = 107, kErrPartials = 108, kErrCoefs = 109 };
 
 struct TopStats {
-    float zmax, lnr, lq, kl;
+    Top top;
     int code;
 };
 struct Coefs {                   // of the tail's gradient
@@ -788,11 +813,10 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_distill_ring(const __grid_c
             bad = __any_sync(0xFFFFFFFFu, bad);
             if (last >= 0 && !wait(&ctl.freed[par], last, kErrRow)) break;
             last = e;
-            float zm, lnr, lq, kl;
-            top_arithmetic(a, K, lane, col, z, t, en, zm, lnr, lq, kl);
+            const Top top = top_arithmetic(a, K, lane, col, z, t, en);
             __syncwarp();
             if (lane == 0) {
-                ctl.top[par] = TopStats{zm, lnr, lq, kl, bad ? VCE_ERR_TEACHER : 0};
+                ctl.top[par] = TopStats{top, bad ? VCE_ERR_TEACHER : 0};
                 tc::mbar_arrive(&ctl.topped[par]);
             }
         }
@@ -819,7 +843,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_distill_ring(const __grid_c
             for (int off = kWarps / 2; off > 0; off >>= 1) {   // lanes 0 .. kWarps - 1 into lane 0
                 const float m2 = __shfl_xor_sync(0xFFFFFFFFu, M, off);
                 const float s2 = __shfl_xor_sync(0xFFFFFFFFu, S0, off);
-                pair_merge(M, S0, m2, s2, a.k2);
+                pair_merge(M, S0, m2, s2);
             }
             M = __shfl_sync(0xFFFFFFFFu, M, 0);
             S0 = __shfl_sync(0xFFFFFFFFu, S0, 0);
@@ -849,16 +873,16 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_distill_ring(const __grid_c
                 code = 0;
                 for (int p = 0; p < C; ++p) {   // the same order in every block
                     const float4 o = ctl.slot[par][p];
-                    pair_merge(M, S0, o.x, o.y, a.k2);
+                    pair_merge(M, S0, o.x, o.y);
                     code = max(code, __float_as_int(o.z));
                 }
             }
-            const Finish f = finish_row(a, M, S0, ts.zmax, ts.lnr, ts.lq, R, code);
+            const Finish f = finish_row(a, M, S0, ts.top, R, code);
             if (lane == 0) {
                 ctl.coefs[par] = Coefs{go * f.d, f.lt > -kInf ? f.lt * kLog2e : 0.f, f.dead};
                 tc::mbar_arrive(&ctl.finished[par]);
                 if (rank == 0) {
-                    a.loss_rows[row] = loss_of(a, f, ts.kl);
+                    a.loss_rows[row] = loss_of(a, f, ts.top.kl);
                     a.row_stats[row] = make_float4(f.lt, f.dead ? 0.f : f.d, 0.f, f.code ? -(float)f.code : 1.f);
                 }
             }
@@ -883,7 +907,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_distill_ring(const __grid_c
     } else {
         // ---------------- consumers ----------------
         struct Pair {
-            float m, s, mb;
+            float m, s;
         };
         // stages [j0, j1) of a row, at ring positions from `at` on
         auto forward = [&](Cursor<nbuf>& at, int j0, int j1, const Slice& sl, Pair& p) {
@@ -898,12 +922,12 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_distill_ring(const __grid_c
                 float v[U][G];
 #pragma unroll
                 for (int u = 0; u < U; ++u) Elt<S>::unpack(x[u], v[u]);
-                pair_push<G>(v, p.m, p.s, p.mb, a.k2);
+                pair_push<G>(v, p.m, p.s, a.k2);
             }
         };
         auto publish = [&](int64_t e, Pair p) {
             const int par = (int)(e & 1);
-            pair_warp_reduce(p.m, p.s, a.k2);
+            pair_warp_reduce(p.m, p.s);
             // row e - 2's pairs have been read (in one pass that follows from its gradient)
             if (!kGrad && e >= 2) wait(&ctl.finished[par], e - 2, kErrCoefs);
             if (lane == 0) {
@@ -929,7 +953,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_distill_ring(const __grid_c
         for (int64_t e = -1; (row >= 0 || row2 >= 0) && !*reinterpret_cast<volatile int*>(&ctl.abort); ++e) {
             Row r2{};
             Slice sl2{};
-            Pair p{-kInf, 0.f, 0.f};
+            Pair p{-kInf, 0.f};
             int pre = 0;
             if (row2 >= 0) {
                 r2 = make_row<S>(a.logits, row2, a.ld, a.V);

@@ -51,7 +51,7 @@ struct Args {
     const void* logits;
     int64_t T, V, ld;
     int K;
-    float scale, k2;
+    float k2;                       // log2(e) / temperature
     float* values;
     int64_t* ids;
     float *lse, *tail;
@@ -62,8 +62,8 @@ constexpr int kRowsPerSm = 2;               // rows for each SM from which the p
 
 // What the selecting threads share.
 struct alignas(16) SelCtl {
-    float4 tail[kMaxCluster];       // in a cluster's first block: each block's pair of the columns left out
-    float red_m[8], red_s[8];       // by the selecting warp
+    float4 tail[kMaxCluster];       // in a cluster's first block: each block's rest (m, s, largest) and whether its copies landed
+    float4 rest[8];                 // by the selecting warp
     int count[2][8];
     int nsel, ncand;
     float bound;
@@ -127,40 +127,63 @@ __device__ __forceinline__ int block_sum(const Team<NS>& tm, int n, SelCtl& ctl,
     for (int w = 0; w < Team<NS>::kWarps; ++w) t += ctl.count[it & 1][w];
     return t;
 }
-// Merges the selecting threads' pairs; every thread has the result.
-template <int NS>
-__device__ __forceinline__ void block_pair(const Team<NS>& team, float& m, float& s, SelCtl& ctl, float k2) {
-    pair_warp_reduce(m, s, k2);
-    if (team.lane() == 0) {
-        ctl.red_m[team.warp()] = m;
-        ctl.red_s[team.warp()] = s;
+// The columns left out: their pair, and the largest of them, which stands for their log-sum-exp where
+// its product with k2 passes fp32 (masks of the type's lowest value; such values are in no pair).
+struct Rest {
+    float m, s, top;
+    __device__ __forceinline__ void merge(float m2, float s2, float top2) {
+        pair_merge(m, s, m2, s2);
+        top = fmaxf(top, top2);
     }
+    // a value, `times` over
+    __device__ __forceinline__ void add(float v, float k2, float times = 1.f) {
+        const float r = v * k2;
+        if (r > -kInf) pair_merge(m, s, r, times * ex2(fmaf(v, k2, -r)));
+        top = fmaxf(top, v);
+    }
+    __device__ __forceinline__ float lse(float scale) const { return s > 0.f ? m * kLn2 + logf(s) : top * scale; }
+};
+
+// Merges the selecting threads' rests; every thread has the result.
+__device__ __forceinline__ void warp_rest(Rest& t) {
+    pair_warp_reduce(t.m, t.s);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) t.top = fmaxf(t.top, __shfl_xor_sync(0xFFFFFFFFu, t.top, off));
+}
+template <int NS>
+__device__ __forceinline__ void block_rest(const Team<NS>& team, Rest& t, SelCtl& ctl) {
+    warp_rest(t);
+    if (team.lane() == 0) ctl.rest[team.warp()] = make_float4(t.m, t.s, t.top, 0.f);
     team.sync();
-    m = -kInf;
-    s = 0.f;
-    for (int w = 0; w < Team<NS>::kWarps; ++w) pair_merge(m, s, ctl.red_m[w], ctl.red_s[w], k2);
+    t = Rest{-kInf, 0.f, -kInf};
+    for (int w = 0; w < Team<NS>::kWarps; ++w) t.merge(ctl.rest[w].x, ctl.rest[w].y, ctl.rest[w].z);
 }
 
-// The pair of G values, -inf left out.
 template <int G>
-__device__ __forceinline__ float2 pair_of(const float (&v)[G], float k2) {
+__device__ __forceinline__ float max_of_vector(const float (&v)[G]) {
     float m = v[0];
 #pragma unroll
     for (int k = 1; k < G; ++k) m = fmaxf(m, v[k]);
+    return m;
+}
+
+// The pair of G values (the reference: the largest times k2), -inf left out.
+template <int G>
+__device__ __forceinline__ float2 pair_of(const float (&v)[G], float k2) {
+    const float m = max_of_vector<G>(v) * k2;
     if (m == -kInf) return make_float2(-kInf, 0.f);
-    const float mb = m * k2;
     float s = 0.f;
 #pragma unroll
-    for (int k = 0; k < G; ++k) s += ex2(fmaf(v[k], k2, -mb));
+    for (int k = 0; k < G; ++k) s += ex2(fmaf(v[k], k2, -m));
     return make_float2(m, s);
 }
 
 // The K largest of the slice by the exact K-th value, every value read from global memory as often
 // as its search takes: for slices where the bound from the groups admits too many.  Candidates go
-// to cand (ctl.ncand of them), everything else into this thread's pair (tm, ts).
+// to cand (ctl.ncand of them), everything else into this thread's rest.
 template <typename S, int NS>
 __device__ __noinline__ void exact_threshold(const Args& a, const Row& r, const Slice& sl, SelCtl& ctl, uint64_t* cand,
-                                             Team<NS> team, float& tm, float& ts) {
+                                             Team<NS> team, Rest& rest) {
     constexpr int G = Elt<S>::kGroup;
     const int tid = team.tid, lane = team.lane(), warp = team.warp();
     int it = 0;
@@ -197,9 +220,10 @@ __device__ __noinline__ void exact_threshold(const Args& a, const Row& r, const 
             }
             eq += key == t;
             if (key >= t) v[k] = -kInf;
+            rest.top = fmaxf(rest.top, v[k]);
         }
         const float2 p = pair_of<G>(v, a.k2);
-        pair_merge(tm, ts, p.x, p.y, a.k2);
+        rest.merge(p.x, p.y, -kInf);
     }
     const int total_eq = block_sum(team, eq, ctl, it++);
     const int above = min(ctl.ncand, kMaxCand);
@@ -237,7 +261,7 @@ __device__ __noinline__ void exact_threshold(const Args& a, const Row& r, const 
     }
     if (tid == 0) {
         ctl.ncand = above + want;
-        if (total_eq > want) pair_merge(tm, ts, value_of(t), (float)(total_eq - want), a.k2);
+        if (total_eq > want) rest.add(value_of(t), a.k2, (float)(total_eq - want));
     }
     team.sync();
 }
@@ -249,7 +273,7 @@ __device__ __noinline__ void exact_threshold(const Args& a, const Row& r, const 
 // shared memory, if they are all there.
 template <typename S, int GT, int NS>
 __device__ __forceinline__ void select(const Args& a, const Row& r, const Slice& sl, int stages, SelCtl& ctl,
-                                       uint8_t* scratch, float* gm, float* gs, const Team<NS>& team, float& tm, float& ts,
+                                       uint8_t* scratch, float* gm, float* gs, const Team<NS>& team, Rest& rest,
                                        const uint8_t* held = nullptr) {
     constexpr int G = Elt<S>::kGroup;
     static_assert(GT % NS == 0, "whole rounds of groups");
@@ -337,8 +361,7 @@ __device__ __forceinline__ void select(const Args& a, const Row& r, const Slice&
     }
     team.sync();
     const int nsel = ctl.nsel;
-    tm = -kInf;
-    ts = 0.f;                                  // this thread's pair of the columns left out
+    rest = Rest{-kInf, 0.f, -kInf};            // this thread's columns left out
     if (nsel <= kMaxSel) {
         // vectors of the listed groups, two in flight a thread
         const int tasks = nsel * kU;
@@ -359,7 +382,7 @@ __device__ __forceinline__ void select(const Args& a, const Row& r, const Slice&
             }
 #pragma unroll 1
             for (int h = 0; h < 2 && task0 + h * NS < tasks; ++h) {
-                float2 p = make_float2(-kInf, 0.f);
+                float2 p = make_float2(-kInf, 0.f);   // the largest value left, and its sum of exponentials
                 if (at[0] >= 0) {
                     float v[G];
                     Elt<S>::unpack(x[0], v);
@@ -377,6 +400,7 @@ __device__ __forceinline__ void select(const Args& a, const Row& r, const Slice&
                             }
                     }
                     p = pair_of<G>(v, a.k2);
+                    p.x = max_of_vector<G>(v);
                 }
                 part[task0 + h * NS] = p;
                 x[0] = x[1];
@@ -386,21 +410,28 @@ __device__ __forceinline__ void select(const Args& a, const Row& r, const Slice&
         team.sync();
     }
     if (nsel > kMaxSel || ctl.ncand > kMaxCand) {
-        exact_threshold<S, NS>(a, r, sl, ctl, cand, team, tm, ts);
+        exact_threshold<S, NS>(a, r, sl, ctl, cand, team, rest);
     } else {
         for (int i = tid; i < nsel; i += NS) {
-            float m = -kInf, s = 0.f;
+            float top = -kInf;
 #pragma unroll
-            for (int u = 0; u < kU; ++u) pair_merge(m, s, part[i * kU + u].x, part[i * kU + u].y, a.k2);
-            gm[sel[i]] = m;
+            for (int u = 0; u < kU; ++u) top = fmaxf(top, part[i * kU + u].x);
+            gm[sel[i]] = top;
+            const float ref = top * a.k2;
+            float s = 0.f;
+            if (ref > -kInf) {
+#pragma unroll
+                for (int u = 0; u < kU; ++u) s += part[i * kU + u].y * ex2(part[i * kU + u].x * a.k2 - ref);   // 0 * 0 for -inf
+            }
             gs[sel[i]] = s;
         }
         team.sync();
 #pragma unroll 4
-        for (int g = tid; g < groups; g += NS) tm = fmaxf(tm, gm[g]);
-        if (tm > -kInf) {
+        for (int g = tid; g < groups; g += NS) rest.top = fmaxf(rest.top, gm[g]);
+        rest.m = rest.top * a.k2;
+        if (rest.m > -kInf) {
 #pragma unroll 4
-            for (int g = tid; g < groups; g += NS) ts += gs[g] * ex2((gm[g] - tm) * a.k2);   // 0 * 0 for -inf
+            for (int g = tid; g < groups; g += NS) rest.s += gs[g] * ex2(gm[g] * a.k2 - rest.m);   // 0 * 0 for -inf
         }
     }
     // ---- 3. ranks ----
@@ -414,13 +445,13 @@ __device__ __forceinline__ void select(const Args& a, const Row& r, const Slice&
     }
     for (int i = n + tid; i < K; i += NS) list[i] = 0;
     team.sync();
-    for (int i = K + tid; i < n; i += NS) pair_merge(tm, ts, value_of(cand_key(list[i])), 1.f, a.k2);
-    block_pair(team, tm, ts, ctl, a.k2);
+    for (int i = K + tid; i < n; i += NS) rest.add(value_of(cand_key(list[i])), a.k2);
+    block_rest(team, rest, ctl);
 }
 
 // The row's outputs from its sorted list and the pair of the rest (of the team's first warp), by a team.
 template <int NS>
-__device__ __forceinline__ void outputs(const Args& a, int64_t row, const uint64_t* top, bool ok, float tm, float ts,
+__device__ __forceinline__ void outputs(const Args& a, int64_t row, const uint64_t* top, bool ok, Rest rest,
                                         const Team<NS>& team) {
     const int tid = team.tid;
     const float bad = __int_as_float(0x7FC00000);
@@ -430,20 +461,24 @@ __device__ __forceinline__ void outputs(const Args& a, int64_t row, const uint64
         a.ids[row * a.K + k] = ok && c ? cand_col(c) : -1;
     }
     if (tid < 32) {
-        float m = top[0] ? value_of(cand_key(top[0])) : -kInf, s = 0.f;
-        for (int k = tid; k < a.K; k += 32)
-            if (top[k]) s += ex2((value_of(cand_key(top[k])) - m) * a.k2);
+        const float scale = a.k2 * kLn2;
+        const float bad = __int_as_float(0x7FC00000);
+        Rest all{-kInf, 0.f, top[0] ? value_of(cand_key(top[0])) : -kInf};
+        all.m = all.top * a.k2;
+        if (all.m > -kInf)
+            for (int k = tid; k < a.K; k += 32)
+                if (top[k]) all.s += ex2(fmaf(value_of(cand_key(top[k])), a.k2, -all.m));
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
-        pair_merge(m, s, tm, ts, a.k2);
+        for (int off = 16; off > 0; off >>= 1) all.s += __shfl_xor_sync(0xFFFFFFFFu, all.s, off);
+        all.merge(rest.m, rest.s, rest.top);
         if (tid == 0) {
-            a.lse[row] = !ok ? bad : s > 0.f ? m * a.scale + logf(s) : -kInf;
-            a.tail[row] = !ok ? bad : ts > 0.f ? tm * a.scale + logf(ts) : -kInf;
+            a.lse[row] = ok ? all.lse(scale) : bad;
+            a.tail[row] = ok ? rest.lse(scale) : bad;
         }
     }
 }
 
-// A group's maximum and the sum of its exponentials relative to it.
+// A group's maximum and the sum of its exponentials relative to it (to its product with k2, as rounded).
 template <typename S>
 __device__ __forceinline__ void group_of(const uint4 (&x)[kU], float k2, float& m, float& s) {
     constexpr int G = Elt<S>::kGroup;
@@ -452,7 +487,8 @@ __device__ __forceinline__ void group_of(const uint4 (&x)[kU], float k2, float& 
 #pragma unroll
     for (int u = 0; u < kU; ++u) Elt<S>::unpack(x[u], v[u]);
     m = top;
-    s = top == -kInf ? 0.f : sum_exp<G>(v, k2, top * k2);
+    const float ref = top * k2;
+    s = ref == -kInf ? 0.f : sum_exp<G>(v, k2, ref);
 }
 
 // ---- one cluster per row -------------------------------------------------------------------------
@@ -500,18 +536,18 @@ __global__ void __launch_bounds__(kThreads, 3) k_topk(const __grid_constant__ Ar
     if (!ok && tid == kConsumers) drain(ctl.bar, a.nbuf, issued);
     if (!ok) __syncthreads();                  // the scratch overlies the stages
 
-    float tm = -kInf, ts = 0.f;
-    if (tid < NS) select<S, kConsumers, NS>(a, r, sl, sl.nst, ctl.sel, scratch, gm, gs, team, tm, ts,
+    Rest rest{-kInf, 0.f, -kInf};
+    if (tid < NS) select<S, kConsumers, NS>(a, r, sl, sl.nst, ctl.sel, scratch, gm, gs, team, rest,
                                                a.max_stages <= a.nbuf ? smem : nullptr);
     if (C == 1) {
-        if (tid < NS) outputs(a, row, list, ok, tm, ts, team);
+        if (tid < NS) outputs(a, row, list, ok, rest, team);
         return;
     }
     // ---- 4. every block's list and pair into the first block, which merges them ----
     cluster_wait();                            // the first block runs
     if (tid < NS)
         for (int i = tid; i < K; i += NS) st_peer_u64(peer_addr(in + rank * K + i, 0), list[i]);
-    if (tid == 0) st_peer(peer_addr(&ctl.sel.tail[rank], 0), make_float4(tm, ts, ok ? 1.f : 0.f, 0.f));
+    if (tid == 0) st_peer(peer_addr(&ctl.sel.tail[rank], 0), make_float4(rest.m, rest.s, rest.top, ok ? 1.f : 0.f));
     cluster_arrive();
     cluster_wait();
     if (rank != 0 || tid >= NS) return;
@@ -545,15 +581,15 @@ __global__ void __launch_bounds__(kThreads, 3) k_topk(const __grid_constant__ Ar
     team.sync();
     // the columns left out, by the warp that writes their log-sum-exp: the blocks' and the lists' rest
     bool all_ok = true;
-    for (int p = 0; p < C; ++p) all_ok = all_ok && ctl.sel.tail[p].z != 0.f;
+    for (int p = 0; p < C; ++p) all_ok = all_ok && ctl.sel.tail[p].w != 0.f;
     if (tid < 32) {
-        tm = tid < C ? ctl.sel.tail[tid].x : -kInf;
-        ts = tid < C ? ctl.sel.tail[tid].y : 0.f;
+        rest = Rest{-kInf, 0.f, -kInf};
+        if (tid < C) rest.merge(ctl.sel.tail[tid].x, ctl.sel.tail[tid].y, ctl.sel.tail[tid].z);
         for (int i = K + tid; i < n; i += 32)
-            if (out[i]) pair_merge(tm, ts, value_of(cand_key(out[i])), 1.f, a.k2);
-        pair_warp_reduce(tm, ts, a.k2);
+            if (out[i]) rest.add(value_of(cand_key(out[i])), a.k2);
+        warp_rest(rest);
     }
-    outputs(a, row, out, all_ok, tm, ts, team);
+    outputs(a, row, out, all_ok, rest, team);
 }
 
 // ---- many rows: a persistent kernel -----------------------------------------------------------------
@@ -676,11 +712,11 @@ __global__ void __launch_bounds__(kPThreads, 1) k_topk_rows(const __grid_constan
             const Row r = make_row<S>(a.logits, row, a.ld, a.V);
             const Slice sl = slice_of(r);
             tc::mbar_wait(&ctl.grouped[par], phase_of, &ctl.abort, &ctl.err, kErrFull, tc::kWaitNs, kSuspend);
-            float tm, ts;
-            select<S, kPNT, kPTeam>(a, r, sl, sl.nst, ctl.sel[par], mine, gm, gm + kPStages * kPNT, team, tm, ts);
+            Rest rest;
+            select<S, kPNT, kPTeam>(a, r, sl, sl.nst, ctl.sel[par], mine, gm, gm + kPStages * kPNT, team, rest);
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&ctl.taken[par]);
-            outputs(a, row, reinterpret_cast<const uint64_t*>(mine + kListAt), !*abort, tm, ts, team);
+            outputs(a, row, reinterpret_cast<const uint64_t*>(mine + kListAt), !*abort, rest, team);
             team.sync();                       // the list has been read
         }
     }
@@ -724,7 +760,7 @@ extern "C" int ce_topk(const void* logits, vce_dtype dt, int64_t T, int64_t V, i
         return VCE_ERR_ALIGN;
     const int rc = require_sm100();
     if (rc) return rc;
-    topk::Args a{logits, T, V, ld, K, 1.f / temperature, kLog2e / temperature, values, ids, lse, tail_lse, 1, 1, 1};
+    topk::Args a{logits, T, V, ld, K, kLog2e / temperature, values, ids, lse, tail_lse, 1, 1, 1};
     const int sms = device_sm_count();
     const cudaError_t e = dt == VCE_BF16 ? topk::run<uint16_t>(a, sms, s) : topk::run<float>(a, sms, s);
     return record_cuda(e) == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;

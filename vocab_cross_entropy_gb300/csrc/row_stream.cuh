@@ -33,6 +33,7 @@ constexpr int kU = 4;                                // vectors of a stage per c
 constexpr int kStageVecs = kU * kConsumers;          // 1024
 constexpr int kStageBytes = kStageVecs * 16;         // 16 KB
 constexpr int kMaxBufs = 12;
+constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMaxCluster = 8;
 enum { kErrEmpty = 105, kErrFull = 106 };
 
@@ -174,24 +175,26 @@ __device__ __forceinline__ void load_stage(const uint8_t* bufs, int nbuf, const 
     }
 }
 
-// ---- (max, sum-exp) pairs of k2-scaled logits: s * 2^(m k2) = sum 2^(v k2), k2 = log2(e) / temperature
+// ---- (reference, sum-exp) pairs: s * 2^m = sum 2^(z k2), k2 = log2(e) / temperature
 //
-// As vce_device.cuh's pairs, the logits scaled in the exponent only.
+// As vce_device.cuh's pairs, but the reference m is in the exponent's units: whatever fp32 number it is,
+// z k2 - m is one fma with one rounding, where a reference among the logits would round its product with
+// k2 alike in every term.
 
-__device__ __forceinline__ void pair_merge(float& m, float& s, float m2, float s2, float k2) {
+__device__ __forceinline__ void pair_merge(float& m, float& s, float m2, float s2) {
     const float M = fmaxf(m, m2);
-    const float a = (m == M) ? 1.f : ex2((m - M) * k2);
-    const float b = (m2 == M) ? 1.f : ex2((m2 - M) * k2);
+    const float a = (m == M) ? 1.f : ex2(m - M);
+    const float b = (m2 == M) ? 1.f : ex2(m2 - M);
     s = s * a + s2 * b;
     m = M;
 }
 
-__device__ __forceinline__ void pair_warp_reduce(float& m, float& s, float k2) {
+__device__ __forceinline__ void pair_warp_reduce(float& m, float& s) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
         const float m2 = __shfl_xor_sync(0xFFFFFFFFu, m, off);
         const float s2 = __shfl_xor_sync(0xFFFFFFFFu, s, off);
-        pair_merge(m, s, m2, s2, k2);
+        pair_merge(m, s, m2, s2);
     }
 }
 
@@ -204,10 +207,10 @@ __device__ __forceinline__ void fadd2(float a0, float a1, float b0, float b1, fl
         : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
 
-// sum of 2^(v k2 - mb) over a thread's vectors of a stage: exponents and sums two at a time (even and
+// sum of 2^(v k2 - m) over a thread's vectors of a stage: exponents and sums two at a time (even and
 // odd values summed apart), since the issue slots are what these kernels run short of
 template <int G, int U>
-__device__ __forceinline__ float sum_exp(const float (&v)[U][G], float k2, float mb) {
+__device__ __forceinline__ float sum_exp(const float (&v)[U][G], float k2, float m) {
     constexpr int N = U * G;
     float e[N];
 #pragma unroll
@@ -215,7 +218,7 @@ __device__ __forceinline__ float sum_exp(const float (&v)[U][G], float k2, float
 #pragma unroll
         for (int k = 0; k < G; k += 2) {
             float a0, a1;
-            ffma2(v[u][k], v[u][k + 1], k2, -mb, a0, a1);
+            ffma2(v[u][k], v[u][k + 1], k2, -m, a0, a1);
             e[u * G + k] = ex2(a0);
             e[u * G + k + 1] = ex2(a1);
         }
@@ -236,25 +239,23 @@ __device__ __forceinline__ float max_of(const float (&v)[U][G]) {
     return m;
 }
 
-// Adds a stage's values to a pair whose reference m moves only when a term would pass 2^32
-// (m is then one of the values, so s >= 1 and nothing overflows).
+// Adds a stage's values to a pair whose reference moves only when a term would pass 2^32 (it is then one
+// of the values', so s is about 1 or more and nothing overflows).  Values whose product with k2 passes
+// fp32 (masks of the type's lowest value) count as -inf.
 template <int G, int U>
-__device__ __forceinline__ void pair_push(const float (&v)[U][G], float& m, float& s, float& mb, float k2) {
+__device__ __forceinline__ void pair_push(const float (&v)[U][G], float& m, float& s, float k2) {
     if (m == -kInf) {
-        const float vm = max_of<G>(v);
-        if (vm == -kInf) return;
-        m = vm;
-        mb = m * k2;
+        m = max_of<G>(v) * k2;
+        if (m == -kInf) return;
     }
     float t;
 #pragma unroll 1
     for (int again = 0;; again = 1) {   // one copy of the sum's code, for the instruction cache
-        t = sum_exp<G>(v, k2, mb);
+        t = sum_exp<G>(v, k2, m);
         if (again || t < 4294967296.f) break;
-        const float vm = fmaxf(m, max_of<G>(v));   // a value far above the reference: take the new maximum
-        s *= ex2((m - vm) * k2);
+        const float vm = fmaxf(m, max_of<G>(v) * k2);   // a value far above the reference: take the new maximum
+        s *= ex2(m - vm);
         m = vm;
-        mb = m * k2;
     }
     s += t;
 }
