@@ -66,6 +66,7 @@ struct Args {
 // and e^{s (t - max)} (0: no mass, NaN stays), and sum qh phi(log r/qh).
 struct Top {
     float zmax, zsum, tmax, tsum, kl;
+    float wt, q, inv_z;          // wt = q_T / Q (see Finish), Q = 1 / (1 + wt), 1 / zsum
 };
 
 struct alignas(16) Ctl {
@@ -195,10 +196,19 @@ __device__ __forceinline__ bool grads_aligned(const Row& r, const O* grow) {
 
 // ---- a row's scalars -------------------------------------------------------------------------------
 
+// c - a b as hi + lo: the rounding of a result of size 8 is what is lost most of in its exponential.
+__device__ __forceinline__ float minus_product(float c, float a, float b, float& lo) {
+    const float p = a * b, pe = fmaf(a, b, -p);
+    const float hi = c - p, t = hi - c;
+    lo = ((c - (hi - t)) + (-p - t)) - pe;           // Knuth's TwoSum of c and -p
+    return hi;
+}
+
 // All arithmetic on the K entries, by one warp (lane + 32 i: entry k; col -1: none, z, t -inf there):
 // each entry's (r_k, r_k - qh_k), and the scalars of Top.
 __device__ __forceinline__ Top top_arithmetic(const Args& a, int K, int lane, const int (&col)[kPerLane],
-                                               const float (&z)[kPerLane], const float (&t)[kPerLane], Entry* entry) {
+                                               const float (&z)[kPerLane], const float (&t)[kPerLane], Entry* entry,
+                                               float R) {
     float zm = -kInf, tm = -kInf;
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) {
@@ -211,7 +221,7 @@ __device__ __forceinline__ Top top_arithmetic(const Args& a, int K, int lane, co
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) {
         if (32 * i >= K) break;
-        if (z[i] > -kInf) rs_ += expf((z[i] - zm) * a.scale);
+        if (z[i] > -kInf) rs_ += exp2f((z[i] - zm) * a.k2);   // as the tail's terms
         if (col[i] >= 0 && t[i] != -kInf) qs += expf((t[i] - tm) * a.scale);   // NaN: the row is refused
     }
     rs_ = warp_sum(rs_);
@@ -226,7 +236,7 @@ __device__ __forceinline__ Top top_arithmetic(const Args& a, int K, int lane, co
         float rk = 0.f, diff = 0.f;
         if (col[i] >= 0) {
             float qk = 0.f, y = -kInf;
-            if (z[i] > -kInf) rk = expf((z[i] - zm) * a.scale) * inv_r;
+            if (z[i] > -kInf) rk = exp2f((z[i] - zm) * a.k2) * inv_r;
             if (t[i] > -kInf) qk = expf((t[i] - tm) * a.scale) * inv_q;
             if (z[i] > -kInf && t[i] > -kInf) {
                 // log(r_k / qh_k): differences of logits first, which are exact or nearly so
@@ -240,7 +250,10 @@ __device__ __forceinline__ Top top_arithmetic(const Args& a, int K, int lane, co
         entry[k] = Entry{rk, diff, col[i], 0};
     }
     kl = warp_sum(kl);
-    return Top{zm, rs_, tm, qs, kl};
+    float lo;
+    const float hi = minus_product(R, tm, a.scale, lo);
+    const float wt = expf(hi) * (fabsf(lo) < 1.f ? 1.f + lo : 1.f) * inv_q;   // lo: NaN where hi is infinite
+    return Top{zm, rs_, tm, qs, kl, wt, 1.f / (1.f + wt), inv_r};
 }
 
 // What the gradient needs of a row's masses, in few dependent steps (consumers wait for it), and what
@@ -248,7 +261,7 @@ __device__ __forceinline__ Top top_arithmetic(const Args& a, int K, int lane, co
 // ws = p_T / P = e^-b and wt = q_T / Q = e^-at: a logarithm of size 8 is rounded by 5e-7, which is all
 // the loss's error where the masses are nearly alike, a ratio by 6e-8 of itself.
 struct Finish {
-    float lt, d, q;              // L', p_T - q_T, Q
+    float lt, bias, d, q;        // L', L' log2(e), p_T - q_T, Q
     float ws, wt;
     int code;                    // the row's error
     bool ratios;                 // ws and wt are within range: else the logarithms at and b are used
@@ -263,23 +276,29 @@ __device__ __forceinline__ Finish finish_row(const Args& a, float M, float S0, c
     // no finite teacher mass (comparisons that a NaN fails)
     if (!code && !((t.tsum > 0.f || R > -kInf) && t.tsum < kInf && R < kInf)) f.code = VCE_ERR_TEACHER;
     const bool has_tail = S0 > 0.f, has_top = t.zmax > -kInf;
-    const float gap = fmaf(t.zmax, a.k2, -M);        // one rounding
-    f.ws = (S0 / t.zsum) * exp2f(-gap);
-    f.wt = expf(fmaf(-t.tmax, a.scale, R)) / t.tsum;
+    float lo;
+    const float gap = minus_product(M, t.zmax, a.k2, lo);
+    // expf for this one factor, not the base-2 exponential: that one's error has a mean of 5e-8, which the
+    // sums of both sides share
+    const float x = gap * kLn2;
+    lo = fmaf(gap, kLn2, -x) + fmaf(gap, -1.90465431e-9f, lo * kLn2);   // ln 2 = kLn2 - 1.90465431e-9
+    f.ws = S0 * t.inv_z * expf(x) * (fabsf(lo) < 1.f ? 1.f + lo : 1.f);
+    f.wt = t.wt;
     f.ratios = f.ws > 1e-30f && f.ws < 1e30f && (f.wt > 1e-30f || R == -kInf) && f.wt < 1e30f;
     f.at = f.b = 0.f;
     if (f.ratios) {
-        f.q = 1.f / (1.f + f.wt);
+        f.q = t.q;
         f.d = (f.ws - f.wt) * f.q / (1.f + f.ws);
     } else {
-        if (has_tail && has_top) f.b = gap * kLn2 + (logf(t.zsum) - logf(S0));
+        if (has_tail && has_top) f.b = (logf(t.zsum) - logf(S0)) - gap * kLn2;
         else f.b = has_top ? kInf : -kInf;
         f.at = t.tsum > 0.f ? (t.tmax * a.scale - R) + logf(t.tsum) : -kInf;   // R = -inf: +inf
         f.q = sigmoid(f.at);
         f.d = sigmoid_diff(-f.b, -f.at);             // p_T - q_T
     }
     f.dead = f.code || !(has_tail || has_top);
-    f.lt = has_tail ? M * kLn2 + logf(S0) : -kInf;
+    f.bias = has_tail ? M + log2f(S0) : 0.f;         // of the tail's gradient: 2^(z k2 - bias); no tail: any
+    f.lt = has_tail ? f.bias * kLn2 : -kInf;
     return f;
 }
 
@@ -400,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_distill(const __grid_constant__
                                : Elt<float>::load1(static_cast<const float*>(a.tvals) + row * a.K + k);
             }
         }
-        const Top top = top_arithmetic(a, a.K, lane, col, z, t, entry);
+        const Top top = top_arithmetic(a, a.K, lane, col, z, t, entry, a.tail ? a.tail[row] : -kInf);
         if (lane == 0) ctl.top = top;
     } else {
         float m = -kInf, s = 0.f;
@@ -466,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_distill(const __grid_constant__
     } else {
         const float c = a.go[a.red == VCE_RED_NONE ? row : 0] * (a.red == VCE_RED_MEAN ? *a.inv_n : 1.f) * a.tau;
         if (warp < kConsumerWarps) {
-            const float coef = c * f.d, bias = f.lt > -kInf ? f.lt * kLog2e : 0.f;
+            const float coef = c * f.d, bias = f.bias;
             for (int j = 0; j < sl.nst; ++j) {
                 const int q = held ? j : sl.nst + j;
                 if (!held) wait_stage(ctl.bar, a.nbuf, q);
@@ -771,6 +790,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_distill_ring(const __grid_c
             const int64_t row = walk_next(walk, a);
             if (row < 0) break;
             if ((e & 1) != par) continue;
+            const float R = a.tail ? a.tail[row] : -kInf;
             const int64_t* ids = a.ids + row * K;
             const S* zrow = static_cast<const S*>(a.logits) + row * a.ld;
             int64_t id[kPerLane];
@@ -813,7 +833,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_distill_ring(const __grid_c
             bad = __any_sync(0xFFFFFFFFu, bad);
             if (last >= 0 && !wait(&ctl.freed[par], last, kErrRow)) break;
             last = e;
-            const Top top = top_arithmetic(a, K, lane, col, z, t, en);
+            const Top top = top_arithmetic(a, K, lane, col, z, t, en, R);
             __syncwarp();
             if (lane == 0) {
                 ctl.top[par] = TopStats{top, bad ? VCE_ERR_TEACHER : 0};
@@ -879,7 +899,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_distill_ring(const __grid_c
             }
             const Finish f = finish_row(a, M, S0, ts.top, R, code);
             if (lane == 0) {
-                ctl.coefs[par] = Coefs{go * f.d, f.lt > -kInf ? f.lt * kLog2e : 0.f, f.dead};
+                ctl.coefs[par] = Coefs{go * f.d, f.bias, f.dead};
                 tc::mbar_arrive(&ctl.finished[par]);
                 if (rank == 0) {
                     a.loss_rows[row] = loss_of(a, f, ts.top.kl);
@@ -1226,7 +1246,7 @@ extern "C" int ce_distill_forward(const void* logits, vce_dtype dt, int64_t T, i
     distill::Args a{};
     a.logits = logits, a.T = T, a.V = V, a.ld = ld;
     a.ids = teacher_ids, a.tvals = teacher_values, a.tail = teacher_tail, a.K = K, a.tbf16 = tdt == VCE_BF16;
-    a.tau = temperature, a.scale = 1.f / temperature, a.k2 = kLog2e / temperature;
+    a.tau = temperature, a.scale = 1.f / temperature, a.k2 = (float)(1.4426950408889634 / (double)temperature);
     a.labels = labels, a.ignore_index = ignore_index, a.red = red;
     a.loss_rows = loss_rows, a.row_stats = reinterpret_cast<float4*>(row_stats), a.top_grads = top_grads;
     int rc = forward_checks(a, dt, tdt, temperature, status);
@@ -1263,7 +1283,7 @@ extern "C" int ce_distill_backward(const void* logits, vce_dtype dt, int64_t T, 
     if ((rc = require_sm100())) return rc;
     distill::BwdArgs a{};
     a.logits = logits, a.T = T, a.V = V, a.ld = ld, a.ids = teacher_ids, a.K = K;
-    a.tau = temperature, a.k2 = kLog2e / temperature, a.red = red;
+    a.tau = temperature, a.k2 = (float)(1.4426950408889634 / (double)temperature), a.red = red;
     a.row_stats = reinterpret_cast<const float4*>(row_stats), a.top_grads = top_grads, a.go = grad_output;
     a.grad = grad_logits, a.ld_g = ld_grad;
     cudaError_t e;
@@ -1284,7 +1304,7 @@ extern "C" int ce_distill_forward_backward(const void* logits, vce_dtype dt, int
     distill::Args a{};
     a.logits = logits, a.T = T, a.V = V, a.ld = ld;
     a.ids = teacher_ids, a.tvals = teacher_values, a.tail = teacher_tail, a.K = K, a.tbf16 = tdt == VCE_BF16;
-    a.tau = temperature, a.scale = 1.f / temperature, a.k2 = kLog2e / temperature;
+    a.tau = temperature, a.scale = 1.f / temperature, a.k2 = (float)(1.4426950408889634 / (double)temperature);
     a.labels = labels, a.ignore_index = ignore_index, a.red = red, a.go = grad_output, a.inv_n = loss_out;
     a.loss_rows = loss_rows, a.row_stats = reinterpret_cast<float4*>(row_stats);
     a.grad = grad_logits, a.ld_g = ld_grad;

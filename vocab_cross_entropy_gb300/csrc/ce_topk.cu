@@ -760,7 +760,7 @@ extern "C" int ce_topk(const void* logits, vce_dtype dt, int64_t T, int64_t V, i
         return VCE_ERR_ALIGN;
     const int rc = require_sm100();
     if (rc) return rc;
-    topk::Args a{logits, T, V, ld, K, kLog2e / temperature, values, ids, lse, tail_lse, 1, 1, 1};
+    topk::Args a{logits, T, V, ld, K, (float)(1.4426950408889634 / (double)temperature), values, ids, lse, tail_lse, 1, 1, 1};
     const int sms = device_sm_count();
     const cudaError_t e = dt == VCE_BF16 ? topk::run<uint16_t>(a, sms, s) : topk::run<float>(a, sms, s);
     return record_cuda(e) == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
