@@ -514,11 +514,13 @@ __global__ void __launch_bounds__(kThreads, 3) k_distill(const __grid_constant__
 //
 // One block per SM (a cluster of C blocks per row) walks the rows cid, cid + ncl, ... with the copies
 // of the next rows always in flight.  Its warps have roles, which hand rows on through mbarriers,
-// everything that belongs to a row doubled by the parity of its number in the block's sequence:
+// everything that belongs
+// to a row doubled by the parity of its number in the block's sequence (the
+// entries by top warp):
 //   producer        copies the rows' slices into the stage ring, running ahead as stages are released
 //   patch           overwrites the entries' columns in the loaded stages with -inf, and writes the row's
 //                   partial first and last vectors there, so the consumers' sums need not know of either
-//   top 0, top 1    (even and odd rows) the arithmetic on the K entries
+//   top 0 ..        (two, or four: each takes every second or fourth row) the arithmetic on the K entries
 //   consumers       the tail's pair of a row; in one pass then the first stages of the next row, while
 //                   this row's statistics are exchanged, this row's gradient from the held stages,
 //                   releasing each, and the rest of the next row
@@ -530,10 +532,13 @@ __global__ void __launch_bounds__(kThreads, 3) k_distill(const __grid_constant__
 namespace ring {
 
 constexpr int kWarps = 16, kNT = kWarps * 32;       // consumers
-constexpr int kProducer = kWarps, kPatch = kWarps + 1, kTop = kWarps + 2, kStats = kWarps + 4;
-constexpr int kRingThreads = (kWarps + 5) * 32;
+constexpr int kProducer = kWarps, kPatch = kWarps + 1, kStats = kWarps + 2, kTop = kWarps + 3;
+__host__ __device__ constexpr int ring_threads(int tops) { return (kTop + tops) * 32; }
+// Top warps: rows of at least kLongRow bytes leave two of them time enough, shorter ones take four
+// (4096 x 128256 bf16 forward: 165 us with two, 168 with four; one pass, 16384 rows: 1433 and 1496;
+// 1023 x 32001 bf16 to fp32 one pass: 70 and 59).
+constexpr int64_t kLongRow = 131072;
 constexpr uint32_t kSuspend = 10000;                // ns a poll may sleep: waiting warps leave the issue slots to others
-constexpr int kSeen = 512;                          // slots of a top warp's table of columns (for ids given twice)
 // Stages: in one pass 16 KB, so that a held row gives them back in small steps; 32 KB in the forward
 // alone, whose stages are given back at once (less to do per stage).
 template <bool kGrad>
@@ -554,24 +559,29 @@ struct Coefs {                   // of the tail's gradient
     int dead;
 };
 
+template <int kTops>
 struct alignas(16) RingCtl {
     float4 slot[2][kMaxCluster];
     uint64_t full[13], ready[13], empty[13];   // of the stages: copied, patched, released
-    uint64_t topped[2];          // their arithmetic (the top warp)
+    uint64_t topped[kTops];      // the entries' arithmetic (a top warp)
+    uint64_t freed[kTops];       // the stats warp is done with the entries
     uint64_t paired[2];          // the consumer warps' pairs
     uint64_t exchanged[2];       // the cluster's pairs
     uint64_t finished[2];        // the row's coefficients (stats)
     uint64_t written[2];         // the tail's gradient (consumer warps)
-    uint64_t freed[2];           // the stats warp is done with the entries
-    TopStats top[2];
-    uint32_t seen[2][kSeen];
+    TopStats top[kTops];
     Coefs coefs[2];
     float red_m[2][kWarps], red_s[2][kWarps];
     int abort, err;
 };
 
+// A top warp's entries take at least as much room as its table of columns (for ids given twice), which
+// lies there before: at least 2 K slots of 4 bytes, a power of two, 32 or more.
+__host__ __device__ constexpr int entry_stride(int K) { return K > 8 ? K : 8; }
+
+template <int kTops>
 __host__ __device__ constexpr int ring_smem(int stages_bytes, int K) {
-    return stages_bytes + 2 * K * (int)sizeof(Entry) + (int)sizeof(RingCtl) + 16;
+    return stages_bytes + kTops * entry_stride(K) * (int)sizeof(Entry) + (int)sizeof(RingCtl<kTops>) + 16;
 }
 
 // make_slice in stages of the ring.
@@ -665,20 +675,24 @@ __device__ __forceinline__ void ring_load(const uint8_t* buf8, const Slice& s, i
     }
 }
 
-template <typename S, typename O, bool kGrad>
-__global__ void __launch_bounds__(kRingThreads, 1) k_distill_ring(const __grid_constant__ Args a) {
+template <typename S, typename O, bool kGrad, int kTops>
+__global__ void __launch_bounds__(ring_threads(kTops), 1) k_distill_ring(const __grid_constant__ Args a) {
     constexpr int G = Elt<S>::kGroup;
     extern __shared__ __align__(128) uint8_t smem[];
     using Ge = Geom<kGrad>;
     constexpr int nbuf = Ge::kBufs, U = Ge::kU, kRingVecs = Ge::kVecs, kRingBytes = Ge::kBytes;
-    const int K = a.K, C = a.cluster;
-    Entry* entries = reinterpret_cast<Entry*>(smem + nbuf * kRingBytes);   // [2][K]
-    RingCtl& ctl = *reinterpret_cast<RingCtl*>((reinterpret_cast<uintptr_t>(entries + 2 * K) + 15) / 16 * 16);
+    const int K = a.K, KS = entry_stride(a.K), C = a.cluster;
+    Entry* entries = reinterpret_cast<Entry*>(smem + nbuf * kRingBytes);   // [kTops][KS]
+    constexpr int kRingThreads = ring_threads(kTops);
+    RingCtl<kTops>& ctl = *reinterpret_cast<RingCtl<kTops>*>((reinterpret_cast<uintptr_t>(entries + kTops * KS) + 15) / 16 * 16);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = C > 1 ? (int)cluster_rank() : 0;
     const int64_t cid = blockIdx.x / C, ncl = gridDim.x / C;
     auto wait = [&](uint64_t* bar, int64_t e, int code) {   // the phase of row e of a barrier doubled by parity
         return tc::mbar_wait(bar, (uint32_t)(e >> 1) & 1, &ctl.abort, &ctl.err, code, tc::kWaitNs, kSuspend);
+    };
+    auto wait_top = [&](uint64_t* bar, int64_t e) {         // the phase of row e of one of kTops barriers
+        return tc::mbar_wait(bar + e % kTops, (uint32_t)(e / kTops) & 1, &ctl.abort, &ctl.err, kErrRow, tc::kWaitNs, kSuspend);
     };
 
     if (tid == 0) {
@@ -688,11 +702,13 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_distill_ring(const __grid_c
             tc::mbar_init(&ctl.empty[i], kWarps);
         }
         for (int p = 0; p < 2; ++p) {
-            tc::mbar_init(&ctl.topped[p], 1);
             tc::mbar_init(&ctl.paired[p], kWarps);
             tc::mbar_init(&ctl.exchanged[p], C);
             tc::mbar_init(&ctl.finished[p], 1);
             tc::mbar_init(&ctl.written[p], kWarps);
+        }
+        for (int p = 0; p < kTops; ++p) {
+            tc::mbar_init(&ctl.topped[p], 1);
             tc::mbar_init(&ctl.freed[p], 1);
         }
         ctl.abort = ctl.err = 0;
@@ -739,9 +755,19 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_distill_ring(const __grid_c
     } else if (warp == kPatch) {
         Cursor<nbuf> at{0, 0};
         const S neg = sizeof(S) == 2 ? (S)0xFF80u : (S)-kInf;
-        for (bool ok = true; ok;) {
-            const int64_t row = walk_next(walk, a);
-            if (row < 0) break;
+        // the ids of the next row are on their way while this one's stages are patched
+        int64_t id[kPerLane];
+        auto load_ids = [&](int64_t row) {
+#pragma unroll
+            for (int i = 0; i < kPerLane; ++i) {
+                if (32 * i >= K) break;
+                id[i] = lane + 32 * i < K ? a.ids[row * K + lane + 32 * i] : -1;
+            }
+        };
+        int64_t next = walk_next(walk, a);
+        if (next >= 0) load_ids(next);
+        for (bool ok = true; ok && next >= 0;) {
+            const int64_t row = next;
             const Row r = make_row<S>(a.logits, row, a.ld, a.V);
             const Slice sl = ring_slice<kGrad>(r, C, rank);
             // the entries' places among the slice's elements; anything else is in no stage
@@ -750,9 +776,10 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_distill_ring(const __grid_c
             for (int i = 0; i < kPerLane; ++i) {
                 place[i] = 0xFFFFFFFFu;
                 if (32 * i >= K) continue;
-                const int64_t id = lane + 32 * i < K ? a.ids[row * K + lane + 32 * i] : -1;
-                if (id >= 0 && id < a.V) place[i] = (uint32_t)((int)id + r.shift - sl.v0 * G);
+                if (id[i] >= 0 && id[i] < a.V) place[i] = (uint32_t)((int)id[i] + r.shift - sl.v0 * G);
             }
+            next = walk_next(walk, a);
+            if (next >= 0) load_ids(next);
             // lanes 0 .. G - 1: the first vector, if it is partial and the slice's; G .. 2 G - 1: the last
             const int edge = lane < G ? (r.shift ? 0 : -1) : (r.iv1 < r.nv && (r.nv > 1 || !r.shift) ? r.nv - 1 : -1);
             const int64_t ecol = (int64_t)edge * G - r.shift + lane % G;
@@ -781,15 +808,17 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_distill_ring(const __grid_c
                 if (lane == 0) tc::mbar_arrive(&ctl.ready[at.st]);
             }
         }
-    } else if (warp == kTop || warp == kTop + 1) {
+    } else if (warp >= kTop) {
         const int par = warp - kTop;
-        Entry* en = entries + par * K;
-        uint32_t* seen = ctl.seen[par];
+        Entry* en = entries + par * KS;
+        uint32_t* seen = reinterpret_cast<uint32_t*>(en);
+        int slots = 32;
+        while (slots < 2 * K) slots *= 2;
         int64_t last = -1;
         for (int64_t e = 0;; ++e) {
             const int64_t row = walk_next(walk, a);
             if (row < 0) break;
-            if ((e & 1) != par) continue;
+            if (e % kTops != par) continue;
             const float R = a.tail ? a.tail[row] : -kInf;
             const int64_t* ids = a.ids + row * K;
             const S* zrow = static_cast<const S*>(a.logits) + row * a.ld;
@@ -799,8 +828,6 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_distill_ring(const __grid_c
                 if (32 * i >= K) break;
                 id[i] = lane + 32 * i < K ? ids[lane + 32 * i] : -1;
             }
-            for (int i = lane; i < kSeen; i += 32) seen[i] = 0xFFFFFFFFu;
-            __syncwarp();
             int bad = 0;
             int col[kPerLane];
             float z[kPerLane], t[kPerLane];
@@ -819,20 +846,22 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_distill_ring(const __grid_c
                     bad |= id[i] != -1;
                 }
             }
+            if (last >= 0 && !wait_top(ctl.freed, last)) break;
+            last = e;
             // a column twice: the table (at most half full) already holds it
+            for (int i = lane; i < slots; i += 32) seen[i] = 0xFFFFFFFFu;
+            __syncwarp();
 #pragma unroll
             for (int i = 0; i < kPerLane; ++i) {
                 if (32 * i >= K) break;
                 if (col[i] < 0) continue;
-                uint32_t at = ((uint32_t)col[i] * 2654435761u) >> 8 & (kSeen - 1);
+                uint32_t at = ((uint32_t)col[i] * 2654435761u) >> 8 & (slots - 1);
                 uint32_t was;
                 while ((was = atomicCAS(seen + at, 0xFFFFFFFFu, (uint32_t)col[i])) != 0xFFFFFFFFu && was != (uint32_t)col[i])
-                    at = (at + 1) & (kSeen - 1);
+                    at = (at + 1) & (slots - 1);
                 bad |= was == (uint32_t)col[i];
             }
-            bad = __any_sync(0xFFFFFFFFu, bad);
-            if (last >= 0 && !wait(&ctl.freed[par], last, kErrRow)) break;
-            last = e;
+            bad = __any_sync(0xFFFFFFFFu, bad);          // (and the table has been read)
             const Top top = top_arithmetic(a, K, lane, col, z, t, en, R);
             __syncwarp();
             if (lane == 0) {
@@ -842,6 +871,20 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_distill_ring(const __grid_c
         }
     } else if (warp == kStats) {
         const float inv_n = kGrad && a.red == VCE_RED_MEAN ? *a.inv_n : 1.f;
+        // The losses take longer than anything a consumer waits for: each lane keeps a row, and 32 rows'
+        // are worked out at once.
+        Finish kept{};
+        int64_t kept_row = 0;
+        float kept_kl = 0.f;
+        int pending = 0;
+        auto flush = [&]() {
+            if (lane < pending && rank == 0) {
+                a.loss_rows[kept_row] = loss_of(a, kept, kept_kl);
+                a.row_stats[kept_row] =
+                    make_float4(kept.lt, kept.dead ? 0.f : kept.d, 0.f, kept.code ? -(float)kept.code : 1.f);
+            }
+            pending = 0;
+        };
         for (int64_t e = 0;; ++e) {
             const int par = (int)(e & 1);
             const int64_t row = walk_next(walk, a, [&](int64_t no) {   // an ignored row
@@ -867,8 +910,8 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_distill_ring(const __grid_c
             }
             M = __shfl_sync(0xFFFFFFFFu, M, 0);
             S0 = __shfl_sync(0xFFFFFFFFu, S0, 0);
-            if (!wait(&ctl.topped[par], e, kErrRow)) break;
-            const TopStats ts = ctl.top[par];
+            if (!wait_top(ctl.topped, e)) break;
+            const TopStats ts = ctl.top[e % kTops];
             int code = ts.code;
             if (C > 1) {
                 if (lane < C) {
@@ -901,18 +944,20 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_distill_ring(const __grid_c
             if (lane == 0) {
                 ctl.coefs[par] = Coefs{go * f.d, f.bias, f.dead};
                 tc::mbar_arrive(&ctl.finished[par]);
-                if (rank == 0) {
-                    a.loss_rows[row] = loss_of(a, f, ts.top.kl);
-                    a.row_stats[row] = make_float4(f.lt, f.dead ? 0.f : f.d, 0.f, f.code ? -(float)f.code : 1.f);
-                }
             }
+            if (lane == pending) {
+                kept = f;
+                kept_row = row;
+                kept_kl = ts.top.kl;
+            }
+            if (++pending == 32) flush();
             __syncwarp();
             if (kGrad && !wait(&ctl.written[par], e, kErrCoefs)) break;
             const Row r = make_row<S>(a.logits, row, a.ld, a.V);
             const Slice sl = ring_slice<kGrad>(r, C, rank);
             const float c = kGrad ? go : a.tau;
             for (int k = lane; k < K; k += 32) {
-                const Entry en = entries[par * K + k];
+                const Entry en = entries[(e % kTops) * KS + k];
                 const float g = f.dead || en.col < 0 ? 0.f : c * (f.q * en.diff - f.d * en.r);
                 if (!kGrad) {
                     if (rank == 0) a.top_grads[row * K + k] = g;
@@ -922,8 +967,9 @@ __global__ void __launch_bounds__(kRingThreads, 1) k_distill_ring(const __grid_c
                 }
             }
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&ctl.freed[par]);
+            if (lane == 0) tc::mbar_arrive(&ctl.freed[e % kTops]);
         }
+        flush();
     } else {
         // ---------------- consumers ----------------
         struct Pair {
@@ -1170,16 +1216,24 @@ int ring_cluster(int64_t T, int64_t V, int G, int sms) {
     return kGrad && st(C) > Ge::kHeld ? 0 : C;
 }
 
+template <typename S, typename O, bool kGrad, int kTops>
+cudaError_t run_ring(Args& a, int sms, cudaStream_t s, bool* done) {
+    using Ge = ring::Geom<kGrad>;
+    constexpr auto kern = ring::k_distill_ring<S, O, kGrad, kTops>;
+    const int bytes = ring::ring_smem<kTops>(Ge::kBufs * Ge::kBytes, a.K), threads = ring::ring_threads(kTops);
+    const int64_t clusters = std::min<int64_t>(a.T, resident_clusters<kern>(a.cluster, threads, bytes, sms));
+    *done = clusters > 0;
+    return *done ? launch_clusters<kern>(clusters * a.cluster, a.cluster, threads, bytes, s, a) : cudaSuccess;
+}
+
 template <typename S, typename O, bool kGrad>
 cudaError_t run(Args& a, int sms, cudaStream_t s) {
     a.cluster = ring_cluster<kGrad>(a.T, a.V, Elt<S>::kGroup, sms);
     if (a.cluster) {
-        const int bytes = ring::ring_smem(ring::Geom<kGrad>::kBufs * ring::Geom<kGrad>::kBytes, a.K);
-        const int64_t clusters = std::min<int64_t>(
-            a.T, resident_clusters<ring::k_distill_ring<S, O, kGrad>>(a.cluster, ring::kRingThreads, bytes, sms));
-        if (clusters > 0)
-            return launch_clusters<ring::k_distill_ring<S, O, kGrad>>(clusters * a.cluster, a.cluster,
-                                                                     ring::kRingThreads, bytes, s, a);
+        bool done = false;
+        const cudaError_t e = a.V * (int64_t)sizeof(S) >= ring::kLongRow ? run_ring<S, O, kGrad, 2>(a, sms, s, &done)
+                                                                        : run_ring<S, O, kGrad, 4>(a, sms, s, &done);
+        if (done || e != cudaSuccess) return e;
     }
     shape(a.T, a.V, Elt<S>::kGroup, kGrad, a.K, sms, &a.cluster, &a.nbuf, &a.max_stages);
     const int bytes = smem_bytes(a.nbuf, a.max_stages, a.K);

@@ -205,20 +205,38 @@ def ce_distill_forward_backward(logits, teacher_ids, teacher_values, teacher_tai
 
 
 class _Distill(torch.autograd.Function):
+    """ce_distill_forward and _backward.  What the backward needs lies in one float32 buffer: row_stats
+    [T, 4], top_grads [T, K], loss_rows [T], the status word."""
+
     @staticmethod
     def forward(ctx, logits, ids, values, tail, temperature, labels, ignore_index, reduction):
-        loss_out, loss_rows, row_stats, top_grads, _ = ce_distill_forward(logits, ids, values, tail, temperature,
-                                                                          labels, ignore_index, reduction)
-        ctx.save_for_backward(logits, ids, row_stats, top_grads)
-        ctx.temperature, ctx.reduction = temperature, reduction
-        return loss_rows if reduction == "none" else loss_out.reshape(())
+        dt, T, V, ld = _matrix(logits, "logits")
+        dev = logits.device
+        K, p_ids, p_values, tdt, p_tail = _teacher(ids, values, tail, T, dev)
+        red = RED[reduction]
+        kept = torch.empty(T * (ROW_STATS + K + 1) + 1, dtype=_F32, device=dev)
+        loss = torch.empty((), dtype=_F32, device=dev) if red else torch.empty(T, dtype=_F32, device=dev)
+        stats, p_loss = kept.data_ptr(), loss.data_ptr()
+        tops = stats + 4 * ROW_STATS * T
+        rows = tops + 4 * K * T
+        _run("ce_distill_forward", dev, None, logits.data_ptr(), dt, T, V, ld, p_ids, p_values, tdt, p_tail, K,
+             temperature, _flat(labels, "labels", _I64, (T,), dev), ignore_index, red, rows if red else p_loss,
+             p_loss if red else None, stats, tops, rows + 4 * T)
+        ctx.save_for_backward(logits, ids, kept)
+        ctx.temperature, ctx.red = temperature, red
+        return loss
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
-        logits, ids, row_stats, top_grads = ctx.saved_tensors
-        go = grad.reshape(-1).to(_F32).contiguous()
-        g = ce_distill_backward(logits, ids, row_stats, top_grads, go, ctx.temperature, ctx.reduction)
+        logits, ids, kept = ctx.saved_tensors
+        dt, T, V, ld = _matrix(logits, "logits")
+        if grad.dtype is not _F32 or not grad.is_contiguous():
+            grad = grad.to(_F32).contiguous()
+        g = torch.empty((T, V), dtype=logits.dtype, device=logits.device)
+        K, stats = ids.shape[1], kept.data_ptr()
+        _run("ce_distill_backward", logits.device, None, logits.data_ptr(), dt, T, V, ld, ids.data_ptr(), K,
+             ctx.temperature, ctx.red, stats, stats + 4 * ROW_STATS * T, grad.data_ptr(), g.data_ptr(), dt, V)
         return g, None, None, None, None, None, None, None
 
 
