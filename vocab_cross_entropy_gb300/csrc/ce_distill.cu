@@ -341,6 +341,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_distill(const __grid_constant__
     const int64_t row = blockIdx.x / C;
     const Row r = make_row<S>(a.logits, row, a.ld, a.V);
     const Slice sl = make_slice(r, C, rank);
+    start_next();
     const int64_t* ids = a.ids + row * a.K;
     O* grow = kGrad ? static_cast<O*>(a.grad) + row * a.ld_g : nullptr;
     const bool vec = kGrad && grads_aligned<S, O>(r, grow);
@@ -483,6 +484,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_distill(const __grid_constant__
     } else if (dead) {
         zero_grads<S, O>(r, sl, grow, vec, tid, kThreads);
     } else {
+        if (a.red == VCE_RED_MEAN) wait_previous();   // k_distill_count
         const float c = a.go[a.red == VCE_RED_NONE ? row : 0] * (a.red == VCE_RED_MEAN ? *a.inv_n : 1.f) * a.tau;
         if (warp < kConsumerWarps) {
             const float coef = c * f.d, bias = f.bias;
@@ -582,6 +584,21 @@ __host__ __device__ constexpr int entry_stride(int K) { return K > 8 ? K : 8; }
 template <int kTops>
 __host__ __device__ constexpr int ring_smem(int stages_bytes, int K) {
     return stages_bytes + kTops * entry_stride(K) * (int)sizeof(Entry) + (int)sizeof(RingCtl<kTops>) + 16;
+}
+
+// make_row without its address, in 32-bit arithmetic: what the consumers need of a row, each warp by itself.
+template <typename S>
+__device__ __forceinline__ Row row_extent(const Args& a, int64_t row) {
+    constexpr int G = Elt<S>::kGroup;
+    Row r;
+    r.base = nullptr;
+    r.V = a.V;
+    const uint32_t off = ((uint32_t)reinterpret_cast<uintptr_t>(a.logits) + (uint32_t)row * ((uint32_t)a.ld * (uint32_t)sizeof(S))) & 15u;
+    r.shift = (int)(off / sizeof(S));
+    r.nv = ((int)a.V + r.shift + G - 1) / G;
+    r.iv0 = r.shift ? 1 : 0;
+    r.iv1 = ((int)a.V + r.shift) / G;
+    return r;
 }
 
 // make_slice in stages of the ring.
@@ -695,6 +712,7 @@ __global__ void __launch_bounds__(ring_threads(kTops), 1) k_distill_ring(const _
         return tc::mbar_wait(bar + e % kTops, (uint32_t)(e / kTops) & 1, &ctl.abort, &ctl.err, kErrRow, tc::kWaitNs, kSuspend);
     };
 
+    start_next();
     if (tid == 0) {
         for (int i = 0; i < nbuf; ++i) {
             tc::mbar_init(&ctl.full[i], 1);
@@ -870,6 +888,7 @@ __global__ void __launch_bounds__(ring_threads(kTops), 1) k_distill_ring(const _
             }
         }
     } else if (warp == kStats) {
+        if (kGrad && a.red == VCE_RED_MEAN) wait_previous();   // k_distill_count
         const float inv_n = kGrad && a.red == VCE_RED_MEAN ? *a.inv_n : 1.f;
         // The losses take longer than anything a consumer waits for: each lane keeps a row, and 32 rows'
         // are worked out at once.
@@ -902,14 +921,7 @@ __global__ void __launch_bounds__(ring_threads(kTops), 1) k_distill_ring(const _
             if (!wait(&ctl.paired[par], e, kErrPartials)) break;
             float M = lane < kWarps ? ctl.red_m[par][lane] : -kInf;
             float S0 = lane < kWarps ? ctl.red_s[par][lane] : 0.f;
-#pragma unroll
-            for (int off = kWarps / 2; off > 0; off >>= 1) {   // lanes 0 .. kWarps - 1 into lane 0
-                const float m2 = __shfl_xor_sync(0xFFFFFFFFu, M, off);
-                const float s2 = __shfl_xor_sync(0xFFFFFFFFu, S0, off);
-                pair_merge(M, S0, m2, s2);
-            }
-            M = __shfl_sync(0xFFFFFFFFu, M, 0);
-            S0 = __shfl_sync(0xFFFFFFFFu, S0, 0);
+            pair_warp_reduce(M, S0);
             if (!wait_top(ctl.topped, e)) break;
             const TopStats ts = ctl.top[e % kTops];
             int code = ts.code;
@@ -1007,7 +1019,7 @@ __global__ void __launch_bounds__(ring_threads(kTops), 1) k_distill_ring(const _
         auto next = [&]() {
             return walk_next(walk, a, [&](int64_t no) {    // an ignored row
                 if (!kGrad) return;
-                const Row r = make_row<S>(a.logits, no, a.ld, a.V);
+                const Row r = row_extent<S>(a, no);
                 O* g = static_cast<O*>(a.grad) + no * a.ld_g;
                 zero_grads<S, O>(r, ring_slice<kGrad>(r, C, rank), g, grads_aligned<S, O>(r, g), tid, kNT);
             });
@@ -1022,7 +1034,7 @@ __global__ void __launch_bounds__(ring_threads(kTops), 1) k_distill_ring(const _
             Pair p{-kInf, 0.f};
             int pre = 0;
             if (row2 >= 0) {
-                r2 = make_row<S>(a.logits, row2, a.ld, a.V);
+                r2 = row_extent<S>(a, row2);
                 sl2 = ring_slice<kGrad>(r2, C, rank);
                 // the next row's stages that fit beside this one's (forward alone: all of them)
                 pre = kGrad ? min(sl2.nst, nbuf - sl.nst) : sl2.nst;
@@ -1144,44 +1156,63 @@ __device__ __forceinline__ long long block_count(long long n, long long* sm) {
     return t;
 }
 
-__global__ void __launch_bounds__(kReduceThreads) k_distill_count(const int64_t* ids, int K, const int64_t* labels,
-                                                                  int64_t ignore_index, int64_t T, float* inv_n) {
+struct CountArgs {
+    const int64_t* ids;
+    int K;
+    const int64_t* labels;
+    int64_t ignore_index, T;
+    float* inv_n;
+};
+
+__global__ void __launch_bounds__(kReduceThreads) k_distill_count(const __grid_constant__ CountArgs a) {
     __shared__ long long sm[kReduceThreads / 32];
+    start_next();
     long long n = 0;
 #pragma unroll 8
-    for (int64_t i = threadIdx.x; i < T; i += kReduceThreads)
-        n += ids[i * K] != -1 && !(labels && labels[i] == ignore_index);
+    for (int64_t i = threadIdx.x; i < a.T; i += kReduceThreads)
+        n += a.ids[i * a.K] != -1 && !(a.labels && a.labels[i] == a.ignore_index);
     n = block_count(n, sm);
-    if (threadIdx.x == 0) *inv_n = n > 0 ? (float)(1.0 / (double)n) : 0.f;
+    if (threadIdx.x == 0) *a.inv_n = n > 0 ? (float)(1.0 / (double)n) : 0.f;
 }
 
 // loss_out, status, and the rows' weights (1, a negative error code or 0 on entry; read only where
 // MEAN needs N, the codes always).
-__global__ void __launch_bounds__(kReduceThreads) k_distill_reduce(const float* loss_rows, float4* row_stats, int64_t T,
-                                                                   int red, float* loss_out, int32_t* status) {
+struct ReduceArgs {
+    const float* loss_rows;
+    float4* row_stats;
+    int64_t T;
+    int red;
+    float* loss_out;
+    int32_t* status;
+};
+
+__global__ void __launch_bounds__(kReduceThreads) k_distill_reduce(const __grid_constant__ ReduceArgs a) {
     __shared__ long long sm[kReduceThreads / 32];
     __shared__ float sum[kReduceThreads / 32], comp[kReduceThreads / 32];
     __shared__ int code;
+    wait_previous();
     if (threadIdx.x == 0) code = 0;
     __syncthreads();
     long long n = 0;
     int mine = 0;
 #pragma unroll 8
-    for (int64_t i = threadIdx.x; i < T; i += kReduceThreads) {
-        const float w = row_stats[i].w;
+    for (int64_t i = threadIdx.x; i < a.T; i += kReduceThreads) {
+        const float w = a.row_stats[i].w;
         n += w != 0.f;
         if (w < 0.f) mine = max(mine, (int)-w);
     }
     if (mine) atomicMax(&code, mine);
     n = block_count(n, sm);
-    const float weight = red == VCE_RED_MEAN ? (n > 0 ? (float)(1.0 / (double)n) : 0.f) : 1.f;
+    const float weight = a.red == VCE_RED_MEAN ? (n > 0 ? (float)(1.0 / (double)n) : 0.f) : 1.f;
+    if (weight != 1.f || code) {               // else the weights stand as they are
 #pragma unroll 8
-    for (int64_t i = threadIdx.x; i < T; i += kReduceThreads) {
-        const float w = row_stats[i].w;
-        row_stats[i].w = w > 0.f ? weight : 0.f;
+        for (int64_t i = threadIdx.x; i < a.T; i += kReduceThreads) {
+            const float w = a.row_stats[i].w;
+            a.row_stats[i].w = w > 0.f ? weight : 0.f;
+        }
     }
-    if (red != VCE_RED_NONE) fold::sum_losses<kReduceThreads>(loss_rows, T, n, red, loss_out, sum, comp);
-    if (threadIdx.x == 0) *status = code;
+    if (a.red != VCE_RED_NONE) fold::sum_losses<kReduceThreads>(a.loss_rows, a.T, n, a.red, a.loss_out, sum, comp);
+    if (threadIdx.x == 0) *a.status = code;
 }
 
 // ---- host ----------------------------------------------------------------------------------------------
@@ -1216,6 +1247,12 @@ int ring_cluster(int64_t T, int64_t V, int G, int sms) {
     return kGrad && st(C) > Ge::kHeld ? 0 : C;
 }
 
+// In one pass with MEAN the row kernel starts while k_distill_count runs.
+template <bool kGrad>
+bool early_start(const Args& a) {
+    return kGrad && a.red == VCE_RED_MEAN;
+}
+
 template <typename S, typename O, bool kGrad, int kTops>
 cudaError_t run_ring(Args& a, int sms, cudaStream_t s, bool* done) {
     using Ge = ring::Geom<kGrad>;
@@ -1223,7 +1260,8 @@ cudaError_t run_ring(Args& a, int sms, cudaStream_t s, bool* done) {
     const int bytes = ring::ring_smem<kTops>(Ge::kBufs * Ge::kBytes, a.K), threads = ring::ring_threads(kTops);
     const int64_t clusters = std::min<int64_t>(a.T, resident_clusters<kern>(a.cluster, threads, bytes, sms));
     *done = clusters > 0;
-    return *done ? launch_clusters<kern>(clusters * a.cluster, a.cluster, threads, bytes, s, a) : cudaSuccess;
+    return *done ? launch_clusters<kern>(clusters * a.cluster, a.cluster, threads, bytes, s, a, early_start<kGrad>(a))
+                 : cudaSuccess;
 }
 
 template <typename S, typename O, bool kGrad>
@@ -1237,7 +1275,8 @@ cudaError_t run(Args& a, int sms, cudaStream_t s) {
     }
     shape(a.T, a.V, Elt<S>::kGroup, kGrad, a.K, sms, &a.cluster, &a.nbuf, &a.max_stages);
     const int bytes = smem_bytes(a.nbuf, a.max_stages, a.K);
-    return launch_clusters<k_distill<S, O, kGrad>>(a.T * a.cluster, a.cluster, kThreads, bytes, s, a);
+    return launch_clusters<k_distill<S, O, kGrad>>(a.T * a.cluster, a.cluster, kThreads, bytes, s, a,
+                                                        early_start<kGrad>(a));
 }
 
 template <typename S, typename O>
@@ -1283,8 +1322,8 @@ int forward_checks(const Args& a, vce_dtype dt, vce_dtype tdt, float tau, const 
 }
 
 cudaError_t reduce(const Args& a, float* loss_out, int32_t* status, cudaStream_t s) {
-    k_distill_reduce<<<1, kReduceThreads, 0, s>>>(a.loss_rows, a.row_stats, a.T, a.red, loss_out, status);
-    return cudaGetLastError();
+    const ReduceArgs r{a.loss_rows, a.row_stats, a.T, a.red, loss_out, status};
+    return launch_clusters<k_distill_reduce>(1, 1, kReduceThreads, 0, s, r, a.T > 0);
 }
 
 }  // namespace
@@ -1376,9 +1415,8 @@ extern "C" int ce_distill_forward_backward(const void* logits, vce_dtype dt, int
     cudaError_t e = cudaSuccess;
     if (T) {
         if (red == VCE_RED_MEAN) {
-            distill::k_distill_count<<<1, distill::kReduceThreads, 0, s>>>(teacher_ids, K, labels, ignore_index, T,
-                                                                           loss_out);
-            e = cudaGetLastError();
+            const distill::CountArgs c{teacher_ids, K, labels, ignore_index, T, loss_out};
+            e = rs::launch_clusters<distill::k_distill_count>(1, 1, distill::kReduceThreads, 0, s, c);
         }
         const int sms = device_sm_count();
         if (e != cudaSuccess) ;

@@ -16,19 +16,26 @@ namespace rs {
 
 constexpr int kMaxSmem = 232448;   // shared memory of a block, at most
 
-// Launches `blocks` blocks of kKernel in clusters of `cluster` along x.  A kernel is allowed all of
-// an SM's shared memory once per device (the attribute costs a launch about 2 us on the host); a
+// Launches `blocks` blocks of kKernel in clusters of `cluster` along x.  A kernel that needs more than
+// 48 KB of shared memory (and has none of its own) is allowed all of an SM's once per device (the attribute costs a launch about 2 us on the host); a
 // launch that fails is tried once more with the attribute set again, since a device reset drops it.
+// early: the kernel may start before the stream's previous one has ended (programmatic dependent
+// launch); it waits for that one itself (wait_previous) before it reads what that writes.
 template <auto kKernel, typename Args>
-cudaError_t launch_clusters(int64_t blocks, int cluster, int threads, int smem, cudaStream_t s, const Args& args) {
+cudaError_t launch_clusters(int64_t blocks, int cluster, int threads, int smem, cudaStream_t s, const Args& args,
+                            bool early = false) {
     static std::atomic<uint64_t> allowed{0};   // bit d: device d (kMaxDevices = 64)
     int d = 0;
     cudaError_t e = cudaGetDevice(&d);
     if (e != cudaSuccess) return e;
     const uint64_t bit = d >= 0 && d < kMaxDevices ? 1ull << d : 0;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     int n = 0;
+    if (early) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
     if (cluster > 1) {
         attr[n].id = cudaLaunchAttributeClusterDimension;
         attr[n].val.clusterDim.x = (unsigned)cluster;
@@ -41,9 +48,9 @@ cudaError_t launch_clusters(int64_t blocks, int cluster, int threads, int smem, 
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = (unsigned)n;
-    const bool known = (allowed.load(std::memory_order_acquire) & bit) != 0;
+    const bool known = smem <= 49152 || (allowed.load(std::memory_order_acquire) & bit) != 0;
     for (int tries = known ? 0 : 1; tries < 2; ++tries) {
-        if (tries) {
+        if (tries && smem > 49152) {
             e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
             if (e != cudaSuccess) return e;
             allowed.fetch_or(bit, std::memory_order_release);

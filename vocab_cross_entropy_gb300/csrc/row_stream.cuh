@@ -189,13 +189,15 @@ __device__ __forceinline__ void pair_merge(float& m, float& s, float m2, float s
     m = M;
 }
 
+// The warp's pairs merged, in every lane: to the largest reference first, then one sum.
 __device__ __forceinline__ void pair_warp_reduce(float& m, float& s) {
+    float M = m;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        const float m2 = __shfl_xor_sync(0xFFFFFFFFu, m, off);
-        const float s2 = __shfl_xor_sync(0xFFFFFFFFu, s, off);
-        pair_merge(m, s, m2, s2);
-    }
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, off));
+    s *= (m == M) ? 1.f : ex2(m - M);
+    m = M;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
 }
 
 // (d0, d1) = (a0 + b0, a1 + b1), in one packed instruction; each sum rounds as the scalar one.
@@ -284,6 +286,10 @@ __device__ __forceinline__ float max_of_loaded(const uint4 (&x)[U]) {
                   __uint_as_float(x[u].w));
     return m;
 }
+
+// ---- programmatic dependent launch: the next kernel of the stream may start; the previous one has ended
+__device__ __forceinline__ void start_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ---- thread-block clusters -------------------------------------------------------------------
 
