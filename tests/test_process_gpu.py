@@ -293,4 +293,5 @@ def test_a_decoded_token(vce):
     logp = (values - lse[:, None]).double().cpu().numpy()[open_]
     tol = G.lse_tol(np.abs(host[np.isfinite(host)]).max(), 1.0) + 2.0 ** -23 * 16
     there = np.isfinite(rv[open_])
-    assert np.all(np.abs(logp[there] - (rv - rl[:, None])[open_][there]) <= tol)
+    want = rv[open_] - rl[open_][:, None]
+    assert np.all(np.abs(logp[there] - want[there]) <= tol)

@@ -13,15 +13,20 @@
 //     tail:  tau (p_T - q_T) e^{s z_j - L'}        top:  tau [Q (r_k - qh_k) + (q_T - p_T) r_k]
 // with p_T - q_T a difference of logistic functions taken as a product (sigmoid_diff).
 //
-// Kernels.  k_distill: one thread-block cluster per row, each block a slice of the columns,
-// streamed through shared memory (row_stream.cuh).  One extra warp reads the K entries, marks
-// their columns in a bitmap (a word per consumer thread and stage, so a thread learns from one
-// word whether any of its 32 values is left out) and does all arithmetic on the K entries while
-// the columns stream.  The blocks then exchange (max, sum-exp) pairs through distributed shared
-// memory.  With the gradient (kGrad) the stages are kept and turned into gradient entries once
-// the pairs are merged.  k_distill_bwd: the gradient alone, from the saved statistics.
-// k_distill_reduce sums the losses in a fixed order; k_distill_count counts N before a one-pass
-// call with MEAN.  Nothing is shared between launches.
+// Kernels.
+//   k_distill_ring     forward, and loss and gradient in one pass: persistent, warps with roles, the
+//                      columns streamed through a shared-memory ring (described where it stands)
+//   k_distill_long     one pass over rows that a cluster's shared memory does not hold
+//   k_distill_bwd      the gradient alone, from the saved statistics
+//   k_distill_reduce   the losses' sum in a fixed order, the rows' weights, the status word
+//   k_distill_count    N, before a one-pass call with MEAN
+// Nothing is shared between launches.
+//
+// What bounds them, bf16 with 64 entries a row: the forward reads the logits once (4096 x 128256: 163 us,
+// 6.5 TB/s, 0.95 of the measured copy), one pass also writes the gradient (16384 x 128256: 1448 us, 5.8
+// TB/s, 0.86; a row's exponentials are taken twice, about 20 issue slots a column of 24 that the
+// copy's time leaves), the backward runs at the copy's speed (4096 x 128256: 299 us).  Rows of 32000
+// columns cost the consumer warps about 1 us beside their columns: 84 us for 4096 of them (3.1 TB/s).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -59,7 +64,8 @@ struct Args {
     float* top_grads;            // forward alone
     void* grad;                  // kGrad
     int64_t ld_g;
-    int cluster, nbuf, max_stages;
+    int cluster;
+    int nbuf, max_stages;        // k_distill_long
 };
 
 // Of a row's entries: the largest logits z, t of the student and the teacher, the sums of e^{s (z - max)}
@@ -325,10 +331,13 @@ __device__ __forceinline__ float loss_of(const Args& a, const Finish& f, float k
     return f.dead ? __int_as_float(0x7FC00000) : a.tau * a.tau * kl;
 }
 
-// ---- the row kernel -------------------------------------------------------------------------------
+// ---- one pass over rows longer than shared memory ----------------------------------------------------
+//
+// One cluster of eight blocks a row, every slice streamed twice (the second time mostly from L2): the
+// entries' columns are left out of the sums by a bitmap, a word per consumer thread and stage.
 
-template <typename S, typename O, bool kGrad>
-__global__ void __launch_bounds__(kThreads, 3) k_distill(const __grid_constant__ Args a) {
+template <typename S, typename O>
+__global__ void __launch_bounds__(kThreads, 2) k_distill_long(const __grid_constant__ Args a) {
     constexpr int G = Elt<S>::kGroup;
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t* bufs = smem;
@@ -343,27 +352,22 @@ __global__ void __launch_bounds__(kThreads, 3) k_distill(const __grid_constant__
     const Slice sl = make_slice(r, C, rank);
     start_next();
     const int64_t* ids = a.ids + row * a.K;
-    O* grow = kGrad ? static_cast<O*>(a.grad) + row * a.ld_g : nullptr;
-    const bool vec = kGrad && grads_aligned<S, O>(r, grow);
+    O* grow = static_cast<O*>(a.grad) + row * a.ld_g;
+    const bool vec = grads_aligned<S, O>(r, grow);
 
     // a row without a teacher or with the ignored label: nothing of it is read (all blocks alike)
     if (ids[0] == -1 || (a.labels && a.labels[row] == a.ignore_index)) {
-        if (rank == 0) {
-            if (tid == 0) {
-                a.loss_rows[row] = 0.f;
-                a.row_stats[row] = make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-            if (!kGrad)
-                for (int k = tid; k < a.K; k += kThreads) a.top_grads[row * a.K + k] = 0.f;
+        if (rank == 0 && tid == 0) {
+            a.loss_rows[row] = 0.f;
+            a.row_stats[row] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        if (kGrad) zero_grads<S, O>(r, sl, grow, vec, tid, kThreads);
+        zero_grads<S, O>(r, sl, grow, vec, tid, kThreads);
         return;
     }
 
-    const bool held = sl.nst <= a.nbuf;              // the slice stays in shared memory
-    // a slice that is not held is copied twice; of its second round, the ring's first fill goes out
-    // before the statistics are done (later stages wait for the gradient to release theirs)
-    const int total = kGrad && !held ? 2 * sl.nst : sl.nst;
+    // the slice is copied twice; of its second round, the ring's first fill goes out before the
+    // statistics are done (later stages wait for the gradient to release theirs)
+    const int total = 2 * sl.nst;
     const int early = min(total, sl.nst + a.nbuf);
     int issued = 0;
     if (tid == kProducerWarp * 32) {
@@ -429,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_distill(const __grid_constant__
             wait_stage(ctl.bar, a.nbuf, j);
             uint4 x[kU];
             load_stage<S>(bufs, a.nbuf, r, sl, j, j, tid, x);
-            if (!(kGrad && held)) release_stage(ctl.bar, a.nbuf, j);
+            release_stage(ctl.bar, a.nbuf, j);
             float v[kU][G];
 #pragma unroll
             for (int u = 0; u < kU; ++u) Elt<S>::unpack(x[u], v[u]);
@@ -475,13 +479,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_distill(const __grid_constant__
         // weight: 1, negative for a row with an error, until the reduction writes it
         a.row_stats[row] = make_float4(f.lt, dead ? 0.f : f.d, 0.f, f.code ? -(float)f.code : 1.f);
     }
-    if (!kGrad) {
-        if (rank == 0)
-            for (int k = tid; k < a.K; k += kThreads) {
-                const Entry e = entry[k];
-                a.top_grads[row * a.K + k] = dead || e.col < 0 ? 0.f : a.tau * (f.q * e.diff - f.d * e.r);
-            }
-    } else if (dead) {
+    if (dead) {
         zero_grads<S, O>(r, sl, grow, vec, tid, kThreads);
     } else {
         if (a.red == VCE_RED_MEAN) wait_previous();   // k_distill_count
@@ -489,11 +487,11 @@ __global__ void __launch_bounds__(kThreads, 3) k_distill(const __grid_constant__
         if (warp < kConsumerWarps) {
             const float coef = c * f.d, bias = f.bias;
             for (int j = 0; j < sl.nst; ++j) {
-                const int q = held ? j : sl.nst + j;
-                if (!held) wait_stage(ctl.bar, a.nbuf, q);
+                const int q = sl.nst + j;
+                wait_stage(ctl.bar, a.nbuf, q);
                 uint4 x[kU];
                 load_stage<S>(bufs, a.nbuf, r, sl, j, q, tid, x);
-                if (!held) release_stage(ctl.bar, a.nbuf, q);
+                release_stage(ctl.bar, a.nbuf, q);
                 write_grads<S, O, kU, kConsumers>(x, r, sl, j, tid, grow, vec, coef, a.k2, bias);
             }
         } else if (tid == kProducerWarp * 32) {
@@ -509,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_distill(const __grid_constant__
         }
     }
     // copies that nothing waited for (after an abort, or of a row without a gradient) land first
-    if ((ctl.bar.abort || (kGrad && dead)) && tid == kProducerWarp * 32) drain(ctl.bar, a.nbuf, issued);
+    if ((ctl.bar.abort || dead) && tid == kProducerWarp * 32) drain(ctl.bar, a.nbuf, issued);
 }
 
 // ---- many rows: a persistent kernel -----------------------------------------------------------------
@@ -1217,25 +1215,6 @@ __global__ void __launch_bounds__(kReduceThreads) k_distill_reduce(const __grid_
 
 // ---- host ----------------------------------------------------------------------------------------------
 
-// Blocks of a row: enough that a slice's stages (and, in one pass, the whole slice) leave room for
-// three blocks an SM, and, for few rows, enough blocks for the SMs.
-void shape(int64_t T, int64_t V, int G, bool hold, int K, int sms, int* cluster, int* nbuf, int* stages) {
-    const int64_t nv = (V + 2 * G - 2) / G;   // vectors of a row, at most
-    int C = 1;
-    auto st = [&](int c) { return (int)(((nv + c - 1) / c + kStageVecs - 1) / kStageVecs); };
-    const int fit = 4;                         // stages of 16 KB beside the marks: three blocks an SM
-    while (C < kMaxCluster && ((hold && st(C) > fit) || (T * C < 2 * sms && st(C) > 1))) C *= 2;
-    int nb = std::min(st(C), fit);
-    if (hold && st(C) > fit) {                 // long rows: as much of the slice as fits one block an SM
-        nb = std::min(st(C), kMaxBufs);
-        while (nb > fit && smem_bytes(nb, st(C), K) > kMaxSmem) --nb;
-    }
-    while (C < kMaxCluster && smem_bytes(nb, st(C), K) > kMaxSmem) C *= 2;
-    *cluster = C;
-    *stages = st(C);
-    *nbuf = std::max(1, std::min(nb, st(C)));
-}
-
 // The persistent kernel's blocks of a row; 0: rows too long to hold.
 template <bool kGrad>
 int ring_cluster(int64_t T, int64_t V, int G, int sms) {
@@ -1254,29 +1233,33 @@ bool early_start(const Args& a) {
 }
 
 template <typename S, typename O, bool kGrad, int kTops>
-cudaError_t run_ring(Args& a, int sms, cudaStream_t s, bool* done) {
+cudaError_t run_ring(Args& a, int sms, cudaStream_t s) {
     using Ge = ring::Geom<kGrad>;
     constexpr auto kern = ring::k_distill_ring<S, O, kGrad, kTops>;
     const int bytes = ring::ring_smem<kTops>(Ge::kBufs * Ge::kBytes, a.K), threads = ring::ring_threads(kTops);
     const int64_t clusters = std::min<int64_t>(a.T, resident_clusters<kern>(a.cluster, threads, bytes, sms));
-    *done = clusters > 0;
-    return *done ? launch_clusters<kern>(clusters * a.cluster, a.cluster, threads, bytes, s, a, early_start<kGrad>(a))
-                 : cudaSuccess;
+    if (clusters < 1) return cudaErrorInvalidConfiguration;   // not one cluster of that size fits
+    return launch_clusters<kern>(clusters * a.cluster, a.cluster, threads, bytes, s, a, early_start<kGrad>(a));
+}
+
+template <typename S, typename O>
+cudaError_t run_long(Args& a, cudaStream_t s) {
+    const int64_t nv = (a.V + 2 * Elt<S>::kGroup - 2) / Elt<S>::kGroup;
+    a.cluster = kMaxCluster;
+    a.max_stages = (int)(((nv + kMaxCluster - 1) / kMaxCluster + kStageVecs - 1) / kStageVecs);
+    a.nbuf = 4;
+    return launch_clusters<k_distill_long<S, O>>(a.T * a.cluster, a.cluster, kThreads,
+                                                 smem_bytes(a.nbuf, a.max_stages, a.K), s, a, early_start<true>(a));
 }
 
 template <typename S, typename O, bool kGrad>
 cudaError_t run(Args& a, int sms, cudaStream_t s) {
     a.cluster = ring_cluster<kGrad>(a.T, a.V, Elt<S>::kGroup, sms);
-    if (a.cluster) {
-        bool done = false;
-        const cudaError_t e = a.V * (int64_t)sizeof(S) >= ring::kLongRow ? run_ring<S, O, kGrad, 2>(a, sms, s, &done)
-                                                                        : run_ring<S, O, kGrad, 4>(a, sms, s, &done);
-        if (done || e != cudaSuccess) return e;
+    if constexpr (kGrad) {
+        if (a.cluster == 0) return run_long<S, O>(a, s);
     }
-    shape(a.T, a.V, Elt<S>::kGroup, kGrad, a.K, sms, &a.cluster, &a.nbuf, &a.max_stages);
-    const int bytes = smem_bytes(a.nbuf, a.max_stages, a.K);
-    return launch_clusters<k_distill<S, O, kGrad>>(a.T * a.cluster, a.cluster, kThreads, bytes, s, a,
-                                                        early_start<kGrad>(a));
+    return a.V * (int64_t)sizeof(S) >= ring::kLongRow ? run_ring<S, O, kGrad, 2>(a, sms, s)
+                                                      : run_ring<S, O, kGrad, 4>(a, sms, s);
 }
 
 template <typename S, typename O>

@@ -62,6 +62,22 @@ def _new(shape, dtype, dev, stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
+def _out(t, name, dtype, shape, dev, stream):
+    """An output, the caller's or a new one, and its address."""
+    if t is None:
+        t = _new(shape, dtype, dev, stream)
+        return t, t.data_ptr()
+    return t, _flat(t, name, dtype, shape, dev)
+
+
+def _matrix_out(t, name, T, V, dtype, dev, stream):
+    """A [T, V] output, the caller's or a new one, its address, dtype code and leading dimension."""
+    if t is None:
+        t = _new((T, V), dtype, dev, stream)
+    code, _, _, ld = _matrix(t, name, dev, (T, V))
+    return t, t.data_ptr(), code, ld
+
+
 def _run(fn, dev, stream, *args):
     """Calls the library on the tensors' device and stream."""
     if stream is None:
@@ -92,17 +108,11 @@ def ce_topk(logits, k, temperature=1.0, *, values=None, ids=None, lse=None, tail
     k = int(k)
     if k < 1:
         raise ValueError(f"k: {k}, expected at least 1")
-    if values is None:
-        values = _new((T, k), _F32, dev, stream)
-    if ids is None:
-        ids = _new((T, k), _I64, dev, stream)
-    if lse is None:
-        lse = _new((T,), _F32, dev, stream)
-    if tail_lse is None:
-        tail_lse = _new((T,), _F32, dev, stream)
-    _run("ce_topk", dev, stream, logits.data_ptr(), dt, T, V, ld, k, temperature,
-         _flat(values, "values", _F32, (T, k), dev), _flat(ids, "ids", _I64, (T, k), dev),
-         _flat(lse, "lse", _F32, (T,), dev), _flat(tail_lse, "tail_lse", _F32, (T,), dev))
+    values, p_values = _out(values, "values", _F32, (T, k), dev, stream)
+    ids, p_ids = _out(ids, "ids", _I64, (T, k), dev, stream)
+    lse, p_lse = _out(lse, "lse", _F32, (T,), dev, stream)
+    tail_lse, p_tail = _out(tail_lse, "tail_lse", _F32, (T,), dev, stream)
+    _run("ce_topk", dev, stream, logits.data_ptr(), dt, T, V, ld, k, temperature, p_values, p_ids, p_lse, p_tail)
     return values, ids, lse, tail_lse
 
 
@@ -131,21 +141,16 @@ def ce_distill_forward(logits, teacher_ids, teacher_values, teacher_tail=None, t
     dev = logits.device
     K, p_ids, p_values, tdt, p_tail = _teacher(teacher_ids, teacher_values, teacher_tail, T, dev)
     red = RED[reduction]
-    if loss_rows is None:
-        loss_rows = _new((T,), _F32, dev, stream)
-    if row_stats is None:
-        row_stats = _new((T, ROW_STATS), _F32, dev, stream)
-    if top_grads is None:
-        top_grads = _new((T, K), _F32, dev, stream)
-    if status is None:
-        status = _new((1,), _I32, dev, stream)
-    if red and loss_out is None:
-        loss_out = _new((1,), _F32, dev, stream)
+    loss_rows, p_rows = _out(loss_rows, "loss_rows", _F32, (T,), dev, stream)
+    row_stats, p_stats = _out(row_stats, "row_stats", _F32, (T, ROW_STATS), dev, stream)
+    top_grads, p_tops = _out(top_grads, "top_grads", _F32, (T, K), dev, stream)
+    status, p_status = _out(status, "status", _I32, (1,), dev, stream)
+    p_loss = None
+    if red or loss_out is not None:
+        loss_out, p_loss = _out(loss_out, "loss_out", _F32, (1,), dev, stream)
     _run("ce_distill_forward", dev, stream, logits.data_ptr(), dt, T, V, ld, p_ids, p_values, tdt, p_tail, K,
-         temperature, _flat(labels, "labels", _I64, (T,), dev), ignore_index, red,
-         _flat(loss_rows, "loss_rows", _F32, (T,), dev), _flat(loss_out, "loss_out", _F32, (1,), dev),
-         _flat(row_stats, "row_stats", _F32, (T, ROW_STATS), dev), _flat(top_grads, "top_grads", _F32, (T, K), dev),
-         _flat(status, "status", _I32, (1,), dev))
+         temperature, _flat(labels, "labels", _I64, (T,), dev), ignore_index, red, p_rows, p_loss, p_stats, p_tops,
+         p_status)
     return loss_out, loss_rows, row_stats, top_grads, status
 
 
@@ -158,13 +163,11 @@ def ce_distill_backward(logits, teacher_ids, row_stats, top_grads, grad_output, 
         raise ValueError("teacher_ids: expected a [T, K] tensor")
     K = teacher_ids.shape[1]
     red = RED[reduction]
-    if grad_logits is None:
-        grad_logits = _new((T, V), grad_dtype or logits.dtype, dev, stream)
-    gdt, _, _, gld = _matrix(grad_logits, "grad_logits", dev, (T, V))
+    grad_logits, p_grad, gdt, gld = _matrix_out(grad_logits, "grad_logits", T, V, grad_dtype or logits.dtype, dev, stream)
     _run("ce_distill_backward", dev, stream, logits.data_ptr(), dt, T, V, ld,
          _flat(teacher_ids, "teacher_ids", _I64, (T, K), dev), K, temperature, red,
          _flat(row_stats, "row_stats", _F32, (T, ROW_STATS), dev), _flat(top_grads, "top_grads", _F32, (T, K), dev),
-         _flat(grad_output, "grad_output", _F32, (1,) if red else (T,), dev), grad_logits.data_ptr(), gdt, gld)
+         _flat(grad_output, "grad_output", _F32, (1,) if red else (T,), dev), p_grad, gdt, gld)
     return grad_logits
 
 
@@ -184,23 +187,17 @@ def ce_distill_forward_backward(logits, teacher_ids, teacher_values, teacher_tai
         grad_output = _new((1,) if red else (T,), _F32, dev, stream)
         with torch.cuda.stream(stream):   # None: the current stream
             grad_output.fill_(1.0)
-    if grad_logits is None:
-        grad_logits = _new((T, V), grad_dtype or logits.dtype, dev, stream)
-    if loss_rows is None:
-        loss_rows = _new((T,), _F32, dev, stream)
-    if row_stats is None:
-        row_stats = _new((T, ROW_STATS), _F32, dev, stream)
-    if status is None:
-        status = _new((1,), _I32, dev, stream)
-    if red and loss_out is None:
-        loss_out = _new((1,), _F32, dev, stream)
-    gdt, _, _, gld = _matrix(grad_logits, "grad_logits", dev, (T, V))
+    grad_logits, p_grad, gdt, gld = _matrix_out(grad_logits, "grad_logits", T, V, grad_dtype or logits.dtype, dev, stream)
+    loss_rows, p_rows = _out(loss_rows, "loss_rows", _F32, (T,), dev, stream)
+    row_stats, p_stats = _out(row_stats, "row_stats", _F32, (T, ROW_STATS), dev, stream)
+    status, p_status = _out(status, "status", _I32, (1,), dev, stream)
+    p_loss = None
+    if red or loss_out is not None:
+        loss_out, p_loss = _out(loss_out, "loss_out", _F32, (1,), dev, stream)
     _run("ce_distill_forward_backward", dev, stream, logits.data_ptr(), dt, T, V, ld, p_ids, p_values, tdt, p_tail, K,
          temperature, _flat(labels, "labels", _I64, (T,), dev), ignore_index, red,
-         _flat(grad_output, "grad_output", _F32, (1,) if red else (T,), dev),
-         _flat(loss_rows, "loss_rows", _F32, (T,), dev), _flat(loss_out, "loss_out", _F32, (1,), dev),
-         _flat(row_stats, "row_stats", _F32, (T, ROW_STATS), dev), grad_logits.data_ptr(), gdt, gld,
-         _flat(status, "status", _I32, (1,), dev))
+         _flat(grad_output, "grad_output", _F32, (1,) if red else (T,), dev), p_rows, p_loss, p_stats, p_grad, gdt, gld,
+         p_status)
     return loss_out, loss_rows, grad_logits, status
 
 
@@ -290,11 +287,8 @@ def logits_process(logits, *, temperature=None, repetition_penalty=None, frequen
     """
     dt, T, V, ld = _matrix(logits, "logits")
     dev = logits.device
-    if out is None:
-        out = _new((T, V), out_dtype or logits.dtype, dev, stream)
-    odt, _, _, old = _matrix(out, "out", dev, (T, V))
-    if row_status is None:
-        row_status = _new((T,), _I32, dev, stream)
+    out, p_out, odt, old = _matrix_out(out, "out", T, V, out_dtype or logits.dtype, dev, stream)
+    row_status, p_status = _out(row_status, "row_status", _I32, (T,), dev, stream)
     h, n_h, h_off = _list(history_ids, history_offsets, "history", T, dev)
     b, n_b, b_off = _list(bias_ids, bias_offsets, "bias", T, dev)
     if b is not None and bias_values is None:
@@ -306,8 +300,8 @@ def logits_process(logits, *, temperature=None, repetition_penalty=None, frequen
          _flat(repetition_penalty, "repetition_penalty", _F32, (T,), dev),
          _flat(frequency_penalty, "frequency_penalty", _F32, (T,), dev),
          _flat(presence_penalty, "presence_penalty", _F32, (T,), dev), h, n_h, h_off,
-         _flat(prompt_lens, "prompt_lens", _I64, (T,), dev), b, bv, n_b, b_off, m, mld, out.data_ptr(), odt, old,
-         _flat(row_status, "row_status", _I32, (T,), dev))
+         _flat(prompt_lens, "prompt_lens", _I64, (T,), dev), b, bv, n_b, b_off, m, mld, p_out, odt, old,
+         p_status)
     return out, row_status
 
 
@@ -322,17 +316,15 @@ def logits_process_backward(grad_out, logits=None, *, temperature=None, repetiti
     if logits is not None:
         zdt, _, _, zld = _matrix(logits, "logits", dev, (T, V))
         z = logits.data_ptr()
-    if grad_logits is None:
-        grad_logits = _new((T, V), grad_dtype or (grad_out if logits is None else logits).dtype, dev, stream)
-    odt, _, _, old = _matrix(grad_logits, "grad_logits", dev, (T, V))
-    if row_status is None:
-        row_status = _new((T,), _I32, dev, stream)
+    grad_logits, p_grad, odt, old = _matrix_out(grad_logits, "grad_logits", T, V,
+                                           grad_dtype or (grad_out if logits is None else logits).dtype, dev, stream)
+    row_status, p_status = _out(row_status, "row_status", _I32, (T,), dev, stream)
     h, n_h, h_off = _list(history_ids, history_offsets, "history", T, dev)
     m, mld = _mask(mask, T, V, dev)
     _run("logits_process_backward", dev, stream, grad_out.data_ptr(), gdt, T, V, gld, z, zdt, zld,
          _flat(temperature, "temperature", _F32, (T,), dev),
          _flat(repetition_penalty, "repetition_penalty", _F32, (T,), dev), h, n_h, h_off, m, mld,
-         grad_logits.data_ptr(), odt, old, _flat(row_status, "row_status", _I32, (T,), dev))
+         p_grad, odt, old, p_status)
     return grad_logits, row_status
 
 
