@@ -512,11 +512,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_distill_long(const __grid_const
 
 // ---- many rows: a persistent kernel -----------------------------------------------------------------
 //
-// One block per SM (a cluster of C blocks per row) walks the rows cid, cid + ncl, ... with the copies
+// Each block (a cluster of C of them per row) walks the rows cid, cid + ncl, ... with the copies
 // of the next rows always in flight.  Its warps have roles, which hand rows on through mbarriers,
-// everything that belongs
-// to a row doubled by the parity of its number in the block's sequence (the
-// entries by top warp):
+// everything that belongs to a row doubled by the parity of its number in the
+// block's sequence (the entries by top warp):
 //   producer        copies the rows' slices into the stage ring, running ahead as stages are released
 //   patch           overwrites the entries' columns in the loaded stages with -inf, and writes the row's
 //                   partial first and last vectors there, so the consumers' sums need not know of either
@@ -531,23 +530,30 @@ __global__ void __launch_bounds__(kThreads, 2) k_distill_long(const __grid_const
 
 namespace ring {
 
-constexpr int kWarps = 16, kNT = kWarps * 32;       // consumers
-constexpr int kProducer = kWarps, kPatch = kWarps + 1, kStats = kWarps + 2, kTop = kWarps + 3;
-__host__ __device__ constexpr int ring_threads(int tops) { return (kTop + tops) * 32; }
-// Top warps: rows of at least kLongRow bytes leave two of them time enough, shorter ones take four
-// (4096 x 128256 bf16 forward: 165 us with two, 168 with four; one pass, 16384 rows: 1433 and 1496;
-// 1023 x 32001 bf16 to fp32 one pass: 70 and 59).
+// Four forms, each direction's for rows of kLongRow bytes and more (kBig) and for shorter ones.
+//  - Forward: of a long row one block an SM, 16 consumer warps and 32 KB stages (less to do per stage).
+//    A short row costs a block's consumers about 1 us beside its columns (the merge of their pairs, the
+//    hand-over, the next row's extent); so two blocks an SM take them, with 8 warps and 16 KB stages, and
+//    each covers the other's (4096 x 32000 bf16: 67 us, and 78 with one block).
+//  - One pass: one block an SM, whose shared memory holds a row and the beginning of the next (two blocks
+//    at 4096 x 32000 bf16: 194 us against 125); 16 KB stages, so that a held row gives them back in small
+//    steps.  Two top warps have time enough for long rows, short ones take four (16384 x 128256 bf16: 1433
+//    us with two, 1496 with four; 1023 x 32001 bf16 to fp32: 70 and 59).
 constexpr int64_t kLongRow = 131072;
-constexpr uint32_t kSuspend = 10000;                // ns a poll may sleep: waiting warps leave the issue slots to others
-// Stages: in one pass 16 KB, so that a held row gives them back in small steps; 32 KB in the forward
-// alone, whose stages are given back at once (less to do per stage).
-template <bool kGrad>
-struct Geom {
-    static constexpr int kU = kGrad ? 2 : 4;        // vectors of a stage per consumer thread
-    static constexpr int kVecs = kU * kNT, kBytes = kVecs * 16;
+template <bool kGrad, bool kBig>
+struct Form {
+    static constexpr bool kPair = !kGrad && !kBig;                            // two blocks an SM
+    static constexpr int kBlocks = kPair ? 2 : 1;
+    static constexpr int kWarps = kPair ? 8 : 16, kNT = kWarps * 32;          // consumers
+    static constexpr int kTops = kGrad && !kBig ? 4 : 2;                      // top warps
+    static constexpr int kProducer = kWarps, kPatch = kWarps + 1, kStats = kWarps + 2, kTop = kWarps + 3;
+    static constexpr int kThreads = (kTop + kTops) * 32;
+    static constexpr int kU = kGrad ? 2 : 4;                                  // vectors of a stage per consumer thread
+    static constexpr int kVecs = kU * kNT, kBytes = kVecs * 16;               // of a stage
     static constexpr int kBufs = kGrad ? 13 : 6;
-    static constexpr int kHeld = 8;                 // stages of a slice that is held, at most
+    static constexpr int kHeld = 8;                                           // stages of a slice that is held, at most
 };
+constexpr uint32_t kSuspend = 10000;                // ns a poll may sleep: waiting warps leave the issue slots to others
 enum { kErrRow = 107, kErrPartials = 108, kErrCoefs = 109 };
 
 struct TopStats {
@@ -559,10 +565,10 @@ struct Coefs {                   // of the tail's gradient
     int dead;
 };
 
-template <int kTops>
+template <int kTops, int kWarps, int kBufs>
 struct alignas(16) RingCtl {
     float4 slot[2][kMaxCluster];
-    uint64_t full[13], ready[13], empty[13];   // of the stages: copied, patched, released
+    uint64_t full[kBufs], ready[kBufs], empty[kBufs];   // of the stages: copied, patched, released
     uint64_t topped[kTops];      // the entries' arithmetic (a top warp)
     uint64_t freed[kTops];       // the stats warp is done with the entries
     uint64_t paired[2];          // the consumer warps' pairs
@@ -579,9 +585,12 @@ struct alignas(16) RingCtl {
 // lies there before: at least 2 K slots of 4 bytes, a power of two, 32 or more.
 __host__ __device__ constexpr int entry_stride(int K) { return K > 8 ? K : 8; }
 
-template <int kTops>
-__host__ __device__ constexpr int ring_smem(int stages_bytes, int K) {
-    return stages_bytes + kTops * entry_stride(K) * (int)sizeof(Entry) + (int)sizeof(RingCtl<kTops>) + 16;
+template <typename F>
+using CtlOf = RingCtl<F::kTops, F::kWarps, F::kBufs>;
+
+template <typename F>
+__host__ __device__ constexpr int ring_smem(int K) {
+    return F::kBufs * F::kBytes + F::kTops * entry_stride(K) * (int)sizeof(Entry) + (int)sizeof(CtlOf<F>) + 16;
 }
 
 // make_row without its address, in 32-bit arithmetic: what the consumers need of a row, each warp by itself.
@@ -600,13 +609,13 @@ __device__ __forceinline__ Row row_extent(const Args& a, int64_t row) {
 }
 
 // make_slice in stages of the ring.
-template <bool kGrad>
+template <typename F>
 __device__ __forceinline__ Slice ring_slice(const Row& r, int parts, int part) {
     Slice s;
     const int per = (r.nv + parts - 1) >> (31 - __clz(parts));   // parts: a power of two
     s.v0 = min(r.nv, part * per);
     s.n = min(r.nv - s.v0, per);
-    s.nst = (s.n + Geom<kGrad>::kVecs - 1) / Geom<kGrad>::kVecs;
+    s.nst = (s.n + F::kVecs - 1) / F::kVecs;
     return s;
 }
 
@@ -677,7 +686,7 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity)
 }
 
 // This thread's vectors of stage j of the slice; -inf beyond its end.
-template <typename S, int U>
+template <typename S, int U, int kNT>
 __device__ __forceinline__ void ring_load(const uint8_t* buf8, const Slice& s, int j, int tid, uint4 (&x)[U]) {
     const uint4* buf = reinterpret_cast<const uint4*>(buf8) + tid;
     const int left = s.n - j * (U * kNT);
@@ -690,16 +699,18 @@ __device__ __forceinline__ void ring_load(const uint8_t* buf8, const Slice& s, i
     }
 }
 
-template <typename S, typename O, bool kGrad, int kTops>
-__global__ void __launch_bounds__(ring_threads(kTops), 1) k_distill_ring(const __grid_constant__ Args a) {
+template <typename S, typename O, bool kGrad, bool kBig>
+__global__ void __launch_bounds__(Form<kGrad, kBig>::kThreads, Form<kGrad, kBig>::kBlocks)
+    k_distill_ring(const __grid_constant__ Args a) {
     constexpr int G = Elt<S>::kGroup;
     extern __shared__ __align__(128) uint8_t smem[];
-    using Ge = Geom<kGrad>;
-    constexpr int nbuf = Ge::kBufs, U = Ge::kU, kRingVecs = Ge::kVecs, kRingBytes = Ge::kBytes;
+    using F = Form<kGrad, kBig>;
+    constexpr int nbuf = F::kBufs, U = F::kU, kRingVecs = F::kVecs, kRingBytes = F::kBytes;
+    constexpr int kWarps = F::kWarps, kNT = F::kNT, kTops = F::kTops, kTop = F::kTop, kProducer = F::kProducer;
+    constexpr int kPatch = F::kPatch, kStats = F::kStats, kRingThreads = F::kThreads;
     const int K = a.K, KS = entry_stride(a.K), C = a.cluster;
     Entry* entries = reinterpret_cast<Entry*>(smem + nbuf * kRingBytes);   // [kTops][KS]
-    constexpr int kRingThreads = ring_threads(kTops);
-    RingCtl<kTops>& ctl = *reinterpret_cast<RingCtl<kTops>*>((reinterpret_cast<uintptr_t>(entries + kTops * KS) + 15) / 16 * 16);
+    CtlOf<F>& ctl = *reinterpret_cast<CtlOf<F>*>((reinterpret_cast<uintptr_t>(entries + kTops * KS) + 15) / 16 * 16);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = C > 1 ? (int)cluster_rank() : 0;
     const int64_t cid = blockIdx.x / C, ncl = gridDim.x / C;
@@ -744,7 +755,7 @@ __global__ void __launch_bounds__(ring_threads(kTops), 1) k_distill_ring(const _
             if (row < 0 || *reinterpret_cast<volatile int*>(&ctl.abort)) break;
             if (lane == 0) {
                 const Row r = make_row<S>(a.logits, row, a.ld, a.V);
-                const Slice sl = ring_slice<kGrad>(r, C, rank);
+                const Slice sl = ring_slice<F>(r, C, rank);
                 for (int j = 0; j < sl.nst; ++j, ++q, at.step()) {
                     const int st = at.st;
                     if (!tc::mbar_wait(&ctl.empty[st], at.phase, &ctl.abort, &ctl.err, kErrEmpty)) break;
@@ -785,7 +796,7 @@ __global__ void __launch_bounds__(ring_threads(kTops), 1) k_distill_ring(const _
         for (bool ok = true; ok && next >= 0;) {
             const int64_t row = next;
             const Row r = make_row<S>(a.logits, row, a.ld, a.V);
-            const Slice sl = ring_slice<kGrad>(r, C, rank);
+            const Slice sl = ring_slice<F>(r, C, rank);
             // the entries' places among the slice's elements; anything else is in no stage
             uint32_t place[kPerLane];
 #pragma unroll
@@ -964,7 +975,7 @@ __global__ void __launch_bounds__(ring_threads(kTops), 1) k_distill_ring(const _
             __syncwarp();
             if (kGrad && !wait(&ctl.written[par], e, kErrCoefs)) break;
             const Row r = make_row<S>(a.logits, row, a.ld, a.V);
-            const Slice sl = ring_slice<kGrad>(r, C, rank);
+            const Slice sl = ring_slice<F>(r, C, rank);
             const float c = kGrad ? go : a.tau;
             for (int k = lane; k < K; k += 32) {
                 const Entry en = entries[(e % kTops) * KS + k];
@@ -990,7 +1001,7 @@ __global__ void __launch_bounds__(ring_threads(kTops), 1) k_distill_ring(const _
             for (int j = j0; j < j1; ++j, at.step()) {
                 tc::mbar_wait(&ctl.ready[at.st], at.phase, &ctl.abort, &ctl.err, kErrFull, tc::kWaitNs, kSuspend);
                 uint4 x[U];
-                ring_load<S, U>(smem + at.st * kRingBytes, sl, j, tid, x);
+                ring_load<S, U, kNT>(smem + at.st * kRingBytes, sl, j, tid, x);
                 if (!kGrad) {
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&ctl.empty[at.st]);
@@ -1019,7 +1030,7 @@ __global__ void __launch_bounds__(ring_threads(kTops), 1) k_distill_ring(const _
                 if (!kGrad) return;
                 const Row r = row_extent<S>(a, no);
                 O* g = static_cast<O*>(a.grad) + no * a.ld_g;
-                zero_grads<S, O>(r, ring_slice<kGrad>(r, C, rank), g, grads_aligned<S, O>(r, g), tid, kNT);
+                zero_grads<S, O>(r, ring_slice<F>(r, C, rank), g, grads_aligned<S, O>(r, g), tid, kNT);
             });
         };
         int64_t row = -1, row2 = next();                   // the row held, and the next one
@@ -1033,7 +1044,7 @@ __global__ void __launch_bounds__(ring_threads(kTops), 1) k_distill_ring(const _
             int pre = 0;
             if (row2 >= 0) {
                 r2 = row_extent<S>(a, row2);
-                sl2 = ring_slice<kGrad>(r2, C, rank);
+                sl2 = ring_slice<F>(r2, C, rank);
                 // the next row's stages that fit beside this one's (forward alone: all of them)
                 pre = kGrad ? min(sl2.nst, nbuf - sl.nst) : sl2.nst;
             }
@@ -1048,7 +1059,7 @@ __global__ void __launch_bounds__(ring_threads(kTops), 1) k_distill_ring(const _
                 const bool vec = grads_aligned<S, O>(r, grow);
                 for (int j = 0; j < sl.nst; ++j, back.step()) {
                     uint4 x[U];
-                    ring_load<S, U>(smem + back.st * kRingBytes, sl, j, tid, x);
+                    ring_load<S, U, kNT>(smem + back.st * kRingBytes, sl, j, tid, x);
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&ctl.empty[back.st]);
                     write_grads<S, O, U, kNT>(x, r, sl, j, tid, grow, vec, cf.coef, a.k2, cf.bias, cf.dead);
@@ -1216,14 +1227,13 @@ __global__ void __launch_bounds__(kReduceThreads) k_distill_reduce(const __grid_
 // ---- host ----------------------------------------------------------------------------------------------
 
 // The persistent kernel's blocks of a row; 0: rows too long to hold.
-template <bool kGrad>
+template <typename F, bool kGrad>
 int ring_cluster(int64_t T, int64_t V, int G, int sms) {
-    using Ge = ring::Geom<kGrad>;
     const int64_t nv = (V + 2 * G - 2) / G;
-    auto st = [&](int c) { return (int)(((nv + c - 1) / c + Ge::kVecs - 1) / Ge::kVecs); };
+    auto st = [&](int c) { return (int)(((nv + c - 1) / c + F::kVecs - 1) / F::kVecs); };
     int C = 1;
-    while (C < kMaxCluster && ((kGrad && st(C) > Ge::kHeld) || (T * C < sms && st(C) > 1))) C *= 2;
-    return kGrad && st(C) > Ge::kHeld ? 0 : C;
+    while (C < kMaxCluster && ((kGrad && st(C) > F::kHeld) || (T * C < sms && st(C) > 1))) C *= 2;
+    return kGrad && st(C) > F::kHeld ? 0 : C;
 }
 
 // In one pass with MEAN the row kernel starts while k_distill_count runs.
@@ -1232,14 +1242,16 @@ bool early_start(const Args& a) {
     return kGrad && a.red == VCE_RED_MEAN;
 }
 
-template <typename S, typename O, bool kGrad, int kTops>
+template <typename S, typename O, bool kGrad, bool kBig>
 cudaError_t run_ring(Args& a, int sms, cudaStream_t s) {
-    using Ge = ring::Geom<kGrad>;
-    constexpr auto kern = ring::k_distill_ring<S, O, kGrad, kTops>;
-    const int bytes = ring::ring_smem<kTops>(Ge::kBufs * Ge::kBytes, a.K), threads = ring::ring_threads(kTops);
-    const int64_t clusters = std::min<int64_t>(a.T, resident_clusters<kern>(a.cluster, threads, bytes, sms));
+    using F = ring::Form<kGrad, kBig>;
+    constexpr auto kern = ring::k_distill_ring<S, O, kGrad, kBig>;
+    a.cluster = ring_cluster<F, kGrad>(a.T, a.V, Elt<S>::kGroup, sms);
+    const int bytes = ring::ring_smem<F>(a.K);
+    const int64_t clusters = std::min<int64_t>(
+        a.T, resident_clusters<kern>(a.cluster, F::kThreads, bytes, sms * (a.cluster == 1 ? F::kBlocks : 1)));
     if (clusters < 1) return cudaErrorInvalidConfiguration;   // not one cluster of that size fits
-    return launch_clusters<kern>(clusters * a.cluster, a.cluster, threads, bytes, s, a, early_start<kGrad>(a));
+    return launch_clusters<kern>(clusters * a.cluster, a.cluster, F::kThreads, bytes, s, a, early_start<kGrad>(a));
 }
 
 template <typename S, typename O>
@@ -1254,12 +1266,11 @@ cudaError_t run_long(Args& a, cudaStream_t s) {
 
 template <typename S, typename O, bool kGrad>
 cudaError_t run(Args& a, int sms, cudaStream_t s) {
-    a.cluster = ring_cluster<kGrad>(a.T, a.V, Elt<S>::kGroup, sms);
     if constexpr (kGrad) {
-        if (a.cluster == 0) return run_long<S, O>(a, s);
+        if (ring_cluster<ring::Form<true, true>, true>(a.T, a.V, Elt<S>::kGroup, sms) == 0) return run_long<S, O>(a, s);
     }
-    return a.V * (int64_t)sizeof(S) >= ring::kLongRow ? run_ring<S, O, kGrad, 2>(a, sms, s)
-                                                      : run_ring<S, O, kGrad, 4>(a, sms, s);
+    return a.V * (int64_t)sizeof(S) >= ring::kLongRow ? run_ring<S, O, kGrad, true>(a, sms, s)
+                                                      : run_ring<S, O, kGrad, false>(a, sms, s);
 }
 
 template <typename S, typename O>
