@@ -132,7 +132,7 @@ VCE_API int ce_distill_forward_backward(const void* logits, vce_dtype dt, int64_
  *     y = (y + bias) / temperature
  *     out = y where the mask allows the column, -inf elsewhere
  * Each parameter may be NULL (none).  Masked logits have no effect, whatever they hold.
- *   logits, dt, T, V, ld         as ce_forward
+ *   logits, dt, T, V, ld         as ce_forward; V <= 2^28
  *   temperature, repetition, frequency, presence   [T] fp32
  *   history_ids, n_history       [n_history] int64: all rows' tokens, oldest first
  *   history_offsets              [T + 1] int64: row i's tokens are [offsets[i], offsets[i + 1])
@@ -147,8 +147,9 @@ VCE_API int ce_distill_forward_backward(const void* logits, vce_dtype dt, int64_
  *                                bias id outside [0, V), skipped, or bias ids not ascending);
  *                                VCE_ERR_PARAM (a temperature or repetition penalty that is not
  *                                finite and > 0, or a temperature without a finite reciprocal: it
- *                                counts as NaN); VCE_ERR_OFFSETS (the list counts
- *                                as empty).  A row with an error holds unspecified values.
+ *                                counts as NaN); VCE_ERR_OFFSETS (also a history of 2^30 tokens or
+ *                                more; the list counts as empty).  A row with an error holds
+ *                                unspecified values.
  */
 VCE_API int logits_process(const void* logits, vce_dtype dt, int64_t T, int64_t V, int64_t ld,
                            const float* temperature, const float* repetition, const float* frequency,

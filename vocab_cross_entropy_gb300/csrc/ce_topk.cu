@@ -18,6 +18,11 @@
 // Where the bound admits too many values (few columns per K, or many equal values), the K-th
 // largest value itself is found by the same search over all values, read from L2, and the values
 // equal to it are taken in column order.
+//
+// What bounds it: many rows (k_topk_rows) the stream, with the selection of a row beside the next
+// one's copies (8192 x 128256 bf16, K 64: 384 us, 5.5 TB/s, 0.81 of the measured copy); few rows (k_topk)
+// the chain of a launch: copies, maxima, search, read again, rank, merge (one row of 128256: 10.3 us;
+// 64 x 32001 fp32: 13.1 us, 0.6 TB/s).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
