@@ -23,9 +23,11 @@
 // scattered accesses a column, one of them to logits that nothing else reads (64 bytes of DRAM
 // each).  A stream that looked at the words beside its vectors took 190 us (most warps meet one of
 // the columns), a second kernel for the listed columns 151 us.  At 256 x 128256 bf16 with about
-// 3000 tokens a row: 43 us, 15 without the history; the tokens' loads wait up to 3 us each, behind the
-// streams of other blocks.  Sorting out a range's own tokens first, so that full warps count them, took 52
-// us there and 25 us instead of 14 at 37 x 32001 fp32 with 15000 tokens a row.
+// 3000 tokens a row: 40 us, 26 without the tokens; at 37 x 32001 fp32 with 15000: 11.3 us, 3.6 without
+// them.  What the tokens cost is their instructions (each of a row's blocks looks at all of them) and the
+// wait for them behind other blocks' streams.  Tried at these two shapes: a range's own tokens sorted out
+// first, so that full warps count them, 52 and 25 us; the tokens shared out among a cluster's blocks, which
+// count into one another's shared memory, 15.5 us at the second.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -44,7 +46,7 @@ constexpr int kThreads = 256, kLongThreads = 512;
 constexpr int kLong = 1024;                   // tokens a row, on average, from which a block has kLongThreads
 constexpr int kUnroll = 4;                    // 16-byte vectors a thread has in flight
 constexpr int kBlocksPerSm = 4;               // blocks wanted for each SM before rows are taken whole
-constexpr int kTokens = 4;                    // tokens a thread has in flight
+constexpr int kTokens = 4, kDenseTokens = 4;  // tokens a thread has in flight (hash table, a word a column)
 constexpr int kDense = 8192;                  // columns of a range, at most, that all have a word
 constexpr int kMinSlots = 1024, kMaxSlots = 16384;   // of a hash table (8 bytes each)
 constexpr int kList = 2048;                   // listed columns; beyond, all words are looked through
@@ -119,13 +121,16 @@ __device__ __forceinline__ float inv_temperature(const Args& a, int64_t row, int
     return __int_as_float(0x7FC00000);
 }
 
-// z * inv_t where allowed (bits ok), `masked` elsewhere.
-template <typename S>
+// z * inv_t where allowed (bits ok), `masked` elsewhere.  kWhole: vectors that the mask leaves whole, most
+// of those that are read, skip the selection (512 threads, 256 x 128256 bf16: 40.2 against 42.9 us; with 256
+// threads, the backward at 4096 x 32000: 109 against 104).
+template <typename S, bool kWhole>
 __device__ __forceinline__ void scale(uint4 x, uint32_t ok, float inv_t, float masked, float (&z)[Elt<S>::kGroup]) {
     constexpr int G = Elt<S>::kGroup;
     Elt<S>::unpack(x, z);
 #pragma unroll
     for (int k = 0; k < G; k += 2) fmul2(z[k], z[k + 1], inv_t, z[k], z[k + 1]);
+    if (kWhole && (ok & ((1u << G) - 1)) == (1u << G) - 1) return;
 #pragma unroll
     for (int k = 0; k < G; ++k) z[k] = ((ok >> k) & 1u) ? z[k] : masked;
 }
@@ -157,7 +162,7 @@ __device__ __forceinline__ void stream_batch(const Row& r, O* out0, const uint32
 #pragma unroll
             for (int k = 0; k < G; ++k) z[k] = masked;
         } else {
-            scale<S>(x[q], kMask ? ok[q] : 0xFFFFFFFFu, inv_t, masked, z);
+            scale<S, NT == kLongThreads>(x[q], kMask ? ok[q] : 0xFFFFFFFFu, inv_t, masked, z);
         }
         GroupStore<O, G>::run(out0 + (size_t)v * G, z);
     }
@@ -194,7 +199,7 @@ __device__ __forceinline__ void stream(const Args& a, const Row& r, const S* iro
             uint4 x = make_uint4(0, 0, 0, 0);
             if (ok) x = ld_stream16(r.base + (size_t)v * 16);
             float z[G];
-            scale<S>(x, ok, inv_t, a.masked, z);
+            scale<S, false>(x, ok, inv_t, a.masked, z);
 #pragma unroll
             for (int k = 0; k < G; ++k) Elt<O>::store1(out0 + (size_t)v * G + k, z[k]);
         }
@@ -300,7 +305,7 @@ __device__ __forceinline__ bool range(const Args& a, Ctl& ctl, uint32_t* words, 
     O* orow = static_cast<O*>(a.out) + row * a.ld_out;
     const uint32_t* mrow = a.mask ? a.mask + row * a.mask_ld : nullptr;
     // the columns [lo, hi) of the vectors [va, vb)
-    const int lo = max(0, va * G - r.shift), hi = min((int)a.V, vb * G - r.shift);
+    const int lo = max(0, va * G - r.shift), hi = max(lo, min((int)a.V, vb * G - r.shift));
     if (tid == 0) ctl.n = 0;
     if (kHash) {
 #pragma unroll 1
@@ -314,25 +319,41 @@ __device__ __forceinline__ bool range(const Args& a, Ctl& ctl, uint32_t* words, 
     }
     __syncthreads();
     // ---- count ----
-    // The tokens as (low, high) halves, kTokens of them in flight; one copy of the code that counts
-    // them, the ids moving up to it (unrolled, it outgrows the instruction cache).
-    const int n = ctl.tokens;
+    // The tokens as (low, high) halves, several of them in flight.  Of a hash table one copy of the code
+    // that counts them, the ids moving up to it (unrolled, it outgrows the instruction cache).
+    const int n = ctl.tokens, np = ctl.prompt;
     const uint2* ids = reinterpret_cast<const uint2*>(a.hist + ctl.h0);
+    const uint32_t ulo = (uint32_t)lo, width = (uint32_t)(hi - lo);
+    constexpr int kAhead = kHash ? kTokens : kDenseTokens;
+    bool bad = false;
 #pragma unroll 1
-    for (int i0 = tid; i0 < n; i0 += kTokens * NT) {
-        uint2 id[kTokens];
+    for (int i0 = tid; i0 < n; i0 += kAhead * NT) {
+        uint2 id[kAhead];
 #pragma unroll
-        for (int q = 0; q < kTokens; ++q) id[q] = i0 + q * NT < n ? ids[i0 + q * NT] : make_uint2(0, 0);
+        for (int q = 0; q < kAhead; ++q) id[q] = i0 + q * NT < n ? ids[i0 + q * NT] : make_uint2(ulo, 0);
+        if constexpr (kHash) {
 #pragma unroll 1
-        for (int i = i0, q = 0; q < kTokens && i < n; ++q, i += NT) {
-            const uint2 t = id[0];
+            for (int i = i0, q = 0; q < kAhead && i < n; ++q, i += NT) {
+                const uint2 t = id[0];
 #pragma unroll
-            for (int k = 1; k < kTokens; ++k) id[k - 1] = id[k];
-            if (t.y | (t.x >= (uint32_t)a.V)) ctl.code = VCE_ERR_LABEL;
-            else if (t.x - (uint32_t)lo < (uint32_t)(hi - lo))
-                count_one<NT, kHash>(a, ctl, words, cols, t.x - lo, i < ctl.prompt ? kPrompt : 0u);
+                for (int k = 1; k < kAhead; ++k) id[k - 1] = id[k];
+                if (t.y | (t.x >= (uint32_t)a.V)) bad = true;
+                else if (t.x - ulo < width) count_one<NT, kHash>(a, ctl, words, cols, t.x - ulo, i < np ? kPrompt : 0u);
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) {
+                const int i = i0 + q * NT;
+                const uint32_t c = id[q].x - ulo;
+                bad |= id[q].y != 0 || id[q].x >= (uint32_t)a.V;
+                if (c < width && id[q].y == 0) {
+                    if (i < np) atomicOr(words + c, kPrompt);
+                    else if (i < n) atomicAdd(words + c, 1u);
+                }
+            }
         }
     }
+    if (bad) ctl.code = VCE_ERR_LABEL;
     if (!kBack) {
 #pragma unroll 1
         for (int64_t i = ctl.b0 + tid; i < ctl.b1; i += NT) {
@@ -458,7 +479,7 @@ cudaError_t run(Args& a, int sms, cudaStream_t s) {
         while (a.slots < kMaxSlots && a.slots < 2 * (mean / a.parts)) a.slots *= 2;
     }
     // Long histories: more threads to count them (37 x 32001 fp32 with 15000 tokens a row: 13.6 against
-    // 19.3 us); short ones: more blocks an SM (4096 x 32000 bf16 backward with 384: 104 against 115 us).
+    // 19.5 us); short ones: more blocks an SM (4096 x 32000 bf16 backward with 384: 104 against 115 us).
     return mean >= kLong ? launch_lists<S, O, kLongThreads, kBack>(a, dense, s) : launch_lists<S, O, kThreads, kBack>(a, dense, s);
 }
 
