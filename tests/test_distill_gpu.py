@@ -262,6 +262,21 @@ def test_distill_bad_teachers(vce):
             G.check_distill_grad(g[others].double().cpu(), part, *good.sizes(), 2.0 ** -7)
 
 
+@pytest.mark.parametrize("T,V,K,dtype,pad,left", [
+    (700, 20000, 256, BF16, 0, 0),     # short rows of several stages, most entries
+    (650, 17001, 40, F32, 3, 1), (1300, 2500, 7, BF16, 1, 0),
+    (330, 70001, 100, BF16, 0, 0), (320, 40000, 200, F32, 2, 1)])   # rows of 128 KB and more
+def test_distill_several_rows_a_block(vce, T, V, K, dtype, pad, left):
+    c = Case(T, V, K, dtype, 2.0, True, pad=pad, left=left)
+    c.labels = torch.arange(T, device="cuda") % 50 + 1
+    c.labels[::7] = -100
+    c.labels[40:80] = -100             # more ignored rows in a row than a warp looks ahead
+    c.ids[5::11, K // 2:] = -1
+    c.ids[3::13] = -1
+    check(vce, c)
+    check(vce, c, "none", BF16 if dtype is F32 else F32)
+
+
 @pytest.mark.parametrize("V,dtype", [(900001, BF16), (450000, F32)])
 def test_distill_rows_longer_than_shared_memory(vce, V, dtype):
     check(vce, Case(3, V, 40, dtype, 1.0, True))
