@@ -6,6 +6,10 @@ lie on the logits' device; outputs that the caller does not pass are allocated o
 the call runs on (``stream``, default the device's current stream), which becomes their stream.
 Shape, type and device errors raise ValueError or TypeError before anything is enqueued; the
 library's own refusals raise VceError.
+
+The calls may be captured into CUDA graphs.  Of the two autograd functions, forward and backward
+are captured together, and no graph of the same leaves built outside the capture may still be alive
+then (PyTorch ties a leaf's gradient to the stream that first used it).
 """
 from __future__ import annotations
 
