@@ -340,6 +340,31 @@ def test_distill_streams_and_graphs(vce):
     assert torch.equal(grad, vce.ce_distill_backward(d.z, d.ids, fresh[2], fresh[3], up))
 
 
+def test_distill_autograd_in_a_graph(vce):
+    """Forward and backward captured together, replayed with new contents."""
+    c, d = Case(9, 3001, 7, BF16, 2.0, True), Case(9, 3001, 7, BF16, 2.0, True, seed=9)
+    z = c.z.clone().requires_grad_(True)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        vce.distill_cross_entropy(z, *c.teacher()).backward()
+    torch.cuda.current_stream().wait_stream(side)
+    z.grad = None
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        loss = vce.distill_cross_entropy(z, *c.teacher())
+        loss.backward()
+    with torch.no_grad():
+        z.copy_(d.z)
+    for name in ("ids", "values", "tail"):
+        getattr(c, name).copy_(getattr(d, name))
+    graph.replay()
+    fresh = d.z.clone().requires_grad_(True)
+    want = vce.distill_cross_entropy(fresh, *d.teacher())
+    want.backward()
+    assert torch.equal(loss, want) and torch.equal(z.grad, fresh.grad)
+
+
 def test_distill_refusals(vce):
     c = Case(4, 100, 5)
     go = torch.ones(1, device="cuda")
