@@ -196,3 +196,24 @@ def test_topk_refusals(vce):
         vce.ce_topk(z, 5, values=torch.empty(4, 6, device="cuda"))
     out = vce.ce_topk(z[:0], 5)
     assert [tuple(x.shape) for x in out] == [(0, 5), (0, 5), (0,), (0,)]
+
+
+@pytest.mark.parametrize("V,pad", [(2097150, 0), (2097151, 0), (2097152, 1)])
+def test_topk_the_longest_fp32_rows(vce, V, pad):
+    """Unaligned rows of the most columns have one vector more than eight times 64 stages: the largest
+    logits in the last vector of each block's slice, and everywhere else."""
+    T = 4
+    z = logits_of(T, V, torch.float32, V, pad)
+    for i in range(T):
+        shift = z[i].data_ptr() % 16 // 4
+        vectors = (V + shift + 3) // 4
+        per = -(-vectors // 8)                      # vectors of a slice
+        for p in range(8):
+            last = min((p + 1) * per, vectors) - 1
+            for q in range(4):
+                c = last * 4 - shift + q
+                if 0 <= c < V:
+                    z[i, c] = 12.0 + (p * 5 + i) % 8 + q / 8
+    check(vce, z, 1)
+    check(vce, z, 20)
+    check(vce, z, 256, 2.0)

@@ -284,7 +284,7 @@ __device__ __forceinline__ void select(const Args& a, const Row& r, const Slice&
     static_assert(GT % NS == 0, "whole rounds of groups");
     constexpr int SP = kSets / NS;             // sets of a thread
     const int tid = team.tid, lane = team.lane(), warp = team.warp();
-    const int K = a.K, rounds = stages * (GT / NS), groups = stages * GT;   // rounds <= 64
+    const int K = a.K, rounds = stages * (GT / NS), groups = stages * GT;
     uint64_t* cand = reinterpret_cast<uint64_t*>(scratch + kCandAt);
     uint64_t* list = reinterpret_cast<uint64_t*>(scratch + kListAt);
     int* sel = reinterpret_cast<int*>(scratch + kSelAt);
@@ -344,12 +344,15 @@ __device__ __forceinline__ void select(const Args& a, const Row& r, const Slice&
     team.sync();
     const float t = ctl.bound;
     // ---- 2. candidates ----
-    // the groups with a value >= t: a place on the list for each lane's, one atomic a warp
-    {
-        uint64_t mine = 0;                     // bit i: group tid + i NS
+    // the groups with a value >= t: a place on the list for each lane's, one atomic a warp (and for each 64
+    // rounds: a slice of the longest fp32 rows has 65)
+#pragma unroll 1
+    for (int i0 = 0; i0 < rounds; i0 += 64) {
+        uint64_t mine = 0;                     // bit i: group tid + (i0 + i) NS
         if (most_mine >= t) {
+            const int n = min(64, rounds - i0);
 #pragma unroll 4
-            for (int i = 0; i < rounds; ++i) mine |= (uint64_t)(gm[i * NS + tid] >= t) << i;
+            for (int i = 0; i < n; ++i) mine |= (uint64_t)(gm[(i0 + i) * NS + tid] >= t) << i;
         }
         const int n = __popcll(mine);
         int at = n;
@@ -362,7 +365,7 @@ __device__ __forceinline__ void select(const Args& a, const Row& r, const Slice&
         if (lane == 31 && at) base = atomicAdd(&ctl.nsel, at);
         at += __shfl_sync(0xFFFFFFFFu, base, 31) - n;
         for (; mine; mine &= mine - 1, ++at)
-            if (at < kMaxSel) sel[at] = tid + (__ffsll((long long)mine) - 1) * NS;
+            if (at < kMaxSel) sel[at] = tid + (i0 + __ffsll((long long)mine) - 1) * NS;
     }
     team.sync();
     const int nsel = ctl.nsel;
