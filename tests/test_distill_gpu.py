@@ -386,3 +386,37 @@ def test_distill_refusals(vce):
         vce.ce_distill_forward(c.z, c.ids.cpu(), c.values)
     out = vce.ce_distill_forward_backward(c.z[:0], c.ids[:0], c.values[:0], reduction="sum")
     assert out[0].item() == 0 and out[2].shape == (0, 100) and vce.vce_get_status(out[3]) == 0
+
+
+@pytest.mark.parametrize("V,dtype", [(600, F32), (20000, BF16), (70001, BF16), (900001, BF16), (450000, F32)])
+@pytest.mark.parametrize("tail", [True, False])
+def test_distill_nan_and_infinite_students(vce, V, dtype, tail):
+    """NaN or +inf among a student's logits, in the tail or on an entry, alone among -inf too: the row's
+    loss and its whole gradient are NaN, whatever kernel takes it, and the other rows are as they were."""
+    nan, inf = float("nan"), float("inf")
+    c = Case(8, V, 5, dtype, 1.0, tail)
+    ref = c.oracle("sum")
+    free = [next(j for j in range(V // 2 + 7, V) if j not in c.ids[i].tolist()) for i in range(8)]
+    c.z[1, free[1]] = nan
+    c.z[2, c.ids[2, 3]] = nan
+    c.z[3, free[3]] = inf
+    c.z[4, c.ids[4, 0]] = inf
+    keep = c.z[5, c.ids[5]].clone()
+    c.z[5] = -inf                                   # NaN, and nothing else, in the tail
+    c.z[5, c.ids[5]] = keep
+    c.z[5, free[5]] = nan
+    c.z[6, c.ids[6]] = nan                          # every entry
+    bad, good = [1, 2, 3, 4, 5, 6], [0, 7]
+    up = torch.ones(1, device="cuda")
+    loss, rows, stats, tops, status = vce.ce_distill_forward(c.z, *c.teacher(), reduction="sum")
+    g2 = vce.ce_distill_backward(c.z, c.ids, stats, tops, up, c.tau, "sum")
+    l1, r1, g1, s1 = vce.ce_distill_forward_backward(c.z, *c.teacher(), reduction="sum", grad_output=up)
+    size = (float(c.z[good].float().abs().max()), *c.sizes()[1:])
+    part = {k: (v[good] if isinstance(v, np.ndarray) and v.ndim else v) for k, v in ref.items()}
+    for l, r, g, s in ((loss, rows, g2, status), (l1, r1, g1, s1)):
+        assert vce.vce_get_status(s) == 0 and torch.isnan(l).all()
+        assert torch.isnan(r).nonzero().flatten().tolist() == bad
+        assert torch.isnan(g[bad]).all()
+        G.check_distill_loss(r[good].cpu(), part, *size)
+        G.check_distill_grad(g[good].double().cpu(), part, *size, 2.0 ** -7 if dtype is BF16 else 2.0 ** -23)
+    assert torch.isnan(tops[bad]).all() and not torch.isnan(tops[good]).any()

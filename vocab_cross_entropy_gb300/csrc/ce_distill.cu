@@ -228,7 +228,7 @@ __device__ __forceinline__ Top top_arithmetic(const Args& a, int K, int lane, co
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) {
         if (32 * i >= K) break;
-        if (z[i] > -kInf) rs_ += exp2f((z[i] - zm) * a.k2);   // as the tail's terms
+        if (z[i] != -kInf) rs_ += exp2f((z[i] - zm) * a.k2);   // as the tail's terms; NaN and +inf: NaN
         if (col[i] >= 0 && t[i] != -kInf) qs += expf((t[i] - tm) * a.scale);   // NaN: the row is refused
     }
     rs_ = warp_sum(rs_);
@@ -283,6 +283,7 @@ __device__ __forceinline__ Finish finish_row(const Args& a, float M, float S0, c
     // no finite teacher mass (comparisons that a NaN fails)
     if (!code && !((t.tsum > 0.f || R > -kInf) && t.tsum < kInf && R < kInf)) f.code = VCE_ERR_TEACHER;
     const bool has_tail = S0 > 0.f, has_top = t.zmax > -kInf;
+    bool lost = false;                               // a NaN or +inf among the student's logits: NaN throughout
     float lo;
     const float gap = minus_product(M, t.zmax, a.k2, lo);
     // expf for this one factor, not the base-2 exponential: that one's error has a mean of 5e-8, which the
@@ -302,10 +303,12 @@ __device__ __forceinline__ Finish finish_row(const Args& a, float M, float S0, c
         f.at = t.tsum > 0.f ? (t.tmax * a.scale - R) + logf(t.tsum) : -kInf;   // R = -inf: +inf
         f.q = sigmoid(f.at);
         f.d = sigmoid_diff(-f.b, -f.at);             // p_T - q_T
+        lost = !(S0 + t.zsum >= 0.f);                // then ws is no ratio within range either
     }
-    f.dead = f.code || !(has_tail || has_top);
+    f.dead = f.code || !(has_tail || has_top || lost);
     f.bias = has_tail ? M + log2f(S0) : 0.f;         // of the tail's gradient: 2^(z k2 - bias); no tail: any
     f.lt = has_tail ? f.bias * kLn2 : -kInf;
+    if (lost) f.q = f.d = f.lt = __int_as_float(0x7FC00000);
     return f;
 }
 
@@ -329,7 +332,7 @@ __device__ __forceinline__ float loss_of(const Args& a, const Finish& f, float k
     }
     float kl = q_phi(f.q, P, x1) + q_phi(qT, pT, x2);
     if (f.q > 0.f) kl += f.q * kl_top;
-    return f.dead ? __int_as_float(0x7FC00000) : a.tau * a.tau * kl;
+    return f.dead || f.q != f.q ? __int_as_float(0x7FC00000) : a.tau * a.tau * kl;
 }
 
 // ---- one pass over rows longer than shared memory ----------------------------------------------------

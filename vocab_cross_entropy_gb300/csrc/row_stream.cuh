@@ -231,19 +231,21 @@ __device__ __forceinline__ float sum_exp(const float (&v)[U][G], float k2, float
     return e[0] + e[1];
 }
 
+// The largest value; NaN if there is one (which fmaxf would pass over).
 template <int G, int U>
 __device__ __forceinline__ float max_of(const float (&v)[U][G]) {
     float m = v[0][0];
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int k = 0; k < G; ++k) m = fmaxf(m, v[u][k]);
+        for (int k = 0; k < G; ++k)
+            if (u || k) asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(m), "f"(v[u][k]));
     return m;
 }
 
 // Adds a stage's values to a pair whose reference moves only when a term would pass 2^32 (it is then one
 // of the values', so s is about 1 or more and nothing overflows).  Values whose product with k2 passes
-// fp32 (masks of the type's lowest value) count as -inf.
+// fp32 (masks of the type's lowest value) count as -inf.  A NaN or +inf makes s NaN.
 template <int G, int U>
 __device__ __forceinline__ void pair_push(const float (&v)[U][G], float& m, float& s, float k2) {
     if (m == -kInf) {
