@@ -85,8 +85,9 @@ VCE_API int ce_topk(const void* logits, vce_dtype dt, int64_t T, int64_t V, int6
  *   top_grads              [T, K] fp32: tau (p_k - q_k), 0 where there is no entry
  *   status                 [1] int32: 0, VCE_ERR_TEACHER, or 106 when a bounded device-side wait
  *                          gave up.  A row with an error has a NaN loss and no gradient.
- * A student row of -inf only has a NaN loss and no gradient; an entry with q_k > 0 on a logit of
- * -inf makes the loss +inf.  A NaN or +inf among a student's logits makes its loss and its whole
+ * A student row of nothing but masks (-inf, or logits whose product with log2(e) / temperature passes
+ * fp32, as the type's lowest value does) has a NaN loss and no gradient; an entry with q_k > 0 on a
+ * logit of -inf makes the loss +inf.  A NaN or +inf among a student's logits makes its loss and its whole
  * gradient NaN (not the status).
  */
 VCE_API int ce_distill_forward(const void* logits, vce_dtype dt, int64_t T, int64_t V, int64_t ld,

@@ -420,3 +420,31 @@ def test_distill_nan_and_infinite_students(vce, V, dtype, tail):
         G.check_distill_loss(r[good].cpu(), part, *size)
         G.check_distill_grad(g[good].double().cpu(), part, *size, 2.0 ** -7 if dtype is BF16 else 2.0 ** -23)
     assert torch.isnan(tops[bad]).all() and not torch.isnan(tops[good]).any()
+
+
+@pytest.mark.parametrize("V,dtype", [(300, F32), (20000, BF16), (70001, F32), (900001, BF16), (450000, F32)])
+@pytest.mark.parametrize("tail", [True, False])
+def test_distill_students_of_the_lowest_value(vce, V, dtype, tail):
+    """A student row whose mask (the type's lowest value) leaves nothing is a row of nothing else, as one
+    of -inf: NaN loss, no gradient.  Such masks beside open columns carry no mass."""
+    low = torch.finfo(dtype).min
+    c = Case(4, V, 4, dtype, 1.0, tail)
+    c.z[1] = low
+    c.z[2, ::2] = low
+    c.z[2, c.ids[2]] = 1.0
+    clean = c.z.clone()
+    c.z[1] = 0.0
+    c.z[2] = torch.where(c.z[2] == low, -float("inf"), c.z[2])
+    ref, size = c.oracle("sum"), c.sizes()
+    c.z.copy_(clean)
+    good = [0, 2, 3]
+    part = {k: (v[good] if isinstance(v, np.ndarray) and v.ndim else v) for k, v in ref.items()}
+    up = torch.ones(1, device="cuda")
+    loss, rows, stats, tops, status = vce.ce_distill_forward(c.z, *c.teacher(), reduction="sum")
+    g2 = vce.ce_distill_backward(c.z, c.ids, stats, tops, up, c.tau, "sum")
+    l1, r1, g1, s1 = vce.ce_distill_forward_backward(c.z, *c.teacher(), reduction="sum", grad_output=up)
+    for r, g, s in ((rows, g2, status), (r1, g1, s1)):
+        assert vce.vce_get_status(s) == 0
+        assert torch.isnan(r).nonzero().flatten().tolist() == [1] and torch.all(g[1] == 0)
+        G.check_distill_loss(r[good].cpu(), part, *size)
+        G.check_distill_grad(g[good].double().cpu(), part, *size, 2.0 ** -7 if dtype is BF16 else 2.0 ** -23)

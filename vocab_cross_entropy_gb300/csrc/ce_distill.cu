@@ -272,7 +272,7 @@ struct Finish {
     float ws, wt;
     int code;                    // the row's error
     bool ratios;                 // ws and wt are within range: else the logarithms at and b are used
-    bool dead;                   // no gradient (an error, or a student row of -inf only)
+    bool dead;                   // no gradient (an error, or a student row of masks only)
     float at, b;
 };
 
@@ -282,7 +282,8 @@ __device__ __forceinline__ Finish finish_row(const Args& a, float M, float S0, c
     f.code = code;
     // no finite teacher mass (comparisons that a NaN fails)
     if (!code && !((t.tsum > 0.f || R > -kInf) && t.tsum < kInf && R < kInf)) f.code = VCE_ERR_TEACHER;
-    const bool has_tail = S0 > 0.f, has_top = t.zmax > -kInf;
+    // entries whose product with k2 passes fp32 hold nothing, as in the tail's pairs
+    const bool has_tail = S0 > 0.f, has_top = t.zmax * a.k2 > -kInf;
     bool lost = false;                               // a NaN or +inf among the student's logits: NaN throughout
     float lo;
     const float gap = minus_product(M, t.zmax, a.k2, lo);
