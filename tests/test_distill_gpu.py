@@ -448,3 +448,27 @@ def test_distill_students_of_the_lowest_value(vce, V, dtype, tail):
         assert torch.isnan(r).nonzero().flatten().tolist() == [1] and torch.all(g[1] == 0)
         G.check_distill_loss(r[good].cpu(), part, *size)
         G.check_distill_grad(g[good].double().cpu(), part, *size, 2.0 ** -7 if dtype is BF16 else 2.0 ** -23)
+
+
+@pytest.mark.parametrize("T", [1, 2, 9])
+@pytest.mark.parametrize("V,dtype", [(900001, BF16), (450000, F32)])
+def test_distill_long_rows_that_are_all_ignored_or_refused(vce, V, dtype, T):
+    """MEAN over rows longer than shared memory none of which has a gradient: NaN whatever ran when, not
+    the count's 1 / N, which uses the same word before."""
+    g = torch.Generator().manual_seed(V + T)
+    z = torch.randn(T, V, generator=g).to(dtype).cuda()
+    ids = torch.randint(0, V // 2, (T, 3), generator=g).cuda()
+    ids[:, 1] = ids[:, 0] + V // 4
+    values = torch.randn(T, 3, generator=g).cuda()
+    grad = torch.empty_like(z)
+    loss = torch.empty(1, device="cuda")
+    for first, status in ((-1, 0), (V, 2)):
+        bad = ids.clone()
+        bad[:, 0] = first
+        for _ in range(20):
+            loss.fill_(5.0)
+            grad.fill_(5.0)
+            out = vce.ce_distill_forward_backward(z, bad, values, loss_out=loss, grad_logits=grad)
+            assert torch.isnan(loss).all() and vce.vce_get_status(out[3]) == status
+            assert torch.all(grad == 0)
+            assert torch.all(out[1] == 0) if first == -1 else torch.isnan(out[1]).all()

@@ -367,6 +367,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_distill_long(const __grid_const
             a.row_stats[row] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
         zero_grads<S, O>(r, sl, grow, vec, tid, kThreads);
+        if (a.red == VCE_RED_MEAN) wait_previous();
         return;
     }
 
@@ -484,10 +485,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_distill_long(const __grid_const
         // weight: 1, negative for a row with an error, until the reduction writes it
         a.row_stats[row] = make_float4(f.lt, dead ? 0.f : f.d, 0.f, f.code ? -(float)f.code : 1.f);
     }
-    if (dead) {
-        zero_grads<S, O>(r, sl, grow, vec, tid, kThreads);
-    } else {
-        if (a.red == VCE_RED_MEAN) wait_previous();   // k_distill_count
+    if (dead) zero_grads<S, O>(r, sl, grow, vec, tid, kThreads);
+    // k_distill_count: every block, with a gradient or without one, since the reduction waits for this kernel
+    // alone and writes the word that the count does
+    if (a.red == VCE_RED_MEAN) wait_previous();
+    if (!dead) {
         const float c = a.go[a.red == VCE_RED_NONE ? row : 0] * (a.red == VCE_RED_MEAN ? *a.inv_n : 1.f) * a.tau;
         if (warp < kConsumerWarps) {
             const float coef = c * f.d, bias = f.bias;
