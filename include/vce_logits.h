@@ -49,7 +49,8 @@ enum {
  *   K                     1 .. min(V, VCE_MAX_TOPK)
  *   temperature           finite, > 0, with a finite reciprocal
  *   values [T, K] fp32, ids [T, K] int64, lse [T] fp32, tail_lse [T] fp32, written
- * A device-side wait that gives up after 2 s makes the row's outputs NaN (ids -1).
+ * A device-side wait that gives up after 2 s makes the outputs of the rows it may have touched NaN
+ * (ids -1).
  */
 VCE_API int ce_topk(const void* logits, vce_dtype dt, int64_t T, int64_t V, int64_t ld, int K,
                     float temperature, float* values, int64_t* ids, float* lse, float* tail_lse,
@@ -83,8 +84,9 @@ VCE_API int ce_topk(const void* logits, vce_dtype dt, int64_t T, int64_t V, int6
  *   row_stats              [T * VCE_ROW_STATS] fp32, 16-byte aligned; per row (log-sum-exp of the
  *                          other columns' z / tau, p_T - q_T, 0, weight), weight as ce_forward's
  *   top_grads              [T, K] fp32: tau (p_k - q_k), 0 where there is no entry
- *   status                 [1] int32: 0, VCE_ERR_TEACHER, or 106 when a bounded device-side wait
- *                          gave up.  A row with an error has a NaN loss and no gradient.
+ *   status                 [1] int32: 0, VCE_ERR_TEACHER, or 105 .. 109 when a bounded device-side
+ *                          wait gave up (the largest of the rows' codes).  A row with an error has a
+ *                          NaN loss and no gradient (the one pass's of 105 .. 109: unspecified).
  * A student row of nothing but masks (-inf, or logits whose product with log2(e) / temperature passes
  * fp32, as the type's lowest value does) has a NaN loss and no gradient; an entry with q_k > 0 on a
  * logit of -inf makes the loss +inf.  A NaN or +inf among a student's logits makes its loss and its whole
@@ -104,7 +106,8 @@ VCE_API int ce_distill_forward(const void* logits, vce_dtype dt, int64_t T, int6
  * with c_i as in ce_backward.  Ignored rows are written as +0.0 and their logits are not read.
  *   logits .. temperature: as given to the forward;  row_stats, top_grads: from it
  *   grad_output  fp32 [1] (SUM, MEAN) or [T] (NONE);  grad_logits [T, ld_grad] of dtype grad_dt,
- *                written; VCE_ERR_ARG if it overlaps the logits
+ *                written; VCE_ERR_ARG if it overlaps the logits.  Columns behind a device-side wait
+ *                that gave up after 2 s hold NaN.
  */
 VCE_API int ce_distill_backward(const void* logits, vce_dtype dt, int64_t T, int64_t V, int64_t ld,
                                 const int64_t* teacher_ids, int K, float temperature, vce_reduction red,
@@ -177,6 +180,26 @@ VCE_API int logits_process_backward(const void* grad_out, vce_dtype gdt, int64_t
                                     const int64_t* history_offsets, const int32_t* mask, int64_t mask_ld,
                                     void* grad_logits, vce_dtype grad_dt, int64_t ld_grad,
                                     int32_t* row_status, vce_stream_t s);
+
+/*
+ * Test hooks for the paths of waits that give up, every wait bounded by wait_ns (1 ms .. 2 s), bf16
+ * logits and gradients (ld = V), temperature 1, reduction SUM, no tail, no labels.  The kernels return,
+ * with their copies landed, and the context stays usable.
+ *   vce_test_topk_stall         ce_topk with the last stage of every slice never copied
+ *   vce_test_distill_stall      ce_distill_forward_backward where the last block of every cluster never
+ *                               gets what its gradient waits for (its coefficients; in rows longer than
+ *                               shared memory the last stage), after the statistics have been exchanged
+ *   vce_test_distill_bwd_stall  ce_distill_backward where a row's last block never gets its last stage
+ */
+VCE_API int vce_test_topk_stall(const void* logits, int64_t T, int64_t V, int K, float* values, int64_t* ids,
+                                float* lse, float* tail_lse, uint64_t wait_ns, vce_stream_t s);
+VCE_API int vce_test_distill_stall(const void* logits, int64_t T, int64_t V, const int64_t* teacher_ids,
+                                   const float* teacher_values, int K, const float* grad_output, float* loss_rows,
+                                   float* loss_out, float* row_stats, void* grad_logits, uint64_t wait_ns,
+                                   int32_t* status, vce_stream_t s);
+VCE_API int vce_test_distill_bwd_stall(const void* logits, int64_t T, int64_t V, const int64_t* teacher_ids, int K,
+                                       const float* row_stats, const float* top_grads, const float* grad_output,
+                                       void* grad_logits, uint64_t wait_ns, vce_stream_t s);
 
 #ifdef __cplusplus
 }

@@ -472,3 +472,32 @@ def test_distill_long_rows_that_are_all_ignored_or_refused(vce, V, dtype, T):
             assert torch.isnan(loss).all() and vce.vce_get_status(out[3]) == status
             assert torch.all(grad == 0)
             assert torch.all(out[1] == 0) if first == -1 else torch.isnan(out[1]).all()
+
+
+@pytest.mark.parametrize("T,V", [(3, 70000), (2, 20000), (400, 9000), (2, 900000)])
+def test_distill_waits_that_give_up_are_reported(vce, T, V):
+    """The last block of every cluster waits in vain for what its gradient needs, once the statistics
+    have been exchanged and the first block has its losses: a status, NaN losses, and a context that
+    stays usable."""
+    c = Case(T, V, 5, BF16, 1.0, False)
+    z = c.z.contiguous()
+    loss, rows, _, status = vce.vce_test_distill_stall(z, c.ids, c.values)
+    code = vce.vce_get_status(status)
+    assert 105 <= code <= 109 and "gave up" in vce.vce_status_string(code)
+    assert torch.isnan(rows).all() and torch.isnan(loss).all()
+    check(vce, c, "sum")
+
+
+@pytest.mark.parametrize("T,V", [(3, 20000), (5, 100000)])
+def test_distill_backward_waits_that_give_up_leave_nan(vce, T, V):
+    c = Case(T, V, 5, BF16, 1.0, False)
+    z = c.z.contiguous()
+    _, _, stats, tops, _ = vce.ce_distill_forward(z, *c.teacher(), reduction="sum")
+    want = vce.ce_distill_backward(z, c.ids, stats, tops, torch.ones(1, device="cuda"), 1.0, "sum")
+    got = vce.vce_test_distill_bwd_stall(z, c.ids, stats, tops)
+    vectors = V // 8                                  # both are multiples of 8: rows of whole vectors
+    parts = -(-vectors // 4096)
+    last = -(-vectors // parts) * (parts - 1) * 8     # the first column of the last block
+    assert torch.isnan(got[:, last:]).all() and torch.equal(got[:, :last], want[:, :last])
+    again = vce.ce_distill_backward(z, c.ids, stats, tops, torch.ones(1, device="cuda"), 1.0, "sum")
+    assert torch.equal(again, want)

@@ -157,3 +157,14 @@ def test_exported(vce):
                  "distill_cross_entropy", "logits_process", "logits_process_backward", "process_logits"):
         assert name in vce.__all__ and inspect.getdoc(getattr(vce, name))
     assert ctypes.sizeof(ctypes.c_void_p) == 8
+
+
+def test_refusals_of_the_give_up_hooks(vce):
+    x, lib = 0x1000, vce.lib
+    topk = lambda ns=50_000_000, V=64: lib.vce_test_topk_stall(x, 4, V, 8, x, x, x, x, ns, None)
+    assert topk(ns=999_999) == -8 and topk(ns=2_000_000_001) == -8 and topk(V=0) == -3
+    one = lambda ns=50_000_000, status=x: lib.vce_test_distill_stall(x, 4, 64, x, x, 8, x, x, x, x, 0x900000, ns, status,
+                                                                     None)
+    assert one(ns=999_999) == -8 and one(ns=2_000_000_001) == -8 and one(status=None) == -1
+    bwd = lambda ns=50_000_000, go=x: lib.vce_test_distill_bwd_stall(x, 4, 64, x, 8, x, x, go, 0x900000, ns, None)
+    assert bwd(ns=999_999) == -8 and bwd(ns=2_000_000_001) == -8 and bwd(go=None) == -1

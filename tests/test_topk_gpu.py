@@ -217,3 +217,13 @@ def test_topk_the_longest_fp32_rows(vce, V, pad):
     check(vce, z, 1)
     check(vce, z, 20)
     check(vce, z, 256, 2.0)
+
+
+@pytest.mark.parametrize("T,V", [(3, 50001), (40, 5000), (330, 20000)])
+def test_topk_waits_that_give_up_leave_nan(vce, T, V):
+    """Slices whose last stage is never copied: NaN and -1 in every output, and a context that stays
+    usable."""
+    z = logits_of(T, V, torch.bfloat16, T + V).contiguous()
+    values, ids, lse, tail = vce.vce_test_topk_stall(z, 9)
+    assert torch.isnan(values).all() and torch.all(ids == -1) and torch.isnan(lse).all() and torch.isnan(tail).all()
+    check(vce, z[:3], 9)

@@ -106,12 +106,17 @@ def _load(path=None):
                                  p]
     L.logits_process_backward.argtypes = [p, i32, i64, i64, i64, p, i32, i64, p, p, p, i64, p, p, i64, p, i32, i64, p,
                                           p]
+    if hasattr(L, "vce_test_topk_stall"):
+        u64 = ctypes.c_uint64
+        L.vce_test_topk_stall.argtypes = [p, i64, i64, i32, p, p, p, p, u64, p]
+        L.vce_test_distill_stall.argtypes = [p, i64, i64, p, p, i32, p, p, p, p, p, u64, p, p]
+        L.vce_test_distill_bwd_stall.argtypes = [p, i64, i64, p, i32, p, p, p, p, u64, p]
     for name in ("ce_topk", "ce_distill_forward", "ce_distill_backward", "ce_distill_forward_backward",
                  "logits_process", "logits_process_backward", "ce_forward", "ce_backward", "ce_forward_ls", "ce_backward_ls", "ce_forward_backward",
                  "ce_forward_backward_ls", "ce_merge_chunks_ls",
                  "ce_merge_chunks", "ce_merge_chunks_noalloc",
                  "linear_ce_fwd_bwd", "linear_ce_fwd_bwd_filtered", "linear_ce_fwd_bwd_timed",
-                 "vce_get_status"):
+                 "vce_get_status", "vce_test_topk_stall", "vce_test_distill_stall", "vce_test_distill_bwd_stall"):
         if hasattr(L, name):
             getattr(L, name).restype = i32
     return L
@@ -563,4 +568,5 @@ def cross_entropy(logits, labels, ignore_index=IGNORE_INDEX, reduction="mean", l
 
 
 from .logits_ops import (MAX_TOPK, ce_distill_backward, ce_distill_forward, ce_distill_forward_backward,  # noqa: E402
-                         ce_topk, distill_cross_entropy, logits_process, logits_process_backward, process_logits)
+                         ce_topk, distill_cross_entropy, logits_process, logits_process_backward, process_logits,
+                         vce_test_distill_bwd_stall, vce_test_distill_stall, vce_test_topk_stall)

@@ -67,6 +67,8 @@ struct Args {
     int64_t ld_g;
     int cluster;
     int nbuf, max_stages;        // k_distill_long
+    uint64_t wait_ns;            // bound of every wait
+    int withhold;                // n > 0 (test hook): in a cluster's block n - 1 the gradient waits in vain
 };
 
 // Of a row's entries: the largest logits z, t of the student and the teacher, the sums of e^{s (z - max)}
@@ -179,18 +181,21 @@ __device__ __forceinline__ void write_grads(const uint4 (&x)[U], const Row& r, c
     }
 }
 
-// +0.0 over the slice's columns, by NT threads.
+// One value (+0.0 for a row without a gradient) over the slice's columns, by NT threads.
 template <typename S, typename O>
-__device__ __forceinline__ void zero_grads(const Row& r, const Slice& s, O* grow, bool vec, int tid, int NT) {
+__device__ __forceinline__ void fill_grads(const Row& r, const Slice& s, O* grow, bool vec, int tid, int NT,
+                                           float value = 0.f) {
     constexpr int G = Elt<S>::kGroup;
-    const float zero[G] = {};
+    float same[G];
+#pragma unroll
+    for (int k = 0; k < G; ++k) same[k] = value;
     for (int v = s.v0 + tid; v < s.v0 + s.n; v += NT) {
         const int64_t c0 = (int64_t)v * G - r.shift;
         if (vec && v >= r.iv0 && v < r.iv1) {
-            GroupStore<O, G>::run(grow + c0, zero);
+            GroupStore<O, G>::run(grow + c0, same);
         } else {
             for (int k = 0; k < G; ++k)
-                if (c0 + k >= 0 && c0 + k < r.V) Elt<O>::store1(grow + c0 + k, 0.f);
+                if (c0 + k >= 0 && c0 + k < r.V) Elt<O>::store1(grow + c0 + k, value);
         }
     }
 }
@@ -366,20 +371,21 @@ __global__ void __launch_bounds__(kThreads, 2) k_distill_long(const __grid_const
             a.loss_rows[row] = 0.f;
             a.row_stats[row] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        zero_grads<S, O>(r, sl, grow, vec, tid, kThreads);
+        fill_grads<S, O>(r, sl, grow, vec, tid, kThreads);
         if (a.red == VCE_RED_MEAN) wait_previous();
         return;
     }
 
     // the slice is copied twice; of its second round, the ring's first fill goes out before the
     // statistics are done (later stages wait for the gradient to release theirs)
-    const int total = 2 * sl.nst;
+    const int total = 2 * sl.nst - (a.withhold == rank + 1);
     const int early = min(total, sl.nst + a.nbuf);
     int issued = 0;
     if (tid == kProducerWarp * 32) {
         init_barriers(ctl.bar, a.nbuf);
         ctl.code = 0;
-        for (; issued < min(sl.nst, a.nbuf); ++issued) issue_stage(bufs, ctl.bar, a.nbuf, r, sl, issued, issued);
+        for (; issued < min(sl.nst, a.nbuf); ++issued)
+            issue_stage(bufs, ctl.bar, a.nbuf, r, sl, issued, issued, a.wait_ns);
     }
     if (C > 1) cluster_arrive();                     // this block runs: peers may write into it
     for (int i = tid; i < sl.nst * kConsumers; i += kThreads) marks[i] = 0;
@@ -413,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_distill_long(const __grid_const
         if (lane == 0) {
             for (; issued < early; ++issued) {
                 const int j = issued < sl.nst ? issued : issued - sl.nst;
-                if (!issue_stage(bufs, ctl.bar, a.nbuf, r, sl, j, issued)) break;
+                if (!issue_stage(bufs, ctl.bar, a.nbuf, r, sl, j, issued, a.wait_ns)) break;
             }
         }
     } else if (warp == kTopWarp) {
@@ -436,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_distill_long(const __grid_const
         float m = -kInf, s = 0.f;
         for (int j = 0; j < sl.nst; ++j) {
             const uint32_t word = marks[j * kConsumers + tid];
-            wait_stage(ctl.bar, a.nbuf, j);
+            wait_stage(ctl.bar, a.nbuf, j, a.wait_ns);
             uint4 x[kU];
             load_stage<S>(bufs, a.nbuf, r, sl, j, j, tid, x);
             release_stage(ctl.bar, a.nbuf, j);
@@ -485,7 +491,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_distill_long(const __grid_const
         // weight: 1, negative for a row with an error, until the reduction writes it
         a.row_stats[row] = make_float4(f.lt, dead ? 0.f : f.d, 0.f, f.code ? -(float)f.code : 1.f);
     }
-    if (dead) zero_grads<S, O>(r, sl, grow, vec, tid, kThreads);
+    if (C > 1) cluster_arrive();                     // the first block has written the loss
+    if (dead) fill_grads<S, O>(r, sl, grow, vec, tid, kThreads);
     // k_distill_count: every block, with a gradient or without one, since the reduction waits for this kernel
     // alone and writes the word that the count does
     if (a.red == VCE_RED_MEAN) wait_previous();
@@ -495,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_distill_long(const __grid_const
             const float coef = c * f.d, bias = f.bias;
             for (int j = 0; j < sl.nst; ++j) {
                 const int q = sl.nst + j;
-                wait_stage(ctl.bar, a.nbuf, q);
+                wait_stage(ctl.bar, a.nbuf, q, a.wait_ns);
                 uint4 x[kU];
                 load_stage<S>(bufs, a.nbuf, r, sl, j, q, tid, x);
                 release_stage(ctl.bar, a.nbuf, q);
@@ -503,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_distill_long(const __grid_const
             }
         } else if (tid == kProducerWarp * 32) {
             for (; issued < total; ++issued)
-                if (!issue_stage(bufs, ctl.bar, a.nbuf, r, sl, issued - sl.nst, issued)) break;
+                if (!issue_stage(bufs, ctl.bar, a.nbuf, r, sl, issued - sl.nst, issued, a.wait_ns)) break;
         }
         __syncthreads();                             // the entries' gradients go over the tail's
         for (int k = tid; k < a.K; k += kThreads) {
@@ -515,6 +522,13 @@ __global__ void __launch_bounds__(kThreads, 2) k_distill_long(const __grid_const
     }
     // copies that nothing waited for (after an abort, or of a row without a gradient) land first
     if ((ctl.bar.abort || dead) && tid == kProducerWarp * 32) drain(ctl.bar, a.nbuf, issued);
+    // a wait for the second round gave up: the row's error, over what the first block wrote
+    __syncthreads();
+    if (C > 1) cluster_wait();
+    if (ctl.bar.abort && tid == 0) {
+        a.loss_rows[row] = __int_as_float(0x7FC00000);
+        a.row_stats[row].w = -(float)ctl.bar.err;
+    }
 }
 
 // ---- many rows: a persistent kernel -----------------------------------------------------------------
@@ -722,10 +736,10 @@ __global__ void __launch_bounds__(Form<kGrad, kBig>::kThreads, Form<kGrad, kBig>
     const int rank = C > 1 ? (int)cluster_rank() : 0;
     const int64_t cid = blockIdx.x / C, ncl = gridDim.x / C;
     auto wait = [&](uint64_t* bar, int64_t e, int code) {   // the phase of row e of a barrier doubled by parity
-        return tc::mbar_wait(bar, (uint32_t)(e >> 1) & 1, &ctl.abort, &ctl.err, code, tc::kWaitNs, kSuspend);
+        return tc::mbar_wait(bar, (uint32_t)(e >> 1) & 1, &ctl.abort, &ctl.err, code, a.wait_ns, kSuspend);
     };
     auto wait_top = [&](uint64_t* bar, int64_t e) {         // the phase of row e of one of kTops barriers
-        return tc::mbar_wait(bar + e % kTops, (uint32_t)(e / kTops) & 1, &ctl.abort, &ctl.err, kErrRow, tc::kWaitNs, kSuspend);
+        return tc::mbar_wait(bar + e % kTops, (uint32_t)(e / kTops) & 1, &ctl.abort, &ctl.err, kErrRow, a.wait_ns, kSuspend);
     };
 
     start_next();
@@ -765,7 +779,7 @@ __global__ void __launch_bounds__(Form<kGrad, kBig>::kThreads, Form<kGrad, kBig>
                 const Slice sl = ring_slice<F>(r, C, rank);
                 for (int j = 0; j < sl.nst; ++j, ++q, at.step()) {
                     const int st = at.st;
-                    if (!tc::mbar_wait(&ctl.empty[st], at.phase, &ctl.abort, &ctl.err, kErrEmpty)) break;
+                    if (!tc::mbar_wait(&ctl.empty[st], at.phase, &ctl.abort, &ctl.err, kErrEmpty, a.wait_ns)) break;
                     const int v = sl.v0 + j * kRingVecs;
                     const int lo = max(v, r.iv0), hi = min(min(v + kRingVecs, sl.v0 + sl.n), r.iv1);
                     if (hi > lo && dbg::ok(lo >= 0 && hi <= r.nv, dbg::kCols)) {
@@ -783,7 +797,7 @@ __global__ void __launch_bounds__(Form<kGrad, kBig>::kThreads, Form<kGrad, kBig>
         if (lane == 0 && *reinterpret_cast<volatile int*>(&ctl.abort)) {
             int never = 0;
             for (int p = max(0, q - nbuf); p < q; ++p)
-                tc::mbar_wait(&ctl.full[p % nbuf], (p / nbuf) & 1, &never, nullptr, 0);
+                tc::mbar_wait(&ctl.full[p % nbuf], (p / nbuf) & 1, &never, nullptr, 0, a.wait_ns);
         }
         __syncwarp();
     } else if (warp == kPatch) {
@@ -822,7 +836,7 @@ __global__ void __launch_bounds__(Form<kGrad, kBig>::kThreads, Form<kGrad, kBig>
             if (mine && ecol >= 0 && ecol < a.V) evalue = static_cast<const S*>(a.logits)[row * a.ld + ecol];
             const uint32_t eplace = mine ? (uint32_t)((edge - sl.v0) * G + lane % G) : 0xFFFFFFFFu;
             for (int j = 0; j < sl.nst; ++j, at.step()) {
-                ok = tc::mbar_wait(&ctl.full[at.st], at.phase, &ctl.abort, &ctl.err, kErrFull, tc::kWaitNs, kSuspend);
+                ok = tc::mbar_wait(&ctl.full[at.st], at.phase, &ctl.abort, &ctl.err, kErrFull, a.wait_ns, kSuspend);
                 if (!__all_sync(0xFFFFFFFFu, ok)) {
                     ok = false;
                     break;
@@ -951,7 +965,7 @@ __global__ void __launch_bounds__(Form<kGrad, kBig>::kThreads, Form<kGrad, kBig>
                 bool ok = true;
                 while (!try_wait_cluster(&ctl.exchanged[par], (uint32_t)(e >> 1) & 1)) {
                     ok = !*reinterpret_cast<volatile int*>(&ctl.abort);
-                    if (ok && tc::globaltimer() - t0 > tc::kWaitNs) {
+                    if (ok && tc::globaltimer() - t0 > a.wait_ns) {
                         ctl.abort = 1;
                         atomicCAS(&ctl.err, 0, (int)kErrRow);
                         ok = false;
@@ -971,7 +985,7 @@ __global__ void __launch_bounds__(Form<kGrad, kBig>::kThreads, Form<kGrad, kBig>
             const Finish f = finish_row(a, M, S0, ts.top, R, code);
             if (lane == 0) {
                 ctl.coefs[par] = Coefs{go * f.d, f.bias, f.dead};
-                tc::mbar_arrive(&ctl.finished[par]);
+                if (a.withhold != rank + 1) tc::mbar_arrive(&ctl.finished[par]);
             }
             if (lane == pending) {
                 kept = f;
@@ -1006,7 +1020,7 @@ __global__ void __launch_bounds__(Form<kGrad, kBig>::kThreads, Form<kGrad, kBig>
         // stages [j0, j1) of a row, at ring positions from `at` on
         auto forward = [&](Cursor<nbuf>& at, int j0, int j1, const Slice& sl, Pair& p) {
             for (int j = j0; j < j1; ++j, at.step()) {
-                tc::mbar_wait(&ctl.ready[at.st], at.phase, &ctl.abort, &ctl.err, kErrFull, tc::kWaitNs, kSuspend);
+                tc::mbar_wait(&ctl.ready[at.st], at.phase, &ctl.abort, &ctl.err, kErrFull, a.wait_ns, kSuspend);
                 uint4 x[U];
                 ring_load<S, U, kNT>(smem + at.st * kRingBytes, sl, j, tid, x);
                 if (!kGrad) {
@@ -1037,7 +1051,7 @@ __global__ void __launch_bounds__(Form<kGrad, kBig>::kThreads, Form<kGrad, kBig>
                 if (!kGrad) return;
                 const Row r = row_extent<S>(a, no);
                 O* g = static_cast<O*>(a.grad) + no * a.ld_g;
-                zero_grads<S, O>(r, ring_slice<F>(r, C, rank), g, grads_aligned<S, O>(r, g), tid, kNT);
+                fill_grads<S, O>(r, ring_slice<F>(r, C, rank), g, grads_aligned<S, O>(r, g), tid, kNT);
             });
         };
         int64_t row = -1, row2 = next();                   // the row held, and the next one
@@ -1081,14 +1095,15 @@ __global__ void __launch_bounds__(Form<kGrad, kBig>::kThreads, Form<kGrad, kBig>
             if (row2 >= 0) row2 = next();
         }
     }
-    // after an abort: no row of this block is known to be right
+    // after an abort: no row of this block is known to be right, nor of its cluster, whose first block has
+    // written its losses by then
     __syncthreads();
-    if (ctl.abort && rank == 0)
+    if (C > 1) cluster_arrive(), cluster_wait();       // and no block leaves while a peer may write into it
+    if (ctl.abort)
         for (int64_t row = cid + (int64_t)tid * ncl; row < a.T; row += (int64_t)kRingThreads * ncl) {
             a.loss_rows[row] = __int_as_float(0x7FC00000);
             a.row_stats[row].w = -(float)(ctl.err ? ctl.err : kErrRow);
         }
-    if (C > 1) cluster_arrive(), cluster_wait();       // no block leaves while a peer may write into it
 }
 
 }  // namespace ring
@@ -1108,6 +1123,8 @@ struct BwdArgs {
     void* grad;
     int64_t ld_g;
     int parts, nbuf;
+    uint64_t wait_ns;            // as Args
+    int withhold;                // 1 (test hook): a row's last block waits for its last stage in vain
 };
 
 template <typename S, typename O>
@@ -1118,29 +1135,31 @@ __global__ void __launch_bounds__(kConsumers + 32, 3) k_distill_bwd(const __grid
     const int tid = threadIdx.x, warp = tid >> 5;
     const int64_t row = blockIdx.x / a.parts;
     const Row r = make_row<S>(a.logits, row, a.ld, a.V);
-    const Slice sl = make_slice(r, a.parts, (int)(blockIdx.x - row * a.parts));
+    const int part = (int)(blockIdx.x - row * a.parts);
+    const Slice sl = make_slice(r, a.parts, part);
     O* grow = static_cast<O*>(a.grad) + row * a.ld_g;
     const bool vec = grads_aligned<S, O>(r, grow);
     const float4 st = a.row_stats[row];
     if (st.w == 0.f) {
-        zero_grads<S, O>(r, sl, grow, vec, tid, kConsumers + 32);
+        fill_grads<S, O>(r, sl, grow, vec, tid, kConsumers + 32);
         return;
     }
+    const int copies = sl.nst - (a.withhold && part == a.parts - 1);
     int issued = 0;
     if (tid == kConsumers) {
         init_barriers(bar, a.nbuf);
-        for (; issued < min(sl.nst, a.nbuf); ++issued) issue_stage(smem, bar, a.nbuf, r, sl, issued, issued);
+        for (; issued < min(copies, a.nbuf); ++issued) issue_stage(smem, bar, a.nbuf, r, sl, issued, issued, a.wait_ns);
     }
     const float cw = a.go[a.red == VCE_RED_NONE ? row : 0] * st.w;
     __syncthreads();
     if (warp == kConsumerWarps) {
         if (tid == kConsumers)
-            for (; issued < sl.nst; ++issued)
-                if (!issue_stage(smem, bar, a.nbuf, r, sl, issued, issued)) break;
+            for (; issued < copies; ++issued)
+                if (!issue_stage(smem, bar, a.nbuf, r, sl, issued, issued, a.wait_ns)) break;
     } else {
         const float coef = cw * a.tau * st.y, bias = st.x == -kInf ? 0.f : st.x * kLog2e;
         for (int j = 0; j < sl.nst; ++j) {
-            wait_stage(bar, a.nbuf, j);
+            wait_stage(bar, a.nbuf, j, a.wait_ns);
             uint4 x[kU];
             load_stage<S>(smem, a.nbuf, r, sl, j, j, tid, x);
             release_stage(bar, a.nbuf, j);
@@ -1148,13 +1167,17 @@ __global__ void __launch_bounds__(kConsumers + 32, 3) k_distill_bwd(const __grid
         }
     }
     __syncthreads();
+    if (bar.abort) {                                   // there is no status word: NaN shows what was not worked out
+        fill_grads<S, O>(r, sl, grow, vec, tid, kConsumers + 32, __int_as_float(0x7FC00000));
+        if (tid == kConsumers) drain(bar, a.nbuf, issued);
+        return;
+    }
     for (int k = tid; k < a.K; k += kConsumers + 32) {
         const int64_t id = a.ids[row * a.K + k];
         if (id < 0 || id >= a.V) continue;
         const int v = (int)(id + r.shift) / G - sl.v0;
         if (v >= 0 && v < sl.n) Elt<O>::store1(grow + id, cw * a.top_grads[row * a.K + k]);
     }
-    if (bar.abort && tid == kConsumers) drain(bar, a.nbuf, issued);
 }
 
 // ---- N before a one-pass MEAN, and the losses' sum ----------------------------------------------------
@@ -1254,6 +1277,7 @@ cudaError_t run_ring(Args& a, int sms, cudaStream_t s) {
     using F = ring::Form<kGrad, kBig>;
     constexpr auto kern = ring::k_distill_ring<S, O, kGrad, kBig>;
     a.cluster = ring_cluster<F, kGrad>(a.T, a.V, Elt<S>::kGroup, sms);
+    if (a.withhold) a.withhold = a.cluster;
     const int bytes = ring::ring_smem<F>(a.K);
     const int64_t clusters = std::min<int64_t>(
         a.T, resident_clusters<kern>(a.cluster, F::kThreads, bytes, sms * (a.cluster == 1 ? F::kBlocks : 1)));
@@ -1265,6 +1289,7 @@ template <typename S, typename O>
 cudaError_t run_long(Args& a, cudaStream_t s) {
     const int64_t nv = (a.V + 2 * Elt<S>::kGroup - 2) / Elt<S>::kGroup;
     a.cluster = kMaxCluster;
+    if (a.withhold) a.withhold = a.cluster;
     a.max_stages = (int)(((nv + kMaxCluster - 1) / kMaxCluster + kStageVecs - 1) / kStageVecs);
     a.nbuf = 4;
     return launch_clusters<k_distill_long<S, O>>(a.T * a.cluster, a.cluster, kThreads,
@@ -1343,6 +1368,7 @@ extern "C" int ce_distill_forward(const void* logits, vce_dtype dt, int64_t T, i
     a.tau = temperature, a.scale = 1.f / temperature, a.k2 = (float)(1.4426950408889634 / (double)temperature);
     a.labels = labels, a.ignore_index = ignore_index, a.red = red;
     a.loss_rows = loss_rows, a.row_stats = reinterpret_cast<float4*>(row_stats), a.top_grads = top_grads;
+    a.wait_ns = tc::kWaitNs;
     int rc = forward_checks(a, dt, tdt, temperature, status);
     if (rc) return rc;
     if (red != VCE_RED_NONE && !loss_out) return VCE_ERR_NULL;
@@ -1358,10 +1384,10 @@ extern "C" int ce_distill_forward(const void* logits, vce_dtype dt, int64_t T, i
     return record_cuda(e) == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
 }
 
-extern "C" int ce_distill_backward(const void* logits, vce_dtype dt, int64_t T, int64_t V, int64_t ld,
-                                   const int64_t* teacher_ids, int K, float temperature, vce_reduction red,
-                                   const float* row_stats, const float* top_grads, const float* grad_output,
-                                   void* grad_logits, vce_dtype grad_dt, int64_t ld_grad, vce_stream_t s) {
+static int backward_call(const void* logits, vce_dtype dt, int64_t T, int64_t V, int64_t ld,
+                         const int64_t* teacher_ids, int K, float temperature, vce_reduction red,
+                         const float* row_stats, const float* top_grads, const float* grad_output, void* grad_logits,
+                         vce_dtype grad_dt, int64_t ld_grad, uint64_t wait_ns, int withhold, vce_stream_t s) {
     int rc = distill::check_shape(dt, T, V, ld, K, temperature, red);
     if (rc) return rc;
     if (grad_dt != VCE_F32 && grad_dt != VCE_BF16) return VCE_ERR_DTYPE;
@@ -1380,6 +1406,7 @@ extern "C" int ce_distill_backward(const void* logits, vce_dtype dt, int64_t T, 
     a.tau = temperature, a.k2 = (float)(1.4426950408889634 / (double)temperature), a.red = red;
     a.row_stats = reinterpret_cast<const float4*>(row_stats), a.top_grads = top_grads, a.go = grad_output;
     a.grad = grad_logits, a.ld_g = ld_grad;
+    a.wait_ns = wait_ns, a.withhold = withhold;
     cudaError_t e;
     if (dt == VCE_BF16)
         e = grad_dt == VCE_BF16 ? distill::run_bwd<uint16_t, uint16_t>(a, s) : distill::run_bwd<uint16_t, float>(a, s);
@@ -1388,13 +1415,20 @@ extern "C" int ce_distill_backward(const void* logits, vce_dtype dt, int64_t T, 
     return record_cuda(e) == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
 }
 
-extern "C" int ce_distill_forward_backward(const void* logits, vce_dtype dt, int64_t T, int64_t V, int64_t ld,
-                                           const int64_t* teacher_ids, const void* teacher_values, vce_dtype tdt,
-                                           const float* teacher_tail, int K, float temperature,
-                                           const int64_t* labels, int64_t ignore_index, vce_reduction red,
-                                           const float* grad_output, float* loss_rows, float* loss_out,
-                                           float* row_stats, void* grad_logits, vce_dtype grad_dt, int64_t ld_grad,
-                                           int32_t* status, vce_stream_t s) {
+extern "C" int ce_distill_backward(const void* logits, vce_dtype dt, int64_t T, int64_t V, int64_t ld,
+                                   const int64_t* teacher_ids, int K, float temperature, vce_reduction red,
+                                   const float* row_stats, const float* top_grads, const float* grad_output,
+                                   void* grad_logits, vce_dtype grad_dt, int64_t ld_grad, vce_stream_t s) {
+    return backward_call(logits, dt, T, V, ld, teacher_ids, K, temperature, red, row_stats, top_grads, grad_output,
+                         grad_logits, grad_dt, ld_grad, tc::kWaitNs, 0, s);
+}
+
+static int one_pass_call(const void* logits, vce_dtype dt, int64_t T, int64_t V, int64_t ld,
+                         const int64_t* teacher_ids, const void* teacher_values, vce_dtype tdt,
+                         const float* teacher_tail, int K, float temperature, const int64_t* labels,
+                         int64_t ignore_index, vce_reduction red, const float* grad_output, float* loss_rows,
+                         float* loss_out, float* row_stats, void* grad_logits, vce_dtype grad_dt, int64_t ld_grad,
+                         int32_t* status, uint64_t wait_ns, int withhold, vce_stream_t s) {
     distill::Args a{};
     a.logits = logits, a.T = T, a.V = V, a.ld = ld;
     a.ids = teacher_ids, a.tvals = teacher_values, a.tail = teacher_tail, a.K = K, a.tbf16 = tdt == VCE_BF16;
@@ -1402,6 +1436,7 @@ extern "C" int ce_distill_forward_backward(const void* logits, vce_dtype dt, int
     a.labels = labels, a.ignore_index = ignore_index, a.red = red, a.go = grad_output, a.inv_n = loss_out;
     a.loss_rows = loss_rows, a.row_stats = reinterpret_cast<float4*>(row_stats);
     a.grad = grad_logits, a.ld_g = ld_grad;
+    a.wait_ns = wait_ns, a.withhold = withhold;
     int rc = forward_checks(a, dt, tdt, temperature, status);
     if (rc) return rc;
     if (grad_dt != VCE_F32 && grad_dt != VCE_BF16) return VCE_ERR_DTYPE;
@@ -1430,4 +1465,34 @@ extern "C" int ce_distill_forward_backward(const void* logits, vce_dtype dt, int
     }
     if (e == cudaSuccess) e = reduce(a, loss_out, status, s);
     return record_cuda(e) == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
+}
+
+extern "C" int ce_distill_forward_backward(const void* logits, vce_dtype dt, int64_t T, int64_t V, int64_t ld,
+                                           const int64_t* teacher_ids, const void* teacher_values, vce_dtype tdt,
+                                           const float* teacher_tail, int K, float temperature,
+                                           const int64_t* labels, int64_t ignore_index, vce_reduction red,
+                                           const float* grad_output, float* loss_rows, float* loss_out,
+                                           float* row_stats, void* grad_logits, vce_dtype grad_dt, int64_t ld_grad,
+                                           int32_t* status, vce_stream_t s) {
+    return one_pass_call(logits, dt, T, V, ld, teacher_ids, teacher_values, tdt, teacher_tail, K, temperature, labels,
+                         ignore_index, red, grad_output, loss_rows, loss_out, row_stats, grad_logits, grad_dt, ld_grad,
+                         status, tc::kWaitNs, 0, s);
+}
+
+extern "C" int vce_test_distill_stall(const void* logits, int64_t T, int64_t V, const int64_t* teacher_ids,
+                                      const float* teacher_values, int K, const float* grad_output, float* loss_rows,
+                                      float* loss_out, float* row_stats, void* grad_logits, uint64_t wait_ns,
+                                      int32_t* status, vce_stream_t s) {
+    if (wait_ns < 1000000ull || wait_ns > tc::kWaitNs) return VCE_ERR_ARG;
+    return one_pass_call(logits, VCE_BF16, T, V, V, teacher_ids, teacher_values, VCE_F32, nullptr, K, 1.f, nullptr, 0,
+                         VCE_RED_SUM, grad_output, loss_rows, loss_out, row_stats, grad_logits, VCE_BF16, V, status,
+                         wait_ns, 1, s);
+}
+
+extern "C" int vce_test_distill_bwd_stall(const void* logits, int64_t T, int64_t V, const int64_t* teacher_ids, int K,
+                                          const float* row_stats, const float* top_grads, const float* grad_output,
+                                          void* grad_logits, uint64_t wait_ns, vce_stream_t s) {
+    if (wait_ns < 1000000ull || wait_ns > tc::kWaitNs) return VCE_ERR_ARG;
+    return backward_call(logits, VCE_BF16, T, V, V, teacher_ids, K, 1.f, VCE_RED_SUM, row_stats, top_grads, grad_output,
+                         grad_logits, VCE_BF16, V, wait_ns, 1, s);
 }

@@ -61,6 +61,8 @@ struct Args {
     int64_t* ids;
     float *lse, *tail;
     int cluster, nbuf, max_stages;
+    uint64_t wait_ns;               // bound of every wait
+    int withhold;                   // 1 (test hook): the last stage of a slice is not copied
 };
 
 constexpr int kRowsPerSm = 2;               // rows for each SM from which the persistent kernel runs
@@ -519,20 +521,22 @@ __global__ void __launch_bounds__(kThreads, 3) k_topk(const __grid_constant__ Ar
     const Row r = make_row<S>(a.logits, row, a.ld, a.V);
     const Slice sl = make_slice(r, C, rank);
 
+    const int copies = sl.nst - a.withhold;
     int issued = 0;
     if (tid == kConsumers) {
         init_barriers(ctl.bar, a.nbuf);
-        for (; issued < min(sl.nst, a.nbuf); ++issued) issue_stage(smem, ctl.bar, a.nbuf, r, sl, issued, issued);
+        for (; issued < min(copies, a.nbuf); ++issued)
+            issue_stage(smem, ctl.bar, a.nbuf, r, sl, issued, issued, a.wait_ns);
     }
     if (C > 1) cluster_arrive_relaxed();       // this block runs: peers may write into it
     __syncthreads();
     if (warp == kConsumerWarps) {
         if (lane == 0)
-            for (; issued < sl.nst; ++issued)
-                if (!issue_stage(smem, ctl.bar, a.nbuf, r, sl, issued, issued)) break;
+            for (; issued < copies; ++issued)
+                if (!issue_stage(smem, ctl.bar, a.nbuf, r, sl, issued, issued, a.wait_ns)) break;
     } else {
         for (int j = 0; j < sl.nst; ++j) {
-            wait_stage(ctl.bar, a.nbuf, j);
+            wait_stage(ctl.bar, a.nbuf, j, a.wait_ns);
             uint4 x[kU];
             load_stage<S>(smem, a.nbuf, r, sl, j, j, tid, x);
             release_stage(ctl.bar, a.nbuf, j);
@@ -659,7 +663,8 @@ __global__ void __launch_bounds__(kPThreads, 1) k_topk_rows(const __grid_constan
                 const Row r = make_row<S>(a.logits, row, a.ld, a.V);
                 const Slice sl = slice_of(r);
                 for (int j = 0; j < sl.nst; ++j, ++q, step()) {
-                    if (!tc::mbar_wait(&ctl.empty[st], phase ^ 1, &ctl.abort, &ctl.err, kErrEmpty, tc::kWaitNs, kSuspend)) break;
+                    if (!tc::mbar_wait(&ctl.empty[st], phase ^ 1, &ctl.abort, &ctl.err, kErrEmpty, a.wait_ns, kSuspend)) break;
+                    if (a.withhold && j == sl.nst - 1) continue;
                     const int lo = max(j * kPVecs, r.iv0), hi = min((j + 1) * kPVecs, r.iv1);
                     if (hi > lo && dbg::ok(lo >= 0 && hi <= r.nv, dbg::kCols)) {
                         tc::mbar_arrive_expect_tx(&ctl.full[st], (uint32_t)(hi - lo) * 16);
@@ -673,7 +678,7 @@ __global__ void __launch_bounds__(kPThreads, 1) k_topk_rows(const __grid_constan
             if (*abort) {                      // copies in flight land before the block may leave
                 int never = 0;
                 for (int p = max(0, q - kPBufs); p < q; ++p)
-                    tc::mbar_wait(&ctl.full[p % kPBufs], (p / kPBufs) & 1, &never, nullptr, 0);
+                    tc::mbar_wait(&ctl.full[p % kPBufs], (p / kPBufs) & 1, &never, nullptr, 0, a.wait_ns);
             }
         }
         __syncwarp();
@@ -685,10 +690,10 @@ __global__ void __launch_bounds__(kPThreads, 1) k_topk_rows(const __grid_constan
             const Slice sl = slice_of(r);
             // row e - 2's groups have been selected from
             if (e >= 2) tc::mbar_wait(&ctl.taken[par], (uint32_t)((e - 2) >> 1) & 1, &ctl.abort, &ctl.err, kErrEmpty,
-                                      tc::kWaitNs, kSuspend);
+                                      a.wait_ns, kSuspend);
             float* gm = groups + par * 2 * kPStages * kPNT + tid;
             for (int j = 0; j < sl.nst; ++j, step()) {
-                tc::mbar_wait(&ctl.full[st], phase, &ctl.abort, &ctl.err, kErrFull, tc::kWaitNs, kSuspend);
+                tc::mbar_wait(&ctl.full[st], phase, &ctl.abort, &ctl.err, kErrFull, a.wait_ns, kSuspend);
                 const uint4* buf = reinterpret_cast<const uint4*>(smem + st * kPBytes) + tid;
                 const int at = j * kPVecs + tid;
                 uint4 x[kU];
@@ -719,7 +724,7 @@ __global__ void __launch_bounds__(kPThreads, 1) k_topk_rows(const __grid_constan
         for (int64_t row = blockIdx.x + (int64_t)par * gridDim.x; row < a.T; row += 2 * (int64_t)gridDim.x, phase_of ^= 1) {
             const Row r = make_row<S>(a.logits, row, a.ld, a.V);
             const Slice sl = slice_of(r);
-            tc::mbar_wait(&ctl.grouped[par], phase_of, &ctl.abort, &ctl.err, kErrFull, tc::kWaitNs, kSuspend);
+            tc::mbar_wait(&ctl.grouped[par], phase_of, &ctl.abort, &ctl.err, kErrFull, a.wait_ns, kSuspend);
             Rest rest;
             select<S, kPNT, kPTeam>(a, r, sl, sl.nst, ctl.sel[par], mine, gm, gm + kPStages * kPNT, team, rest);
             __syncwarp();
@@ -754,8 +759,9 @@ VCE_DEBUG_READER(debug_word_topk)
 
 using namespace vce;
 
-extern "C" int ce_topk(const void* logits, vce_dtype dt, int64_t T, int64_t V, int64_t ld, int K, float temperature,
-                       float* values, int64_t* ids, float* lse, float* tail_lse, vce_stream_t s) {
+static int topk_call(const void* logits, vce_dtype dt, int64_t T, int64_t V, int64_t ld, int K, float temperature,
+                     float* values, int64_t* ids, float* lse, float* tail_lse, uint64_t wait_ns, int withhold,
+                     vce_stream_t s) {
     if (dt != VCE_F32 && dt != VCE_BF16) return VCE_ERR_DTYPE;
     if (T < 0 || T > VCE_MAX_TOPK_T || V < 1 || V > VCE_MAX_TOPK_V) return VCE_ERR_SHAPE;
     if (K < 1 || K > VCE_MAX_TOPK || K > V || !rs::temperature_ok(temperature)) return VCE_ERR_ARG;
@@ -768,8 +774,20 @@ extern "C" int ce_topk(const void* logits, vce_dtype dt, int64_t T, int64_t V, i
         return VCE_ERR_ALIGN;
     const int rc = require_sm100();
     if (rc) return rc;
-    topk::Args a{logits, T, V, ld, K, (float)(1.4426950408889634 / (double)temperature), values, ids, lse, tail_lse, 1, 1, 1};
+    topk::Args a{logits, T, V, ld, K, (float)(1.4426950408889634 / (double)temperature), values, ids, lse, tail_lse, 1, 1, 1,
+                 wait_ns, withhold};
     const int sms = device_sm_count();
     const cudaError_t e = dt == VCE_BF16 ? topk::run<uint16_t>(a, sms, s) : topk::run<float>(a, sms, s);
     return record_cuda(e) == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
+}
+
+extern "C" int ce_topk(const void* logits, vce_dtype dt, int64_t T, int64_t V, int64_t ld, int K, float temperature,
+                       float* values, int64_t* ids, float* lse, float* tail_lse, vce_stream_t s) {
+    return topk_call(logits, dt, T, V, ld, K, temperature, values, ids, lse, tail_lse, tc::kWaitNs, 0, s);
+}
+
+extern "C" int vce_test_topk_stall(const void* logits, int64_t T, int64_t V, int K, float* values, int64_t* ids,
+                                   float* lse, float* tail_lse, uint64_t wait_ns, vce_stream_t s) {
+    if (wait_ns < 1000000ull || wait_ns > tc::kWaitNs) return VCE_ERR_ARG;
+    return topk_call(logits, VCE_BF16, T, V, V, K, 1.f, values, ids, lse, tail_lse, wait_ns, 1, s);
 }

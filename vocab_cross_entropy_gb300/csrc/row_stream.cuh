@@ -12,8 +12,9 @@
 // A block has kConsumers threads that work on the columns and a producer warp, whose first lane
 // keeps up to nbuf stages of 16 KB in flight, each with a mbarrier for "loaded" and one for
 // "released".  Consumer thread t owns the vectors t + u * kConsumers, u < kU, of every stage.
-// Every wait is bounded (2 s); one that gives up records its code and sets the block's abort
-// flag, after which every role stops waiting, and the producer lets its copies in flight land.
+// Every wait is bounded (2 s; less in the test hooks); one that gives up records its code and sets the
+// block's abort flag, after which every role stops waiting, and the producer lets its copies in flight
+// land.  Kernels look at the flag once everything is written, and mark what may be wrong.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -91,9 +92,9 @@ __device__ __forceinline__ void init_barriers(Barriers& b, int nbuf) {
 
 // Copies stage j of the slice into ring position q (one thread).  False: a wait gave up.
 __device__ __forceinline__ bool issue_stage(uint8_t* bufs, Barriers& b, int nbuf, const Row& r, const Slice& s, int j,
-                                            int q) {
+                                            int q, uint64_t wait_ns) {
     const int st = q % nbuf;
-    if (q >= nbuf && !tc::mbar_wait(&b.empty[st], ((q / nbuf) & 1) ^ 1, &b.abort, &b.err, kErrEmpty)) return false;
+    if (q >= nbuf && !tc::mbar_wait(&b.empty[st], ((q / nbuf) & 1) ^ 1, &b.abort, &b.err, kErrEmpty, wait_ns)) return false;
     const int a = s.v0 + j * kStageVecs;
     const int lo = max(a, r.iv0), hi = min(min(a + kStageVecs, s.v0 + s.n), r.iv1);
     if (hi > lo && dbg::ok(lo >= 0 && (int64_t)hi * 16 <= (int64_t)r.nv * 16, dbg::kCols)) {
@@ -112,8 +113,8 @@ __device__ __forceinline__ void drain(Barriers& b, int nbuf, int q) {
     for (int p = max(0, q - nbuf); p < q; ++p) tc::mbar_wait(&b.full[p % nbuf], (p / nbuf) & 1, &never, nullptr, 0);
 }
 
-__device__ __forceinline__ bool wait_stage(Barriers& b, int nbuf, int q) {
-    return tc::mbar_wait(&b.full[q % nbuf], (q / nbuf) & 1, &b.abort, &b.err, kErrFull);
+__device__ __forceinline__ bool wait_stage(Barriers& b, int nbuf, int q, uint64_t wait_ns) {
+    return tc::mbar_wait(&b.full[q % nbuf], (q / nbuf) & 1, &b.abort, &b.err, kErrFull, wait_ns);
 }
 
 // A consumer warp is done with ring position q.

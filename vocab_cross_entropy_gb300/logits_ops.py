@@ -360,3 +360,42 @@ def process_logits(logits, *, out_dtype=None, **parameters):
         if name in parameters:
             raise TypeError(f"process_logits takes no {name}")
     return _Process.apply(logits, out_dtype, parameters)
+
+
+# ---- test hooks: waits that give up -------------------------------------------------------------
+
+
+def vce_test_topk_stall(logits, k, wait_ns=50_000_000, *, stream=None):
+    """ce_topk of contiguous bfloat16 logits whose slices' last stages are never copied; its outputs."""
+    T, V = logits.shape
+    dev = logits.device
+    out = (torch.zeros(T, k, device=dev), torch.zeros(T, k, dtype=_I64, device=dev), torch.zeros(T, device=dev),
+           torch.zeros(T, device=dev))
+    _run("vce_test_topk_stall", dev, stream, logits.data_ptr(), T, V, k, *(t.data_ptr() for t in out), int(wait_ns))
+    return out
+
+
+def vce_test_distill_stall(logits, teacher_ids, teacher_values, wait_ns=50_000_000, *, stream=None):
+    """The one pass on contiguous bfloat16 logits, the gradient of each cluster's last block waiting in
+    vain.  Returns (loss_out, loss_rows, grad_logits, status)."""
+    T, V = logits.shape
+    dev = logits.device
+    go, loss, rows = torch.ones(1, device=dev), torch.zeros(1, device=dev), torch.zeros(T, device=dev)
+    stats, grad = torch.zeros(T, ROW_STATS, device=dev), torch.zeros_like(logits)
+    status = torch.full((1,), 0x7FFF1234, dtype=_I32, device=dev)
+    _run("vce_test_distill_stall", dev, stream, logits.data_ptr(), T, V, teacher_ids.data_ptr(),
+         teacher_values.data_ptr(), teacher_ids.shape[1], go.data_ptr(), rows.data_ptr(), loss.data_ptr(),
+         stats.data_ptr(), grad.data_ptr(), int(wait_ns), status.data_ptr())
+    return loss, rows, grad, status
+
+
+def vce_test_distill_bwd_stall(logits, teacher_ids, row_stats, top_grads, wait_ns=50_000_000, *, stream=None):
+    """The backward on contiguous bfloat16 logits, each row's last block waiting for its last stage in
+    vain.  Returns grad_logits."""
+    T, V = logits.shape
+    dev = logits.device
+    go, grad = torch.ones(1, device=dev), torch.zeros_like(logits)
+    _run("vce_test_distill_bwd_stall", dev, stream, logits.data_ptr(), T, V, teacher_ids.data_ptr(),
+         teacher_ids.shape[1], row_stats.data_ptr(), top_grads.data_ptr(), go.data_ptr(), grad.data_ptr(),
+         int(wait_ns))
+    return grad
