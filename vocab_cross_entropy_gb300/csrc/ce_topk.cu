@@ -348,13 +348,11 @@ __device__ __forceinline__ void select(const Args& a, const Row& r, const Slice&
     // ---- 2. candidates ----
     // the groups with a value >= t: a place on the list for each lane's, one atomic a warp (and for each 64
     // rounds: a slice of the longest fp32 rows has 65)
-#pragma unroll 1
-    for (int i0 = 0; i0 < rounds; i0 += 64) {
+    auto list_rounds = [&](int i0, int i1) {
         uint64_t mine = 0;                     // bit i: group tid + (i0 + i) NS
         if (most_mine >= t) {
-            const int n = min(64, rounds - i0);
 #pragma unroll 4
-            for (int i = 0; i < n; ++i) mine |= (uint64_t)(gm[(i0 + i) * NS + tid] >= t) << i;
+            for (int i = i0; i < i1; ++i) mine |= (uint64_t)(gm[i * NS + tid] >= t) << (i - i0);
         }
         const int n = __popcll(mine);
         int at = n;
@@ -368,7 +366,9 @@ __device__ __forceinline__ void select(const Args& a, const Row& r, const Slice&
         at += __shfl_sync(0xFFFFFFFFu, base, 31) - n;
         for (; mine; mine &= mine - 1, ++at)
             if (at < kMaxSel) sel[at] = tid + (i0 + __ffsll((long long)mine) - 1) * NS;
-    }
+    };
+    list_rounds(0, min(rounds, 64));
+    if (rounds > 64) list_rounds(64, rounds);
     team.sync();
     const int nsel = ctl.nsel;
     rest = Rest{-kInf, 0.f, -kInf};            // this thread's columns left out
