@@ -149,12 +149,11 @@ VCE_API int ce_distill_forward_backward(const void* logits, vce_dtype dt, int64_
  *                                mask_ld >= ceil(V / 32) words
  *   out, out_dt, ld_out          [T, ld_out]; VCE_ERR_ARG if it overlaps the logits
  *   row_status                   [T] int32, written for every row: 0; VCE_ERR_LABEL (a history or
- *                                bias id outside [0, V), skipped, or bias ids not ascending);
+ *                                bias id outside [0, V), or bias ids not ascending);
  *                                VCE_ERR_PARAM (a temperature or repetition penalty that is not
- *                                finite and > 0, or a temperature without a finite reciprocal: it
- *                                counts as NaN); VCE_ERR_OFFSETS (also a history of 2^30 tokens or
- *                                more; the list counts as empty).  A row with an error holds
- *                                unspecified values.
+ *                                finite and > 0, or a temperature without a finite reciprocal);
+ *                                VCE_ERR_OFFSETS (also a history of 2^30 tokens or
+ *                                more).  A row with an error is NaN in every column.
  */
 VCE_API int logits_process(const void* logits, vce_dtype dt, int64_t T, int64_t V, int64_t ld,
                            const float* temperature, const float* repetition, const float* frequency,
@@ -168,7 +167,8 @@ VCE_API int logits_process(const void* logits, vce_dtype dt, int64_t T, int64_t 
 /*
  * logits_process_backward -- the gradient w.r.t. the logits of logits_process:
  *     grad_logits = grad_out / temperature * (history: z > 0 ? 1 / r : r; else 1), +0.0 where masked
- * The penalties n f, p and the biases do not enter.
+ * The penalties n f, p and the biases do not enter.  A row with an error (row_status) is +0.0 in every
+ * column.
  *   grad_out, gdt, ld_gout   [T, ld_gout];  logits, dt, ld: the unprocessed ones (read at the
  *                            columns of the history only; may be NULL without a history)
  *   grad_logits, grad_dt, ld_grad   [T, ld_grad]; VCE_ERR_ARG if it overlaps grad_out or the logits

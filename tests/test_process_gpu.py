@@ -295,3 +295,53 @@ def test_a_decoded_token(vce):
     there = np.isfinite(rv[open_])
     want = rv[open_] - rl[open_][:, None]
     assert np.all(np.abs(logp[there] - want[there]) <= tol)
+
+
+@pytest.mark.parametrize("V,history", [(1000, 30), (32001, 3000), (40000, 20000), (128256, 500)])
+@pytest.mark.parametrize("mask", [True, False])
+def test_process_rows_with_an_error_show_it(vce, V, history, mask):
+    """A bad id, bias ids out of order, bad offsets or a bad parameter: that row is NaN, its gradient +0.0,
+    also where nobody looks at row_status (autograd); the other rows are as they were."""
+    c = Case(8, V, F32, history, 5, mask)
+    want, size = c.oracle()
+    kw = c.kwargs()
+    off, b = kw["history_offsets"].tolist(), kw["bias_offsets"].tolist()
+    rows = {}
+    i = next(i for i in range(8) if off[i + 1] > off[i])
+    kw["history_ids"][off[i + 1] - 1] = V
+    rows[i] = 1
+    j = next(j for j in range(8) if j not in rows and b[j + 1] - b[j] >= 2)
+    kw["bias_ids"][b[j]] = V + 7
+    rows[j] = 1
+    k = [x for x in range(7) if x not in rows]
+    kw["temperature"][k[0]], rows[k[0]] = -1.0, 3
+    kw["repetition_penalty"][k[1]], rows[k[1]] = 0.0, 3
+    rows[7] = 4
+    kw["history_offsets"][8] += 1
+    z = c.z.clone().requires_grad_(True)
+    y = vce.process_logits(z, **kw)
+    out, status = vce.logits_process(c.z, **kw)
+    assert {r: s for r, s in enumerate(status.tolist()) if s} == rows
+    good = [r for r in range(8) if r not in rows]
+    bad = list(rows)
+    for o in (y.detach(), out):
+        assert torch.isnan(o[bad]).all()
+        G.check_processed(o[good].double().cpu().numpy(), want[good], size[good], EPS[F32])
+    up = torch.randn(8, V, device="cuda")
+    y.backward(up)
+    back = {r for r, s in rows.items() if r != j}        # the backward does not read the biases
+    wantg, sizeg = c.oracle(up)
+    assert torch.all(z.grad[list(back)] == 0) and not torch.signbit(z.grad[list(back)]).any()
+    fine = good + [j]
+    G.check_processed(z.grad[fine].double().cpu().numpy(), wantg[fine], sizeg[fine], EPS[F32])
+
+
+def test_process_bad_temperatures_without_lists(vce):
+    c = Case(4, 5001, BF16, 0, 0, True)
+    kw = c.kwargs()
+    kw["temperature"][2] = 0.0
+    out, status = vce.logits_process(c.z, **kw)
+    assert status.tolist() == [0, 0, 3, 0]
+    assert torch.isnan(out[2]).all() and not torch.isnan(out[[0, 1, 3]]).any()
+    g, status = vce.logits_process_backward(torch.ones_like(c.z), temperature=kw["temperature"], mask=kw["mask"])
+    assert status.tolist() == [0, 0, 3, 0] and torch.all(g[2] == 0)

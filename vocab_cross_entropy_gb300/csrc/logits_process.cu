@@ -205,7 +205,7 @@ __device__ __forceinline__ void stream(const Args& a, const Row& r, const S* iro
         }
     }
     const int head = va < r.iv0 ? min((int64_t)G - r.shift, a.V) : 0;          // columns [0, head)
-    const int tail = vb > r.iv1 && r.iv1 >= r.iv0 ? r.iv1 * G - r.shift : (int)a.V;   // columns [tail, V)
+    const int tail = va <= r.iv1 && vb > r.iv1 && r.iv1 >= r.iv0 ? r.iv1 * G - r.shift : (int)a.V;   // columns [tail, V)
     if ((int)threadIdx.x < 2 * G) {
         const int c = (int)threadIdx.x < G ? (int)threadIdx.x : tail + (int)threadIdx.x - G;
         if ((int)threadIdx.x < G ? c < head : c < a.V) {
@@ -422,6 +422,30 @@ __device__ __noinline__ void windows(const Args& a, Ctl& ctl, uint32_t* words, i
     }
 }
 
+// The block's place: its row, its part of the row, and the vectors [v0, v1) of that.
+struct Place {
+    int64_t row;
+    int part, v0, v1;
+};
+__device__ __forceinline__ Place place_of(const Args& a, int nv_of_row, int64_t row) {
+    const int part = (int)(blockIdx.x - row * a.parts), v0 = min(nv_of_row, part * a.slice);
+    return Place{row, part, v0, min(nv_of_row, v0 + a.slice)};
+}
+
+// Of a row with an error: every column of the block's NaN, or in the backward without a gradient, so that
+// what was skipped or could not be worked out shows where nobody looks at the status.  Everything is
+// worked out again here: values kept for it would cost the kernel's loops registers.
+template <typename S, typename O, int NT, bool kBack>
+__device__ __noinline__ void refuse(const Args& a) {
+    constexpr int G = Elt<S>::kGroup;
+    const int64_t row = blockIdx.x / a.parts;
+    const Row r = rs::make_row<S>(a.in, row, a.ld, a.V);
+    const Place p = place_of(a, r.nv, row);
+    O* orow = static_cast<O*>(a.out) + row * a.ld_out;
+    const int lo = max(0, p.v0 * G - r.shift), hi = min((int)a.V, p.v1 * G - r.shift);
+    for (int c = lo + (int)threadIdx.x; c < hi; c += NT) Elt<O>::store1(orow + c, kBack ? 0.f : __int_as_float(0x7FC00000));
+}
+
 enum { kNoLists, kDenseRange, kHashed };
 
 template <typename S, typename O, int NT, bool kBack, int kKind>
@@ -429,15 +453,16 @@ __global__ void __launch_bounds__(NT, NT == kThreads ? 5 : 3) k_process(const __
     extern __shared__ __align__(16) uint8_t smem[];
     const int tid = threadIdx.x;
     const int64_t row = blockIdx.x / a.parts;
-    const int part = (int)(blockIdx.x - row * a.parts);
     const Row r = rs::make_row<S>(a.in, row, a.ld, a.V);
-    const int v0 = min(r.nv, part * a.slice), v1 = min(r.nv, v0 + a.slice);
+    const Place p = place_of(a, r.nv, row);
+    const int part = p.part, v0 = p.v0, v1 = p.v1;
     int code = 0;
     const float inv_t = inv_temperature(a, row, code);
     if (kKind == kNoLists) {
         const S* irow = static_cast<const S*>(a.in) + row * a.ld;
         O* orow = static_cast<O*>(a.out) + row * a.ld_out;
-        stream<S, O, NT>(a, r, irow, orow, a.mask ? a.mask + row * a.mask_ld : nullptr, inv_t, v0, v1);
+        if (code) refuse<S, O, NT, kBack>(a);
+        else stream<S, O, NT>(a, r, irow, orow, a.mask ? a.mask + row * a.mask_ld : nullptr, inv_t, v0, v1);
         if (part == 0 && tid == 0) a.row_status[row] = code;
         return;
     }
@@ -446,7 +471,9 @@ __global__ void __launch_bounds__(NT, NT == kThreads ? 5 : 3) k_process(const __
     if (tid == 0) read_row<kBack>(a, row, inv_t, code, ctl);
     if (!range<S, O, NT, kBack, kKind == kHashed>(a, ctl, words, r, row, inv_t, v0, v1))
         windows<S, O, NT, kBack>(a, ctl, words, row, inv_t, v0, v1);
-    if (part == 0 && tid == 0) a.row_status[row] = max(ctl.status, ctl.code);
+    const int error = max(ctl.status, ctl.code);   // every block of a row has seen all its tokens and biases
+    if (error) refuse<S, O, NT, kBack>(a);
+    if (part == 0 && tid == 0) a.row_status[row] = error;
 }
 
 template <typename S, typename O, int NT, bool kBack>

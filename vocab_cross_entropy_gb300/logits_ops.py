@@ -287,7 +287,7 @@ def logits_process(logits, *, temperature=None, repetition_penalty=None, frequen
     another with int64 offsets [T + 1]; prompt_lens int64 [T], how many of a row's first tokens are its
     prompt; mask int32 words, bit j % 32 of word j // 32 allowing column j.
 
-    Returns (out, row_status), row_status int32 [T]: 0, or the row's first error.
+    Returns (out, row_status), row_status int32 [T]: 0, or an error of the row, which is NaN then.
     """
     dt, T, V, ld = _matrix(logits, "logits")
     dev = logits.device
@@ -313,7 +313,7 @@ def logits_process_backward(grad_out, logits=None, *, temperature=None, repetiti
                             history_offsets=None, mask=None, grad_logits=None, grad_dtype=None, row_status=None,
                             stream=None):
     """The gradient through logits_process w.r.t. its logits (the unprocessed ones, needed with a
-    history only).  Returns (grad_logits, row_status)."""
+    history only).  Returns (grad_logits, row_status); a row with an error has no gradient (+0.0)."""
     gdt, T, V, gld = _matrix(grad_out, "grad_out")
     dev = grad_out.device
     zdt, zld, z = gdt, V, None
@@ -355,7 +355,7 @@ class _Process(torch.autograd.Function):
 
 def process_logits(logits, *, out_dtype=None, **parameters):
     """logits_process with autograd (its keyword arguments but out, row_status and stream): the gradient
-    w.r.t. the logits, the parameters as constants."""
+    w.r.t. the logits, the parameters as constants.  Rows with an error are NaN, and have no gradient."""
     for name in ("out", "row_status", "stream"):
         if name in parameters:
             raise TypeError(f"process_logits takes no {name}")
