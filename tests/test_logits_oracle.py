@@ -168,3 +168,11 @@ def test_refusals_of_the_give_up_hooks(vce):
     assert one(ns=999_999) == -8 and one(ns=2_000_000_001) == -8 and one(status=None) == -1
     bwd = lambda ns=50_000_000, go=x: lib.vce_test_distill_bwd_stall(x, 4, 64, x, 8, x, x, go, 0x900000, ns, None)
     assert bwd(ns=999_999) == -8 and bwd(ns=2_000_000_001) == -8 and bwd(go=None) == -1
+
+
+def test_teachers_of_more_entries_than_32_bits_are_refused(vce):
+    """Entries beyond 2^31 (of tensors without storage) before anything else of the teacher is looked at."""
+    from vocab_cross_entropy_gb300 import logits_ops
+    ids = torch.empty(1, 2 ** 32 + 5, dtype=torch.int64, device="meta")
+    with pytest.raises(ValueError, match="expected 1 to 256"):
+        logits_ops._teacher(ids, ids.float(), None, 1, torch.device("cuda", 0))

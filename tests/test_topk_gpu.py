@@ -227,3 +227,13 @@ def test_topk_waits_that_give_up_leave_nan(vce, T, V):
     values, ids, lse, tail = vce.vce_test_topk_stall(z, 9)
     assert torch.isnan(values).all() and torch.all(ids == -1) and torch.isnan(lse).all() and torch.isnan(tail).all()
     check(vce, z[:3], 9)
+
+
+def test_topk_counts_beyond_32_bits_are_refused(vce):
+    """2^32 + 5 is not 5."""
+    z = logits_of(1, 100, torch.float32, 1)
+    held = torch.cuda.memory_allocated()
+    for k in (2 ** 32 + 5, 2 ** 31, -2 ** 32 + 5):
+        with pytest.raises(ValueError):
+            vce.ce_topk(z, k)
+    assert torch.cuda.memory_allocated() == held

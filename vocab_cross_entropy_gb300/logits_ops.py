@@ -100,6 +100,13 @@ def _run(fn, dev, stream, *args):
         raise VceError(fn, rc)
 
 
+def _entries(k):
+    """A number of entries a row that the library's 32-bit argument holds (it refuses those above its limit)."""
+    if k >= 2 ** 31:
+        raise ValueError(f"{k} entries a row, expected 1 to {MAX_TOPK}")
+    return k
+
+
 def ce_topk(logits, k, temperature=1.0, *, values=None, ids=None, lse=None, tail_lse=None, stream=None):
     """The k largest logits of each row in order (ties to the lowest column), their columns, and the
     log-sum-exp of logits / temperature over the row and over the columns left out.
@@ -109,7 +116,7 @@ def ce_topk(logits, k, temperature=1.0, *, values=None, ids=None, lse=None, tail
     """
     dt, T, V, ld = _matrix(logits, "logits")
     dev = logits.device
-    k = int(k)
+    k = _entries(int(k))
     if k < 1:
         raise ValueError(f"k: {k}, expected at least 1")
     values, p_values = _out(values, "values", _F32, (T, k), dev, stream)
@@ -123,7 +130,7 @@ def ce_topk(logits, k, temperature=1.0, *, values=None, ids=None, lse=None, tail
 def _teacher(ids, values, tail, T, dev):
     if ids.dim() != 2:
         raise ValueError("teacher_ids: expected a [T, K] tensor")
-    K = ids.shape[1]
+    K = _entries(ids.shape[1])
     tdt = _DT.get(values.dtype)
     if tdt is None:
         raise TypeError(f"teacher_values: unsupported dtype {values.dtype}; use float32 or bfloat16")
@@ -165,7 +172,7 @@ def ce_distill_backward(logits, teacher_ids, row_stats, top_grads, grad_output, 
     dev = logits.device
     if teacher_ids.dim() != 2:
         raise ValueError("teacher_ids: expected a [T, K] tensor")
-    K = teacher_ids.shape[1]
+    K = _entries(teacher_ids.shape[1])
     red = RED[reduction]
     grad_logits, p_grad, gdt, gld = _matrix_out(grad_logits, "grad_logits", T, V, grad_dtype or logits.dtype, dev, stream)
     _run("ce_distill_backward", dev, stream, logits.data_ptr(), dt, T, V, ld,
