@@ -501,3 +501,28 @@ def test_distill_backward_waits_that_give_up_leave_nan(vce, T, V):
     assert torch.isnan(got[:, last:]).all() and torch.equal(got[:, :last], want[:, :last])
     again = vce.ce_distill_backward(z, c.ids, stats, tops, torch.ones(1, device="cuda"), 1.0, "sum")
     assert torch.equal(again, want)
+
+
+@pytest.mark.parametrize("T,V,dtype,gdtype,pad,left", [
+    (2, 900001, BF16, BF16, 5, 5), (2, 900001, BF16, F32, 5, 5), (3, 450001, F32, BF16, 2, 1),
+    (300, 70001, BF16, F32, 1, 0), (700, 20001, BF16, BF16, 4, 3)])
+def test_distill_gradients_whose_stores_back_up(vce, T, V, dtype, gdtype, pad, left):
+    """Rows that no vector store fits keep a thread's reads of a stage waiting behind its stores: no
+    stage may be copied over before they are done.  The one pass against the two calls, again and again."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    z = torch.empty(T, V + pad, dtype=dtype, device="cuda")[:, left:left + V]
+    z.copy_(4.0 + 4.0 * torch.rand(T, V, generator=g, device="cuda"))
+    ids = torch.randint(0, V // 8, (T, 8), generator=g, device="cuda") * 8 + torch.arange(8, device="cuda")
+    values = torch.randn(T, 8, generator=g, device="cuda")
+    up = torch.ones(1, device="cuda")
+    _, _, stats, tops, status = vce.ce_distill_forward(z, ids, values, reduction="sum")
+    assert vce.vce_get_status(status) == 0
+    want = vce.ce_distill_backward(z, ids, stats, tops, up, reduction="sum", grad_dtype=gdtype).float()
+    # p = e^(z - L') p_T of both, in fp32, their log-sum-exps by other kernels: 2e-5 relative (the two sums' 2 x
+    # 150 units of 2^-24, as in the tests to rounding), and a rounding of each to the gradient's type
+    tol = (2e-5 + (torch.finfo(gdtype).eps if gdtype is BF16 else 0.0)) * want.abs() + 1e-12
+    # the entries are differences: within 2e-5 of the larger of p and q, at most 1
+    tol.scatter_(1, ids, 2e-5 + (torch.finfo(gdtype).eps if gdtype is BF16 else 0.0) * want.gather(1, ids).abs())
+    for _ in range(12):
+        got = vce.ce_distill_forward_backward(z, ids, values, reduction="sum", grad_output=up, grad_dtype=gdtype)[2]
+        assert torch.all((got.float() - want).abs() <= tol)

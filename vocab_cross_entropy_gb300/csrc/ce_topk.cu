@@ -539,8 +539,8 @@ __global__ void __launch_bounds__(kThreads, 3) k_topk(const __grid_constant__ Ar
             wait_stage(ctl.bar, a.nbuf, j, a.wait_ns);
             uint4 x[kU];
             load_stage<S>(smem, a.nbuf, r, sl, j, j, tid, x);
-            release_stage(ctl.bar, a.nbuf, j);
             group_of<S>(x, a.k2, gm[j * kConsumers + tid], gs[j * kConsumers + tid]);
+            release_stage(ctl.bar, a.nbuf, j);
         }
     }
     __syncthreads();
@@ -708,6 +708,7 @@ __global__ void __launch_bounds__(kPThreads, 1) k_topk_rows(const __grid_constan
                         if (v < r.nv) x[u] = v >= r.iv0 && v < r.iv1 ? tc::lds16(buf + u * kPNT) : load_partial<S>(r, v);
                     }
                 }
+                reads_done();                  // before the sums: 395 us at 8192 x 128256, behind them 402
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&ctl.empty[st]);
                 group_of<S>(x, a.k2, gm[j * kPNT], gm[(kPStages + j) * kPNT]);

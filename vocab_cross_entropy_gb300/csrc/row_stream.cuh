@@ -117,8 +117,14 @@ __device__ __forceinline__ bool wait_stage(Barriers& b, int nbuf, int q, uint64_
     return tc::mbar_wait(&b.full[q % nbuf], (q / nbuf) & 1, &b.abort, &b.err, kErrFull, wait_ns);
 }
 
+// This thread's reads of a stage come before the copy that is issued once the stage has been released: the
+// copy writes through another proxy, which the release alone does not order behind reads that are still
+// on their way (behind a thread's stores they take long).
+__device__ __forceinline__ void reads_done() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
 // A consumer warp is done with ring position q.
 __device__ __forceinline__ void release_stage(Barriers& b, int nbuf, int q) {
+    reads_done();
     __syncwarp();
     if ((threadIdx.x & 31) == 0) tc::mbar_arrive(&b.empty[q % nbuf]);
 }
