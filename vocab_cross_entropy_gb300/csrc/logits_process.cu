@@ -164,7 +164,7 @@ __device__ __forceinline__ void stream_batch(const Row& r, O* out0, const uint32
         } else {
             scale<S, NT == kLongThreads>(x[q], kMask ? ok[q] : 0xFFFFFFFFu, inv_t, masked, z);
         }
-        GroupStore<O, G>::run(out0 + (size_t)v * G, z);
+        if (dbg::ok((int)v >= r.iv0 && (int)v < r.iv1, dbg::kCols)) GroupStore<O, G>::run(out0 + (size_t)v * G, z);
     }
 }
 
@@ -278,6 +278,7 @@ __device__ __forceinline__ void count_one(const Args& a, Ctl& ctl, uint32_t* wor
             if (was == kFree || was == c) break;
         }
     }
+    if (!dbg::ok(at < (uint32_t)(kHash ? a.slots : 2 * a.slots), dbg::kStage)) return;
     if (bits) atomicOr(words + at, bits);
     else atomicAdd(words + at, 1u);
 }
@@ -346,7 +347,7 @@ __device__ __forceinline__ bool range(const Args& a, Ctl& ctl, uint32_t* words, 
                 const int i = i0 + q * NT;
                 const uint32_t c = id[q].x - ulo;
                 bad |= id[q].y != 0 || id[q].x >= (uint32_t)a.V;
-                if (c < width && id[q].y == 0) {
+                if (c < width && id[q].y == 0 && dbg::ok(c < 2u * (uint32_t)a.slots, dbg::kStage)) {
                     if (i < np) atomicOr(words + c, kPrompt);
                     else if (i < n) atomicAdd(words + c, 1u);
                 }
@@ -379,7 +380,8 @@ __device__ __forceinline__ bool range(const Args& a, Ctl& ctl, uint32_t* words, 
         for (int i = tid; i < places; i += NT) {
             const int at = listed ? (int)ctl.list[i] : i;
             const int c = lo + (kHash ? (int)cols[at] : at);
-            if (!words[at] || (mrow && !((mrow[c >> 5] >> (c & 31)) & 1u))) continue;
+            if (!dbg::ok(at < (kHash ? a.slots : 2 * a.slots), dbg::kStage)) continue;
+            if (!words[at] || !dbg::ok(c >= lo && c < hi, dbg::kCols) || (mrow && !((mrow[c >> 5] >> (c & 31)) & 1u))) continue;
             const char* z = static_cast<const char*>(a.z) + (row * a.ld_z + c) * (a.z_bf16 ? 2 : 4);
             asm volatile("prefetch.global.L2 [%0];" ::"l"(z));
         }
@@ -391,9 +393,10 @@ __device__ __forceinline__ bool range(const Args& a, Ctl& ctl, uint32_t* words, 
 #pragma unroll 1
     for (int i = tid; i < places; i += NT) {
         const int at = listed ? (int)ctl.list[i] : i;
+        if (!dbg::ok(at < (kHash ? a.slots : 2 * a.slots), dbg::kStage)) continue;
         const uint32_t w = words[at];
         const int c = lo + (kHash ? (int)cols[at] : at);
-        if (!w || (mrow && !((mrow[c >> 5] >> (c & 31)) & 1u))) continue;
+        if (!w || !dbg::ok(c >= lo && c < hi, dbg::kCols) || (mrow && !((mrow[c >> 5] >> (c & 31)) & 1u))) continue;
         const float e = Elt<S>::load1(irow + c);
         const Rule& u = ctl.rule;
         float y;

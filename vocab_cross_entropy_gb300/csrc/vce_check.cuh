@@ -20,7 +20,7 @@ enum {
     kRow = 121,      // a row index outside [0, T)
     kCols = 122,     // a column range outside the row (or the chunk) it belongs to
     kChunk = 123,    // a chunk / segment index outside its table
-    kStage = 124,    // a shared-memory stage or ring slot outside the ring
+    kStage = 124,    // a shared-memory stage, ring or table slot outside its ring or table
     kTile = 125,     // a GEMM output tile row or column outside the output
 };
 
