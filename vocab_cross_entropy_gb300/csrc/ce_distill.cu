@@ -84,6 +84,7 @@ struct alignas(16) Ctl {
     float red_m[kConsumerWarps], red_s[kConsumerWarps];
     Top top;                     // of the entries
     int code;                    // error found among the entries
+    int skip;                    // the row is ignored
 };
 
 struct alignas(8) Entry {        // of each teacher entry
@@ -365,14 +366,20 @@ __global__ void __launch_bounds__(kThreads, 2) k_distill_long(const __grid_const
     O* grow = static_cast<O*>(a.grad) + row * a.ld_g;
     const bool vec = grads_aligned<S, O>(r, grow);
 
-    // a row without a teacher or with the ignored label: nothing of it is read (all blocks alike)
-    if (ids[0] == -1 || (a.labels && a.labels[row] == a.ignore_index)) {
+    // A row without a teacher or with the ignored label: nothing of it is read (all blocks alike; were the
+    // teacher written meanwhile they might not be, so one thread looks for a block, and a block that skips the
+    // row stays while others may write into it).
+    if (tid == 0) ctl.skip = ids[0] == -1 || (a.labels && a.labels[row] == a.ignore_index);
+    __syncthreads();
+    if (ctl.skip) {
         if (rank == 0 && tid == 0) {
             a.loss_rows[row] = 0.f;
             a.row_stats[row] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
         fill_grads<S, O>(r, sl, grow, vec, tid, kThreads);
         if (a.red == VCE_RED_MEAN) wait_previous();
+        if (C > 1)
+            for (int i = 0; i < 3; ++i) cluster_arrive(), cluster_wait();   // as many as below
         return;
     }
 
@@ -1133,11 +1140,20 @@ struct BwdArgs {
     int withhold;                // 1 (test hook): a row's last block waits for its last stage in vain
 };
 
+// One thread reads the row's statistics for the block: were they written meanwhile (a caller that does not
+// wait for the forward's stream), threads that read for themselves could part ways at the row's weight, some
+// of them gone before the barriers are set up that the others use.
+struct alignas(16) BwdCtl {
+    float4 st;
+    Barriers bar;
+};
+
 template <typename S, typename O>
 __global__ void __launch_bounds__(kConsumers + 32, 3) k_distill_bwd(const __grid_constant__ BwdArgs a) {
     constexpr int G = Elt<S>::kGroup;
     extern __shared__ __align__(128) uint8_t smem[];
-    Barriers& bar = *reinterpret_cast<Barriers*>(smem + a.nbuf * kStageBytes);
+    BwdCtl& ctl = *reinterpret_cast<BwdCtl*>(smem + a.nbuf * kStageBytes);
+    Barriers& bar = ctl.bar;
     const int tid = threadIdx.x, warp = tid >> 5;
     const int64_t row = blockIdx.x / a.parts;
     const Row r = make_row<S>(a.logits, row, a.ld, a.V);
@@ -1145,19 +1161,24 @@ __global__ void __launch_bounds__(kConsumers + 32, 3) k_distill_bwd(const __grid
     const Slice sl = make_slice(r, a.parts, part);
     O* grow = static_cast<O*>(a.grad) + row * a.ld_g;
     const bool vec = grads_aligned<S, O>(r, grow);
-    const float4 st = a.row_stats[row];
+    const int copies = sl.nst - (a.withhold && part == a.parts - 1);
+    int issued = 0;
+    if (tid == kConsumers) {
+        const float4 st = a.row_stats[row];
+        ctl.st = st;
+        init_barriers(bar, a.nbuf);
+        if (st.w != 0.f)
+            for (; issued < min(copies, a.nbuf); ++issued)
+                issue_stage(smem, bar, a.nbuf, r, sl, issued, issued, a.wait_ns);
+    }
+    const float go = a.go[a.red == VCE_RED_NONE ? row : 0];
+    __syncthreads();
+    const float4 st = ctl.st;
     if (st.w == 0.f) {
         fill_grads<S, O>(r, sl, grow, vec, tid, kConsumers + 32);
         return;
     }
-    const int copies = sl.nst - (a.withhold && part == a.parts - 1);
-    int issued = 0;
-    if (tid == kConsumers) {
-        init_barriers(bar, a.nbuf);
-        for (; issued < min(copies, a.nbuf); ++issued) issue_stage(smem, bar, a.nbuf, r, sl, issued, issued, a.wait_ns);
-    }
-    const float cw = a.go[a.red == VCE_RED_NONE ? row : 0] * st.w;
-    __syncthreads();
+    const float cw = go * st.w;
     if (warp == kConsumerWarps) {
         if (tid == kConsumers)
             for (; issued < copies; ++issued)
@@ -1317,7 +1338,7 @@ cudaError_t run_bwd(BwdArgs& a, cudaStream_t s) {
     const int64_t nv = (a.V + 2 * G - 2) / G;
     a.parts = (int)((nv + 4 * kStageVecs - 1) / (4 * kStageVecs));   // four stages a block
     a.nbuf = (int)std::min<int64_t>(4, (nv + kStageVecs - 1) / kStageVecs);
-    const int bytes = a.nbuf * kStageBytes + (int)sizeof(Barriers);
+    const int bytes = a.nbuf * kStageBytes + (int)sizeof(BwdCtl);
     return launch_clusters<k_distill_bwd<S, O>>(a.T * a.parts, 1, kConsumers + 32, bytes, s, a);
 }
 
