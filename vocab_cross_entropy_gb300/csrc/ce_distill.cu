@@ -22,12 +22,12 @@
 //   k_distill_count    N, before a one-pass call with MEAN
 // Nothing is shared between launches.
 //
-// What bounds them, bf16 with 64 entries a row: the forward reads the logits once (4096 x 128256: 163 us,
-// 6.5 TB/s, 0.95 of the measured copy), one pass also writes the gradient (16384 x 128256: 1448 us, 5.8
-// TB/s, 0.86; a row's exponentials are taken twice, about 20 issue slots a column of 24 that the
-// copy's time leaves), the backward runs at the copy's speed (4096 x 128256: 299 us).  Short rows cost
-// the consumer warps about 1 us beside their columns: 4096 rows of 32000 take 67 us forward (3.9 TB/s)
-// and 125 us in one pass (4.2 TB/s).
+// What bounds them, bf16 with 64 entries a row: the forward reads the logits once (4096 x 128256: 160 us,
+// 6.6 TB/s, 0.97 of the measured copy), one pass also writes the gradient (16384 x 128256: 1424 us, 5.9
+// TB/s, 0.87; a row's exponentials are taken twice, 17 warp instructions for 32 columns where the
+// copy's time leaves 24), the backward runs at the copy's speed (4096 x 128256: 307 us).  Short rows cost
+// the consumer warps about 1 us beside their columns: 4096 rows of 32000 take 78 us forward (3.4 TB/s)
+// and 134 us in one pass (3.9 TB/s).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -562,11 +562,12 @@ namespace ring {
 //  - Forward: of a long row one block an SM, 16 consumer warps and 32 KB stages (less to do per stage).
 //    A short row costs a block's consumers about 1 us beside its columns (the merge of their pairs, the
 //    hand-over, the next row's extent); so two blocks an SM take them, with 8 warps and 16 KB stages, and
-//    each covers the other's (4096 x 32000 bf16: 67 us, and 78 with one block).
+//    each covers the other's (4096 x 32000 bf16: 80 us a call, and 102 with one block).
 //  - One pass: one block an SM, whose shared memory holds a row and the beginning of the next (two blocks
-//    at 4096 x 32000 bf16: 194 us against 125); 16 KB stages, so that a held row gives them back in small
-//    steps.  Two top warps have time enough for long rows, short ones take four (16384 x 128256 bf16: 1433
-//    us with two, 1496 with four; 1023 x 32001 bf16 to fp32: 70 and 59).
+//    at 4096 x 32000 bf16, measured when stages were released ahead of their use: 194 us against 125);
+//    16 KB stages, so that a held row gives them back in small steps.  Two top warps have time enough for long
+//    rows, short ones take four (16384 x 128256 bf16: 1427 us a call with two, 1526 with four; 1023 x 32001
+//    bf16 to fp32: 75 and 65).
 constexpr int64_t kLongRow = 131072;
 template <bool kGrad, bool kBig>
 struct Form {

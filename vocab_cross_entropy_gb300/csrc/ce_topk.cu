@@ -20,9 +20,9 @@
 // equal to it are taken in column order.
 //
 // What bounds it: many rows (k_topk_rows) the stream, with the selection of a row beside the next
-// one's copies (8192 x 128256 bf16, K 64: 384 us, 5.5 TB/s, 0.81 of the measured copy); few rows (k_topk)
-// the chain of a launch: copies, maxima, search, read again, rank, merge (one row of 128256: 10.3 us;
-// 64 x 32001 fp32: 13.1 us, 0.6 TB/s).
+// one's copies (8192 x 128256 bf16, K 64: 394 us, 5.4 TB/s, 0.79 of the measured copy); few rows (k_topk)
+// the chain of a launch: copies, maxima, search, read again, rank, merge (one row of 128256: 11 us;
+// 64 x 32001 fp32: 13.8 us, 0.6 TB/s).
 #include <cuda_runtime.h>
 #include <stdint.h>
 

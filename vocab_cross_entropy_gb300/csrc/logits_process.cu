@@ -19,15 +19,16 @@
 // column.
 //
 // Measured at 4096 x 32000 bf16, backward, 384 tokens a row, half of the rows masked but for 50
-// columns: 104 us, 66 without the history (a copy of the matrix: 77).  The rest is the touch: three
+// columns: 104 us, 71 without the history (a copy of the matrix: 79).  The rest is the touch: three
 // scattered accesses a column, one of them to logits that nothing else reads (64 bytes of DRAM
 // each).  A stream that looked at the words beside its vectors took 190 us (most warps meet one of
 // the columns), a second kernel for the listed columns 151 us.  At 256 x 128256 bf16 with about
-// 3000 tokens a row: 40 us, 26 without the tokens; at 37 x 32001 fp32 with 15000: 11.3 us, 3.6 without
-// them.  What the tokens cost is their instructions (each of a row's blocks looks at all of them) and the
-// wait for them behind other blocks' streams.  Tried at these two shapes: a range's own tokens sorted out
-// first, so that full warps count them, 52 and 25 us; the tokens shared out among a cluster's blocks, which
-// count into one another's shared memory, 15.5 us at the second.
+// 3000 tokens a row: 40 us; 26 for the same launch when no row has a token, 24 in the form for short
+// histories, 18 without lists.  At 37 x 32001 fp32 with 15000: 11.9 us; 4.5, 4.2 and 3.3.  What the tokens
+// cost is their instructions (each of a row's blocks looks at all of them) and the wait for them behind
+// other blocks' streams.  Tried at these two shapes: a range's own tokens sorted out first, so that full
+// warps count them, 52 and 25 us; the tokens shared out among a cluster's blocks, which count into one
+// another's shared memory, 15.5 us at the second.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
