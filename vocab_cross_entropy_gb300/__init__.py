@@ -21,7 +21,10 @@ __all__ = ["VceError", "lib", "library_path", "ce_forward", "ce_backward", "ce_f
            "restore_library",
            "vce_abi_version", "cross_entropy", "IGNORE_INDEX", "F32", "BF16", "RED",
            "ce_topk", "ce_distill_forward", "ce_distill_backward", "ce_distill_forward_backward",
-           "distill_cross_entropy", "logits_process", "logits_process_backward", "process_logits", "MAX_TOPK"]
+           "distill_cross_entropy", "logits_process", "logits_process_backward", "process_logits", "MAX_TOPK",
+           "ce_logprobs_forward", "ce_logprobs_backward", "token_logprobs", "policy_loss_forward",
+           "policy_loss_backward", "policy_loss_forward_backward", "policy_loss", "preference_loss_forward",
+           "preference_loss_backward", "preference_loss", "quantize_fp8", "linear_fp8", "FP8_BLOCK"]
 
 IGNORE_INDEX = -100
 F32, BF16 = 0, 1
@@ -106,12 +109,24 @@ def _load(path=None):
                                  p]
     L.logits_process_backward.argtypes = [p, i32, i64, i64, i64, p, i32, i64, p, p, p, i64, p, p, i64, p, i32, i64, p,
                                           p]
+    rows = [p, i32, i64, i64, i64]
+    L.ce_logprobs_forward.argtypes = rows + [p, i64, f32, p, p, p, p, p]
+    L.ce_logprobs_backward.argtypes = rows + [p, f32, p, p, p, p, i32, i64, p]
+    L.policy_loss_forward.argtypes = rows + [p, i64, f32, p, p, p, p, p, i32, p, p, p, p, p, p, p]
+    L.policy_loss_backward.argtypes = rows + [p, f32, i32, p, p, p, i32, i64, p]
+    L.policy_loss_forward_backward.argtypes = rows + [p, i64, f32, p, p, p, p, p, i32, p, p, p, p, p, p, p, i32, i64, p, p]
+    L.preference_loss_forward.argtypes = rows + [p, i64, f32, p, i64, p, p, i32, p, p, p, p, p, p, p]
+    L.preference_loss_backward.argtypes = rows + [p, f32, i64, i32, p, p, p, i32, i64, p]
+    L.vce_quantize_fp8.argtypes = rows + [i32, p, p, p]
+    L.vce_linear_fp8.argtypes = [p, p, p, p, i64, i64, i64, p, i32, i64, p]
     if hasattr(L, "vce_test_topk_stall"):
         u64 = ctypes.c_uint64
         L.vce_test_topk_stall.argtypes = [p, i64, i64, i32, p, p, p, p, u64, p]
         L.vce_test_distill_stall.argtypes = [p, i64, i64, p, p, i32, p, p, p, p, p, u64, p, p]
         L.vce_test_distill_bwd_stall.argtypes = [p, i64, i64, p, i32, p, p, p, p, u64, p]
-    for name in ("ce_topk", "ce_distill_forward", "ce_distill_backward", "ce_distill_forward_backward",
+    for name in ("ce_logprobs_forward", "ce_logprobs_backward", "policy_loss_forward", "policy_loss_backward",
+                 "policy_loss_forward_backward", "preference_loss_forward", "preference_loss_backward",
+                 "vce_quantize_fp8", "vce_linear_fp8", "ce_topk", "ce_distill_forward", "ce_distill_backward", "ce_distill_forward_backward",
                  "logits_process", "logits_process_backward", "ce_forward", "ce_backward", "ce_forward_ls", "ce_backward_ls", "ce_forward_backward",
                  "ce_forward_backward_ls", "ce_merge_chunks_ls",
                  "ce_merge_chunks", "ce_merge_chunks_noalloc",
@@ -570,3 +585,7 @@ def cross_entropy(logits, labels, ignore_index=IGNORE_INDEX, reduction="mean", l
 from .logits_ops import (MAX_TOPK, ce_distill_backward, ce_distill_forward, ce_distill_forward_backward,  # noqa: E402
                          ce_topk, distill_cross_entropy, logits_process, logits_process_backward, process_logits,
                          vce_test_distill_bwd_stall, vce_test_distill_stall, vce_test_topk_stall)
+from .policy_ops import (ce_logprobs_backward, ce_logprobs_forward, policy_loss, policy_loss_backward,  # noqa: E402
+                         policy_loss_forward, policy_loss_forward_backward, preference_loss,
+                         preference_loss_backward, preference_loss_forward, token_logprobs)
+from .fp8_ops import FP8_BLOCK, linear_fp8, quantize_fp8  # noqa: E402

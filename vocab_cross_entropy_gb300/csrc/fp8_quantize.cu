@@ -1,0 +1,108 @@
+// A matrix to e4m3 with a power of two for each block of 1 x 128 or 128 x 128 elements.
+//
+// The scale is the least 2^k with max |x| <= 448 * 2^k: with max |x| = f 2^e, 1 <= f < 2, and 448 = 1.75 * 2^8,
+// k = e - 8 or, for f > 1.75, e - 7.  Multiplying by 2^-k is exact, so q carries the one rounding to e4m3.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "row_launch.h"
+#include "vce_device.cuh"
+#include "vce_check.cuh"
+#include "vce_fp8.h"
+#include "vce_host.h"
+
+namespace vce {
+namespace fp8 {
+
+struct QuantArgs {
+    const void* x;
+    int64_t R, D, ld;
+    uint8_t* q;
+    float* scales;
+    int64_t nd;                  // blocks of 128 columns
+};
+
+// Two floats to e4m3 (the first in the low byte), to nearest even.
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// The block's scale and its reciprocal from its largest magnitude.
+__device__ __forceinline__ float scale_of(float amax, float& inv) {
+    if (!(amax < kInf)) return inv = __int_as_float(0x7FC00000);
+    if (amax == 0.f) return inv = 1.f;
+    const uint32_t b = __float_as_uint(amax);
+    int k = (int)(b >> 23) - 127 - 8 + ((b & 0x7FFFFFu) > 0x600000u);
+    k = max(k, -126);                                // subnormal magnitudes too
+    inv = __int_as_float((127 - k) << 23);
+    return __int_as_float((k + 127) << 23);
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+
+constexpr int kThreads = 256;
+
+// One block of the matrix a thread block.
+template <typename S, int kRows>
+__global__ void __launch_bounds__(kThreads) k_quantize(const __grid_constant__ QuantArgs a) {
+    __shared__ float part[kThreads / 32];
+    const int64_t nb = blockIdx.x, rb = nb / a.nd, cb = nb - rb * a.nd;
+    const int64_t r0 = rb * kRows, c0 = cb * 128;
+    const int rows = (int)min((int64_t)kRows, a.R - r0), cols = (int)min((int64_t)128, a.D - c0);
+    const S* x = static_cast<const S*>(a.x) + r0 * a.ld + c0;
+    float m = 0.f;
+    for (int i = threadIdx.x; i < rows * 128; i += kThreads)
+        if (i % 128 < cols) m = max_nan(m, fabsf(Elt<S>::load1(x + (int64_t)(i / 128) * a.ld + i % 128)));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = max_nan(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+    __syncthreads();
+    m = 0.f;
+    for (int w = 0; w < kThreads / 32; ++w) m = max_nan(m, part[w]);
+    float inv;
+    const float scale = scale_of(m, inv);
+    if (threadIdx.x == 0) a.scales[nb] = scale;
+    for (int i = threadIdx.x; i < rows * 128; i += kThreads)
+        if (i % 128 < cols)
+            a.q[(r0 + i / 128) * a.D + c0 + i % 128] =
+                (uint8_t)to_e4m3x2(Elt<S>::load1(x + (int64_t)(i / 128) * a.ld + i % 128) * inv, 0.f);
+}
+
+}  // namespace fp8
+}  // namespace vce
+
+using namespace vce;
+
+extern "C" int vce_quantize_fp8(const void* x, vce_dtype dt, int64_t R, int64_t D, int64_t ld, int block_rows, void* q,
+                                float* scales, vce_stream_t s) {
+    if (dt != VCE_F32 && dt != VCE_BF16) return VCE_ERR_DTYPE;
+    if (R < 0 || R > (int64_t)1 << 27 || D < 1 || D > (int64_t)1 << 24) return VCE_ERR_SHAPE;
+    if (block_rows != 1 && block_rows != VCE_FP8_BLOCK) return VCE_ERR_ARG;
+    if (ld < D) return VCE_ERR_LD;
+    const size_t es = dt == VCE_BF16 ? 2 : 4;
+    if (!fits_bytes(R, ld, es)) return VCE_ERR_SHAPE;
+    const int64_t nd = (D + 127) / 128, blocks = (R + block_rows - 1) / block_rows * nd;
+    if (blocks >= (int64_t)1 << 31) return VCE_ERR_SHAPE;
+    if (R == 0) return VCE_OK;
+    if (!x || !q || !scales) return VCE_ERR_NULL;
+    if (!aligned(x, es) || !aligned(scales, 4)) return VCE_ERR_ALIGN;
+    int rc = require_sm100();
+    if (rc) return rc;
+    const fp8::QuantArgs a{x, R, D, ld, static_cast<uint8_t*>(q), scales, nd};
+    cudaError_t e;
+    if (dt == VCE_BF16)
+        e = block_rows == 1 ? rs::launch_clusters<fp8::k_quantize<uint16_t, 1>>(blocks, 1, fp8::kThreads, 0, s, a)
+                            : rs::launch_clusters<fp8::k_quantize<uint16_t, 128>>(blocks, 1, fp8::kThreads, 0, s, a);
+    else
+        e = block_rows == 1 ? rs::launch_clusters<fp8::k_quantize<float, 1>>(blocks, 1, fp8::kThreads, 0, s, a)
+                            : rs::launch_clusters<fp8::k_quantize<float, 128>>(blocks, 1, fp8::kThreads, 0, s, a);
+    return record_cuda(e) == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
+}

@@ -1,0 +1,221 @@
+// A row's log-probability of one column, its entropy, and their gradient: the arithmetic shared by the
+// post-training losses' kernels (policy_forward.cu, policy_grad.cu).
+//
+// Mathematics.  With k2 = log2(e) / temperature and "rest" the columns but the token's, one read of
+// the row gives (m, s, w): s = sum 2^(z k2 - m), w = sum 2^(z k2 - m) (z k2 - m) over the rest.  Then
+//   u = L' - x_t = ln 2 (m - z_t k2 + log2 s),   log p_t = -softplus(u),   1 - p_t = sigmoid(u)
+//   H' = ln 2 (log2 s - w / s)                   the entropy of the rest among itself
+//   H = p_t softplus(u) + (1 - p_t) (softplus(-u) + H')
+// the chain rule of entropy: a sum of terms >= 0, so neither a confident row nor a flat one cancels.
+// For a loss with derivatives a = dl/dlog p_t and b = dl/dH, p_j = f 2^(z_j k2 - m) with
+// f = (1 - p_t) / s, and log p_j = ln 2 (z_j k2 - m) + ln f:
+//   dl/dz_j = 2^y (c0 + c1 y), y = z_j k2 - m,   c0 = f (-a - b (ln f + H)) / T,  c1 = -b f ln 2 / T
+//   dl/dz_t = (a (1 - p_t) - b p_t (log p_t + H)) / T
+// The exponents are taken from m, not from the log-sum-exp: m is some z_j k2 (or a thread's first
+// maximum), exact, where a log-sum-exp of size 16 would be rounded by 5e-7 of every p_j.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "row_stream.cuh"
+#include "vce_device.cuh"
+
+namespace vce {
+namespace lp {
+
+using rs::kLn2;
+constexpr float kLn2Lo = -1.90465431e-9f;            // ln 2 = kLn2 + kLn2Lo
+
+__device__ __forceinline__ float nan_f() { return __int_as_float(0x7FC00000); }
+
+// ---- (reference, sum, sum of products): s = sum 2^y, w = sum 2^y y, y = z k2 - m ------------------------
+
+struct Sums {
+    float m, s, w;
+};
+
+// (s, w) to the reference M >= m.
+__device__ __forceinline__ void rescale(Sums& x, float M) {
+    const float d = x.m - M;
+    const float e = (x.m == M) ? 1.f : ex2(d);
+    x.w = e == 0.f ? 0.f : e * (x.m == M ? x.w : fmaf(d, x.s, x.w));
+    x.s *= e;
+    x.m = M;
+}
+
+__device__ __forceinline__ void merge(Sums& x, Sums y) {
+    const float M = fmaxf(x.m, y.m);
+    rescale(x, M);
+    rescale(y, M);
+    x.s += y.s;
+    x.w += y.w;
+}
+
+template <bool kEnt>
+__device__ __forceinline__ void warp_merge(Sums& x) {
+    float M = x.m;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, off));
+    rescale(x, M);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        x.s += __shfl_xor_sync(0xFFFFFFFFu, x.s, off);
+        if (kEnt) x.w += __shfl_xor_sync(0xFFFFFFFFu, x.w, off);
+    }
+}
+
+// (d0, d1) = (a0 * b0 + c0, a1 * b1 + c1) in one packed instruction.
+__device__ __forceinline__ void ffma2v(float a0, float a1, float b0, float b1, float c0, float c1, float& d0, float& d1) {
+    asm("{\n\t.reg .b64 pa, pb, pc, pd;\n\t"
+        "mov.b64 pa, {%2, %3};\n\tmov.b64 pb, {%4, %5};\n\tmov.b64 pc, {%6, %7};\n\t"
+        "fma.rn.f32x2 pd, pa, pb, pc;\n\tmov.b64 {%0, %1}, pd;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+
+// s and w of a thread's vectors against the reference m.  An exponent of -inf (a mask) has the product 0:
+// the factor is held at -200, whose power of two is 0.  A NaN stays one (in s).
+template <int G, int U, bool kEnt>
+__device__ __forceinline__ void sums_of(const float (&v)[U][G], float k2, float m, float& s, float& w) {
+    if (!kEnt) {
+        s = rs::sum_exp<G>(v, k2, m);
+        w = 0.f;
+        return;
+    }
+    float s0[U], s1[U], w0[U], w1[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        s0[u] = s1[u] = w0[u] = w1[u] = 0.f;
+#pragma unroll
+        for (int k = 0; k < G; k += 2) {
+            float a0, a1;
+            ffma2(v[u][k], v[u][k + 1], k2, -m, a0, a1);
+            const float e0 = ex2(a0), e1 = ex2(a1);
+            rs::fadd2(s0[u], s1[u], e0, e1, s0[u], s1[u]);
+            ffma2v(e0, e1, fmaxf(a0, -200.f), fmaxf(a1, -200.f), w0[u], w1[u], w0[u], w1[u]);
+        }
+    }
+#pragma unroll
+    for (int d = 1; d < U; d *= 2)
+#pragma unroll
+        for (int u = 0; u + d < U; u += 2 * d) {
+            rs::fadd2(s0[u], s1[u], s0[u + d], s1[u + d], s0[u], s1[u]);
+            rs::fadd2(w0[u], w1[u], w0[u + d], w1[u + d], w0[u], w1[u]);
+        }
+    s = s0[0] + s1[0];
+    w = w0[0] + w1[0];
+}
+
+// Adds a thread's vectors of a stage; the reference moves only when a term would pass 2^32.
+template <int G, int U, bool kEnt>
+__device__ __forceinline__ void push(const float (&v)[U][G], Sums& x, float k2) {
+    if (x.m == -kInf) {
+        x.m = rs::max_of<G>(v) * k2;
+        if (x.m == -kInf) return;
+    }
+    float s, w;
+#pragma unroll 1
+    for (int again = 0;; again = 1) {   // one copy of the sum's code, for the instruction cache
+        sums_of<G, U, kEnt>(v, k2, x.m, s, w);
+        if (again || s < 4294967296.f) break;
+        rescale(x, fmaxf(x.m, rs::max_of<G>(v) * k2));
+    }
+    x.s += s;
+    if (kEnt) x.w += w;
+}
+
+// ---- a row's scalars ---------------------------------------------------------------------------------
+
+// What a row's sums and its token's logit say.  dead: nothing but masks (everything NaN, no gradient).
+struct Row {
+    float m, f, lp, lp_lo, ent;   // lp + lp_lo: log p_t to about twice the digits
+    bool dead;
+};
+
+// c - a b as hi + lo.
+__device__ __forceinline__ float minus_product(float c, float a, float b, float& lo) {
+    const float p = a * b, pe = fmaf(a, b, -p);
+    const float hi = c - p, t = hi - c;
+    lo = ((c - (hi - t)) + (-p - t)) - pe;           // Knuth's TwoSum of c and -p
+    return hi;
+}
+
+// The logarithm of a normal s > 0 as an integer's worth of ln 2 and the logarithm of a number near 1.
+__device__ __forceinline__ float split_log(float s, float& near) {
+    const int e = (__float_as_int(s) - 0x3F3504F3) >> 23;    // s = 2^e r, r in [sqrt 1/2, sqrt 2)
+    near = logf(__int_as_float(__float_as_int(s) - (e << 23)));
+    return (float)e;
+}
+
+__device__ __forceinline__ Row finish(const Sums& x, float zt, float k2) {
+    Row r;
+    r.dead = false;
+    r.lp_lo = 0.f;
+    const bool rest = x.s > 0.f, tok = zt * k2 > -kInf;
+    if (!(x.s >= 0.f && x.s < kInf && zt * k2 < kInf)) {   // a NaN or +inf somewhere
+        r.m = 0.f;
+        r.f = r.lp = r.ent = nan_f();
+        return r;
+    }
+    if (!rest) {                                     // p_t = 1, or nothing at all
+        r.dead = !tok;
+        r.m = r.f = 0.f;
+        r.lp = r.ent = tok ? 0.f : nan_f();
+        return r;
+    }
+    float near;
+    const float e = split_log(x.s, near);
+    const float hrest = fmaxf(0.f, fmaf(e - x.w / x.s, kLn2, near));
+    r.m = x.m;
+    if (!tok) {
+        r.f = 1.f / x.s;
+        r.lp = -kInf;
+        r.ent = hrest;
+        return r;
+    }
+    float lo;
+    const float gap = minus_product(x.m, zt, k2, lo);
+    const float g = gap + e, t = g - gap;            // TwoSum of gap and e
+    lo += (gap - (g - t)) + (e - t);
+    float u = g * kLn2;
+    float ul = fmaf(g, kLn2, -u) + fmaf(g, kLn2Lo, fmaf(lo, kLn2, near));
+    if (!(fabsf(u) < kInf)) ul = 0.f;
+    const float v = u + ul;
+    ul = fabsf(u) < kInf ? ul - (v - u) : 0.f;
+    u = v;
+    // softplus of u + ul, and of its negative
+    const float E = expf(-fabsf(u)), l = log1pf(E), d = 1.f / (1.f + E);
+    const float pnt = u >= 0.f ? d : E * d, pt = u >= 0.f ? E * d : d;
+    const float sp = u >= 0.f ? u + l : l, spn = u >= 0.f ? l : l - u;
+    r.lp = -sp;
+    r.lp_lo = u >= 0.f && u < kInf ? -((u - (sp - l)) + (l - (sp - (sp - l))) + ul * pnt) : -ul * pnt;
+    if (u < 0.f) {
+        const float a = r.lp + r.lp_lo;
+        r.lp_lo -= a - r.lp;
+        r.lp = a;
+    }
+    r.ent = (pt > 0.f ? pt * sp : 0.f) + (pnt > 0.f ? pnt * (spn + hrest) : 0.f);
+    r.f = pnt / x.s;
+    return r;
+}
+
+// The gradient's coefficients (see above).
+struct Coefs {
+    float c0, c1, gt;
+};
+__device__ __forceinline__ Coefs coefs(float f, float lp, float ent, float a, float b, float inv_tau) {
+    const float pt = expf(lp), pnt = -expm1f(lp);
+    Coefs c;
+    c.gt = inv_tau * (a * pnt - (b != 0.f && pt > 0.f ? b * pt * (lp + ent) : 0.f));
+    c.c0 = c.c1 = 0.f;
+    if (f != 0.f) {
+        c.c0 = inv_tau * f * (b != 0.f ? -a - b * (logf(f) + ent) : -a);
+        c.c1 = b != 0.f ? -inv_tau * f * b * kLn2 : 0.f;
+    }
+    if (f != f || lp != lp) c.c0 = c.gt = nan_f();
+    return c;
+}
+
+}  // namespace lp
+}  // namespace vce

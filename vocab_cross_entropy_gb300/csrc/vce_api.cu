@@ -114,7 +114,9 @@ extern "C" int vce_debug_status(int32_t* host_out) {
     int (*const readers[])(int32_t*) = {vce::debug_word_ce_fwd,   vce::debug_word_ce_bwd, vce::debug_word_ce_fwd_ring,
                                         vce::debug_word_ce_bwd_ring, vce::debug_word_ce_ring, vce::debug_word_ce_fused,
                                         vce::debug_word_lce,      vce::debug_word_gemm_hooks, vce::debug_word_topk,
-                                        vce::debug_word_distill,  vce::debug_word_process};
+                                        vce::debug_word_distill,  vce::debug_word_process,
+                                        vce::debug_word_policy,   vce::debug_word_policy_grad,
+                                        vce::debug_word_policy_onepass};
     for (auto rd : readers) {
         int32_t w = 0;
         if (rd(&w) != 0) return VCE_ERR_CUDA;
