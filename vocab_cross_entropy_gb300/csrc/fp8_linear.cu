@@ -1,11 +1,26 @@
-// Logits of a head in e4m3 with block scales.
+// Logits of a head in e4m3 with block scales on the tensor cores (tcgen05, kind::f8f6f4):
+//     out[t][v] = sum_b xs[t][b] ws[v / 128][b] sum_{k in block b} x[t][k] w[v][k]
+//
+// The scales change every 128 columns of K and differ along t and v, so a block's products are summed by the
+// tensor cores into a fresh accumulator of tensor memory (four MMAs of K = 32), and the block's sum is scaled and
+// added to the running sum in registers, while the tensor cores work on the next block in the other accumulator.
+//
+//   k_linear_pair  T > 64: CTA pairs (cta_group::2) on 256 x 256 tiles, 128 rows of x and half of the tile's rows
+//                  of w per CTA and K block.  16 epilogue warps, each 32 rows x 64 columns in registers: per K
+//                  block and SM 32768 fma (256 cycles of the fma pipe) against the MMAs' 512 cycles.
+//   k_linear_few   T <= 64: bound by reading w.  The roles change sides: w's rows are the MMA's 128, the rows of x
+//                  its N (16, 32 or 64 wide), so a stage is w's 16 KB and little else.  Where w has fewer tiles
+//                  than there are SMs, a cluster's CTAs each take a part of K and the first adds the others' sums
+//                  in order.
+// Every wait is bounded (2 s); where one gives up, the CTA's tiles become NaN.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "row_launch.h"
-#include "vce_device.cuh"
+#include "tc_launch.cuh"
 #include "vce_check.cuh"
 #include "vce_fp8.h"
 #include "vce_host.h"
@@ -13,62 +28,546 @@
 namespace vce {
 namespace fp8 {
 
+using namespace tc;
+
+constexpr int kBlock = VCE_FP8_BLOCK;                // K columns (bytes) of a block
+
 struct LinearArgs {
-    const uint8_t* x;
     const float* xs;
-    const uint8_t* w;
     const float* ws;
-    int64_t T, D, V;
-    int nd;
+    int64_t T, V;
+    int nd;                      // blocks of K
     void* out;
     int64_t ld;
+    int tiles_m, tiles_n;        // k_linear_pair
+    int split;                   // k_linear_few: CTAs that share a tile's K
+    int aligned;                 // out's rows start on 16-byte boundaries
 };
 
-__device__ __forceinline__ float from_e4m3(uint8_t v) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)v));
-    float f;
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;\n\t}" : "=f"(f) : "r"(h));
-    return f;
+template <bool kCta2>
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate) {
+    if constexpr (kCta2)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+            : "memory");
 }
 
-constexpr int kTile = 32;
+// Instruction descriptor, kind::f8f6f4: fp32 accumulator, e4m3 A and B (format 0), both K-major, M x N.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
 
-// A 32 x 32 tile of the logits a block, a quarter of a block of 128 columns at a time.
+// 16 consecutive fp32 columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {   // ties r to the wait, as tmem_wait_ld
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+
+// (c0, c1) += (a0, a1) * b, in one packed instruction.
+__device__ __forceinline__ void fma_pair(uint32_t a0, uint32_t a1, float b, float& c0, float& c1) {
+    asm("{\n\t.reg .b64 pa, pb, pc;\n\t"
+        "mov.b64 pa, {%2, %3};\n\tmov.b64 pb, {%4, %4};\n\tmov.b64 pc, {%0, %1};\n\t"
+        "fma.rn.f32x2 pc, pa, pb, pc;\n\tmov.b64 {%0, %1}, pc;\n\t}"
+        : "+f"(c0), "+f"(c1)
+        : "r"(a0), "r"(a1), "f"(b));
+}
+
 template <typename O>
-__global__ void __launch_bounds__(256) k_linear(const __grid_constant__ LinearArgs a) {
-    __shared__ float xt[kTile][33], wt[kTile][33];
-    const int64_t nv = (a.V + kTile - 1) / kTile;
-    const int64_t t0 = blockIdx.x / nv * kTile, v0 = blockIdx.x % nv * kTile;
-    const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
-    float acc[4] = {}, part[4] = {};
-    for (int64_t k0 = 0; k0 < a.D; k0 += 32) {
-        for (int i = 0; i < 4; ++i) {
-            const int r = ty + 8 * i;
-            const int64_t k = k0 + tx;
-            xt[r][tx] = t0 + r < a.T && k < a.D ? from_e4m3(a.x[(t0 + r) * a.D + k]) : 0.f;
-            wt[r][tx] = v0 + r < a.V && k < a.D ? from_e4m3(a.w[(v0 + r) * a.D + k]) : 0.f;
+__device__ __forceinline__ void store_nan(const LinearArgs& a, int64_t t, int64_t v) {
+    if (t < a.T && v < a.V) Elt<O>::store1(static_cast<O*>(a.out) + t * a.ld + v, __int_as_float(0x7FC00000));
+}
+
+// ---- CTA pairs ----------------------------------------------------------------------------------------
+
+constexpr int kM = 128, kN = 256;                    // rows of x per CTA, rows of w per tile
+constexpr int kEpiWarps = 16, kProducer = 16, kIssuer = 17;
+constexpr int kPairThreads = 18 * 32;
+constexpr int kStages = 5;
+constexpr int kTileBytes = kM * kBlock;              // 16 KB: x's rows, and this CTA's half of w's
+constexpr int kStageBytes = 2 * kTileBytes;
+constexpr int kScratch = 32 * 17 * 4;                // per epilogue warp, for the stores
+constexpr int kPairSmem = kStages * kStageBytes + kEpiWarps * kScratch + 1024 /*alignment*/ + 256 /*barriers*/;
+static_assert(kPairSmem <= kMaxSmem, "shared memory");
+
+template <typename O>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    k_linear_pair(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUtensorMap mapW,
+                  const __grid_constant__ LinearArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float* scratch = reinterpret_cast<float*>(smem + kStages * kStageBytes);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes + kEpiWarps * kScratch);
+    uint64_t* empty = full + kStages;
+    uint64_t* acc_full = empty + kStages;
+    uint64_t* acc_free = acc_full + 2;
+    uint64_t* drain = acc_free + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
         }
-        __syncthreads();
-        for (int k = 0; k < 32; ++k)
-            for (int i = 0; i < 4; ++i) part[i] = fmaf(xt[ty + 8 * i][k], wt[tx][k], part[i]);
-        __syncthreads();
-        if ((k0 + 32) % 128 == 0 || k0 + 32 >= a.D) {
-            const int64_t b = k0 / 128;
-            for (int i = 0; i < 4; ++i) {
-                const int64_t t = t0 + ty + 8 * i, v = v0 + tx;
-                if (t < a.T && v < a.V) acc[i] = fmaf(part[i], a.xs[t * a.nd + b] * a.ws[v / 128 * a.nd + b], acc[i]);
-                part[i] = 0.f;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_free[i], 2 * kEpiWarps);   // one arrival per epilogue warp of both CTAs
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        prefetch_map(&mapX);
+        prefetch_map(&mapW);
+    }
+    if (warp == kProducer) {
+        tmem_alloc<true>(tmem_slot, 2 * kN);
+        tmem_relinquish<true>();
+    }
+    tc_fence_before();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    if (threadIdx.x == 0 && rank == 1 && ld_cluster_u32(cluster_addr(tmem_slot, 0)) != tmem) *abort_flag = 1;
+    __syncthreads();
+    const int ntiles = a.tiles_m * a.tiles_n;        // of the pair; tiles that run at once share w's rows
+    const int tile0 = (int)(blockIdx.x >> 1), tstep = (int)(gridDim.x >> 1);
+
+    if (warp == kProducer && lane == 0) {
+        int stage = 0, issued = 0;
+        uint32_t phase = 0;
+        for (int tile = tile0; tile < ntiles && !*abort_flag; tile += tstep) {
+            const int t0 = (tile % a.tiles_m * 2 + (int)rank) * kM, v0 = tile / a.tiles_m * kN + (int)rank * (kN / 2);
+            for (int kb = 0; kb < a.nd; ++kb) {
+                if (!wait_bar<true>(&empty[stage], phase ^ 1u, abort_flag, nullptr, 0, kWaitNs)) break;
+                const uint32_t fb = cluster_addr(&full[stage], 0);   // the even CTA counts both CTAs' bytes
+                if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * kStageBytes);
+                uint8_t* at = smem + stage * kStageBytes;
+                tma_load<true>(at, &mapX, fb, kb * kBlock, t0);
+                tma_load<true>(at + kTileBytes, &mapW, fb, kb * kBlock, v0);
+                issued = issued < kStages ? issued + 1 : kStages;
+                if (++stage == kStages) stage = 0, phase ^= 1u;
+            }
+        }
+        if (*abort_flag) {   // copies in flight land before the CTA may leave
+            const uint64_t t0 = globaltimer();
+            if (rank == 0) {
+                for (int i = 0; i < issued; ++i) {
+                    if (--stage < 0) stage = kStages - 1, phase ^= 1u;
+                    while (!mbar_try_wait(&full[stage], phase) && globaltimer() - t0 < kWaitNs) {
+                    }
+                }
+            } else {         // these complete on the even CTA's barriers: give them time
+                while (globaltimer() - t0 < 1000000ull) {
+                }
+            }
+        }
+    } else if (warp == kIssuer && lane == 0 && rank == 0) {
+        constexpr uint32_t idesc = idesc_e4m3_f32(2 * kM, kN);
+        int stage = 0, acc = 0;
+        uint32_t phase = 0, acc_phase = 0;
+        const uint32_t base = smem_u32(smem);
+        auto commit = [&](uint64_t* bar) {
+            mma_commit<true>(smem_u32(bar));
+            mma_commit<true>(cluster_addr(bar, 1));
+        };
+        for (int tile = tile0; tile < ntiles && !*abort_flag; tile += tstep) {
+            for (int kb = 0; kb < a.nd; ++kb) {
+                if (!wait_bar<true>(&acc_free[acc], acc_phase ^ 1u, abort_flag, nullptr, 0, kWaitNs)) break;
+                if (!wait_bar<false>(&full[stage], phase, abort_flag, nullptr, 0, kWaitNs)) break;
+                tc_fence_after();
+                const uint64_t ad = desc_kmajor_sw128(base + stage * kStageBytes);
+                const uint64_t bd = desc_kmajor_sw128(base + stage * kStageBytes + kTileBytes);
+#pragma unroll
+                for (int k = 0; k < kBlock / 32; ++k)   // 32 bytes of K a step
+                    mma_e4m3<true>(tmem + (uint32_t)(acc * kN), ad + 2 * k, bd + 2 * k, idesc, k ? 1u : 0u);
+                commit(&empty[stage]);
+                commit(&acc_full[acc]);
+                if (++stage == kStages) stage = 0, phase ^= 1u;
+                acc ^= 1;
+                if (acc == 0) acc_phase ^= 1u;
+            }
+        }
+        // every MMA this thread issued has finished before tensor memory can be released
+        mma_commit<true>(smem_u32(drain));
+        const uint64_t t0 = globaltimer();
+        while (!mbar_try_wait(drain, 0) && globaltimer() - t0 < kWaitNs) {
+        }
+    } else if (warp < kEpiWarps) {
+        const int sub = warp & 3, cg = warp >> 2;    // this warp's 32 rows and 64 columns of the CTA's tile
+        const uint32_t taddr = tmem + ((uint32_t)(sub * 32) << 16) + (uint32_t)(cg * 64);
+        float* mine = scratch + warp * (kScratch / 4);
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        bool ok = true;
+        for (int tile = tile0; tile < ntiles && ok; tile += tstep) {
+            const int64_t t0 = (int64_t)(tile % a.tiles_m * 2 + (int)rank) * kM + sub * 32;
+            const int64_t v0 = (int64_t)(tile / a.tiles_m) * kN + cg * 64;
+            const bool active = t0 < a.T && v0 < a.V;
+            const float* xs = a.xs + (t0 + lane < a.T ? t0 + lane : 0) * a.nd;
+            const float* ws = a.ws + (active ? v0 / kBlock : 0) * a.nd;
+            float c[64];
+#pragma unroll
+            for (int i = 0; i < 64; ++i) c[i] = 0.f;
+            float xn = active ? __ldg(xs) : 0.f, wn = active ? __ldg(ws) : 0.f;
+            for (int kb = 0; kb < a.nd; ++kb) {
+                const float s = xn * wn;
+                if (active && kb + 1 < a.nd) xn = __ldg(xs + kb + 1), wn = __ldg(ws + kb + 1);
+                ok = __all_sync(0xFFFFFFFFu, wait_bar<false>(&acc_full[acc], acc_phase, abort_flag, nullptr, 0, kWaitNs));
+                if (!ok) break;
+                tc_fence_after();
+                if (active) {
+                    uint32_t r[2][16];
+                    const uint32_t at = taddr + (uint32_t)(acc * kN);
+                    tmem_ld16(at, r[0]);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        tmem_wait16(r[q & 1]);
+                        if (q < 3) tmem_ld16(at + (q + 1) * 16, r[(q + 1) & 1]);
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2) fma_pair(r[q & 1][i], r[q & 1][i + 1], s, c[q * 16 + i], c[q * 16 + i + 1]);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(cluster_addr(&acc_free[acc], 0));
+                acc ^= 1;
+                if (acc == 0) acc_phase ^= 1u;
+            }
+            if (!ok || !active) continue;
+            O* out = static_cast<O*>(a.out) + t0 * a.ld + v0;
+            if (a.aligned && v0 + 64 <= a.V) {       // each lane its row
+                if (t0 + lane < a.T && dbg::ok(v0 + 64 <= a.ld, dbg::kTile)) {
+                    O* p = out + lane * a.ld;
+#pragma unroll
+                    for (int i = 0; i < 64; i += 8) {
+                        const float g[8] = {c[i], c[i + 1], c[i + 2], c[i + 3], c[i + 4], c[i + 5], c[i + 6], c[i + 7]};
+                        GroupStore<O, 8>::run(p + i, g);
+                    }
+                }
+            } else {                                 // rows of any alignment: 16 columns at a time through shared memory
+                const int rows = (int)min((int64_t)32, a.T - t0);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) mine[lane * 17 + i] = c[q * 16 + i];
+                    __syncwarp();
+                    const int64_t v = v0 + q * 16 + (lane & 15);
+                    if (v < a.V && dbg::ok(v < a.ld, dbg::kTile))
+                        for (int i = lane >> 4; i < rows; i += 2)
+                            Elt<O>::store1(out + i * a.ld + q * 16 + (lane & 15), mine[i * 17 + (lane & 15)]);
+                    __syncwarp();
+                }
             }
         }
     }
-    for (int i = 0; i < 4; ++i) {
-        const int64_t t = t0 + ty + 8 * i, v = v0 + tx;
-        if (t < a.T && v < a.V) Elt<O>::store1(static_cast<O*>(a.out) + t * a.ld + v, acc[i]);
+    tc_fence_before();
+    __syncthreads();
+    if (*abort_flag)
+        for (int tile = tile0; tile < ntiles; tile += tstep)
+            for (int i = threadIdx.x; i < kM * kN; i += kPairThreads)
+                store_nan<O>(a, (int64_t)(tile % a.tiles_m * 2 + (int)rank) * kM + i / kN,
+                             (int64_t)(tile / a.tiles_m) * kN + i % kN);
+    // neither CTA releases its tensor memory or leaves while the other's MMAs, copies or arrivals may reach it
+    cluster_sync_all();
+    if (warp == kProducer) {
+        tc_fence_after();
+        tmem_dealloc<true>(tmem, 2 * kN);
     }
 }
 
+// ---- few rows of x --------------------------------------------------------------------------------------
+
+constexpr int kFewThreads = 6 * 32;                  // 4 epilogue warps, producer, issuer
+template <int N>
+struct Few {
+    static constexpr int kStage = kTileBytes + N * kBlock;
+    static constexpr int kBufs = (kMaxSmem - 2048) / kStage < 12 ? (kMaxSmem - 2048) / kStage : 12;
+    static constexpr int kSmem = kBufs * kStage + 1024 + 512;
+    static constexpr int kCols = 2 * N < 32 ? 32 : 2 * N;            // tensor memory: two accumulators
+    static_assert(kBufs * kStage >= 3 * N * 128 * 4, "the joined sums lie in the stages");
+};
+constexpr int kMaxSplit = 4;
+
+template <typename O, int N>
+__global__ void __launch_bounds__(kFewThreads, 1)
+    k_linear_few(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUtensorMap mapW,
+                 const __grid_constant__ LinearArgs a) {
+    using F = Few<N>;
+    constexpr int S = F::kBufs;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * F::kStage);
+    uint64_t* empty = full + S;
+    uint64_t* acc_full = empty + S;
+    uint64_t* acc_free = acc_full + 2;
+    uint64_t* drain = acc_free + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = a.split > 1 ? (int)cluster_ctarank() : 0;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_free[i], 4);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        prefetch_map(&mapX);
+        prefetch_map(&mapW);
+    }
+    if (warp == 4) {
+        tmem_alloc<false>(tmem_slot, F::kCols);
+        tmem_relinquish<false>();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int ntiles = (int)((a.V + kM - 1) / kM);
+    const int tile0 = (int)blockIdx.x / a.split, tstep = (int)gridDim.x / a.split;
+    const int per = (a.nd + a.split - 1) / a.split, k0 = min(a.nd, rank * per), k1 = min(a.nd, k0 + per);
+
+    float c[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) c[i] = 0.f;
+    if (warp == 4) {
+        if (lane == 0) {
+            int stage = 0, issued = 0;
+            uint32_t phase = 0;
+            for (int tile = tile0; tile < ntiles && !*abort_flag; tile += tstep) {
+                for (int kb = k0; kb < k1; ++kb) {
+                    if (!wait_bar<false>(&empty[stage], phase ^ 1u, abort_flag, nullptr, 0, kWaitNs)) break;
+                    mbar_arrive_expect_tx(&full[stage], F::kStage);
+                    uint8_t* at = smem + stage * F::kStage;
+                    tma_load<false>(at, &mapW, smem_u32(&full[stage]), kb * kBlock, tile * kM);
+                    tma_load<false>(at + kTileBytes, &mapX, smem_u32(&full[stage]), kb * kBlock, 0);
+                    issued = issued < S ? issued + 1 : S;
+                    if (++stage == S) stage = 0, phase ^= 1u;
+                }
+            }
+            if (*abort_flag) {
+                const uint64_t t0 = globaltimer();
+                for (int i = 0; i < issued; ++i) {
+                    if (--stage < 0) stage = S - 1, phase ^= 1u;
+                    while (!mbar_try_wait(&full[stage], phase) && globaltimer() - t0 < kWaitNs) {
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 5) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_e4m3_f32(kM, N);
+            int stage = 0, acc = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            const uint32_t base = smem_u32(smem);
+            for (int tile = tile0; tile < ntiles && !*abort_flag; tile += tstep) {
+                for (int kb = k0; kb < k1; ++kb) {
+                    if (!wait_bar<false>(&acc_free[acc], acc_phase ^ 1u, abort_flag, nullptr, 0, kWaitNs)) break;
+                    if (!wait_bar<false>(&full[stage], phase, abort_flag, nullptr, 0, kWaitNs)) break;
+                    tc_fence_after();
+                    const uint64_t ad = desc_kmajor_sw128(base + stage * F::kStage);
+                    const uint64_t bd = desc_kmajor_sw128(base + stage * F::kStage + kTileBytes);
+#pragma unroll
+                    for (int k = 0; k < kBlock / 32; ++k)
+                        mma_e4m3<false>(tmem + (uint32_t)(acc * N), ad + 2 * k, bd + 2 * k, idesc, k ? 1u : 0u);
+                    mma_commit<false>(smem_u32(&empty[stage]));
+                    mma_commit<false>(smem_u32(&acc_full[acc]));
+                    if (++stage == S) stage = 0, phase ^= 1u;
+                    acc ^= 1;
+                    if (acc == 0) acc_phase ^= 1u;
+                }
+            }
+            mma_commit<false>(smem_u32(drain));
+            const uint64_t t0 = globaltimer();
+            while (!mbar_try_wait(drain, 0) && globaltimer() - t0 < kWaitNs) {
+            }
+        }
+        __syncwarp();
+    } else {
+        // a thread holds row v of w against every row of x; lane t keeps the scales of x's rows t and t + 32
+        const uint32_t taddr = tmem + ((uint32_t)(warp * 32) << 16);
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        bool ok = true;
+        for (int tile = tile0; tile < ntiles && ok; tile += tstep) {
+            const float* ws = a.ws + (int64_t)tile * a.nd;
+            const float* x0 = a.xs + (lane < a.T ? lane : 0) * (int64_t)a.nd;
+            const float* x1 = a.xs + (N > 32 && lane + 32 < a.T ? lane + 32 : 0) * (int64_t)a.nd;
+#pragma unroll
+            for (int i = 0; i < N; ++i) c[i] = 0.f;
+            float n0 = 0.f, n1 = 0.f, wn = 0.f;
+            if (k0 < k1) n0 = __ldg(x0 + k0), n1 = __ldg(x1 + k0), wn = __ldg(ws + k0);
+            for (int kb = k0; kb < k1; ++kb) {
+                const float s0 = n0 * wn, s1 = n1 * wn;
+                if (kb + 1 < k1) n0 = __ldg(x0 + kb + 1), n1 = __ldg(x1 + kb + 1), wn = __ldg(ws + kb + 1);
+                ok = __all_sync(0xFFFFFFFFu, wait_bar<false>(&acc_full[acc], acc_phase, abort_flag, nullptr, 0, kWaitNs));
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t r[N / 16][16];
+#pragma unroll
+                for (int q = 0; q < N / 16; ++q) tmem_ld16(taddr + (uint32_t)(acc * N + q * 16), r[q]);
+#pragma unroll
+                for (int q = 0; q < N / 16; ++q) tmem_wait16(r[q]);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&acc_free[acc]);
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    c[i] = fmaf(__uint_as_float(r[i / 16][i % 16]), __shfl_sync(0xFFFFFFFFu, i < 32 ? s0 : s1, i % 32), c[i]);
+                acc ^= 1;
+                if (acc == 0) acc_phase ^= 1u;
+            }
+            const int64_t v = (int64_t)tile * kM + warp * 32 + lane;
+            if (ok && a.split == 1 && v < a.V && dbg::ok(v < a.ld, dbg::kTile)) {
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    if (i < a.T) Elt<O>::store1(static_cast<O*>(a.out) + i * a.ld + v, c[i]);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (a.split > 1) {
+        // the parts of K: each CTA's sums into the first's stages (its copies have landed and been read), added
+        // there in order
+        cluster_sync_all();
+        if (warp < 4 && rank > 0) {
+            const uint32_t to = cluster_addr(smem, 0) + (uint32_t)(((rank - 1) * N * 128 + threadIdx.x) * 4);
+            const bool bad = *abort_flag != 0;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + i * 512), "f"(bad ? __int_as_float(0x7FC00000) : c[i])
+                             : "memory");
+        }
+        cluster_sync_all();
+        if (warp < 4 && rank == 0) {
+            const float* from = reinterpret_cast<const float*>(smem) + threadIdx.x;
+            const int64_t v = (int64_t)tile0 * kM + threadIdx.x;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                for (int p = 1; p < a.split; ++p) c[i] += from[((p - 1) * N + i) * 128];
+                if (i < a.T && v < a.V && dbg::ok(v < a.ld, dbg::kTile))
+                    Elt<O>::store1(static_cast<O*>(a.out) + i * a.ld + v, c[i]);
+            }
+        }
+        __syncthreads();
+    }
+    if (*abort_flag && rank == 0)
+        for (int tile = tile0; tile < ntiles; tile += tstep)
+            for (int i = threadIdx.x; i < kM * N; i += kFewThreads) store_nan<O>(a, i / kM, (int64_t)tile * kM + i % kM);
+    if (warp == 4) {
+        tc_fence_after();
+        tmem_dealloc<false>(tmem, F::kCols);
+    }
+}
+
+// ---- host --------------------------------------------------------------------------------------------------
+
+// 2-D map over a row-major byte matrix with boxes of 128 bytes (the swizzle span) x box_rows rows.
+bool make_byte_map(CUtensorMap* map, const void* base, int64_t inner, int64_t outer, int box_rows) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
+    cuuint64_t strides[1] = {(cuuint64_t)inner};
+    cuuint32_t box[2] = {(cuuint32_t)kBlock, (cuuint32_t)box_rows};
+    cuuint32_t es[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class K>
+cudaError_t launch(K kern, int blocks, int cluster, int threads, int smem, cudaStream_t s, const CUtensorMap& mx,
+                   const CUtensorMap& mw, const LinearArgs& a) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, mx, mw, a);
+}
+
+template <typename O>
+cudaError_t run_pair(const void* x, const void* w, int64_t D, LinearArgs& a, cudaStream_t s) {
+    CUtensorMap mx, mw;
+    if (!make_byte_map(&mx, x, D, a.T, kM) || !make_byte_map(&mw, w, D, a.V, kN / 2)) return cudaErrorInvalidValue;
+    a.tiles_m = (int)((a.T + 2 * kM - 1) / (2 * kM));
+    a.tiles_n = (int)((a.V + kN - 1) / kN);
+    if ((int64_t)a.tiles_m * a.tiles_n > INT32_MAX / 2) return cudaErrorInvalidValue;
+    static std::atomic<int> ready[kMaxDevices];
+    int clusters = 0;
+    cudaError_t e = prepare_kernel(k_linear_pair<O>, kPairSmem, true, ready, &clusters);
+    if (e != cudaSuccess) return e;
+    if (clusters < 1) return cudaErrorInvalidConfiguration;
+    const int pairs = std::min(a.tiles_m * a.tiles_n, clusters);
+    return launch(k_linear_pair<O>, 2 * pairs, 2, kPairThreads, kPairSmem, s, mx, mw, a);
+}
+
+template <typename O, int N>
+cudaError_t run_few(const void* x, const void* w, int64_t D, LinearArgs& a, cudaStream_t s) {
+    CUtensorMap mx, mw;
+    if (!make_byte_map(&mx, x, D, a.T, N) || !make_byte_map(&mw, w, D, a.V, kM)) return cudaErrorInvalidValue;
+    static std::atomic<int> ready[kMaxDevices];
+    int none = 0;
+    cudaError_t e = prepare_kernel(k_linear_few<O, N>, Few<N>::kSmem, false, ready, &none);
+    if (e != cudaSuccess) return e;
+    const int sms = device_sm_count();
+    const int64_t tiles = (a.V + kM - 1) / kM;
+    a.split = 1;
+    while (a.split < kMaxSplit && tiles * a.split * 2 <= sms && a.nd >= 4 * a.split) a.split *= 2;
+    const int blocks = a.split > 1 ? (int)tiles * a.split : (int)std::min<int64_t>(tiles, sms);
+    return launch(k_linear_few<O, N>, blocks, a.split, kFewThreads, Few<N>::kSmem, s, mx, mw, a);
+}
+
+template <typename O>
+cudaError_t run(const void* x, const void* w, int64_t D, LinearArgs& a, cudaStream_t s) {
+    if (a.T > 64) return run_pair<O>(x, w, D, a, s);
+    if (a.T > 32) return run_few<O, 64>(x, w, D, a, s);
+    if (a.T > 16) return run_few<O, 32>(x, w, D, a, s);
+    return run_few<O, 16>(x, w, D, a, s);
+}
+
 }  // namespace fp8
+
+VCE_DEBUG_READER(debug_word_fp8)
+
 }  // namespace vce
 
 using namespace vce;
@@ -86,10 +585,9 @@ extern "C" int vce_linear_fp8(const void* x, const float* x_scales, const void* 
         return VCE_ERR_ALIGN;
     int rc = require_sm100();
     if (rc) return rc;
-    const fp8::LinearArgs a{static_cast<const uint8_t*>(x), x_scales, static_cast<const uint8_t*>(w), w_scales, T, D, V,
-                            (int)((D + 127) / 128), out, ld};
-    const int64_t blocks = (T + 31) / 32 * ((V + 31) / 32);
-    const cudaError_t e = out_dt == VCE_BF16 ? rs::launch_clusters<fp8::k_linear<uint16_t>>(blocks, 1, 256, 0, s, a)
-                                             : rs::launch_clusters<fp8::k_linear<float>>(blocks, 1, 256, 0, s, a);
+    fp8::LinearArgs a{};
+    a.xs = x_scales, a.ws = w_scales, a.T = T, a.V = V, a.nd = (int)((D + 127) / 128), a.out = out, a.ld = ld, a.split = 1;
+    a.aligned = aligned(out, 16) && ld * (int64_t)es % 16 == 0;
+    const cudaError_t e = out_dt == VCE_BF16 ? fp8::run<uint16_t>(x, w, D, a, s) : fp8::run<float>(x, w, D, a, s);
     return record_cuda(e) == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
 }

@@ -27,12 +27,23 @@ namespace lp {
 using rs::kLn2;
 constexpr float kLn2Lo = -1.90465431e-9f;            // ln 2 = kLn2 + kLn2Lo
 
+// The hardware's base-2 exponential comes out low by this much of itself on the mean (measured over all of
+// [-16, 0] against exp2 in 64 bits: 5.0e-8, each within 1.5e-7), and so does a sum of many.
+constexpr float kEx2Bias = 5.0e-8f;
+
 __device__ __forceinline__ float nan_f() { return __int_as_float(0x7FC00000); }
 
 // ---- (reference, sum, sum of products): s = sum 2^y, w = sum 2^y y, y = z k2 - m ------------------------
 
 struct Sums {
     float m, s, w;
+};
+
+// log2(e) / temperature as hi + lo, lo > 0 (so a mask's -inf has no product of the other sign): a logit's
+// exponent takes both, since hi alone is off by 2^-25 or so of it, 4e-7 of a term at an exponent of 16, alike
+// for all rows, which a sum over a sequence's rows would add up.
+struct Scale {
+    float hi, lo;
 };
 
 // (s, w) to the reference M >= m.
@@ -74,34 +85,47 @@ __device__ __forceinline__ void ffma2v(float a0, float a1, float b0, float b1, f
         : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
 }
 
-// s and w of a thread's vectors against the reference m.  An exponent of -inf (a mask) has the product 0:
-// the factor is held at -200, whose power of two is 0.  A NaN stays one (in s).
-template <int G, int U, bool kEnt>
-__device__ __forceinline__ void sums_of(const float (&v)[U][G], float k2, float m, float& s, float& w) {
-    if (!kEnt) {
-        s = rs::sum_exp<G>(v, k2, m);
-        w = 0.f;
-        return;
+// (d0, d1) = (a0 * b0, a1 * b1) in one packed instruction.
+__device__ __forceinline__ void fmul2v(float a0, float a1, float b0, float b1, float& d0, float& d1) {
+    asm("{\n\t.reg .b64 pa, pb, pd;\n\t"
+        "mov.b64 pa, {%2, %3};\n\tmov.b64 pb, {%4, %5};\n\t"
+        "mul.rn.f32x2 pd, pa, pb;\n\tmov.b64 {%0, %1}, pd;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
+// Adds a vector's terms against the reference m: even and odd values apart, two to an instruction, since the
+// issue slots are what these kernels run short of.  An exponent of -inf (a mask) has the product 0: the
+// factor is held at -200, whose power of two is 0.  A NaN stays one (in s).
+template <int G, bool kEnt>
+__device__ __forceinline__ void add_sums(const float (&v)[G], Scale k, float m, float& s0, float& s1, float& w0,
+                                         float& w1) {
+#pragma unroll
+    for (int i = 0; i < G; i += 2) {
+        float a0, a1;
+        ffma2(v[i], v[i + 1], k.hi, -m, a0, a1);
+        ffma2v(v[i], v[i + 1], k.lo, k.lo, a0, a1, a0, a1);
+        const float e0 = ex2(a0), e1 = ex2(a1);
+        rs::fadd2(s0, s1, e0, e1, s0, s1);
+        if (kEnt) ffma2v(e0, e1, fmaxf(a0, -200.f), fmaxf(a1, -200.f), w0, w1, w0, w1);
     }
+}
+
+// s and w of a thread's vectors against the reference m.
+template <int G, int U, bool kEnt>
+__device__ __forceinline__ void sums_of(const float (&v)[U][G], Scale k, float m, float& s, float& w) {
     float s0[U], s1[U], w0[U], w1[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         s0[u] = s1[u] = w0[u] = w1[u] = 0.f;
-#pragma unroll
-        for (int k = 0; k < G; k += 2) {
-            float a0, a1;
-            ffma2(v[u][k], v[u][k + 1], k2, -m, a0, a1);
-            const float e0 = ex2(a0), e1 = ex2(a1);
-            rs::fadd2(s0[u], s1[u], e0, e1, s0[u], s1[u]);
-            ffma2v(e0, e1, fmaxf(a0, -200.f), fmaxf(a1, -200.f), w0[u], w1[u], w0[u], w1[u]);
-        }
+        add_sums<G, kEnt>(v[u], k, m, s0[u], s1[u], w0[u], w1[u]);
     }
 #pragma unroll
     for (int d = 1; d < U; d *= 2)
 #pragma unroll
         for (int u = 0; u + d < U; u += 2 * d) {
             rs::fadd2(s0[u], s1[u], s0[u + d], s1[u + d], s0[u], s1[u]);
-            rs::fadd2(w0[u], w1[u], w0[u + d], w1[u + d], w0[u], w1[u]);
+            if (kEnt) rs::fadd2(w0[u], w1[u], w0[u + d], w1[u + d], w0[u], w1[u]);
         }
     s = s0[0] + s1[0];
     w = w0[0] + w1[0];
@@ -109,17 +133,17 @@ __device__ __forceinline__ void sums_of(const float (&v)[U][G], float k2, float 
 
 // Adds a thread's vectors of a stage; the reference moves only when a term would pass 2^32.
 template <int G, int U, bool kEnt>
-__device__ __forceinline__ void push(const float (&v)[U][G], Sums& x, float k2) {
+__device__ __forceinline__ void push(const float (&v)[U][G], Sums& x, Scale k) {
     if (x.m == -kInf) {
-        x.m = rs::max_of<G>(v) * k2;
+        x.m = rs::max_of<G>(v) * k.hi;
         if (x.m == -kInf) return;
     }
     float s, w;
 #pragma unroll 1
     for (int again = 0;; again = 1) {   // one copy of the sum's code, for the instruction cache
-        sums_of<G, U, kEnt>(v, k2, x.m, s, w);
+        sums_of<G, U, kEnt>(v, k, x.m, s, w);
         if (again || s < 4294967296.f) break;
-        rescale(x, fmaxf(x.m, rs::max_of<G>(v) * k2));
+        rescale(x, fmaxf(x.m, rs::max_of<G>(v) * k.hi));
     }
     x.s += s;
     if (kEnt) x.w += w;
@@ -148,7 +172,8 @@ __device__ __forceinline__ float split_log(float s, float& near) {
     return (float)e;
 }
 
-__device__ __forceinline__ Row finish(const Sums& x, float zt, float k2) {
+__device__ __forceinline__ Row finish(const Sums& x, float zt, Scale k) {
+    const float k2 = k.hi;
     Row r;
     r.dead = false;
     r.lp_lo = 0.f;
@@ -166,6 +191,7 @@ __device__ __forceinline__ Row finish(const Sums& x, float zt, float k2) {
     }
     float near;
     const float e = split_log(x.s, near);
+    near += kEx2Bias;
     const float hrest = fmaxf(0.f, fmaf(e - x.w / x.s, kLn2, near));
     r.m = x.m;
     if (!tok) {
@@ -176,6 +202,7 @@ __device__ __forceinline__ Row finish(const Sums& x, float zt, float k2) {
     }
     float lo;
     const float gap = minus_product(x.m, zt, k2, lo);
+    lo -= zt * k.lo;
     const float g = gap + e, t = g - gap;            // TwoSum of gap and e
     lo += (gap - (g - t)) + (e - t);
     float u = g * kLn2;

@@ -6,6 +6,7 @@
 #include <cmath>
 
 #include "ce_fold.cuh"
+#include "policy_held.cuh"
 #include "policy_ring.cuh"
 
 namespace vce {
@@ -217,11 +218,13 @@ __global__ void __launch_bounds__(kPairThreads) k_pairs(const __grid_constant__ 
 
 // ---- host ----------------------------------------------------------------------------------------------
 
-// The forward's two forms.  A long row (or one of few rows, which a cluster shares) takes an SM's block of 16
-// consumer warps and 32 KB stages; short rows take four blocks an SM of 4 warps and 8 KB stages, whose
-// hand-overs between rows (about 1 us each) run under the others' sums.
+// The forward's forms.  Rows of at most 4 KB take a warp each, which holds them in registers.  A long row (or
+// one of few rows, which a cluster shares) takes a block of 8 consumer warps and 16 KB stages, two of them an SM;
+// shorter ones four blocks an SM of 4 warps and 8 KB stages: what a row costs beside its columns (about 1 us of
+// merges and hand-overs) runs under the other blocks' columns.
+using Warp = held::Form<32, 8, 4>;
 constexpr int64_t kLongRow = 131072;
-using Long = ring::Form<16, 1, 4, 6, 0>;
+using Long = ring::Form<8, 2, 4, 6, 0>;
 using Short = ring::Form<4, 4, 4, 6, 0>;
 
 template <typename S, bool kEnt, typename F>
@@ -235,13 +238,18 @@ cudaError_t run_rows(Args& a, cudaStream_t s) {
     constexpr int G = Elt<S>::kGroup;
     const int sms = device_sm_count();
     const int64_t nv = (a.V + 2 * G - 2) / G;
+    a.cluster = 1;
+    if (nv <= Warp::kVecs)
+        return launch_clusters<held::k_loss_held<S, float, false, kEnt, Warp>>((a.T + Warp::kPer - 1) / Warp::kPer, 1,
+                                                                              Warp::kThreads, 0, s, a);
     int C = 1;
-    while (C < kMaxCluster && a.T * C < sms && (nv + C - 1) / C > Long::kVecs / 4) C *= 2;
+    while (C < kMaxCluster && a.T * C < sms && (nv + C - 1) / C > 512) C *= 2;
     a.cluster = C;
     if (C == 1 && a.V * (int64_t)sizeof(S) < kLongRow)
         return run_form<S, kEnt, Short>(a, std::min<int64_t>(a.T, (int64_t)sms * Short::kBlocks), s);
     constexpr auto kern = ring::k_loss_ring<S, float, false, kEnt, Long>;
-    const int64_t fit = std::min<int64_t>(a.T, resident_clusters<kern>(C, Long::kThreads, ring::smem_bytes<Long>(), sms));
+    const int64_t fit = std::min<int64_t>(
+        a.T, resident_clusters<kern>(C, Long::kThreads, ring::smem_bytes<Long>(), sms * (C == 1 ? Long::kBlocks : 1)));
     if (fit < 1) return cudaErrorInvalidConfiguration;   // not one cluster of that size fits
     return run_form<S, kEnt, Long>(a, fit * C, s);
 }
@@ -289,7 +297,7 @@ static lp::Args rows_args(const void* logits, int64_t T, int64_t V, int64_t ld, 
                           float tau, int mode, float* logprobs, float* entropy, float* row_stats) {
     lp::Args a{};
     a.logits = logits, a.T = T, a.V = V, a.ld = ld, a.ids = ids, a.ignore_index = ignore_index, a.mode = mode;
-    a.k2 = lp::k2_of(tau), a.inv_tau = 1.f / tau, a.logprobs = logprobs, a.entropy = entropy;
+    a.k2 = lp::k2_of(tau, &a.k2_lo), a.inv_tau = 1.f / tau, a.logprobs = logprobs, a.entropy = entropy;
     a.row_stats = reinterpret_cast<float4*>(row_stats), a.wait_ns = tc::kWaitNs;
     return a;
 }
@@ -358,7 +366,7 @@ extern "C" int policy_loss_forward_backward(const void* logits, vce_dtype dt, in
     if (e == cudaSuccess) e = lp::finish_rows(a, loss_out, status, !held && red == VCE_RED_MEAN, s);
     if (e == cudaSuccess && T && !held) {
         lp::GradArgs g{};
-        g.logits = logits, g.T = T, g.V = V, g.ld = ld, g.ids = actions, g.mode = lp::kPolicy, g.k2 = a.k2;
+        g.logits = logits, g.T = T, g.V = V, g.ld = ld, g.ids = actions, g.mode = lp::kPolicy, g.k2 = a.k2, g.k2_lo = a.k2_lo;
         g.inv_tau = a.inv_tau, g.row_stats = a.row_stats, g.go = grad_output, g.go_each = red == VCE_RED_NONE;
         g.scale = 1.f, g.grad = grad_logits, g.ld_g = ld_grad, g.wait_ns = tc::kWaitNs;
         e = lp::launch_grad(dt, grad_dt, g, s);

@@ -76,14 +76,21 @@ __global__ void __launch_bounds__(kConsumers + 32, 3) k_row_grads(const __grid_c
         const Coefs c = ctl.c;
         const float bias = ctl.bias;
         const int target = ctl.target;
+        const Scale sc{a.k2, a.k2_lo};
         for (int j = 0; j < sl.nst; ++j) {
             wait_stage(bar, a.nbuf, j, a.wait_ns);
             uint4 x[kU];
             load_stage<S>(smem, a.nbuf, r, sl, j, j, tid, x);
+            const int v0 = sl.v0 + j * kStageVecs, v1 = sl.v0 + sl.n;
+            const bool fast = vec && v0 >= r.iv0 && v0 + kStageVecs <= min(r.iv1, v1);
             if (c.c1 != 0.f)
-                write_grads<S, O, kU, kConsumers, true>(x, r, sl, j, tid, grow, vec, c, bias, a.k2, target);
+                write_grads<S, O, kU, kConsumers, true>(x, r, v0 + tid, v1, fast, grow, vec, c, bias, sc);
             else
-                write_grads<S, O, kU, kConsumers, false>(x, r, sl, j, tid, grow, vec, c, bias, a.k2, target);
+                write_grads<S, O, kU, kConsumers, false>(x, r, v0 + tid, v1, fast, grow, vec, c, bias, sc);
+            // the token's entry, over what its thread has just written there
+            const int rel = target >= 0 ? (target + r.shift) / Elt<S>::kGroup - v0 - tid : -1;
+            if (rel >= 0 && rel < kStageVecs && rel % kConsumers == 0 && v0 + tid + rel < v1)
+                Elt<O>::store1(grow + target, c.gt);
             release_stage(bar, a.nbuf, j);
         }
     }
@@ -125,7 +132,7 @@ static int backward(vce_dtype dt, vce_dtype gdt, lp::GradArgs& a, float tau, cud
     if (!aligned(a.ids, 8) || !aligned(a.row_stats, 16) || !aligned(a.go, 4) || !aligned(a.ga, 4) || !aligned(a.gb, 4))
         return VCE_ERR_ALIGN;
     if ((rc = require_sm100())) return rc;
-    a.k2 = lp::k2_of(tau), a.inv_tau = 1.f / tau;
+    a.k2 = lp::k2_of(tau, &a.k2_lo), a.inv_tau = 1.f / tau;
     if (!a.wait_ns) a.wait_ns = tc::kWaitNs;
     return record_cuda(lp::launch_grad(dt, gdt, a, s)) == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
 }

@@ -21,6 +21,7 @@
 #include <algorithm>
 
 #include "logprob_rows.cuh"
+#include "policy_finish.cuh"
 #include "policy_rows.h"
 #include "row_grads.cuh"
 
@@ -172,105 +173,11 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity)
     return ok != 0;
 }
 
-// This thread's vectors of stage j of the slice; -inf beyond its end.
-template <typename S, int U, int kNT>
-__device__ __forceinline__ void ring_load(const uint8_t* buf8, const Slice& s, int j, int tid, uint4 (&x)[U]) {
-    const uint4* buf = reinterpret_cast<const uint4*>(buf8) + tid;
-    const int left = s.n - j * (U * kNT);
-    if (left >= U * kNT) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) x[u] = tc::lds16(buf + u * kNT);
-    } else {
-#pragma unroll
-        for (int u = 0; u < U; ++u) x[u] = tid + u * kNT < left ? tc::lds16(buf + u * kNT) : stage::neg_inf16<S>();
-    }
-}
-
-// What a row's finish reads besides its sums.
-struct RowIn {
-    float zt, old, adv, ref, w;
-};
-template <typename S>
-__device__ __forceinline__ RowIn row_in(const Args& a, int64_t row, int token) {
-    RowIn in{Elt<S>::load1(static_cast<const S*>(a.logits) + row * a.ld + token), 0.f, 0.f, 0.f, 1.f};
-    if (a.mode == kPolicy) {
-        if (a.old) in.old = a.old[row];
-        in.adv = a.adv[row];
-        if (a.kl != 0.f) in.ref = a.ref[row];
-        if (a.weights) in.w = a.weights[row];
-    }
-    return in;
-}
-
-// e^d - 1 - d >= 0: its power series near 0 (to d^9 / 9!, 2e-9 relative at 0.5), else as it stands.
-__device__ __forceinline__ float exp_minus_line(float d) {
-    if (fabsf(d) < 0.5f) {
-        float c = 1.f / 362880.f;
-        c = fmaf(c, d, 1.f / 40320.f);
-        c = fmaf(c, d, 1.f / 5040.f);
-        c = fmaf(c, d, 1.f / 720.f);
-        c = fmaf(c, d, 1.f / 120.f);
-        c = fmaf(c, d, 1.f / 24.f);
-        c = fmaf(c, d, 1.f / 6.f);
-        c = fmaf(c, d, 0.5f);
-        return d * d * c;
-    }
-    return expm1f(d) - d;
-}
-
-// What a row that is left out (code 0), or one with an error, returns.
-__device__ __forceinline__ void write_none(const Args& a, int64_t row, int code) {
-    const float v = code ? nan_f() : 0.f;
-    a.logprobs[row] = v;
-    if (a.entropy) a.entropy[row] = v;
-    if (a.mode == kPolicy) a.loss_rows[row] = v;
-    a.row_stats[row] = make_float4(kInf, -(float)code, 0.f, 0.f);
-}
-
-// The row's statistics as they are saved, and for the policy loss its value; scale is on the gradient.
-__device__ __forceinline__ float4 row_result(const Args& a, const Row& r, const RowIn& in, float scale, float& loss) {
-    float4 st = make_float4(r.m, r.f, r.lp, a.mode == kPreference ? r.lp_lo : a.entropy ? r.ent : nan_f());
-    if (a.mode == kPolicy) {
-        const float A = in.adv;
-        const float ratio = a.old ? expf((r.lp - in.old) + r.lp_lo) : 1.f;
-        const float gain = ratio * A, clipped = fminf(fmaxf(ratio, a.lo), a.hi) * A;
-        bool open = gain <= clipped;                 // the minimum is the unclipped one
-        float got = open ? gain : clipped;
-        if (a.dual > 0.f && A < 0.f && got < a.dual * A) {
-            got = a.dual * A;
-            open = false;
-        }
-        float da = open ? -gain : 0.f;
-        if (A == 0.f) got = da = 0.f;
-        if (ratio != ratio || A != A || r.lp != r.lp) got = da = nan_f();
-        loss = -got;
-        if (a.kl != 0.f) {
-            const float d = (in.ref - r.lp) - r.lp_lo;
-            loss += a.kl * exp_minus_line(d);
-            da -= a.kl * expm1f(d);
-        }
-        if (a.ent != 0.f) loss -= a.ent * r.ent;
-        loss *= in.w;
-        const float w = in.w * scale;
-        const Coefs c = coefs(r.f, r.lp, r.ent, w * da, -w * a.ent, a.inv_tau);
-        st = make_float4(r.m, c.c0, c.c1, c.gt);
-    }
-    if (r.dead) st = make_float4(kInf, 0.f, 0.f, 1.f);
-    return st;
-}
-
-__device__ __forceinline__ void write_result(const Args& a, int64_t row, const Row& r, float4 st, float loss) {
-    a.logprobs[row] = r.lp;
-    if (a.entropy) a.entropy[row] = r.ent;
-    if (a.mode == kPolicy) a.loss_rows[row] = loss;
-    a.row_stats[row] = st;
-}
-
 template <typename S, typename O, bool kGrad, bool kEnt, typename F>
 __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_ring(const __grid_constant__ Args a) {
     constexpr int G = Elt<S>::kGroup;
     extern __shared__ __align__(128) uint8_t smem[];
-    constexpr int nbuf = F::kBufs, U = F::kU, kVecs = F::kVecs, kWarps = F::kWarps, kNT = F::kNT;
+    constexpr int nbuf = F::kBufs, U = F::kU, B = U < 4 ? U : 4, kVecs = F::kVecs, kWarps = F::kWarps, kNT = F::kNT;
     Ctl<kWarps, nbuf>& ctl = *reinterpret_cast<Ctl<kWarps, nbuf>*>(smem + nbuf * F::kBytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int C = a.cluster;
@@ -380,7 +287,7 @@ __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_ring(const __g
         auto flush = [&]() {
             if (!kGrad && lane < pending && rank == 0) {
                 const RowIn in = row_in<S>(a, kept_row, kept_token);
-                const Row r = finish(kept, in.zt, a.k2);
+                const Row r = finish(kept, in.zt, Scale{a.k2, a.k2_lo});
                 float loss = 0.f;
                 const float4 st = row_result(a, r, in, 1.f, loss);
                 write_result(a, kept_row, r, st, loss);
@@ -432,7 +339,7 @@ __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_ring(const __g
                 warp_merge<kEnt>(x);                   // the same order in every block
             }
             if (kGrad) {
-                const Row r = finish(x, in.zt, a.k2);
+                const Row r = finish(x, in.zt, Scale{a.k2, a.k2_lo});
                 float loss = 0.f;
                 const float4 st = row_result(a, r, in, go, loss);
                 if (lane == 0) {
@@ -463,21 +370,35 @@ __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_ring(const __g
         auto forward = [&](Cursor<nbuf>& at, int j0, int j1, const Slice& sl, int tv, int tk, Sums& x) {
             for (int j = j0; j < j1; ++j, at.step()) {
                 tc::mbar_wait(&ctl.full[at.st], at.phase, &ctl.abort, &ctl.err, kErrFull, a.wait_ns, kSuspend);
-                uint4 raw[U];
-                ring_load<S, U, kNT>(smem + at.st * F::kBytes, sl, j, tid, raw);
-                if (!kGrad) release(at.st);
-                float v[U][G];
-#pragma unroll
-                for (int u = 0; u < U; ++u) Elt<S>::unpack(raw[u], v[u]);
+                const uint4* buf = reinterpret_cast<const uint4*>(smem + at.st * F::kBytes) + tid;
+                const int all = sl.n - j * kVecs, left = all - tid;     // vectors from the stage's, this thread's first on
                 const int rel = tv - j * kVecs - tid;
-                if (rel >= 0 && rel < kVecs && rel % kNT == 0) {   // the token's column is left out
+                const bool token = rel >= 0 && rel < kVecs && rel % kNT == 0;
+#pragma unroll 1
+                for (int h = 0; h < U; h += B) {
+                    if (h * kNT >= all) break;
+                    uint4 raw[B];
+                    if (left > (h + B - 1) * kNT) {
 #pragma unroll
-                    for (int u = 0; u < U; ++u)
+                        for (int u = 0; u < B; ++u) raw[u] = tc::lds16(buf + (h + u) * kNT);
+                    } else {
 #pragma unroll
-                        for (int k = 0; k < G; ++k)
-                            if (rel == u * kNT && k == tk) v[u][k] = -kInf;
+                        for (int u = 0; u < B; ++u)
+                            raw[u] = left > (h + u) * kNT ? tc::lds16(buf + (h + u) * kNT) : stage::neg_inf16<S>();
+                    }
+                    if (!kGrad && (h + B >= U || (h + B) * kNT >= all)) release(at.st);
+                    float v[B][G];
+#pragma unroll
+                    for (int u = 0; u < B; ++u) Elt<S>::unpack(raw[u], v[u]);
+                    if (token) {                                   // the token's column is left out
+#pragma unroll
+                        for (int u = 0; u < B; ++u)
+#pragma unroll
+                            for (int k = 0; k < G; ++k)
+                                if (rel == (h + u) * kNT && k == tk) v[u][k] = -kInf;
+                    }
+                    push<G, B, kEnt>(v, x, Scale{a.k2, a.k2_lo});
                 }
-                push<G, U, kEnt>(v, x, a.k2);
             }
         };
         auto publish = [&](int64_t e, Sums x) {
@@ -522,25 +443,44 @@ __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_ring(const __g
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {         // the next row's first stages, this row, the rest
                 if (row2 >= 0) forward(at, half ? pre : 0, half ? sl2.nst : pre, sl2, tv, tk, x);
+                // the sums are handed on as soon as they are there: the statistics are exchanged and finished
+                // under this row's gradient where the next row fits beside it
+                if (row2 >= 0 && half == (pre < sl2.nst)) publish(e + 1, x);
                 if (!kGrad || half || row < 0) continue;
                 const int par = (int)(e & 1);
-                if (!wait(&ctl.finished[par], e, kErrCoefs)) break;
+                if (!wait(&ctl.finished[par], e, kErrCoefs)) continue;
                 const RowCoefs cf = ctl.coefs[par];
                 O* grow = static_cast<O*>(a.grad) + row * a.ld_g;
                 const bool vec = grads_aligned<S, O>(r, grow);
+                const Scale sc{a.k2, a.k2_lo};
+                const int fast0 = vec ? r.iv0 : r.nv, fast1 = min(r.iv1, sl.v0 + sl.n);
                 for (int j = 0; j < sl.nst; ++j, back.step()) {
-                    uint4 raw[U];
-                    ring_load<S, U, kNT>(smem + back.st * F::kBytes, sl, j, tid, raw);
-                    if (cf.none)
-                        write_zeros<S, O, U, kNT>(r, sl, j, tid, grow, vec);
-                    else if (kEnt && cf.c.c1 != 0.f)
-                        write_grads<S, O, U, kNT, true>(raw, r, sl, j, tid, grow, vec, cf.c, cf.bias, a.k2, tok);
-                    else
-                        write_grads<S, O, U, kNT, false>(raw, r, sl, j, tid, grow, vec, cf.c, cf.bias, a.k2, tok);
+                    const uint4* buf = reinterpret_cast<const uint4*>(smem + back.st * F::kBytes) + tid;
+                    const int first = sl.v0 + j * kVecs;
+                    if (cf.none) {
+                        fill_grads<S, O>(r, Slice{first, min(sl.n - j * kVecs, kVecs), 1}, grow, vec, tid, kNT);
+                    } else {
+#pragma unroll 1
+                        for (int h = 0; h < U; h += B) {
+                            const int v0 = first + h * kNT, v1 = sl.v0 + sl.n;
+                            if (v0 >= v1) break;
+                            uint4 raw[B];
+#pragma unroll
+                            for (int u = 0; u < B; ++u) raw[u] = tc::lds16(buf + (h + u) * kNT);
+                            const bool fast = v0 >= fast0 && v0 + B * kNT <= fast1;
+                            if (kEnt && cf.c.c1 != 0.f)
+                                write_grads<S, O, B, kNT, true>(raw, r, v0 + tid, v1, fast, grow, vec, cf.c, cf.bias, sc);
+                            else
+                                write_grads<S, O, B, kNT, false>(raw, r, v0 + tid, v1, fast, grow, vec, cf.c, cf.bias, sc);
+                        }
+                        // the token's entry, over what its thread has just written there
+                        const int rel = (tok + r.shift) / G - first - tid;
+                        if (rel >= 0 && rel < kVecs && rel % kNT == 0 && first + tid + rel < sl.v0 + sl.n)
+                            Elt<O>::store1(grow + tok, cf.c.gt);
+                    }
                     release(back.st);
                 }
             }
-            if (row2 >= 0) publish(e + 1, x);
             row = row2;
             r = r2;
             sl = sl2;

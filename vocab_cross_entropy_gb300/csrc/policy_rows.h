@@ -24,7 +24,7 @@ struct Args {
     const int64_t* ids;
     int64_t ignore_index;
     int mode;
-    float k2, inv_tau;           // log2(e) / temperature, 1 / temperature
+    float k2, k2_lo, inv_tau;    // log2(e) / temperature as k2 + k2_lo, 1 / temperature
     float* logprobs;
     float* entropy;              // or null
     float4* row_stats;
@@ -52,7 +52,7 @@ struct GradArgs {
     int64_t T, V, ld;
     const int64_t* ids;
     int mode;
-    float k2, inv_tau;
+    float k2, k2_lo, inv_tau;
     const float4* row_stats;
     const float* go;             // kPolicy, kPreference
     int go_each;                 // one for each row (pair), else one
@@ -70,7 +70,14 @@ bool one_pass_holds(vce_dtype dt, int64_t V);
 cudaError_t launch_one_pass(vce_dtype dt, vce_dtype gdt, Args& a, cudaStream_t s);
 cudaError_t launch_grad(vce_dtype dt, vce_dtype gdt, GradArgs& a, cudaStream_t s);
 
-inline float k2_of(float tau) { return (float)(1.4426950408889634 / (double)tau); }
+// log2(e) / tau rounded down, and what is left of it (> 0).
+inline float k2_of(float tau, float* rest = nullptr) {
+    const double exact = 1.4426950408889634 / (double)tau;
+    float k = (float)exact;
+    if ((double)k >= exact) k = std::nextafter(k, 0.f);
+    if (rest) *rest = (float)(exact - (double)k);
+    return k;
+}
 
 inline int check_shape(vce_dtype dt, int64_t T, int64_t V, int64_t ld, float tau) {
     if (dt != VCE_F32 && dt != VCE_BF16) return VCE_ERR_DTYPE;

@@ -1,4 +1,5 @@
-// Writing gradients 2^y (c0 + c1 y), y = z k2 - bias, of a row's streamed stages (logprob_rows.cuh).
+// Writing the gradients 2^y (c0 + c1 y), y = z k2 - bias, of a row's vectors (logprob_rows.cuh).  The token's entry
+// is the caller's to write over them.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -45,47 +46,70 @@ __device__ __forceinline__ void write_zeros(const rs::Row& r, const Slice& s, in
     fill_grads<S, O>(r, part, grow, vec, tid, NT);
 }
 
-// The gradient of a thread's U vectors of stage j of the slice; the token's column takes c.gt.
-// kEnt: c.c1 is not 0.  A mask's exponent of -inf is held at -200, as in the sums.
-template <typename S, typename O, int U, int NT, bool kEnt>
-__device__ __forceinline__ void write_grads(const uint4 (&x)[U], const rs::Row& r, const Slice& s, int j, int tid,
-                                            O* grow, bool vec, const Coefs& c, float bias, float k2, int target) {
+// The gradients of a vector's G logits, in their place.  kEnt: c.c1 is not 0.  A mask's exponent of -inf is
+// held at -200 there, as in the sums.
+template <int G, bool kEnt>
+__device__ __forceinline__ void grads_of(float (&g)[G], const Coefs& c, float bias, Scale sc) {
+#pragma unroll
+    for (int k = 0; k < G; k += 2) {
+        float a0, a1;
+        ffma2(g[k], g[k + 1], sc.hi, -bias, a0, a1);
+        ffma2v(g[k], g[k + 1], sc.lo, sc.lo, a0, a1, a0, a1);
+        const float e0 = ex2(a0), e1 = ex2(a1);
+        if (kEnt) {
+            float f0, f1;
+            ffma2(fmaxf(a0, -200.f), fmaxf(a1, -200.f), c.c1, c.c0, f0, f1);
+            fmul2v(e0, e1, f0, f1, g[k], g[k + 1]);
+        } else {
+            fmul2(e0, e1, c.c0, g[k], g[k + 1]);
+        }
+    }
+}
+
+// A vector of the row from its first column c0 on (before the row's start where it is partial), element by
+// element: partial vectors, and gradients that are not aligned as the logits are.
+template <typename S, typename O>
+__device__ __noinline__ void write_single(uint4 x, int64_t c0, int64_t V, O* grow, Coefs c, float bias, Scale sc) {
     constexpr int G = Elt<S>::kGroup;
-    constexpr int B = U * NT;                        // vectors of a stage
-    const int v0 = s.v0 + j * B + tid;
-    const bool inside = vec && s.v0 + j * B >= r.iv0 && s.v0 + (j + 1) * B <= min(s.v0 + s.n, r.iv1);
-    const int tv = target >= 0 ? (target + r.shift) / G - v0 : -1;   // the token's vector, from this thread's first
+    float g[G];
+    Elt<S>::unpack(x, g);
+    grads_of<G, true>(g, c, bias, sc);
+#pragma unroll
+    for (int k = 0; k < G; ++k)
+        if (c0 + k >= 0 && c0 + k < V) Elt<O>::store1(grow + c0 + k, g[k]);
+}
+
+// The gradients of U vectors of a thread, vector v0 + u * NT of the row each, the slice's end at v1.  fast: all of
+// them lie wholly in the row and the slice, and are aligned in the gradient too.
+template <typename S, typename O, int U, int NT, bool kEnt>
+__device__ __forceinline__ void write_grads(const uint4 (&x)[U], const rs::Row& r, int v0, int v1, bool fast, O* grow,
+                                            bool vec, const Coefs& c, float bias, Scale sc) {
+    constexpr int G = Elt<S>::kGroup;
+    if (fast) {
+        O* p = grow + ((int64_t)v0 * G - r.shift);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float g[G];
+            Elt<S>::unpack(x[u], g);
+            grads_of<G, kEnt>(g, c, bias, sc);
+            GroupStore<O, G>::run(p + u * NT * G, g);
+        }
+        return;
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int v = v0 + u * NT;
-        if (!inside && v >= s.v0 + s.n) continue;
-        float g[G];
-        Elt<S>::unpack(x[u], g);
-#pragma unroll
-        for (int k = 0; k < G; k += 2) {
-            float a0, a1;
-            ffma2(g[k], g[k + 1], k2, -bias, a0, a1);
-            const float e0 = ex2(a0), e1 = ex2(a1);
-            if (kEnt) {
-                float f0, f1;
-                ffma2(fmaxf(a0, -200.f), fmaxf(a1, -200.f), c.c1, c.c0, f0, f1);
-                g[k] = e0 * f0;
-                g[k + 1] = e1 * f1;
-            } else {
-                fmul2(e0, e1, c.c0, g[k], g[k + 1]);
-            }
-        }
+        if (v >= v1) continue;
         const int64_t c0 = (int64_t)v * G - r.shift;
-        if (inside || (vec && v >= r.iv0 && v < r.iv1)) {
+        if (vec && v >= r.iv0 && v < r.iv1) {
+            float g[G];
+            Elt<S>::unpack(x[u], g);
+            grads_of<G, kEnt>(g, c, bias, sc);
             GroupStore<O, G>::run(grow + c0, g);
         } else {
-#pragma unroll
-            for (int k = 0; k < G; ++k)
-                if (c0 + k >= 0 && c0 + k < r.V) Elt<O>::store1(grow + c0 + k, g[k]);
+            write_single<S, O>(x[u], c0, r.V, grow, c, bias, sc);
         }
     }
-    // over what this thread has just written there
-    if (tv >= 0 && tv < B && tv % NT == 0 && v0 + tv < s.v0 + s.n) Elt<O>::store1(grow + target, c.gt);
 }
 
 }  // namespace lp

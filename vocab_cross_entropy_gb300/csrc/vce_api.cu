@@ -116,7 +116,7 @@ extern "C" int vce_debug_status(int32_t* host_out) {
                                         vce::debug_word_lce,      vce::debug_word_gemm_hooks, vce::debug_word_topk,
                                         vce::debug_word_distill,  vce::debug_word_process,
                                         vce::debug_word_policy,   vce::debug_word_policy_grad,
-                                        vce::debug_word_policy_onepass};
+                                        vce::debug_word_policy_onepass, vce::debug_word_fp8};
     for (auto rd : readers) {
         int32_t w = 0;
         if (rd(&w) != 0) return VCE_ERR_CUDA;

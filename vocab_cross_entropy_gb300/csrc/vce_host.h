@@ -50,6 +50,7 @@ int debug_word_distill(int32_t* out);
 int debug_word_process(int32_t* out);
 int debug_word_gemm_hooks(int32_t* out);
 int debug_word_policy(int32_t* out);
+int debug_word_fp8(int32_t* out);
 int debug_word_policy_grad(int32_t* out);
 int debug_word_policy_onepass(int32_t* out);
 
