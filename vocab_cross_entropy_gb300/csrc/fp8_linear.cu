@@ -6,7 +6,7 @@
 // added to the running sum in registers, while the tensor cores work on the next block in the other accumulator.
 //
 //   k_linear_pair  T > 64: CTA pairs (cta_group::2) on 256 x 256 tiles, 128 rows of x and half of the tile's rows
-//                  of w per CTA and K block.  16 epilogue warps, each 32 rows x 64 columns in registers: per K
+//                  of w per CTA and K block.  8 epilogue warps, each 32 rows x 128 columns in registers: per K
 //                  block and SM 32768 fma (256 cycles of the fma pipe) against the MMAs' 512 cycles.
 //   k_linear_few   T <= 64: bound by reading w.  The roles change sides: w's rows are the MMA's 128, the rows of x
 //                  its N (16, 32 or 64 wide), so a stage is w's 16 KB and little else.  Where w has fewer tiles
@@ -85,6 +85,28 @@ __device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {   // ties r to 
                  : "memory");
 }
 
+// Arrive on a barrier of either CTA of a pair.  What it orders is tensor memory (its loads have been waited for, and
+// tcgen05.fence stands before), nothing that a release at cluster scope would have to flush: that one, 32 of them a K
+// block, held the epilogue warps for two fifths of their time (2670 cycles a K block).
+__device__ __forceinline__ void arrive_either(uint32_t addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+// Arrive on the barrier at this shared-memory address in both CTAs of a pair once every MMA issued so far is done.
+__device__ __forceinline__ void commit_both(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+// Scales k .. k + 3 of a row of nd (0 behind its end).
+__device__ __forceinline__ float4 four_scales(const float* s, int k, int nd) {
+    if (nd % 4 == 0 && (reinterpret_cast<uintptr_t>(s) & 15u) == 0) return __ldg(reinterpret_cast<const float4*>(s + k));
+    return make_float4(__ldg(s + k), k + 1 < nd ? __ldg(s + k + 1) : 0.f, k + 2 < nd ? __ldg(s + k + 2) : 0.f,
+                       k + 3 < nd ? __ldg(s + k + 3) : 0.f);
+}
+
 // (c0, c1) += (a0, a1) * b, in one packed instruction.
 __device__ __forceinline__ void fma_pair(uint32_t a0, uint32_t a1, float b, float& c0, float& c1) {
     asm("{\n\t.reg .b64 pa, pb, pc;\n\t"
@@ -102,9 +124,14 @@ __device__ __forceinline__ void store_nan(const LinearArgs& a, int64_t t, int64_
 // ---- CTA pairs ----------------------------------------------------------------------------------------
 
 constexpr int kM = 128, kN = 256;                    // rows of x per CTA, rows of w per tile
-constexpr int kEpiWarps = 16, kProducer = 16, kIssuer = 17;
-constexpr int kPairThreads = 18 * 32;
-constexpr int kStages = 5;
+constexpr int kEpiWarps = 8, kEpi0 = 4, kProducer = 0, kIssuer = 1;   // warps 2 and 3 are there for the warpgroup
+constexpr int kCols = 4 * kN / kEpiWarps;            // columns of an epilogue warp
+constexpr int kPairThreads = (kEpi0 + kEpiWarps) * 32;
+// Registers of a thread: at launch, and of the two kinds of warpgroups once they are split.  An epilogue thread holds
+// 128 running sums and two loads of 32 columns.
+constexpr int kLaunchRegs = 168, kRoleRegs = 56, kEpiRegs = 224;
+static_assert(128 * kRoleRegs + 32 * kEpiWarps * kEpiRegs <= kPairThreads * kLaunchRegs, "the split fits what the launch has");
+constexpr int kStages = 6;
 constexpr int kTileBytes = kM * kBlock;              // 16 KB: x's rows, and this CTA's half of w's
 constexpr int kStageBytes = 2 * kTileBytes;
 constexpr int kScratch = 32 * 17 * 4;                // per epilogue warp, for the stores
@@ -156,114 +183,128 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const int ntiles = a.tiles_m * a.tiles_n;        // of the pair; tiles that run at once share w's rows
     const int tile0 = (int)(blockIdx.x >> 1), tstep = (int)(gridDim.x >> 1);
 
-    if (warp == kProducer && lane == 0) {
-        int stage = 0, issued = 0;
-        uint32_t phase = 0;
-        for (int tile = tile0; tile < ntiles && !*abort_flag; tile += tstep) {
-            const int t0 = (tile % a.tiles_m * 2 + (int)rank) * kM, v0 = tile / a.tiles_m * kN + (int)rank * (kN / 2);
-            for (int kb = 0; kb < a.nd; ++kb) {
-                if (!wait_bar<true>(&empty[stage], phase ^ 1u, abort_flag, nullptr, 0, kWaitNs)) break;
-                const uint32_t fb = cluster_addr(&full[stage], 0);   // the even CTA counts both CTAs' bytes
-                if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * kStageBytes);
-                uint8_t* at = smem + stage * kStageBytes;
-                tma_load<true>(at, &mapX, fb, kb * kBlock, t0);
-                tma_load<true>(at + kTileBytes, &mapW, fb, kb * kBlock, v0);
-                issued = issued < kStages ? issued + 1 : kStages;
-                if (++stage == kStages) stage = 0, phase ^= 1u;
+    if (warp < kEpi0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegs));
+        if (warp == kProducer && lane == 0) {
+            int stage = 0, issued = 0;
+            uint32_t phase = 0;
+            for (int tile = tile0; tile < ntiles && !*abort_flag; tile += tstep) {
+                const int t0 = (tile % a.tiles_m * 2 + (int)rank) * kM, v0 = tile / a.tiles_m * kN + (int)rank * (kN / 2);
+                for (int kb = 0; kb < a.nd; ++kb) {
+                    if (!wait_bar<false>(&empty[stage], phase ^ 1u, abort_flag, nullptr, 0, kWaitNs)) break;
+                    const uint32_t fb = cluster_addr(&full[stage], 0);   // the even CTA counts both CTAs' bytes
+                    if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * kStageBytes);
+                    uint8_t* at = smem + stage * kStageBytes;
+                    tma_load<true>(at, &mapX, fb, kb * kBlock, t0);
+                    tma_load<true>(at + kTileBytes, &mapW, fb, kb * kBlock, v0);
+                    issued = issued < kStages ? issued + 1 : kStages;
+                    if (++stage == kStages) stage = 0, phase ^= 1u;
+                }
             }
-        }
-        if (*abort_flag) {   // copies in flight land before the CTA may leave
-            const uint64_t t0 = globaltimer();
-            if (rank == 0) {
-                for (int i = 0; i < issued; ++i) {
-                    if (--stage < 0) stage = kStages - 1, phase ^= 1u;
-                    while (!mbar_try_wait(&full[stage], phase) && globaltimer() - t0 < kWaitNs) {
+            if (*abort_flag) {   // copies in flight land before the CTA may leave
+                const uint64_t t0 = globaltimer();
+                if (rank == 0) {
+                    for (int i = 0; i < issued; ++i) {
+                        if (--stage < 0) stage = kStages - 1, phase ^= 1u;
+                        while (!mbar_try_wait(&full[stage], phase) && globaltimer() - t0 < kWaitNs) {
+                        }
+                    }
+                } else {         // these complete on the even CTA's barriers: give them time
+                    while (globaltimer() - t0 < 1000000ull) {
                     }
                 }
-            } else {         // these complete on the even CTA's barriers: give them time
-                while (globaltimer() - t0 < 1000000ull) {
+            }
+        } else if (warp == kIssuer && lane == 0 && rank == 0) {
+            constexpr uint32_t idesc = idesc_e4m3_f32(2 * kM, kN);
+            int stage = 0, acc = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            const uint32_t base = smem_u32(smem);
+            for (int tile = tile0; tile < ntiles && !*abort_flag; tile += tstep) {
+                for (int kb = 0; kb < a.nd; ++kb) {
+                    if (!wait_bar<false>(&full[stage], phase, abort_flag, nullptr, 0, kWaitNs)) break;
+                    if (!wait_bar<false>(&acc_free[acc], acc_phase ^ 1u, abort_flag, nullptr, 0, kWaitNs)) break;
+                    tc_fence_after();
+                    const uint64_t ad = desc_kmajor_sw128(base + stage * kStageBytes);
+                    const uint64_t bd = desc_kmajor_sw128(base + stage * kStageBytes + kTileBytes);
+#pragma unroll
+                    for (int k = 0; k < kBlock / 32; ++k)   // 32 bytes of K a step
+                        mma_e4m3<true>(tmem + (uint32_t)(acc * kN), ad + 2 * k, bd + 2 * k, idesc, k ? 1u : 0u);
+                    commit_both(smem_u32(&acc_full[acc]));
+                    commit_both(smem_u32(&empty[stage]));
+                    if (++stage == kStages) stage = 0, phase ^= 1u;
+                    acc ^= 1;
+                    if (acc == 0) acc_phase ^= 1u;
                 }
             }
-        }
-    } else if (warp == kIssuer && lane == 0 && rank == 0) {
-        constexpr uint32_t idesc = idesc_e4m3_f32(2 * kM, kN);
-        int stage = 0, acc = 0;
-        uint32_t phase = 0, acc_phase = 0;
-        const uint32_t base = smem_u32(smem);
-        auto commit = [&](uint64_t* bar) {
-            mma_commit<true>(smem_u32(bar));
-            mma_commit<true>(cluster_addr(bar, 1));
-        };
-        for (int tile = tile0; tile < ntiles && !*abort_flag; tile += tstep) {
-            for (int kb = 0; kb < a.nd; ++kb) {
-                if (!wait_bar<true>(&acc_free[acc], acc_phase ^ 1u, abort_flag, nullptr, 0, kWaitNs)) break;
-                if (!wait_bar<false>(&full[stage], phase, abort_flag, nullptr, 0, kWaitNs)) break;
-                tc_fence_after();
-                const uint64_t ad = desc_kmajor_sw128(base + stage * kStageBytes);
-                const uint64_t bd = desc_kmajor_sw128(base + stage * kStageBytes + kTileBytes);
-#pragma unroll
-                for (int k = 0; k < kBlock / 32; ++k)   // 32 bytes of K a step
-                    mma_e4m3<true>(tmem + (uint32_t)(acc * kN), ad + 2 * k, bd + 2 * k, idesc, k ? 1u : 0u);
-                commit(&empty[stage]);
-                commit(&acc_full[acc]);
-                if (++stage == kStages) stage = 0, phase ^= 1u;
-                acc ^= 1;
-                if (acc == 0) acc_phase ^= 1u;
+            // every MMA this thread issued has finished before tensor memory can be released
+            mma_commit<true>(smem_u32(drain));
+            const uint64_t t0 = globaltimer();
+            while (!mbar_try_wait(drain, 0) && globaltimer() - t0 < kWaitNs) {
             }
         }
-        // every MMA this thread issued has finished before tensor memory can be released
-        mma_commit<true>(smem_u32(drain));
-        const uint64_t t0 = globaltimer();
-        while (!mbar_try_wait(drain, 0) && globaltimer() - t0 < kWaitNs) {
-        }
-    } else if (warp < kEpiWarps) {
-        const int sub = warp & 3, cg = warp >> 2;    // this warp's 32 rows and 64 columns of the CTA's tile
-        const uint32_t taddr = tmem + ((uint32_t)(sub * 32) << 16) + (uint32_t)(cg * 64);
-        float* mine = scratch + warp * (kScratch / 4);
+        __syncwarp();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
+        const int sub = warp & 3, cg = (warp - kEpi0) >> 2;   // this warp's 32 rows and kCols columns of the CTA's tile
+        const uint32_t taddr = tmem + ((uint32_t)(sub * 32) << 16) + (uint32_t)(cg * kCols);
+        float* mine = scratch + (warp - kEpi0) * (kScratch / 4);
         int acc = 0;
         uint32_t acc_phase = 0;
         bool ok = true;
         for (int tile = tile0; tile < ntiles && ok; tile += tstep) {
             const int64_t t0 = (int64_t)(tile % a.tiles_m * 2 + (int)rank) * kM + sub * 32;
-            const int64_t v0 = (int64_t)(tile / a.tiles_m) * kN + cg * 64;
+            const int64_t v0 = (int64_t)(tile / a.tiles_m) * kN + cg * kCols;
             const bool active = t0 < a.T && v0 < a.V;
+            // the scales of four blocks at a time, the next four on their way: a thread's row has its own, so each load
+            // touches 32 lines (one block at a time, the epilogue waited for them longer than for the MMAs)
             const float* xs = a.xs + (t0 + lane < a.T ? t0 + lane : 0) * a.nd;
             const float* ws = a.ws + (active ? v0 / kBlock : 0) * a.nd;
-            float c[64];
+            float c[kCols];
 #pragma unroll
-            for (int i = 0; i < 64; ++i) c[i] = 0.f;
-            float xn = active ? __ldg(xs) : 0.f, wn = active ? __ldg(ws) : 0.f;
+            for (int i = 0; i < kCols; ++i) c[i] = 0.f;
+            float4 sc = make_float4(0.f, 0.f, 0.f, 0.f), xn = sc, wn = sc;
+            if (active) xn = four_scales(xs, 0, a.nd), wn = four_scales(ws, 0, a.nd);
             for (int kb = 0; kb < a.nd; ++kb) {
-                const float s = xn * wn;
-                if (active && kb + 1 < a.nd) xn = __ldg(xs + kb + 1), wn = __ldg(ws + kb + 1);
+                if (kb % 4 == 0) {
+                    sc = make_float4(xn.x * wn.x, xn.y * wn.y, xn.z * wn.z, xn.w * wn.w);
+                    if (active && kb + 4 < a.nd) xn = four_scales(xs, kb + 4, a.nd), wn = four_scales(ws, kb + 4, a.nd);
+                }
+                const float s = sc.x;
+                sc = make_float4(sc.y, sc.z, sc.w, 0.f);
                 ok = __all_sync(0xFFFFFFFFu, wait_bar<false>(&acc_full[acc], acc_phase, abort_flag, nullptr, 0, kWaitNs));
                 if (!ok) break;
                 tc_fence_after();
+                const uint32_t to = cluster_addr(&acc_free[acc], 0);
+                auto release = [&]() {               // every load of this accumulator has landed
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_either(to);
+                };
                 if (active) {
-                    uint32_t r[2][16];
+                    uint32_t r[2][32];
                     const uint32_t at = taddr + (uint32_t)(acc * kN);
-                    tmem_ld16(at, r[0]);
+                    tmem_ld32(at, r[0]);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        tmem_wait16(r[q & 1]);
-                        if (q < 3) tmem_ld16(at + (q + 1) * 16, r[(q + 1) & 1]);
+                    for (int q = 0; q < kCols / 32; ++q) {
+                        tmem_wait_ld(r[q & 1]);
+                        if (q + 1 < kCols / 32) tmem_ld32(at + (q + 1) * 32, r[(q + 1) & 1]);
+                        else release();
 #pragma unroll
-                        for (int i = 0; i < 16; i += 2) fma_pair(r[q & 1][i], r[q & 1][i + 1], s, c[q * 16 + i], c[q * 16 + i + 1]);
+                        for (int i = 0; i < 32; i += 2) fma_pair(r[q & 1][i], r[q & 1][i + 1], s, c[q * 32 + i], c[q * 32 + i + 1]);
                     }
+                } else {
+                    release();
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(cluster_addr(&acc_free[acc], 0));
                 acc ^= 1;
                 if (acc == 0) acc_phase ^= 1u;
             }
             if (!ok || !active) continue;
             O* out = static_cast<O*>(a.out) + t0 * a.ld + v0;
-            if (a.aligned && v0 + 64 <= a.V) {       // each lane its row
-                if (t0 + lane < a.T && dbg::ok(v0 + 64 <= a.ld, dbg::kTile)) {
+            if (a.aligned && v0 + kCols <= a.V) {   // each lane its row
+                if (t0 + lane < a.T && dbg::ok(v0 + kCols <= a.ld, dbg::kTile)) {
                     O* p = out + lane * a.ld;
 #pragma unroll
-                    for (int i = 0; i < 64; i += 8) {
+                    for (int i = 0; i < kCols; i += 8) {
                         const float g[8] = {c[i], c[i + 1], c[i + 2], c[i + 3], c[i + 4], c[i + 5], c[i + 6], c[i + 7]};
                         GroupStore<O, 8>::run(p + i, g);
                     }
@@ -271,7 +312,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             } else {                                 // rows of any alignment: 16 columns at a time through shared memory
                 const int rows = (int)min((int64_t)32, a.T - t0);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < kCols / 16; ++q) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) mine[lane * 17 + i] = c[q * 16 + i];
                     __syncwarp();
@@ -536,6 +577,15 @@ cudaError_t run_pair(const void* x, const void* w, int64_t D, LinearArgs& a, cud
     cudaError_t e = prepare_kernel(k_linear_pair<O>, kPairSmem, true, ready, &clusters);
     if (e != cudaSuccess) return e;
     if (clusters < 1) return cudaErrorInvalidConfiguration;
+    // the warpgroups' split waits for registers that the launch has to have
+    static std::atomic<int> regs{0};
+    int r = regs.load();
+    if (r == 0) {
+        cudaFuncAttributes f;
+        if ((e = cudaFuncGetAttributes(&f, k_linear_pair<O>)) != cudaSuccess) return e;
+        regs.store(r = f.numRegs);
+    }
+    if (r * kPairThreads < 128 * kRoleRegs + 32 * kEpiWarps * kEpiRegs) return cudaErrorInvalidConfiguration;
     const int pairs = std::min(a.tiles_m * a.tiles_n, clusters);
     return launch(k_linear_pair<O>, 2 * pairs, 2, kPairThreads, kPairSmem, s, mx, mw, a);
 }
