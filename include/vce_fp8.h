@@ -50,6 +50,15 @@ VCE_API int vce_linear_fp8(const void* x, const float* x_scales, const void* w, 
                            int64_t T, int64_t D, int64_t V, void* out, vce_dtype out_dt, int64_t ld,
                            vce_stream_t s);
 
+/*
+ * vce_test_linear_fp8_stall -- test hook: vce_linear_fp8 to fp32 (ld = V) with its producer announcing 16
+ * more bytes per stage than its copies deliver, so no stage ever completes and every wait, bounded by
+ * wait_ns (1 ms .. 2 s), gives up.  out is NaN; the context stays usable.
+ */
+VCE_API int vce_test_linear_fp8_stall(const void* x, const float* x_scales, const void* w, const float* w_scales,
+                                      int64_t T, int64_t D, int64_t V, float* out, uint64_t wait_ns,
+                                      vce_stream_t s);
+
 #ifdef __cplusplus
 }
 #endif

@@ -175,6 +175,23 @@ VCE_API int preference_loss_backward(const void* logits, vce_dtype dt, int64_t T
                                      const float* row_stats, const float* grad_output, void* grad_logits,
                                      vce_dtype grad_dt, int64_t ld_grad, vce_stream_t s);
 
+/*
+ * Test hooks for the paths of waits that give up, every wait bounded by wait_ns (1 ms .. 2 s), bf16
+ * logits and gradients (ld = V), temperature 1, reduction SUM, no row left out.  The kernels return,
+ * with their copies landed, and the context stays usable.
+ *   vce_test_policy_stall      policy_loss_forward_backward (clipped at 0.2, nothing else) where the last
+ *                              block of every cluster never gets its gradient's coefficients, after the
+ *                              statistics have been exchanged
+ *   vce_test_policy_bwd_stall  policy_loss_backward where a row's last block never gets its last stage
+ */
+VCE_API int vce_test_policy_stall(const void* logits, int64_t T, int64_t V, const int64_t* actions,
+                                  const float* advantages, const float* grad_output, float* loss_rows,
+                                  float* loss_out, float* logprobs, float* row_stats, void* grad_logits,
+                                  uint64_t wait_ns, int32_t* status, vce_stream_t s);
+VCE_API int vce_test_policy_bwd_stall(const void* logits, int64_t T, int64_t V, const int64_t* actions,
+                                      const float* row_stats, const float* grad_output, void* grad_logits,
+                                      uint64_t wait_ns, vce_stream_t s);
+
 #ifdef __cplusplus
 }
 #endif

@@ -190,6 +190,14 @@ def test_linear_same_bits_on_streams_and_in_graphs(vce, T, D, V):
     assert all(torch.equal(o, want) for o in outs)
 
 
+@pytest.mark.parametrize("T", [1, 20, 50, 200, 700])
+def test_linear_waits_that_give_up_leave_nan(vce, T):
+    ops = operands(T, 400, 900)
+    want = vce.linear_fp8(*ops, out_dtype=F32)
+    assert torch.isnan(vce.vce_test_linear_fp8_stall(*ops)).all()
+    assert torch.equal(vce.linear_fp8(*ops, out_dtype=F32), want)
+
+
 def test_head_into_the_losses(vce):
     """As they are used together: a frozen head's logits from quantised hidden states and weights, the reference's
     and the old policy's log-probabilities from those, and the losses of a policy near it; top K of the same logits."""
@@ -210,7 +218,7 @@ def test_head_into_the_losses(vce):
     z.requires_grad_(True)
     adv = torch.randn(T, generator=g).cuda()
     r = O.rows(host(frozen), tokens.cpu().numpy())
-    zm = float(max(frozen.abs().max(), z.abs().max()))
+    zm = float(max(frozen.abs().max(), z.detach().abs().max()))
     G.check_rows(host(ref), None, r, zm, 1.0)
     loss = vce.policy_loss(z, tokens, adv, ref, ref, clip_low=0.9, clip_high=9.0, kl_coef=0.1, entropy_coef=0.01)
     loss.backward()

@@ -531,3 +531,34 @@ def test_refusals(vce):
     with pytest.raises(ValueError):
         vce.preference_loss_backward(z, ids, stats, one, 1, reduction="none", grad_logits=torch.empty(6, 299, device="cuda"))
     torch.cuda.synchronize()
+
+
+# ---- waits that give up -----------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("T,V", [(3, 70000), (2, 20000), (400, 9000), (2, 200000), (170, 128256)])
+def test_waits_that_give_up_are_reported(vce, T, V):
+    """The last block of every cluster waits in vain for its gradient's coefficients, once the statistics have been
+    exchanged and the first block has its results: a status, NaN, and a context that stays usable."""
+    z, ids = logits(T, V, BF16).contiguous(), tokens(T, V)
+    adv = torch.linspace(-1, 1, T).cuda()
+    loss, rows, lp, _, status = vce.vce_test_policy_stall(z, ids, adv)
+    code = vce.vce_get_status(status)
+    assert 105 <= code <= 109 and "gave up" in vce.vce_status_string(code)
+    assert torch.isnan(rows).all() and torch.isnan(lp).all() and torch.isnan(loss).all()
+    one = vce.policy_loss_forward_backward(z, ids, adv, reduction="sum")
+    assert vce.vce_get_status(one[5]) == 0 and torch.isfinite(one[4]).all() and torch.isfinite(one[2]).all()
+
+
+@pytest.mark.parametrize("T,V", [(3, 20000), (5, 100000)])
+def test_backward_waits_that_give_up_leave_nan(vce, T, V):
+    z, ids = logits(T, V, BF16).contiguous(), tokens(T, V)
+    stats = vce.policy_loss_forward(z, ids, torch.ones(T, device="cuda"), reduction="sum")[4]
+    one = torch.ones(1, device="cuda")
+    want = vce.policy_loss_backward(z, ids, stats, one, reduction="sum")
+    got = vce.vce_test_policy_bwd_stall(z, ids, stats)
+    vectors = V // 8                                  # both are multiples of 8: rows of whole vectors
+    parts = -(-vectors // 4096)
+    last = -(-vectors // parts) * (parts - 1) * 8     # the first column of the last block
+    assert torch.isnan(got[:, last:]).all() and torch.equal(got[:, :last], want[:, :last])
+    assert torch.equal(vce.policy_loss_backward(z, ids, stats, one, reduction="sum"), want)

@@ -85,3 +85,49 @@ def test_quantize_keeps_blocks_within_range():
         wide = np.repeat(np.repeat(s, rows, 0)[:130], 128, 1)[:, :200]
         assert np.all(np.abs(q * wide - x) <= np.maximum(2.0 ** -4 * np.abs(x), wide * 2.0 ** -10))
         assert s[-1, 0] == 1.0
+
+
+def test_argument_errors_need_no_gpu():
+    """The C entry points refuse what they can see before any CUDA call."""
+    import ctypes
+    from vocab_cross_entropy_gb300 import build
+    lib = ctypes.CDLL(build.build())
+    P, i64, i32, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
+    x, rows = P(0x1000), [P, i32, i64, i64, i64]
+    f = lib.ce_logprobs_forward
+    f.argtypes = rows + [P, i64, f32, P, P, P, P, P]
+    call = lambda dt=1, T=4, V=8, ld=8, ids=x, tau=1.0, stats=x, status=x: f(x, dt, T, V, ld, ids, -100, tau, x, None, stats, status, None)
+    assert call(dt=7) == -2 and call(V=0) == -3 and call(T=-1) == -3 and call(T=1 << 24) == -3 and call(V=1 << 22, ld=1 << 22) == -3
+    assert call(ld=7) == -4 and call(ids=None) == -1 and call(status=None) == -1
+    assert call(tau=0.0) == call(tau=float("nan")) == call(tau=-1.0) == -8
+    assert call(ids=P(0x1004)) == -5 and call(stats=P(0x1008)) == -5
+    b = lib.ce_logprobs_backward
+    b.argtypes = rows + [P, f32, P, P, P, P, i32, i64, P]
+    assert b(x, 1, 4, 8, 8, x, 1.0, x, x, None, x, 1, 8, None) == -8          # in place
+    assert b(x, 1, 4, 8, 8, x, 1.0, None, x, None, P(0x9000), 1, 8, None) == -1
+    assert b(x, 1, 4, 8, 8, x, 1.0, x, x, None, P(0x9000), 1, 7, None) == -4
+    params = (f32 * 5)(0.2, 0.2, 0.0, 0.0, 0.0)
+    g = lib.policy_loss_forward
+    g.argtypes = rows + [P, i64, f32, P, P, P, P, P, i32, P, P, P, P, P, P, P]
+    call = lambda p=params, red=2, adv=x, ref=None, loss=x: g(x, 1, 4, 8, 8, x, -100, 1.0, None, adv, ref, None, p, red, x, loss, x, None, x, x, None)
+    assert call(p=None) == -1 and call(red=3) == -2 and call(adv=None) == -1 and call(loss=None) == -1
+    for bad in ((-0.1, 0.2, 0, 0, 0), (0.2, -1, 0, 0, 0), (0.2, 0.2, 0.5, 0, 0), (0.2, 0.2, 0, 0.1, 0), (0.2, 0.2, 0, 0, float("inf"))):
+        assert call(p=(f32 * 5)(*bad)) == -8
+    class Pref(ctypes.Structure):
+        _fields_ = [("kind", i32), ("beta", f32), ("eps", f32), ("margin", f32), ("average", i32)]
+    h = lib.preference_loss_forward
+    h.argtypes = rows + [P, i64, f32, P, i64, P, P, i32, P, P, P, P, P, P, P]
+    call = lambda p, n=2, off=x: h(x, 1, 4, 8, 8, x, -100, 1.0, off, n, None, ctypes.byref(p), 2, x, x, x, x, x, x, None)
+    ok = (0, 0.1, 0.0, 0.0, 0)
+    assert call(Pref(*ok), n=-1) == -3 and call(Pref(*ok), off=None) == -1
+    for bad in ((3, 0.1, 0, 0, 0), (0, 0.0, 0, 0, 0), (0, 0.1, 0.6, 0, 0), (1, 0.1, 0.1, 0, 0), (0, 0.1, 0, float("nan"), 0), (0, 0.1, 0, 0, 2)):
+        assert call(Pref(*bad)) == -8
+    q = lib.vce_quantize_fp8
+    q.argtypes = rows + [i32, P, P, P]
+    assert q(x, 1, 4, 0, 8, 1, x, x, None) == -3 and q(x, 1, 4, 8, 8, 64, x, x, None) == -8 and q(x, 1, 4, 8, 7, 1, x, x, None) == -4
+    assert q(x, 5, 4, 8, 8, 1, x, x, None) == -2 and q(x, 1, 4, 8, 8, 1, None, x, None) == -1
+    l = lib.vce_linear_fp8
+    l.argtypes = [P, P, P, P, i64, i64, i64, P, i32, i64, P]
+    assert l(x, x, x, x, 4, 24, 8, x, 1, 8, None) == -3 and l(x, x, x, x, 4, 32, 8, x, 1, 7, None) == -4
+    assert l(P(0x1008), x, x, x, 4, 32, 8, x, 1, 8, None) == -5 and l(x, None, x, x, 4, 32, 8, x, 1, 8, None) == -1
+    assert l(x, x, x, x, 4, 32, 8, x, 9, 8, None) == -2

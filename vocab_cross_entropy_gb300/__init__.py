@@ -124,9 +124,13 @@ def _load(path=None):
         L.vce_test_topk_stall.argtypes = [p, i64, i64, i32, p, p, p, p, u64, p]
         L.vce_test_distill_stall.argtypes = [p, i64, i64, p, p, i32, p, p, p, p, p, u64, p, p]
         L.vce_test_distill_bwd_stall.argtypes = [p, i64, i64, p, i32, p, p, p, p, u64, p]
+        L.vce_test_policy_stall.argtypes = [p, i64, i64, p, p, p, p, p, p, p, p, u64, p, p]
+        L.vce_test_policy_bwd_stall.argtypes = [p, i64, i64, p, p, p, p, u64, p]
+        L.vce_test_linear_fp8_stall.argtypes = [p, p, p, p, i64, i64, i64, p, u64, p]
     for name in ("ce_logprobs_forward", "ce_logprobs_backward", "policy_loss_forward", "policy_loss_backward",
                  "policy_loss_forward_backward", "preference_loss_forward", "preference_loss_backward",
-                 "vce_quantize_fp8", "vce_linear_fp8", "ce_topk", "ce_distill_forward", "ce_distill_backward", "ce_distill_forward_backward",
+                 "vce_quantize_fp8", "vce_linear_fp8", "vce_test_policy_stall", "vce_test_policy_bwd_stall",
+                 "vce_test_linear_fp8_stall", "ce_topk", "ce_distill_forward", "ce_distill_backward", "ce_distill_forward_backward",
                  "logits_process", "logits_process_backward", "ce_forward", "ce_backward", "ce_forward_ls", "ce_backward_ls", "ce_forward_backward",
                  "ce_forward_backward_ls", "ce_merge_chunks_ls",
                  "ce_merge_chunks", "ce_merge_chunks_noalloc",
@@ -587,5 +591,6 @@ from .logits_ops import (MAX_TOPK, ce_distill_backward, ce_distill_forward, ce_d
                          vce_test_distill_bwd_stall, vce_test_distill_stall, vce_test_topk_stall)
 from .policy_ops import (ce_logprobs_backward, ce_logprobs_forward, policy_loss, policy_loss_backward,  # noqa: E402
                          policy_loss_forward, policy_loss_forward_backward, preference_loss,
-                         preference_loss_backward, preference_loss_forward, token_logprobs)
-from .fp8_ops import FP8_BLOCK, linear_fp8, quantize_fp8  # noqa: E402
+                         preference_loss_backward, preference_loss_forward, token_logprobs,
+                         vce_test_policy_bwd_stall, vce_test_policy_stall)
+from .fp8_ops import FP8_BLOCK, linear_fp8, quantize_fp8, vce_test_linear_fp8_stall  # noqa: E402

@@ -42,6 +42,8 @@ struct LinearArgs {
     int tiles_m, tiles_n;        // k_linear_pair
     int split;                   // k_linear_few: CTAs that share a tile's K
     int aligned;                 // out's rows start on 16-byte boundaries
+    uint32_t tx_extra;           // 0; > 0 only in the test hook (no stage ever completes)
+    uint64_t wait_ns;            // bound of every wait
 };
 
 template <bool kCta2>
@@ -191,9 +193,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             for (int tile = tile0; tile < ntiles && !*abort_flag; tile += tstep) {
                 const int t0 = (tile % a.tiles_m * 2 + (int)rank) * kM, v0 = tile / a.tiles_m * kN + (int)rank * (kN / 2);
                 for (int kb = 0; kb < a.nd; ++kb) {
-                    if (!wait_bar<false>(&empty[stage], phase ^ 1u, abort_flag, nullptr, 0, kWaitNs)) break;
+                    if (!wait_bar<false>(&empty[stage], phase ^ 1u, abort_flag, nullptr, 0, a.wait_ns)) break;
                     const uint32_t fb = cluster_addr(&full[stage], 0);   // the even CTA counts both CTAs' bytes
-                    if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * kStageBytes);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * kStageBytes + a.tx_extra);
                     uint8_t* at = smem + stage * kStageBytes;
                     tma_load<true>(at, &mapX, fb, kb * kBlock, t0);
                     tma_load<true>(at + kTileBytes, &mapW, fb, kb * kBlock, v0);
@@ -206,7 +208,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 if (rank == 0) {
                     for (int i = 0; i < issued; ++i) {
                         if (--stage < 0) stage = kStages - 1, phase ^= 1u;
-                        while (!mbar_try_wait(&full[stage], phase) && globaltimer() - t0 < kWaitNs) {
+                        while (!mbar_try_wait(&full[stage], phase) && globaltimer() - t0 < a.wait_ns) {
                         }
                     }
                 } else {         // these complete on the even CTA's barriers: give them time
@@ -221,8 +223,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const uint32_t base = smem_u32(smem);
             for (int tile = tile0; tile < ntiles && !*abort_flag; tile += tstep) {
                 for (int kb = 0; kb < a.nd; ++kb) {
-                    if (!wait_bar<false>(&full[stage], phase, abort_flag, nullptr, 0, kWaitNs)) break;
-                    if (!wait_bar<false>(&acc_free[acc], acc_phase ^ 1u, abort_flag, nullptr, 0, kWaitNs)) break;
+                    if (!wait_bar<false>(&full[stage], phase, abort_flag, nullptr, 0, a.wait_ns)) break;
+                    if (!wait_bar<false>(&acc_free[acc], acc_phase ^ 1u, abort_flag, nullptr, 0, a.wait_ns)) break;
                     tc_fence_after();
                     const uint64_t ad = desc_kmajor_sw128(base + stage * kStageBytes);
                     const uint64_t bd = desc_kmajor_sw128(base + stage * kStageBytes + kTileBytes);
@@ -239,7 +241,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             // every MMA this thread issued has finished before tensor memory can be released
             mma_commit<true>(smem_u32(drain));
             const uint64_t t0 = globaltimer();
-            while (!mbar_try_wait(drain, 0) && globaltimer() - t0 < kWaitNs) {
+            while (!mbar_try_wait(drain, 0) && globaltimer() - t0 < a.wait_ns) {
             }
         }
         __syncwarp();
@@ -271,7 +273,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 }
                 const float s = sc.x;
                 sc = make_float4(sc.y, sc.z, sc.w, 0.f);
-                ok = __all_sync(0xFFFFFFFFu, wait_bar<false>(&acc_full[acc], acc_phase, abort_flag, nullptr, 0, kWaitNs));
+                ok = __all_sync(0xFFFFFFFFu, wait_bar<false>(&acc_full[acc], acc_phase, abort_flag, nullptr, 0, a.wait_ns));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t to = cluster_addr(&acc_free[acc], 0);
@@ -406,8 +408,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             uint32_t phase = 0;
             for (int tile = tile0; tile < ntiles && !*abort_flag; tile += tstep) {
                 for (int kb = k0; kb < k1; ++kb) {
-                    if (!wait_bar<false>(&empty[stage], phase ^ 1u, abort_flag, nullptr, 0, kWaitNs)) break;
-                    mbar_arrive_expect_tx(&full[stage], F::kStage);
+                    if (!wait_bar<false>(&empty[stage], phase ^ 1u, abort_flag, nullptr, 0, a.wait_ns)) break;
+                    mbar_arrive_expect_tx(&full[stage], F::kStage + a.tx_extra);
                     uint8_t* at = smem + stage * F::kStage;
                     tma_load<false>(at, &mapW, smem_u32(&full[stage]), kb * kBlock, tile * kM);
                     tma_load<false>(at + kTileBytes, &mapX, smem_u32(&full[stage]), kb * kBlock, 0);
@@ -419,7 +421,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 const uint64_t t0 = globaltimer();
                 for (int i = 0; i < issued; ++i) {
                     if (--stage < 0) stage = S - 1, phase ^= 1u;
-                    while (!mbar_try_wait(&full[stage], phase) && globaltimer() - t0 < kWaitNs) {
+                    while (!mbar_try_wait(&full[stage], phase) && globaltimer() - t0 < a.wait_ns) {
                     }
                 }
             }
@@ -433,8 +435,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             const uint32_t base = smem_u32(smem);
             for (int tile = tile0; tile < ntiles && !*abort_flag; tile += tstep) {
                 for (int kb = k0; kb < k1; ++kb) {
-                    if (!wait_bar<false>(&acc_free[acc], acc_phase ^ 1u, abort_flag, nullptr, 0, kWaitNs)) break;
-                    if (!wait_bar<false>(&full[stage], phase, abort_flag, nullptr, 0, kWaitNs)) break;
+                    if (!wait_bar<false>(&acc_free[acc], acc_phase ^ 1u, abort_flag, nullptr, 0, a.wait_ns)) break;
+                    if (!wait_bar<false>(&full[stage], phase, abort_flag, nullptr, 0, a.wait_ns)) break;
                     tc_fence_after();
                     const uint64_t ad = desc_kmajor_sw128(base + stage * F::kStage);
                     const uint64_t bd = desc_kmajor_sw128(base + stage * F::kStage + kTileBytes);
@@ -450,7 +452,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             }
             mma_commit<false>(smem_u32(drain));
             const uint64_t t0 = globaltimer();
-            while (!mbar_try_wait(drain, 0) && globaltimer() - t0 < kWaitNs) {
+            while (!mbar_try_wait(drain, 0) && globaltimer() - t0 < a.wait_ns) {
             }
         }
         __syncwarp();
@@ -471,7 +473,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             for (int kb = k0; kb < k1; ++kb) {
                 const float s0 = n0 * wn, s1 = n1 * wn;
                 if (kb + 1 < k1) n0 = __ldg(x0 + kb + 1), n1 = __ldg(x1 + kb + 1), wn = __ldg(ws + kb + 1);
-                ok = __all_sync(0xFFFFFFFFu, wait_bar<false>(&acc_full[acc], acc_phase, abort_flag, nullptr, 0, kWaitNs));
+                ok = __all_sync(0xFFFFFFFFu, wait_bar<false>(&acc_full[acc], acc_phase, abort_flag, nullptr, 0, a.wait_ns));
                 if (!ok) break;
                 tc_fence_after();
                 uint32_t r[N / 16][16];
@@ -622,8 +624,9 @@ VCE_DEBUG_READER(debug_word_fp8)
 
 using namespace vce;
 
-extern "C" int vce_linear_fp8(const void* x, const float* x_scales, const void* w, const float* w_scales, int64_t T,
-                              int64_t D, int64_t V, void* out, vce_dtype out_dt, int64_t ld, vce_stream_t s) {
+static int linear_call(const void* x, const float* x_scales, const void* w, const float* w_scales, int64_t T, int64_t D,
+                       int64_t V, void* out, vce_dtype out_dt, int64_t ld, uint32_t tx_extra, uint64_t wait_ns,
+                       vce_stream_t s) {
     if (out_dt != VCE_F32 && out_dt != VCE_BF16) return VCE_ERR_DTYPE;
     if (T < 0 || T > (int64_t)1 << 24 || V < 1 || V > (int64_t)1 << 24 || D < 16 || D > 65536 || D % 16) return VCE_ERR_SHAPE;
     if (ld < V) return VCE_ERR_LD;
@@ -638,6 +641,18 @@ extern "C" int vce_linear_fp8(const void* x, const float* x_scales, const void* 
     fp8::LinearArgs a{};
     a.xs = x_scales, a.ws = w_scales, a.T = T, a.V = V, a.nd = (int)((D + 127) / 128), a.out = out, a.ld = ld, a.split = 1;
     a.aligned = aligned(out, 16) && ld * (int64_t)es % 16 == 0;
+    a.tx_extra = tx_extra, a.wait_ns = wait_ns;
     const cudaError_t e = out_dt == VCE_BF16 ? fp8::run<uint16_t>(x, w, D, a, s) : fp8::run<float>(x, w, D, a, s);
     return record_cuda(e) == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
+}
+
+extern "C" int vce_linear_fp8(const void* x, const float* x_scales, const void* w, const float* w_scales, int64_t T,
+                              int64_t D, int64_t V, void* out, vce_dtype out_dt, int64_t ld, vce_stream_t s) {
+    return linear_call(x, x_scales, w, w_scales, T, D, V, out, out_dt, ld, 0, tc::kWaitNs, s);
+}
+
+extern "C" int vce_test_linear_fp8_stall(const void* x, const float* x_scales, const void* w, const float* w_scales,
+                                         int64_t T, int64_t D, int64_t V, float* out, uint64_t wait_ns, vce_stream_t s) {
+    if (wait_ns < 1000000ull || wait_ns > tc::kWaitNs) return VCE_ERR_ARG;
+    return linear_call(x, x_scales, w, w_scales, T, D, V, out, VCE_F32, V, 16, wait_ns, s);
 }

@@ -27,52 +27,53 @@ namespace lp {
 using rs::kLn2;
 constexpr float kLn2Lo = -1.90465431e-9f;            // ln 2 = kLn2 + kLn2Lo
 
-// The hardware's base-2 exponential comes out low by this much of itself on the mean (measured over all of
-// [-16, 0] against exp2 in 64 bits: 5.0e-8, each within 1.5e-7), and so does a sum of many.
-constexpr float kEx2Bias = 5.0e-8f;
+// The hardware's base-2 exponential comes out low on the mean, and so does a sum of many: by 4.9e-8 of itself over the
+// terms of a row (measured against exp2 in 64 bits; each is within 1.5e-7), and by about 2e-8 more where the sums of
+// threads and warps are brought to one reference (the mean error of log p_t at 2048 x 32000 and 128256: 1.5e-7 without
+// either correction, 2e-8 with both).
+constexpr float kEx2Bias = 7.0e-8f;
 
 __device__ __forceinline__ float nan_f() { return __int_as_float(0x7FC00000); }
 
-// ---- (reference, sum, sum of products): s = sum 2^y, w = sum 2^y y, y = z k2 - m ------------------------
+// ---- (reference, sum, sum of products): s = sum 2^y, y = z k2 - m, and by kind w = nothing, sum 2^y z (for the
+// mean logit) or sum 2^y y (for the entropy) ---------------------------------------------------------------
+
+enum Kind { kSum = 0, kMean = 1, kEntropy = 2 };
 
 struct Sums {
     float m, s, w;
 };
 
-// log2(e) / temperature as hi + lo, lo > 0 (so a mask's -inf has no product of the other sign): a logit's
-// exponent takes both, since hi alone is off by 2^-25 or so of it, 4e-7 of a term at an exponent of 16, alike
-// for all rows, which a sum over a sequence's rows would add up.
+// log2(e) / temperature as hi + lo.  The exponents take hi alone, which is off by up to 2^-25 of itself: the
+// logarithm of a sum is then off by ln 2 lo E[z], 5e-8 at E[z] = 4, alike for all rows, which a sum over a
+// sequence's rows would add up.  E[z] comes out of w, and what is known to be missing is added.  (Adding z lo to
+// the exponents does nothing: they are rounded by more than that.)
 struct Scale {
     float hi, lo;
 };
 
 // (s, w) to the reference M >= m.
+template <int kKind>
 __device__ __forceinline__ void rescale(Sums& x, float M) {
     const float d = x.m - M;
     const float e = (x.m == M) ? 1.f : ex2(d);
-    x.w = e == 0.f ? 0.f : e * (x.m == M ? x.w : fmaf(d, x.s, x.w));
+    if (kKind == kEntropy) x.w = e == 0.f ? 0.f : e * (x.m == M ? x.w : fmaf(d, x.s, x.w));
+    if (kKind == kMean) x.w *= e;
     x.s *= e;
     x.m = M;
 }
 
-__device__ __forceinline__ void merge(Sums& x, Sums y) {
-    const float M = fmaxf(x.m, y.m);
-    rescale(x, M);
-    rescale(y, M);
-    x.s += y.s;
-    x.w += y.w;
-}
-
-template <bool kEnt>
+// Merges each kSpan lanes' sums, in all of them.
+template <int kKind, int kSpan = 32>
 __device__ __forceinline__ void warp_merge(Sums& x) {
     float M = x.m;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, off));
-    rescale(x, M);
+    for (int off = kSpan / 2; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, off));
+    rescale<kKind>(x, M);
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
+    for (int off = kSpan / 2; off > 0; off >>= 1) {
         x.s += __shfl_xor_sync(0xFFFFFFFFu, x.s, off);
-        if (kEnt) x.w += __shfl_xor_sync(0xFFFFFFFFu, x.w, off);
+        if (kKind != kSum) x.w += __shfl_xor_sync(0xFFFFFFFFu, x.w, off);
     }
 }
 
@@ -95,58 +96,60 @@ __device__ __forceinline__ void fmul2v(float a0, float a1, float b0, float b1, f
 }
 
 // Adds a vector's terms against the reference m: even and odd values apart, two to an instruction, since the
-// issue slots are what these kernels run short of.  An exponent of -inf (a mask) has the product 0: the
-// factor is held at -200, whose power of two is 0.  A NaN stays one (in s).
-template <int G, bool kEnt>
-__device__ __forceinline__ void add_sums(const float (&v)[G], Scale k, float m, float& s0, float& s1, float& w0,
+// issue slots are what these kernels run short of.  For the entropy an exponent of -inf (a mask) is held at -200,
+// whose power of two is 0; for the mean a mask makes w NaN, and push takes the reference's logit for the batch's mean
+// instead.  A NaN stays one (in s).
+template <int G, int kKind>
+__device__ __forceinline__ void add_sums(const float (&v)[G], float k2, float m, float& s0, float& s1, float& w0,
                                          float& w1) {
 #pragma unroll
     for (int i = 0; i < G; i += 2) {
         float a0, a1;
-        ffma2(v[i], v[i + 1], k.hi, -m, a0, a1);
-        ffma2v(v[i], v[i + 1], k.lo, k.lo, a0, a1, a0, a1);
+        ffma2(v[i], v[i + 1], k2, -m, a0, a1);
         const float e0 = ex2(a0), e1 = ex2(a1);
         rs::fadd2(s0, s1, e0, e1, s0, s1);
-        if (kEnt) ffma2v(e0, e1, fmaxf(a0, -200.f), fmaxf(a1, -200.f), w0, w1, w0, w1);
+        if (kKind == kEntropy) ffma2v(e0, e1, fmaxf(a0, -200.f), fmaxf(a1, -200.f), w0, w1, w0, w1);
+        if (kKind == kMean) ffma2v(e0, e1, v[i], v[i + 1], w0, w1, w0, w1);
     }
 }
 
 // s and w of a thread's vectors against the reference m.
-template <int G, int U, bool kEnt>
-__device__ __forceinline__ void sums_of(const float (&v)[U][G], Scale k, float m, float& s, float& w) {
+template <int G, int U, int kKind>
+__device__ __forceinline__ void sums_of(const float (&v)[U][G], float k2, float m, float& s, float& w) {
     float s0[U], s1[U], w0[U], w1[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         s0[u] = s1[u] = w0[u] = w1[u] = 0.f;
-        add_sums<G, kEnt>(v[u], k, m, s0[u], s1[u], w0[u], w1[u]);
+        add_sums<G, kKind>(v[u], k2, m, s0[u], s1[u], w0[u], w1[u]);
     }
 #pragma unroll
     for (int d = 1; d < U; d *= 2)
 #pragma unroll
         for (int u = 0; u + d < U; u += 2 * d) {
             rs::fadd2(s0[u], s1[u], s0[u + d], s1[u + d], s0[u], s1[u]);
-            if (kEnt) rs::fadd2(w0[u], w1[u], w0[u + d], w1[u + d], w0[u], w1[u]);
+            if (kKind != kSum) rs::fadd2(w0[u], w1[u], w0[u + d], w1[u + d], w0[u], w1[u]);
         }
     s = s0[0] + s1[0];
     w = w0[0] + w1[0];
 }
 
 // Adds a thread's vectors of a stage; the reference moves only when a term would pass 2^32.
-template <int G, int U, bool kEnt>
-__device__ __forceinline__ void push(const float (&v)[U][G], Sums& x, Scale k) {
+template <int G, int U, int kKind>
+__device__ __forceinline__ void push(const float (&v)[U][G], Sums& x, float k2) {
     if (x.m == -kInf) {
-        x.m = rs::max_of<G>(v) * k.hi;
+        x.m = rs::max_of<G>(v) * k2;
         if (x.m == -kInf) return;
     }
     float s, w;
 #pragma unroll 1
     for (int again = 0;; again = 1) {   // one copy of the sum's code, for the instruction cache
-        sums_of<G, U, kEnt>(v, k, x.m, s, w);
+        sums_of<G, U, kKind>(v, k2, x.m, s, w);
         if (again || s < 4294967296.f) break;
-        rescale(x, fmaxf(x.m, rs::max_of<G>(v) * k.hi));
+        rescale<kKind>(x, fmaxf(x.m, rs::max_of<G>(v) * k2));
     }
     x.s += s;
-    if (kEnt) x.w += w;
+    if (kKind == kMean && !(fabsf(w) < kInf)) w = s * (x.m / k2);
+    if (kKind != kSum) x.w += w;
 }
 
 // ---- a row's scalars ---------------------------------------------------------------------------------
@@ -172,6 +175,7 @@ __device__ __forceinline__ float split_log(float s, float& near) {
     return (float)e;
 }
 
+template <int kKind>
 __device__ __forceinline__ Row finish(const Sums& x, float zt, Scale k) {
     const float k2 = k.hi;
     Row r;
@@ -191,8 +195,12 @@ __device__ __forceinline__ Row finish(const Sums& x, float zt, Scale k) {
     }
     float near;
     const float e = split_log(x.s, near);
+    // what the exponentials' mean error and the scale's low part leave out
+    const float ratio = kKind == kSum ? 0.f : x.w / x.s;
+    const float mean = kKind == kMean ? ratio : (ratio + x.m) / k2;
     near += kEx2Bias;
-    const float hrest = fmaxf(0.f, fmaf(e - x.w / x.s, kLn2, near));
+    if (kKind != kSum && fabsf(mean) < kInf) near += kLn2 * k.lo * mean;
+    const float hrest = kKind == kEntropy ? fmaxf(0.f, fmaf(e - ratio, kLn2, near)) : 0.f;
     r.m = x.m;
     if (!tok) {
         r.f = 1.f / x.s;

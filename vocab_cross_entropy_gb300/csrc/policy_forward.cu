@@ -245,6 +245,7 @@ cudaError_t run_rows(Args& a, cudaStream_t s) {
     int C = 1;
     while (C < kMaxCluster && a.T * C < sms && (nv + C - 1) / C > 512) C *= 2;
     a.cluster = C;
+    a.per = (int)((nv + C - 1) / C);
     if (C == 1 && a.V * (int64_t)sizeof(S) < kLongRow)
         return run_form<S, kEnt, Short>(a, std::min<int64_t>(a.T, (int64_t)sms * Short::kBlocks), s);
     constexpr auto kern = ring::k_loss_ring<S, float, false, kEnt, Long>;
@@ -297,7 +298,7 @@ static lp::Args rows_args(const void* logits, int64_t T, int64_t V, int64_t ld, 
                           float tau, int mode, float* logprobs, float* entropy, float* row_stats) {
     lp::Args a{};
     a.logits = logits, a.T = T, a.V = V, a.ld = ld, a.ids = ids, a.ignore_index = ignore_index, a.mode = mode;
-    a.k2 = lp::k2_of(tau, &a.k2_lo), a.inv_tau = 1.f / tau, a.logprobs = logprobs, a.entropy = entropy;
+    a.k2 = lp::k2_of(tau), a.k2_lo = lp::k2_rest(tau), a.inv_tau = 1.f / tau, a.logprobs = logprobs, a.entropy = entropy;
     a.row_stats = reinterpret_cast<float4*>(row_stats), a.wait_ns = tc::kWaitNs;
     return a;
 }
@@ -335,16 +336,17 @@ extern "C" int policy_loss_forward(const void* logits, vce_dtype dt, int64_t T, 
     return record_cuda(e) == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
 }
 
-extern "C" int policy_loss_forward_backward(const void* logits, vce_dtype dt, int64_t T, int64_t V, int64_t ld,
-                                            const int64_t* actions, int64_t ignore_index, float temperature,
-                                            const float* old_logprobs, const float* advantages,
-                                            const float* ref_logprobs, const float* weights, const vce_policy_params* p,
-                                            vce_reduction red, const float* grad_output, float* loss_rows,
-                                            float* loss_out, float* logprobs, float* entropy, float* row_stats,
-                                            void* grad_logits, vce_dtype grad_dt, int64_t ld_grad, int32_t* status,
-                                            vce_stream_t s) {
+static int one_pass_call(const void* logits, vce_dtype dt, int64_t T, int64_t V, int64_t ld,
+                          const int64_t* actions, int64_t ignore_index, float temperature,
+                          const float* old_logprobs, const float* advantages,
+                          const float* ref_logprobs, const float* weights, const vce_policy_params* p,
+                          vce_reduction red, const float* grad_output, float* loss_rows,
+                          float* loss_out, float* logprobs, float* entropy, float* row_stats,
+                          void* grad_logits, vce_dtype grad_dt, int64_t ld_grad, int32_t* status,
+                          uint64_t wait_ns, int withhold, vce_stream_t s) {
     lp::Args a = rows_args(logits, T, V, ld, actions, ignore_index, temperature, lp::kPolicy, logprobs, entropy, row_stats);
     a.old = old_logprobs, a.adv = advantages, a.ref = ref_logprobs, a.weights = weights, a.red = red, a.loss_rows = loss_rows;
+    a.wait_ns = wait_ns, a.withhold = withhold;
     int rc = lp::rows_checks(a, dt, temperature, status);
     if (rc || (rc = lp::policy_checks(a, p, loss_out))) return rc;
     if ((rc = lp::check_grad(dt, logits, T, V, ld, grad_logits, grad_dt, ld_grad))) return rc;
@@ -366,12 +368,36 @@ extern "C" int policy_loss_forward_backward(const void* logits, vce_dtype dt, in
     if (e == cudaSuccess) e = lp::finish_rows(a, loss_out, status, !held && red == VCE_RED_MEAN, s);
     if (e == cudaSuccess && T && !held) {
         lp::GradArgs g{};
-        g.logits = logits, g.T = T, g.V = V, g.ld = ld, g.ids = actions, g.mode = lp::kPolicy, g.k2 = a.k2, g.k2_lo = a.k2_lo;
+        g.logits = logits, g.T = T, g.V = V, g.ld = ld, g.ids = actions, g.mode = lp::kPolicy, g.k2 = a.k2;
         g.inv_tau = a.inv_tau, g.row_stats = a.row_stats, g.go = grad_output, g.go_each = red == VCE_RED_NONE;
         g.scale = 1.f, g.grad = grad_logits, g.ld_g = ld_grad, g.wait_ns = tc::kWaitNs;
         e = lp::launch_grad(dt, grad_dt, g, s);
     }
     return record_cuda(e) == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
+}
+
+extern "C" int policy_loss_forward_backward(const void* logits, vce_dtype dt, int64_t T, int64_t V, int64_t ld,
+                                            const int64_t* actions, int64_t ignore_index, float temperature,
+                                            const float* old_logprobs, const float* advantages,
+                                            const float* ref_logprobs, const float* weights, const vce_policy_params* p,
+                                            vce_reduction red, const float* grad_output, float* loss_rows,
+                                            float* loss_out, float* logprobs, float* entropy, float* row_stats,
+                                            void* grad_logits, vce_dtype grad_dt, int64_t ld_grad, int32_t* status,
+                                            vce_stream_t s) {
+    return one_pass_call(logits, dt, T, V, ld, actions, ignore_index, temperature, old_logprobs, advantages, ref_logprobs,
+                         weights, p, red, grad_output, loss_rows, loss_out, logprobs, entropy, row_stats, grad_logits,
+                         grad_dt, ld_grad, status, tc::kWaitNs, 0, s);
+}
+
+extern "C" int vce_test_policy_stall(const void* logits, int64_t T, int64_t V, const int64_t* actions,
+                                     const float* advantages, const float* grad_output, float* loss_rows,
+                                     float* loss_out, float* logprobs, float* row_stats, void* grad_logits,
+                                     uint64_t wait_ns, int32_t* status, vce_stream_t s) {
+    if (wait_ns < 1000000ull || wait_ns > tc::kWaitNs) return VCE_ERR_ARG;
+    const vce_policy_params p{0.2f, 0.2f, 0.f, 0.f, 0.f};
+    return one_pass_call(logits, VCE_BF16, T, V, V, actions, -100, 1.f, nullptr, advantages, nullptr, nullptr, &p,
+                         VCE_RED_SUM, grad_output, loss_rows, loss_out, logprobs, nullptr, row_stats, grad_logits,
+                         VCE_BF16, V, status, wait_ns, 1, s);
 }
 
 extern "C" int preference_loss_forward(const void* logits, vce_dtype dt, int64_t T, int64_t V, int64_t ld,

@@ -76,7 +76,6 @@ __global__ void __launch_bounds__(kConsumers + 32, 3) k_row_grads(const __grid_c
         const Coefs c = ctl.c;
         const float bias = ctl.bias;
         const int target = ctl.target;
-        const Scale sc{a.k2, a.k2_lo};
         for (int j = 0; j < sl.nst; ++j) {
             wait_stage(bar, a.nbuf, j, a.wait_ns);
             uint4 x[kU];
@@ -84,9 +83,9 @@ __global__ void __launch_bounds__(kConsumers + 32, 3) k_row_grads(const __grid_c
             const int v0 = sl.v0 + j * kStageVecs, v1 = sl.v0 + sl.n;
             const bool fast = vec && v0 >= r.iv0 && v0 + kStageVecs <= min(r.iv1, v1);
             if (c.c1 != 0.f)
-                write_grads<S, O, kU, kConsumers, true>(x, r, v0 + tid, v1, fast, grow, vec, c, bias, sc);
+                write_grads<S, O, kU, kConsumers, true>(x, r, v0 + tid, v1, fast, grow, vec, c, bias, a.k2);
             else
-                write_grads<S, O, kU, kConsumers, false>(x, r, v0 + tid, v1, fast, grow, vec, c, bias, sc);
+                write_grads<S, O, kU, kConsumers, false>(x, r, v0 + tid, v1, fast, grow, vec, c, bias, a.k2);
             // the token's entry, over what its thread has just written there
             const int rel = target >= 0 ? (target + r.shift) / Elt<S>::kGroup - v0 - tid : -1;
             if (rel >= 0 && rel < kStageVecs && rel % kConsumers == 0 && v0 + tid + rel < v1)
@@ -132,7 +131,7 @@ static int backward(vce_dtype dt, vce_dtype gdt, lp::GradArgs& a, float tau, cud
     if (!aligned(a.ids, 8) || !aligned(a.row_stats, 16) || !aligned(a.go, 4) || !aligned(a.ga, 4) || !aligned(a.gb, 4))
         return VCE_ERR_ALIGN;
     if ((rc = require_sm100())) return rc;
-    a.k2 = lp::k2_of(tau, &a.k2_lo), a.inv_tau = 1.f / tau;
+    a.k2 = lp::k2_of(tau), a.inv_tau = 1.f / tau;
     if (!a.wait_ns) a.wait_ns = tc::kWaitNs;
     return record_cuda(lp::launch_grad(dt, gdt, a, s)) == cudaSuccess ? VCE_OK : VCE_ERR_CUDA;
 }
@@ -171,4 +170,15 @@ extern "C" int preference_loss_backward(const void* logits, vce_dtype dt, int64_
     a.row_stats = reinterpret_cast<const float4*>(row_stats), a.go = grad_output, a.go_each = red == VCE_RED_NONE;
     a.scale = red == VCE_RED_MEAN && P > 0 ? (float)(1.0 / (double)P) : 1.f, a.grad = grad_logits, a.ld_g = ld_grad;
     return backward(dt, grad_dt, a, temperature, s);
+}
+
+extern "C" int vce_test_policy_bwd_stall(const void* logits, int64_t T, int64_t V, const int64_t* actions,
+                                         const float* row_stats, const float* grad_output, void* grad_logits,
+                                         uint64_t wait_ns, vce_stream_t s) {
+    if (wait_ns < 1000000ull || wait_ns > tc::kWaitNs) return VCE_ERR_ARG;
+    lp::GradArgs a{};
+    a.logits = logits, a.T = T, a.V = V, a.ld = V, a.ids = actions, a.mode = lp::kPolicy;
+    a.row_stats = reinterpret_cast<const float4*>(row_stats), a.go = grad_output, a.scale = 1.f, a.grad = grad_logits;
+    a.ld_g = V, a.wait_ns = wait_ns, a.withhold = 1;
+    return backward(VCE_BF16, VCE_BF16, a, 1.f, s);
 }

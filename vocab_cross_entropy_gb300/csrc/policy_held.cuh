@@ -39,6 +39,7 @@ template <typename S, typename O, bool kGrad, bool kEnt, typename F>
 __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_held(const __grid_constant__ Args a) {
     constexpr int G = Elt<S>::kGroup, NT = F::kNT, U = F::kU, kWarps = NT / 32;
     static_assert(U % 2 == 0, "vectors go in pairs");
+    constexpr int kKind = kEnt ? kEntropy : kGrad ? kSum : kMean;    // as the ring's
     __shared__ Sums part[kWarps > 1 ? kWarps : 1];
     __shared__ float4 slot[kMaxCluster];
     __shared__ RowCoefs coefs_of_row;
@@ -108,7 +109,6 @@ __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_held(const __g
     // the sums, the token's column left out
     const int at = (int)t + r.shift, tv = at / G - sl.v0 - tid, tk = at % G;
     const int tu = tv >= 0 && tv < F::kVecs && tv % NT == 0 ? tv / NT : -1;
-    const Scale sc{a.k2, a.k2_lo};
     Sums sum{-kInf, 0.f, 0.f};
 #pragma unroll
     for (int u = 0; u < U; u += 2) {
@@ -122,15 +122,15 @@ __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_held(const __g
                 if (k == tk && tu == u + 1) v[1][k] = -kInf;
             }
         }
-        push<G, 2, kEnt>(v, sum, sc);
+        push<G, 2, kKind>(v, sum, a.k2);
     }
-    warp_merge<kEnt>(sum);
+    warp_merge<kKind>(sum);
     if (kWarps > 1) {
         if (lane == 0) part[warp] = sum;
         __syncthreads();
         if (warp == 0) {
             sum = lane < kWarps ? part[lane] : Sums{-kInf, 0.f, 0.f};
-            warp_merge<kEnt>(sum);
+            warp_merge<kKind>(sum);
         }
         if (C > 1) {
             cluster_wait();                                          // every peer runs
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_held(const __g
                     const float4 o = slot[lane];
                     sum = Sums{o.x, o.y, o.z};
                 }
-                warp_merge<kEnt>(sum);                               // the same order in every block
+                warp_merge<kKind>(sum);                               // the same order in every block
             }
         }
     }
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_held(const __g
             wait_previous();                                         // the count of the rows
             go *= *a.inv_n;
         }
-        const lp::Row res = finish(sum, in.zt, Scale{a.k2, a.k2_lo});
+        const lp::Row res = finish<kKind>(sum, in.zt, Scale{a.k2, a.k2_lo});
         float loss = 0.f;
         const float4 st = row_result(a, res, in, kGrad ? go : 1.f, loss);
         cf = RowCoefs{Coefs{st.y, st.z, st.w}, res.m, res.dead};
@@ -179,9 +179,9 @@ __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_held(const __g
     const int v0 = sl.v0, v1 = sl.v0 + sl.n;
     const bool fast = vec && v0 >= r.iv0 && v0 + F::kVecs <= min(r.iv1, v1);
     if (kEnt && cf.c.c1 != 0.f)
-        write_grads<S, O, U, NT, true>(x, r, v0 + tid, v1, fast, grow, vec, cf.c, cf.bias, sc);
+        write_grads<S, O, U, NT, true>(x, r, v0 + tid, v1, fast, grow, vec, cf.c, cf.bias, a.k2);
     else
-        write_grads<S, O, U, NT, false>(x, r, v0 + tid, v1, fast, grow, vec, cf.c, cf.bias, sc);
+        write_grads<S, O, U, NT, false>(x, r, v0 + tid, v1, fast, grow, vec, cf.c, cf.bias, a.k2);
     if (tu >= 0 && sl.v0 + tid + tu * NT < v1) Elt<O>::store1(grow + t, cf.c.gt);   // over what this thread wrote there
 }
 

@@ -20,8 +20,8 @@ using Block = held::Form<128, 8, 8>;
 // Rows (or a cluster's slices of one) of up to 64 KB: two blocks an SM, four consumer warps each, so that what a row
 // costs beside its columns runs under the other block's columns; longer ones have a whole SM.
 using Pair = ring::Form<4, 2, 8, 6, 4>;
-using Whole = ring::Form<16, 1, 2, 13, 8>;
-constexpr int64_t kLongRow = 131072;
+using Whole = ring::Form<14, 1, 2, 15, 10>;
+constexpr int64_t kLongRow = 65536;
 
 template <typename S>
 int64_t vectors(int64_t V) { return (V + 2 * Elt<S>::kGroup - 2) / Elt<S>::kGroup; }
@@ -44,6 +44,7 @@ cudaError_t run_ring(Args& a, cudaStream_t s) {
     int C = 1;
     while (C < kMaxCluster && (stages<F>(nv, C) > F::kHeld || (a.T * C < sms && stages<F>(nv, C) > 1))) C *= 2;
     a.cluster = C;
+    a.per = (int)((nv + C - 1) / C);
     if (a.withhold) a.withhold = C;
     const int64_t fit = std::min<int64_t>(
         a.T, resident_clusters<kern>(C, F::kThreads, ring::smem_bytes<F>(), sms * (C == 1 ? F::kBlocks : 1)));

@@ -35,6 +35,7 @@ template <int kWarps_, int kBlocks_, int kU_, int kBufs_, int kHeld_>
 struct Form {
     static constexpr int kWarps = kWarps_, kNT = kWarps * 32;                 // consumers
     static constexpr int kBlocks = kBlocks_;                                  // of an SM
+    static constexpr int kSpan = kWarps > 16 ? 32 : kWarps > 8 ? 16 : 8;      // lanes that merge the warps' sums
     static constexpr int kProducer = kWarps, kStats = kWarps + 1;
     static constexpr int kThreads = (kWarps + 2) * 32;
     static constexpr int kU = kU_;                                            // vectors of a stage per consumer thread
@@ -85,11 +86,10 @@ __device__ __forceinline__ rs::Row row_extent(const Args& a, int64_t row) {
     return r;
 }
 
-// make_slice in stages of the ring; parts is a power of two.
+// The vectors of a row that a block takes, per of them, in stages of the ring.
 template <typename F>
-__device__ __forceinline__ Slice ring_slice(const rs::Row& r, int parts, int part) {
+__device__ __forceinline__ Slice ring_slice(const rs::Row& r, int per, int part) {
     Slice s;
-    const int per = (r.nv + parts - 1) >> (31 - __clz(parts));
     s.v0 = min(r.nv, part * per);
     s.n = min(r.nv - s.v0, per);
     s.nst = (s.n + F::kVecs - 1) / F::kVecs;
@@ -176,6 +176,8 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity)
 template <typename S, typename O, bool kGrad, bool kEnt, typename F>
 __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_ring(const __grid_constant__ Args a) {
     constexpr int G = Elt<S>::kGroup;
+    // with a gradient the sums are taken against the same scale as its entries, and no mean is needed
+    constexpr int kKind = kEnt ? kEntropy : kGrad ? kSum : kMean;
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int nbuf = F::kBufs, U = F::kU, B = U < 4 ? U : 4, kVecs = F::kVecs, kWarps = F::kWarps, kNT = F::kNT;
     Ctl<kWarps, nbuf>& ctl = *reinterpret_cast<Ctl<kWarps, nbuf>*>(smem + nbuf * F::kBytes);
@@ -221,7 +223,7 @@ __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_ring(const __g
             Edge e{0xFFFFFFFFu, neg};
             if (row < 0) return e;
             const rs::Row r = row_extent<S>(a, row);
-            const Slice sl = ring_slice<F>(r, C, rank);
+            const Slice sl = ring_slice<F>(r, a.per, rank);
             const int edge = lane < G ? (r.shift ? 0 : -1) : (r.iv1 < r.nv && (r.nv > 1 || !r.shift) ? r.nv - 1 : -1);
             if (lane < 2 * G && edge >= sl.v0 && edge < sl.v0 + sl.n) {
                 const int64_t col = (int64_t)edge * G - r.shift + lane % G;
@@ -234,7 +236,7 @@ __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_ring(const __g
         Edge edge = load_edge(row);
         while (row >= 0 && !*reinterpret_cast<volatile int*>(&ctl.abort)) {
             const rs::Row r = make_row<S>(a.logits, row, a.ld, a.V);
-            const Slice sl = ring_slice<F>(r, C, rank);
+            const Slice sl = ring_slice<F>(r, a.per, rank);
             const int64_t next = walk_next(walk, a, token);
             const Edge later = load_edge(next);
             const bool edges = __any_sync(0xFFFFFFFFu, edge.place != 0xFFFFFFFFu);
@@ -287,7 +289,7 @@ __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_ring(const __g
         auto flush = [&]() {
             if (!kGrad && lane < pending && rank == 0) {
                 const RowIn in = row_in<S>(a, kept_row, kept_token);
-                const Row r = finish(kept, in.zt, Scale{a.k2, a.k2_lo});
+                const Row r = finish<kKind>(kept, in.zt, Scale{a.k2, a.k2_lo});
                 float loss = 0.f;
                 const float4 st = row_result(a, r, in, 1.f, loss);
                 write_result(a, kept_row, r, st, loss);
@@ -308,13 +310,13 @@ __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_ring(const __g
             }
             if (!wait(&ctl.paired[par], e, kErrPartials)) break;
             Sums x = lane < kWarps ? ctl.red[par][lane] : Sums{-kInf, 0.f, 0.f};
-            warp_merge<kEnt>(x);
+            warp_merge<kKind, kGrad ? F::kSpan : 32>(x);  // (with a gradient lane 0 alone goes on with it)
             if (!kGrad) {                              // (every lane has read its warp's sums)
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&ctl.finished[par]);
             }
             if (C > 1) {
-                if (lane < C) {
+                if (lane < C) {                        // C <= kSpan: these lanes have the sums
                     st_peer(peer_addr(&ctl.slot[par][rank], lane), make_float4(x.m, x.s, x.w, 0.f));
                     arrive_peer(peer_addr(&ctl.exchanged[par], lane));
                 }
@@ -336,10 +338,10 @@ __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_ring(const __g
                     const float4 o = ctl.slot[par][lane];
                     x = Sums{o.x, o.y, o.z};
                 }
-                warp_merge<kEnt>(x);                   // the same order in every block
+                warp_merge<kKind, kGrad ? kMaxCluster : 32>(x);   // the same order in every block
             }
             if (kGrad) {
-                const Row r = finish(x, in.zt, Scale{a.k2, a.k2_lo});
+                const Row r = finish<kKind>(x, in.zt, Scale{a.k2, a.k2_lo});
                 float loss = 0.f;
                 const float4 st = row_result(a, r, in, go, loss);
                 if (lane == 0) {
@@ -397,13 +399,13 @@ __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_ring(const __g
                             for (int k = 0; k < G; ++k)
                                 if (rel == (h + u) * kNT && k == tk) v[u][k] = -kInf;
                     }
-                    push<G, B, kEnt>(v, x, Scale{a.k2, a.k2_lo});
+                    push<G, B, kKind>(v, x, a.k2);
                 }
             }
         };
         auto publish = [&](int64_t e, Sums x) {
             const int par = (int)(e & 1);
-            warp_merge<kEnt>(x);
+            warp_merge<kKind>(x);
             // row e - 2's sums have been read (with a gradient that follows from its coefficients)
             if (!kGrad && e >= 2) wait(&ctl.finished[par], e - 2, kErrCoefs);
             if (lane == 0) {
@@ -418,7 +420,7 @@ __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_ring(const __g
                 if (!kGrad) return;
                 const rs::Row r = row_extent<S>(a, no);
                 O* g = static_cast<O*>(a.grad) + no * a.ld_g;
-                fill_grads<S, O>(r, ring_slice<F>(r, C, rank), g, grads_aligned<S, O>(r, g), tid, kNT);
+                fill_grads<S, O>(r, ring_slice<F>(r, a.per, rank), g, grads_aligned<S, O>(r, g), tid, kNT);
             });
         };
         int tok = 0, tok2 = 0;
@@ -433,7 +435,7 @@ __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_ring(const __g
             int pre = 0, tv = -1, tk = 0;
             if (row2 >= 0) {
                 r2 = row_extent<S>(a, row2);
-                sl2 = ring_slice<F>(r2, C, rank);
+                sl2 = ring_slice<F>(r2, a.per, rank);
                 const int p = tok2 + r2.shift;
                 tv = p / G - sl2.v0;
                 tk = p % G;
@@ -452,7 +454,6 @@ __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_ring(const __g
                 const RowCoefs cf = ctl.coefs[par];
                 O* grow = static_cast<O*>(a.grad) + row * a.ld_g;
                 const bool vec = grads_aligned<S, O>(r, grow);
-                const Scale sc{a.k2, a.k2_lo};
                 const int fast0 = vec ? r.iv0 : r.nv, fast1 = min(r.iv1, sl.v0 + sl.n);
                 for (int j = 0; j < sl.nst; ++j, back.step()) {
                     const uint4* buf = reinterpret_cast<const uint4*>(smem + back.st * F::kBytes) + tid;
@@ -469,9 +470,9 @@ __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_ring(const __g
                             for (int u = 0; u < B; ++u) raw[u] = tc::lds16(buf + (h + u) * kNT);
                             const bool fast = v0 >= fast0 && v0 + B * kNT <= fast1;
                             if (kEnt && cf.c.c1 != 0.f)
-                                write_grads<S, O, B, kNT, true>(raw, r, v0 + tid, v1, fast, grow, vec, cf.c, cf.bias, sc);
+                                write_grads<S, O, B, kNT, true>(raw, r, v0 + tid, v1, fast, grow, vec, cf.c, cf.bias, a.k2);
                             else
-                                write_grads<S, O, B, kNT, false>(raw, r, v0 + tid, v1, fast, grow, vec, cf.c, cf.bias, sc);
+                                write_grads<S, O, B, kNT, false>(raw, r, v0 + tid, v1, fast, grow, vec, cf.c, cf.bias, a.k2);
                         }
                         // the token's entry, over what its thread has just written there
                         const int rel = (tok + r.shift) / G - first - tid;

@@ -41,7 +41,7 @@ struct Args {
     const float* inv_n;          // MEAN
     void* grad;
     int64_t ld_g;
-    int cluster;
+    int cluster, per;            // blocks of a row, vectors of a block
     uint64_t wait_ns;            // bound of every wait
     int withhold;                // n > 0 (test hook): in a cluster's block n - 1 the gradient waits in vain
 };
@@ -52,7 +52,7 @@ struct GradArgs {
     int64_t T, V, ld;
     const int64_t* ids;
     int mode;
-    float k2, k2_lo, inv_tau;
+    float k2, inv_tau;
     const float4* row_stats;
     const float* go;             // kPolicy, kPreference
     int go_each;                 // one for each row (pair), else one
@@ -70,14 +70,9 @@ bool one_pass_holds(vce_dtype dt, int64_t V);
 cudaError_t launch_one_pass(vce_dtype dt, vce_dtype gdt, Args& a, cudaStream_t s);
 cudaError_t launch_grad(vce_dtype dt, vce_dtype gdt, GradArgs& a, cudaStream_t s);
 
-// log2(e) / tau rounded down, and what is left of it (> 0).
-inline float k2_of(float tau, float* rest = nullptr) {
-    const double exact = 1.4426950408889634 / (double)tau;
-    float k = (float)exact;
-    if ((double)k >= exact) k = std::nextafter(k, 0.f);
-    if (rest) *rest = (float)(exact - (double)k);
-    return k;
-}
+// log2(e) / tau, and what is left of it.
+inline float k2_of(float tau) { return (float)(1.4426950408889634 / (double)tau); }
+inline float k2_rest(float tau) { return (float)(1.4426950408889634 / (double)tau - (double)k2_of(tau)); }
 
 inline int check_shape(vce_dtype dt, int64_t T, int64_t V, int64_t ld, float tau) {
     if (dt != VCE_F32 && dt != VCE_BF16) return VCE_ERR_DTYPE;

@@ -49,12 +49,11 @@ __device__ __forceinline__ void write_zeros(const rs::Row& r, const Slice& s, in
 // The gradients of a vector's G logits, in their place.  kEnt: c.c1 is not 0.  A mask's exponent of -inf is
 // held at -200 there, as in the sums.
 template <int G, bool kEnt>
-__device__ __forceinline__ void grads_of(float (&g)[G], const Coefs& c, float bias, Scale sc) {
+__device__ __forceinline__ void grads_of(float (&g)[G], const Coefs& c, float bias, float k2) {
 #pragma unroll
     for (int k = 0; k < G; k += 2) {
         float a0, a1;
-        ffma2(g[k], g[k + 1], sc.hi, -bias, a0, a1);
-        ffma2v(g[k], g[k + 1], sc.lo, sc.lo, a0, a1, a0, a1);
+        ffma2(g[k], g[k + 1], k2, -bias, a0, a1);
         const float e0 = ex2(a0), e1 = ex2(a1);
         if (kEnt) {
             float f0, f1;
@@ -69,11 +68,11 @@ __device__ __forceinline__ void grads_of(float (&g)[G], const Coefs& c, float bi
 // A vector of the row from its first column c0 on (before the row's start where it is partial), element by
 // element: partial vectors, and gradients that are not aligned as the logits are.
 template <typename S, typename O>
-__device__ __noinline__ void write_single(uint4 x, int64_t c0, int64_t V, O* grow, Coefs c, float bias, Scale sc) {
+__device__ __noinline__ void write_single(uint4 x, int64_t c0, int64_t V, O* grow, Coefs c, float bias, float k2) {
     constexpr int G = Elt<S>::kGroup;
     float g[G];
     Elt<S>::unpack(x, g);
-    grads_of<G, true>(g, c, bias, sc);
+    grads_of<G, true>(g, c, bias, k2);
 #pragma unroll
     for (int k = 0; k < G; ++k)
         if (c0 + k >= 0 && c0 + k < V) Elt<O>::store1(grow + c0 + k, g[k]);
@@ -83,7 +82,7 @@ __device__ __noinline__ void write_single(uint4 x, int64_t c0, int64_t V, O* gro
 // them lie wholly in the row and the slice, and are aligned in the gradient too.
 template <typename S, typename O, int U, int NT, bool kEnt>
 __device__ __forceinline__ void write_grads(const uint4 (&x)[U], const rs::Row& r, int v0, int v1, bool fast, O* grow,
-                                            bool vec, const Coefs& c, float bias, Scale sc) {
+                                            bool vec, const Coefs& c, float bias, float k2) {
     constexpr int G = Elt<S>::kGroup;
     if (fast) {
         O* p = grow + ((int64_t)v0 * G - r.shift);
@@ -91,7 +90,7 @@ __device__ __forceinline__ void write_grads(const uint4 (&x)[U], const rs::Row& 
         for (int u = 0; u < U; ++u) {
             float g[G];
             Elt<S>::unpack(x[u], g);
-            grads_of<G, kEnt>(g, c, bias, sc);
+            grads_of<G, kEnt>(g, c, bias, k2);
             GroupStore<O, G>::run(p + u * NT * G, g);
         }
         return;
@@ -104,10 +103,10 @@ __device__ __forceinline__ void write_grads(const uint4 (&x)[U], const rs::Row& 
         if (vec && v >= r.iv0 && v < r.iv1) {
             float g[G];
             Elt<S>::unpack(x[u], g);
-            grads_of<G, kEnt>(g, c, bias, sc);
+            grads_of<G, kEnt>(g, c, bias, k2);
             GroupStore<O, G>::run(grow + c0, g);
         } else {
-            write_single<S, O>(x[u], c0, r.V, grow, c, bias, sc);
+            write_single<S, O>(x[u], c0, r.V, grow, c, bias, k2);
         }
     }
 }

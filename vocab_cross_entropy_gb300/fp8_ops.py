@@ -50,3 +50,12 @@ def linear_fp8(x, x_scales, w, w_scales, *, out=None, out_dtype=torch.bfloat16, 
     out, p_out, odt, ld = _matrix_out(out, "out", T, V, out_dtype, dev, stream)
     _run("vce_linear_fp8", dev, stream, *p, T, D, V, p_out, odt, ld)
     return out
+
+
+def vce_test_linear_fp8_stall(x, x_scales, w, w_scales, wait_ns=50_000_000, *, stream=None):
+    """Test hook: linear_fp8 whose stages never complete.  Returns out (float32)."""
+    (T, D), V = x.shape, w.shape[0]
+    out = torch.zeros(T, V, device=x.device)
+    _run("vce_test_linear_fp8_stall", x.device, stream, x.data_ptr(), x_scales.data_ptr(), w.data_ptr(),
+         w_scales.data_ptr(), T, D, V, out.data_ptr(), int(wait_ns))
+    return out

@@ -83,10 +83,21 @@ def _as_f32(grad):
 
 
 class _LogProbs(torch.autograd.Function):
+    """What the backward needs, and the status word, lie in one float32 buffer (of the functions below too: an
+    allocation costs a call more than its marshalling)."""
+
     @staticmethod
     def forward(ctx, logits, ids, temperature, ignore_index, want_entropy):
-        lp, ent, stats, _ = ce_logprobs_forward(logits, ids, temperature, ignore_index, want_entropy=want_entropy)
-        ctx.save_for_backward(logits, ids, stats)
+        dt, T, V, ld = _matrix(logits, "logits")
+        dev = logits.device
+        p_ids = _given(ids, "ids", _I64, (T,), dev)
+        lp = torch.empty(T, dtype=_F32, device=dev)
+        ent = torch.empty(T, dtype=_F32, device=dev) if want_entropy else None
+        kept = torch.empty(ROW_STATS * T + 1, dtype=_F32, device=dev)
+        stats = kept.data_ptr()
+        _run("ce_logprobs_forward", dev, None, logits.data_ptr(), dt, T, V, ld, p_ids, ignore_index, temperature,
+             lp.data_ptr(), ent.data_ptr() if want_entropy else None, stats, stats + 4 * ROW_STATS * T)
+        ctx.save_for_backward(logits, ids, kept)
         ctx.temperature = temperature
         ctx.set_materialize_grads(False)
         return (lp, ent) if want_entropy else lp
@@ -94,8 +105,13 @@ class _LogProbs(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad_lp, grad_ent=None):
-        logits, ids, stats = ctx.saved_tensors
-        g = ce_logprobs_backward(logits, ids, stats, _as_f32(grad_lp), _as_f32(grad_ent), ctx.temperature)
+        logits, ids, kept = ctx.saved_tensors
+        dt, T, V, ld = _matrix(logits, "logits")
+        grad_lp, grad_ent = _as_f32(grad_lp), _as_f32(grad_ent)
+        g = torch.empty((T, V), dtype=logits.dtype, device=logits.device)
+        _run("ce_logprobs_backward", logits.device, None, logits.data_ptr(), dt, T, V, ld, ids.data_ptr(),
+             ctx.temperature, kept.data_ptr(), None if grad_lp is None else grad_lp.data_ptr(),
+             None if grad_ent is None else grad_ent.data_ptr(), g.data_ptr(), dt, V)
         return g, None, None, None, None
 
 
@@ -108,7 +124,7 @@ def token_logprobs(logits, ids, temperature=1.0, ignore_index=IGNORE_INDEX, want
 # ---- policy loss --------------------------------------------------------------------------------
 
 
-def _policy_args(logits, actions, advantages, old_logprobs, ref_logprobs, weights, T, dev):
+def _policy_args(actions, advantages, old_logprobs, ref_logprobs, weights, T, dev):
     return (_given(actions, "actions", _I64, (T,), dev), _flat(old_logprobs, "old_logprobs", _F32, (T,), dev),
             _given(advantages, "advantages", _F32, (T,), dev), _flat(ref_logprobs, "ref_logprobs", _F32, (T,), dev),
             _flat(weights, "weights", _F32, (T,), dev))
@@ -128,7 +144,7 @@ def policy_loss_forward(logits, actions, advantages, old_logprobs=None, ref_logp
     """
     dt, T, V, ld = _matrix(logits, "logits")
     dev = logits.device
-    p_act, p_old, p_adv, p_ref, p_w = _policy_args(logits, actions, advantages, old_logprobs, ref_logprobs, weights, T, dev)
+    p_act, p_old, p_adv, p_ref, p_w = _policy_args(actions, advantages, old_logprobs, ref_logprobs, weights, T, dev)
     params = _PolicyParams(clip_low, clip_high, dual_clip, kl_coef, entropy_coef)
     red = RED[reduction]
     loss_rows, p_rows = _out(loss_rows, "loss_rows", _F32, (T,), dev, stream)
@@ -171,7 +187,7 @@ def policy_loss_forward_backward(logits, actions, advantages, old_logprobs=None,
     """
     dt, T, V, ld = _matrix(logits, "logits")
     dev = logits.device
-    p_act, p_old, p_adv, p_ref, p_w = _policy_args(logits, actions, advantages, old_logprobs, ref_logprobs, weights, T, dev)
+    p_act, p_old, p_adv, p_ref, p_w = _policy_args(actions, advantages, old_logprobs, ref_logprobs, weights, T, dev)
     params = _PolicyParams(clip_low, clip_high, dual_clip, kl_coef, entropy_coef)
     red = RED[reduction]
     if grad_output is None:
@@ -198,20 +214,32 @@ def policy_loss_forward_backward(logits, actions, advantages, old_logprobs=None,
 
 class _Policy(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, logits, actions, advantages, old, ref, weights, kw):
-        loss, rows, _, _, stats, _ = policy_loss_forward(logits, actions, advantages, old, ref, weights, **kw)
-        ctx.save_for_backward(logits, actions, stats)
-        ctx.temperature, ctx.reduction = kw["temperature"], kw["reduction"]
-        return rows if ctx.reduction == "none" else loss.view(())
+    def forward(ctx, logits, actions, advantages, old, ref, weights, params, temperature, ignore_index, reduction):
+        dt, T, V, ld = _matrix(logits, "logits")
+        dev = logits.device
+        p_act, p_old, p_adv, p_ref, p_w = _policy_args(actions, advantages, old, ref, weights, T, dev)
+        red = RED[reduction]
+        loss = torch.empty(() if red else T, dtype=_F32, device=dev)
+        kept = torch.empty((ROW_STATS + 2) * T + 1, dtype=_F32, device=dev)   # row_stats, loss_rows, logprobs, status
+        stats = kept.data_ptr()
+        rows = stats + 4 * ROW_STATS * T
+        _run("policy_loss_forward", dev, None, logits.data_ptr(), dt, T, V, ld, p_act, ignore_index, temperature, p_old,
+             p_adv, p_ref, p_w, ctypes.byref(params), red, rows if red else loss.data_ptr(),
+             loss.data_ptr() if red else None, rows + 4 * T, None, stats, rows + 8 * T)
+        ctx.save_for_backward(logits, actions, kept)
+        ctx.temperature, ctx.red = temperature, red
+        return loss
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
-        logits, actions, stats = ctx.saved_tensors
+        logits, actions, kept = ctx.saved_tensors
+        dt, T, V, ld = _matrix(logits, "logits")
         grad = _as_f32(grad)
-        g = policy_loss_backward(logits, actions, stats, grad if ctx.reduction == "none" else grad.view(1),
-                                 ctx.temperature, ctx.reduction)
-        return (g,) + (None,) * 6
+        g = torch.empty((T, V), dtype=logits.dtype, device=logits.device)
+        _run("policy_loss_backward", logits.device, None, logits.data_ptr(), dt, T, V, ld, actions.data_ptr(),
+             ctx.temperature, ctx.red, kept.data_ptr(), grad.data_ptr(), g.data_ptr(), dt, V)
+        return (g,) + (None,) * 9
 
 
 def policy_loss(logits, actions, advantages, old_logprobs=None, ref_logprobs=None, weights=None, *, clip_low=0.2,
@@ -219,9 +247,9 @@ def policy_loss(logits, actions, advantages, old_logprobs=None, ref_logprobs=Non
                 ignore_index=IGNORE_INDEX, reduction="mean"):
     """policy_loss_forward with autograd: the loss (the rows' with reduction "none"), its gradient w.r.t. the
     logits; everything else is a constant."""
-    kw = dict(clip_low=clip_low, clip_high=clip_high, dual_clip=dual_clip, kl_coef=kl_coef, entropy_coef=entropy_coef,
-              temperature=float(temperature), ignore_index=ignore_index, reduction=reduction)
-    return _Policy.apply(logits, actions, advantages, old_logprobs, ref_logprobs, weights, kw)
+    return _Policy.apply(logits, actions, advantages, old_logprobs, ref_logprobs, weights,
+                         _PolicyParams(clip_low, clip_high, dual_clip, kl_coef, entropy_coef), float(temperature),
+                         ignore_index, reduction)
 
 
 # ---- preference loss ----------------------------------------------------------------------------
@@ -282,26 +310,71 @@ def preference_loss_backward(logits, labels, row_stats, grad_output, pairs, temp
 
 class _Preference(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, logits, labels, offsets, ref, kw):
-        loss, pairs, _, _, stats, _ = preference_loss_forward(logits, labels, offsets, ref, **kw)
-        ctx.save_for_backward(logits, labels, stats)
-        ctx.pairs, ctx.temperature, ctx.reduction = pairs.shape[0], kw["temperature"], kw["reduction"]
-        return pairs if ctx.reduction == "none" else loss.view(())
+    def forward(ctx, logits, labels, offsets, ref, params, temperature, ignore_index, reduction):
+        dt, T, V, ld = _matrix(logits, "logits")
+        dev = logits.device
+        P, p_off = _pairs(offsets, dev)
+        p_lab = _given(labels, "labels", _I64, (T,), dev)
+        red = RED[reduction]
+        loss = torch.empty(() if red else P, dtype=_F32, device=dev)
+        # row_stats, logprobs, rewards, pair_losses, status
+        kept = torch.empty((ROW_STATS + 1) * T + 3 * P + 1, dtype=_F32, device=dev)
+        stats = kept.data_ptr()
+        lp = stats + 4 * ROW_STATS * T
+        rewards = lp + 4 * T
+        pairs = rewards + 8 * P
+        _run("preference_loss_forward", dev, None, logits.data_ptr(), dt, T, V, ld, p_lab, ignore_index, temperature,
+             p_off, P, _flat(ref, "ref_logprobs", _F32, (T,), dev), ctypes.byref(params), red,
+             pairs if red else loss.data_ptr(), loss.data_ptr() if red else None, rewards, lp, stats, pairs + 4 * P)
+        ctx.save_for_backward(logits, labels, kept)
+        ctx.pairs, ctx.temperature, ctx.red = P, temperature, red
+        return loss
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
-        logits, labels, stats = ctx.saved_tensors
+        logits, labels, kept = ctx.saved_tensors
+        dt, T, V, ld = _matrix(logits, "logits")
         grad = _as_f32(grad)
-        g = preference_loss_backward(logits, labels, stats, grad if ctx.reduction == "none" else grad.view(1),
-                                     ctx.pairs, ctx.temperature, ctx.reduction)
-        return g, None, None, None, None
+        g = torch.empty((T, V), dtype=logits.dtype, device=logits.device)
+        _run("preference_loss_backward", logits.device, None, logits.data_ptr(), dt, T, V, ld, labels.data_ptr(),
+             ctx.temperature, ctx.pairs, ctx.red, kept.data_ptr(), grad.data_ptr(), g.data_ptr(), dt, V)
+        return (g,) + (None,) * 7
 
 
 def preference_loss(logits, labels, offsets, ref_logprobs=None, *, beta=0.1, kind="sigmoid", label_smoothing=0.0,
                     margin=0.0, average=False, temperature=1.0, ignore_index=IGNORE_INDEX, reduction="mean"):
     """preference_loss_forward with autograd: the loss (the pairs' with reduction "none"), its gradient w.r.t.
     the logits; ref_logprobs are constants."""
-    kw = dict(beta=beta, kind=kind, label_smoothing=label_smoothing, margin=margin, average=average,
-              temperature=float(temperature), ignore_index=ignore_index, reduction=reduction)
-    return _Preference.apply(logits, labels, offsets, ref_logprobs, kw)
+    return _Preference.apply(logits, labels, offsets, ref_logprobs,
+                             _PreferenceParams(PREFERENCE_KINDS[kind], beta, label_smoothing, margin, bool(average)),
+                             float(temperature), ignore_index, reduction)
+
+
+# ---- test hooks: waits that give up -------------------------------------------------------------
+
+
+def vce_test_policy_stall(logits, actions, advantages, wait_ns=50_000_000, *, stream=None):
+    """The one pass on contiguous bfloat16 logits, the gradient of each cluster's last block waiting in vain.
+    Returns (loss_out, loss_rows, logprobs, grad_logits, status)."""
+    T, V = logits.shape
+    dev = logits.device
+    go, loss, rows, lp = (torch.ones(1, device=dev), torch.zeros(1, device=dev), torch.zeros(T, device=dev),
+                          torch.zeros(T, device=dev))
+    stats, grad = torch.zeros(T, ROW_STATS, device=dev), torch.zeros_like(logits)
+    status = torch.full((1,), 0x7FFF1234, dtype=_I32, device=dev)
+    _run("vce_test_policy_stall", dev, stream, logits.data_ptr(), T, V, actions.data_ptr(), advantages.data_ptr(),
+         go.data_ptr(), rows.data_ptr(), loss.data_ptr(), lp.data_ptr(), stats.data_ptr(), grad.data_ptr(), int(wait_ns),
+         status.data_ptr())
+    return loss, rows, lp, grad, status
+
+
+def vce_test_policy_bwd_stall(logits, actions, row_stats, wait_ns=50_000_000, *, stream=None):
+    """The backward on contiguous bfloat16 logits, each row's last block waiting for its last stage in vain.
+    Returns grad_logits."""
+    T, V = logits.shape
+    dev = logits.device
+    go, grad = torch.ones(1, device=dev), torch.zeros_like(logits)
+    _run("vce_test_policy_bwd_stall", dev, stream, logits.data_ptr(), T, V, actions.data_ptr(), row_stats.data_ptr(),
+         go.data_ptr(), grad.data_ptr(), int(wait_ns))
+    return grad
