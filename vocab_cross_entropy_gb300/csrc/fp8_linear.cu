@@ -9,7 +9,7 @@
 //                  of w per CTA and K block.  8 epilogue warps, each 32 rows x 128 columns in registers: per K
 //                  block and SM 32768 fma (256 cycles of the fma pipe) against the MMAs' 512 cycles.
 //   k_linear_few   T <= 64: bound by reading w.  The roles change sides: w's rows are the MMA's 128, the rows of x
-//                  its N (16, 32 or 64 wide), so a stage is w's 16 KB and little else.  Where w has fewer tiles
+//                  its N (16, 32 or 64 wide), so a stage is w's 16 KB and the few rows of x.  Where w has fewer tiles
 //                  than there are SMs, a cluster's CTAs each take a part of K and the first adds the others' sums
 //                  in order.
 // Every wait is bounded (2 s); where one gives up, the CTA's tiles become NaN.
@@ -344,19 +344,23 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 
 // ---- few rows of x --------------------------------------------------------------------------------------
 
-constexpr int kFewThreads = 6 * 32;                  // 4 epilogue warps, producer, issuer
+constexpr int kAccs = 4;                             // accumulators: an MMA waits for what an epilogue three blocks before freed
 template <int N>
 struct Few {
+    static constexpr int kEach = N > 32 ? N / 2 : N;                 // rows of x of an epilogue warp
+    static constexpr int kEpi = 4 * (N / kEach);                     // epilogue warps
+    static constexpr int kProducer = kEpi, kIssuer = kEpi + 1, kThreads = (kEpi + 2) * 32;
     static constexpr int kStage = kTileBytes + N * kBlock;
     static constexpr int kBufs = (kMaxSmem - 2048) / kStage < 12 ? (kMaxSmem - 2048) / kStage : 12;
     static constexpr int kSmem = kBufs * kStage + 1024 + 512;
-    static constexpr int kCols = 2 * N < 32 ? 32 : 2 * N;            // tensor memory: two accumulators
-    static_assert(kBufs * kStage >= 3 * N * 128 * 4, "the joined sums lie in the stages");
+    static constexpr int kCols = kAccs * N;                          // of tensor memory
+    // the other CTAs' sums lie in the first's stages
+    static constexpr int kSplit = kBufs * kStage >= 3 * N * kM * 4 ? 4 : 2;
+    static_assert(kBufs * kStage >= (kSplit - 1) * N * kM * 4 && kCols >= 32 && kCols <= 512, "tile");
 };
-constexpr int kMaxSplit = 4;
 
 template <typename O, int N>
-__global__ void __launch_bounds__(kFewThreads, 1)
+__global__ void __launch_bounds__(Few<N>::kThreads, 1)
     k_linear_few(const __grid_constant__ CUtensorMap mapX, const __grid_constant__ CUtensorMap mapW,
                  const __grid_constant__ LinearArgs a) {
     using F = Few<N>;
@@ -366,8 +370,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * F::kStage);
     uint64_t* empty = full + S;
     uint64_t* acc_full = empty + S;
-    uint64_t* acc_free = acc_full + 2;
-    uint64_t* drain = acc_free + 2;
+    uint64_t* acc_free = acc_full + kAccs;
+    uint64_t* drain = acc_free + kAccs;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -377,9 +381,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kAccs; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_free[i], 4);
+            mbar_init(&acc_free[i], F::kEpi);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -387,7 +391,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         prefetch_map(&mapX);
         prefetch_map(&mapW);
     }
-    if (warp == 4) {
+    if (warp == F::kProducer) {
         tmem_alloc<false>(tmem_slot, F::kCols);
         tmem_relinquish<false>();
     }
@@ -399,10 +403,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     const int tile0 = (int)blockIdx.x / a.split, tstep = (int)gridDim.x / a.split;
     const int per = (a.nd + a.split - 1) / a.split, k0 = min(a.nd, rank * per), k1 = min(a.nd, k0 + per);
 
-    float c[N];
+    constexpr int NC = F::kEach;
+    const int half = warp / 4 * NC;                  // the first row of x of this epilogue warp
+    float c[NC];
 #pragma unroll
-    for (int i = 0; i < N; ++i) c[i] = 0.f;
-    if (warp == 4) {
+    for (int i = 0; i < NC; ++i) c[i] = 0.f;
+    if (warp == F::kProducer) {
         if (lane == 0) {
             int stage = 0, issued = 0;
             uint32_t phase = 0;
@@ -427,7 +433,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp == 5) {
+    } else if (warp == F::kIssuer) {
         if (lane == 0) {
             constexpr uint32_t idesc = idesc_e4m3_f32(kM, N);
             int stage = 0, acc = 0;
@@ -446,8 +452,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                     mma_commit<false>(smem_u32(&empty[stage]));
                     mma_commit<false>(smem_u32(&acc_full[acc]));
                     if (++stage == S) stage = 0, phase ^= 1u;
-                    acc ^= 1;
-                    if (acc == 0) acc_phase ^= 1u;
+                    if (++acc == kAccs) acc = 0, acc_phase ^= 1u;
                 }
             }
             mma_commit<false>(smem_u32(drain));
@@ -457,17 +462,17 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         }
         __syncwarp();
     } else {
-        // a thread holds row v of w against every row of x; lane t keeps the scales of x's rows t and t + 32
-        const uint32_t taddr = tmem + ((uint32_t)(warp * 32) << 16);
+        // a thread holds row v of w against NC rows of x; lane t keeps the scales of the t-th and t + 32nd of them
+        const uint32_t taddr = tmem + ((uint32_t)(warp % 4 * 32) << 16) + (uint32_t)half;
         int acc = 0;
         uint32_t acc_phase = 0;
         bool ok = true;
         for (int tile = tile0; tile < ntiles && ok; tile += tstep) {
             const float* ws = a.ws + (int64_t)tile * a.nd;
-            const float* x0 = a.xs + (lane < a.T ? lane : 0) * (int64_t)a.nd;
-            const float* x1 = a.xs + (N > 32 && lane + 32 < a.T ? lane + 32 : 0) * (int64_t)a.nd;
+            const float* x0 = a.xs + (half + lane < a.T ? half + lane : 0) * (int64_t)a.nd;
+            const float* x1 = a.xs + (NC > 32 && half + lane + 32 < a.T ? half + lane + 32 : 0) * (int64_t)a.nd;
 #pragma unroll
-            for (int i = 0; i < N; ++i) c[i] = 0.f;
+            for (int i = 0; i < NC; ++i) c[i] = 0.f;
             float n0 = 0.f, n1 = 0.f, wn = 0.f;
             if (k0 < k1) n0 = __ldg(x0 + k0), n1 = __ldg(x1 + k0), wn = __ldg(ws + k0);
             for (int kb = k0; kb < k1; ++kb) {
@@ -476,25 +481,24 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 ok = __all_sync(0xFFFFFFFFu, wait_bar<false>(&acc_full[acc], acc_phase, abort_flag, nullptr, 0, a.wait_ns));
                 if (!ok) break;
                 tc_fence_after();
-                uint32_t r[N / 16][16];
+                uint32_t r[NC / 16][16];
 #pragma unroll
-                for (int q = 0; q < N / 16; ++q) tmem_ld16(taddr + (uint32_t)(acc * N + q * 16), r[q]);
+                for (int q = 0; q < NC / 16; ++q) tmem_ld16(taddr + (uint32_t)(acc * N + q * 16), r[q]);
 #pragma unroll
-                for (int q = 0; q < N / 16; ++q) tmem_wait16(r[q]);
+                for (int q = 0; q < NC / 16; ++q) tmem_wait16(r[q]);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&acc_free[acc]);
 #pragma unroll
-                for (int i = 0; i < N; ++i)
+                for (int i = 0; i < NC; ++i)
                     c[i] = fmaf(__uint_as_float(r[i / 16][i % 16]), __shfl_sync(0xFFFFFFFFu, i < 32 ? s0 : s1, i % 32), c[i]);
-                acc ^= 1;
-                if (acc == 0) acc_phase ^= 1u;
+                if (++acc == kAccs) acc = 0, acc_phase ^= 1u;
             }
-            const int64_t v = (int64_t)tile * kM + warp * 32 + lane;
+            const int64_t v = (int64_t)tile * kM + warp % 4 * 32 + lane;
             if (ok && a.split == 1 && v < a.V && dbg::ok(v < a.ld, dbg::kTile)) {
 #pragma unroll
-                for (int i = 0; i < N; ++i)
-                    if (i < a.T) Elt<O>::store1(static_cast<O*>(a.out) + i * a.ld + v, c[i]);
+                for (int i = 0; i < NC; ++i)
+                    if (half + i < a.T) Elt<O>::store1(static_cast<O*>(a.out) + (half + i) * a.ld + v, c[i]);
             }
         }
     }
@@ -504,31 +508,33 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         // the parts of K: each CTA's sums into the first's stages (its copies have landed and been read), added
         // there in order
         cluster_sync_all();
-        if (warp < 4 && rank > 0) {
-            const uint32_t to = cluster_addr(smem, 0) + (uint32_t)(((rank - 1) * N * 128 + threadIdx.x) * 4);
+        const int place = half * kM + warp % 4 * 32 + lane;   // [rows of x][128]
+        if (warp < F::kEpi && rank > 0) {
+            const uint32_t to = cluster_addr(smem, 0) + (uint32_t)(((rank - 1) * N * kM + place) * 4);
             const bool bad = *abort_flag != 0;
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + i * 512), "f"(bad ? __int_as_float(0x7FC00000) : c[i])
+            for (int i = 0; i < NC; ++i)
+                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + i * (kM * 4)),
+                             "f"(bad ? __int_as_float(0x7FC00000) : c[i])
                              : "memory");
         }
         cluster_sync_all();
-        if (warp < 4 && rank == 0) {
-            const float* from = reinterpret_cast<const float*>(smem) + threadIdx.x;
-            const int64_t v = (int64_t)tile0 * kM + threadIdx.x;
+        if (warp < F::kEpi && rank == 0) {
+            const float* from = reinterpret_cast<const float*>(smem) + place;
+            const int64_t v = (int64_t)tile0 * kM + warp % 4 * 32 + lane;
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                for (int p = 1; p < a.split; ++p) c[i] += from[((p - 1) * N + i) * 128];
-                if (i < a.T && v < a.V && dbg::ok(v < a.ld, dbg::kTile))
-                    Elt<O>::store1(static_cast<O*>(a.out) + i * a.ld + v, c[i]);
+            for (int i = 0; i < NC; ++i) {
+                for (int p = 1; p < a.split; ++p) c[i] += from[((p - 1) * N + i) * kM];
+                if (half + i < a.T && v < a.V && dbg::ok(v < a.ld, dbg::kTile))
+                    Elt<O>::store1(static_cast<O*>(a.out) + (half + i) * a.ld + v, c[i]);
             }
         }
         __syncthreads();
     }
     if (*abort_flag && rank == 0)
         for (int tile = tile0; tile < ntiles; tile += tstep)
-            for (int i = threadIdx.x; i < kM * N; i += kFewThreads) store_nan<O>(a, i / kM, (int64_t)tile * kM + i % kM);
-    if (warp == 4) {
+            for (int i = threadIdx.x; i < kM * N; i += F::kThreads) store_nan<O>(a, i / kM, (int64_t)tile * kM + i % kM);
+    if (warp == F::kProducer) {
         tc_fence_after();
         tmem_dealloc<false>(tmem, F::kCols);
     }
@@ -603,9 +609,9 @@ cudaError_t run_few(const void* x, const void* w, int64_t D, LinearArgs& a, cuda
     const int sms = device_sm_count();
     const int64_t tiles = (a.V + kM - 1) / kM;
     a.split = 1;
-    while (a.split < kMaxSplit && tiles * a.split * 2 <= sms && a.nd >= 4 * a.split) a.split *= 2;
+    while (a.split < Few<N>::kSplit && tiles * a.split * 2 <= sms && a.nd >= 4 * a.split) a.split *= 2;
     const int blocks = a.split > 1 ? (int)tiles * a.split : (int)std::min<int64_t>(tiles, sms);
-    return launch(k_linear_few<O, N>, blocks, a.split, kFewThreads, Few<N>::kSmem, s, mx, mw, a);
+    return launch(k_linear_few<O, N>, blocks, a.split, Few<N>::kThreads, Few<N>::kSmem, s, mx, mw, a);
 }
 
 template <typename O>

@@ -35,9 +35,9 @@ __global__ void __launch_bounds__(kConsumers + 32, 3) k_row_grads(const __grid_c
     GradCtl& ctl = *reinterpret_cast<GradCtl*>(smem + a.nbuf * kStageBytes);
     Barriers& bar = ctl.bar;
     const int tid = threadIdx.x, warp = tid >> 5;
-    const int64_t row = blockIdx.x / a.parts;
+    const int64_t row = a.T - 1 - blockIdx.x / a.parts;   // the rows that a forward read last first: some are in L2 still
     const rs::Row r = make_row<S>(a.logits, row, a.ld, a.V);
-    const int part = (int)(blockIdx.x - row * a.parts);
+    const int part = (int)(blockIdx.x % a.parts);
     const Slice sl = make_slice(r, a.parts, part);
     O* grow = static_cast<O*>(a.grad) + row * a.ld_g;
     const bool vec = grads_aligned<S, O>(r, grow);
