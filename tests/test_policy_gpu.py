@@ -336,6 +336,16 @@ def test_preference_bad_inputs(vce):
     assert torch.all(g[6:] == 0) and torch.isfinite(g).all()
 
 
+def test_preference_statistics_of_another_call_name_no_pair(vce):
+    """Rows whose saved pair is not among the call's have no gradient, and read no upstream one."""
+    z, ids = logits(12, 400, F32), tokens(12, 400)
+    off = torch.tensor([0, 3, 6, 9, 12]).cuda()
+    stats = vce.preference_loss_forward(z, ids, off, reduction="none")[4]
+    two = vce.preference_loss_backward(z, ids, stats, torch.ones(2, device="cuda"), 2, reduction="none")
+    one = vce.preference_loss_backward(z, ids, stats, torch.ones(1, device="cuda"), 1, reduction="none")
+    assert torch.equal(one[:6], two[:6]) and (two[6:] != 0).any() and torch.all(one[6:] == 0)
+
+
 def test_preference_without_pairs(vce):
     z, ids = logits(3, 50, F32), tokens(3, 50)
     off = torch.tensor([1]).cuda()

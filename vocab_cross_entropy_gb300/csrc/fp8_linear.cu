@@ -12,6 +12,14 @@
 //                  its N (16, 32 or 64 wide), so a stage is w's 16 KB and the few rows of x.  Where w has fewer tiles
 //                  than there are SMs, a cluster's CTAs each take a part of K and the first adds the others' sums
 //                  in order.
+// What bounds them.  8192 x 4096 by 128256 to bf16: 4.0 ms, 2140 TFLOP/s (1.25 of the bf16 product's measured
+// sustained rate, 0.57 of twice its burst rate).  With neither the scaling nor the hand-over of accumulators the
+// pipeline of loads and MMAs itself takes 2630 TFLOP/s at the clock that the power limit leaves; the hand-over (a block's
+// MMAs are done, the sums are read, the accumulator is free: two blocks' time at most) takes 12% of that and the
+// reading and scaling 11%.  N = 128 accumulators, four of them, would hide the hand-over but read x's tile twice as often
+// from shared memory, which is then the limit (4.9 ms).  16 epilogue warps of 64 columns spill at 104 registers (8.2
+// ms).  A row for T = 1: 88 us, 6.0 TB/s of w (0.90 of the measured copy: 1002 tiles on 152 SMs leave 6% idle in
+// the seventh round); T = 64: 110 us, and 144 on CTA pairs at T = 100.
 // Every wait is bounded (2 s); where one gives up, the CTA's tiles become NaN.
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -2,14 +2,19 @@
 //
 // The scale is the least 2^k with max |x| <= 448 * 2^k: with max |x| = f 2^e, 1 <= f < 2, and 448 = 1.75 * 2^8,
 // k = e - 8 or, for f > 1.75, e - 7.  Multiplying by 2^-k is exact, so q carries the one rounding to e4m3.
+//
+// Bound by memory: a block's elements wait in registers between its largest magnitude and its conversion, so x is
+// read once.  128256 x 4096 bf16 in blocks of 128 x 128: 236 us, 6.7 TB/s (0.99 of the measured copy); in blocks of
+// 1 x 128: 242 us.  Rows that are not whole 16-byte vectors go element by element (602 us at that size, measured
+// before the vectors).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
 #include <algorithm>
 
 #include "row_launch.h"
-#include "vce_device.cuh"
 #include "vce_check.cuh"
+#include "vce_device.cuh"
 #include "vce_fp8.h"
 #include "vce_host.h"
 

@@ -1,4 +1,13 @@
-// Token log-probabilities, the policy loss and the preference loss: the row sums and what comes of them.
+// Token log-probabilities, the policy loss and the preference loss: the forward kernels' forms, and what comes of the
+// rows (the mathematics: logprob_rows.cuh; the kernels: policy_ring.cuh, policy_held.cuh).
+//
+// A call is the rows' kernel, for the preference loss one block a pair, and one block that sums the losses in a fixed
+// order, writes the status word and, for a mean, scales the saved coefficients; each starts while the one ahead of it
+// runs (programmatic dependent launch).  Nothing is shared between calls.
+//
+// What bounds them, bf16: the forward reads the logits once (16384 x 128256: 608 us, 6.8 TB/s, 1.02 of the measured
+// copy; with entropies 4096 x 128256: 181 us, 5.8 TB/s, one fma and one maximum more a column); short rows cost about
+// 1 us beside their columns (4096 x 32000: 53 us, 4.9 TB/s).  Few rows are latency: one of 128256 takes 8.1 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -218,11 +227,16 @@ __global__ void __launch_bounds__(kPairThreads) k_pairs(const __grid_constant__ 
 
 // ---- host ----------------------------------------------------------------------------------------------
 
-// The forward's forms.  Rows of at most 4 KB take a warp each, which holds them in registers.  A long row (or
-// one of few rows, which a cluster shares) takes a block of 8 consumer warps and 16 KB stages, two of them an SM;
-// shorter ones four blocks an SM of 4 warps and 8 KB stages: what a row costs beside its columns (about 1 us of
-// merges and hand-overs) runs under the other blocks' columns.
-using Warp = held::Form<32, 8, 4>;
+// The forward's forms (us a call in a graph, bf16):
+//  - Rows of at most 16 KB, a row for every SM at least, are held in registers (8192 x 4000: 19.5, and 28.4 in the
+//    ring; 8192 x 8000: 30.8 and 39.8).  At 32 KB it depends on the rows' alignment (8192 x 16000: 55.4 and 59.4; 4096 x
+//    8001 fp32: 31.0 and 28.9), so those stay with the ring.  Rows of at most 4 KB are held however few they are.
+//  - Few rows are shared by clusters of up to eight blocks, so that every SM streams (one of 128256: 8.1).
+//  - Rows below 128 KB take four blocks an SM of 4 consumer warps and 8 KB stages: what a row costs beside its columns
+//    (about 1 us of merges and hand-overs) runs under the other blocks' columns.  4096 x 32000: 57.4, and 59.6 with two
+//    blocks of 8 warps and 16 KB stages, 74.5 with one of 16 and 32 KB.
+//  - Longer rows take two blocks an SM of 8 warps and 16 KB stages.  4096 x 128256: 162, and 168 with four blocks, 185
+//    with one.
 constexpr int64_t kLongRow = 131072;
 using Long = ring::Form<8, 2, 4, 6, 0>;
 using Short = ring::Form<4, 4, 4, 6, 0>;
@@ -239,9 +253,7 @@ cudaError_t run_rows(Args& a, cudaStream_t s) {
     const int sms = device_sm_count();
     const int64_t nv = (a.V + 2 * G - 2) / G;
     a.cluster = 1;
-    if (nv <= Warp::kVecs)
-        return launch_clusters<held::k_loss_held<S, float, false, kEnt, Warp>>((a.T + Warp::kPer - 1) / Warp::kPer, 1,
-                                                                              Warp::kThreads, 0, s, a);
+    if (nv <= held::Warp::kVecs || (nv <= held::Block16::kVecs && a.T >= sms)) return held::run<S, float, false, kEnt>(a, nv, s);
     int C = 1;
     while (C < kMaxCluster && a.T * C < sms && (nv + C - 1) / C > 512) C *= 2;
     a.cluster = C;

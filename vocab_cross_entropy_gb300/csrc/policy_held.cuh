@@ -1,10 +1,7 @@
-// Rows held in registers: a block (a cluster of C of them, or a warp of a block for the shortest rows) loads
-// all of a row at once, U vectors a thread, sums it, finishes it, and turns the registers into the gradient.
-// No stage is staged, nothing is read again, and several blocks share an SM, so that one's loads run under
-// another's exchange and stores.
-//
-// Of a row's vectors thread t of NT takes t, t + NT, ... of its block's slice.  The cluster's blocks exchange
-// their sums through distributed shared memory, ordered by the cluster's hardware barrier.
+// Short rows held in registers: a block (or a warp of a block for the shortest) loads all of a row at once, U
+// vectors a thread, sums it, finishes it, and turns the registers into the gradient.  There is nothing to
+// stage or to hand on, and many blocks share an SM, so that one's loads run under the others' scalars and
+// stores.  Of a row's vectors thread t of NT takes t, t + NT, ...
 #pragma once
 
 #include <cuda_runtime.h>
@@ -26,7 +23,7 @@ struct Form {
     static constexpr int kNT = kNT_, kU = kU_, kBlocks = kBlocks_;
     static constexpr int kPer = kNT == 32 ? 4 : 1;                // rows of a block
     static constexpr int kThreads = kNT * kPer;
-    static constexpr int kVecs = kNT * kU;                        // of a slice, at most
+    static constexpr int kVecs = kNT * kU;                        // of a row, at most
 };
 
 struct RowCoefs {
@@ -35,20 +32,23 @@ struct RowCoefs {
     int none;
 };
 
+// A warp for rows of at most 4 KB, then blocks of 64, 128 and 256 threads for 8, 16 and 32 KB.
+using Warp = Form<32, 8, 4>;
+using Block8 = Form<64, 8, 16>;
+using Block16 = Form<128, 8, 8>;
+using Block32 = Form<256, 8, 4>;
+
 template <typename S, typename O, bool kGrad, bool kEnt, typename F>
 __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_held(const __grid_constant__ Args a) {
     constexpr int G = Elt<S>::kGroup, NT = F::kNT, U = F::kU, kWarps = NT / 32;
     static_assert(U % 2 == 0, "vectors go in pairs");
     constexpr int kKind = kEnt ? kEntropy : kGrad ? kSum : kMean;    // as the ring's
     __shared__ Sums part[kWarps > 1 ? kWarps : 1];
-    __shared__ float4 slot[kMaxCluster];
     __shared__ RowCoefs coefs_of_row;
     __shared__ int64_t token_of_row;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tid = threadIdx.x % NT;
-    const int C = a.cluster;
-    const int rank = kWarps > 1 && C > 1 ? (int)cluster_rank() : 0;
-    const int64_t row = F::kPer > 1 ? (int64_t)blockIdx.x * F::kPer + warp : blockIdx.x / C;
+    const int64_t row = F::kPer > 1 ? (int64_t)blockIdx.x * F::kPer + warp : blockIdx.x;
     start_next();
     if (F::kPer > 1 && row >= a.T) return;
 
@@ -70,27 +70,25 @@ __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_held(const __g
         t = __shfl_sync(0xFFFFFFFFu, t, 0);
     }
     const rs::Row r = make_row<S>(a.logits, row, a.ld, a.V);
-    const Slice sl = make_slice(r, C, rank);
+    const Slice sl{0, r.nv, 1};
     O* grow = kGrad ? static_cast<O*>(a.grad) + row * a.ld_g : nullptr;
     const bool vec = kGrad && grads_aligned<S, O>(r, grow);
-    if (kWarps > 1 && C > 1) cluster_arrive_relaxed();               // this block runs: peers may write into it
 
     if (t == a.ignore_index || t < 0 || t >= a.V) {
-        if (rank == 0 && tid == 0) write_none(a, row, t == a.ignore_index ? 0 : VCE_ERR_LABEL);
+        if (tid == 0) write_none(a, row, t == a.ignore_index ? 0 : VCE_ERR_LABEL);
         if (kGrad) fill_grads<S, O>(r, sl, grow, vec, tid, NT);
         if (kGrad && a.red == VCE_RED_MEAN) wait_previous();
-        if (kWarps > 1 && C > 1) cluster_wait(), cluster_arrive(), cluster_wait();   // as many as below
         return;
     }
 
-    // all of the slice is on its way before any of it is used
-    const bool inside = sl.v0 >= r.iv0 && sl.v0 + sl.n <= r.iv1;     // no partial vector
+    // all of the row is on its way before any of it is used
+    const bool inside = r.iv0 == 0 && r.iv1 == r.nv;                 // no partial vector
     uint4 x[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int v = sl.v0 + tid + u * NT;
+        const int v = tid + u * NT;
         x[u] = stage::neg_inf16<S>();
-        if (v < sl.v0 + sl.n && (inside || (v >= r.iv0 && v < r.iv1))) x[u] = ld_stream16(r.base + (int64_t)v * 16);
+        if (v < r.nv && (inside || (v >= r.iv0 && v < r.iv1))) x[u] = ld_stream16(r.base + (int64_t)v * 16);
     }
     RowIn in{};
     float go = 0.f;
@@ -101,13 +99,13 @@ __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_held(const __g
     if (!inside) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int v = sl.v0 + tid + u * NT;
-            if (v < sl.v0 + sl.n && (v < r.iv0 || v >= r.iv1)) x[u] = load_partial<S>(r, v);
+            const int v = tid + u * NT;
+            if (v < r.nv && (v < r.iv0 || v >= r.iv1)) x[u] = load_partial<S>(r, v);
         }
     }
 
     // the sums, the token's column left out
-    const int at = (int)t + r.shift, tv = at / G - sl.v0 - tid, tk = at % G;
+    const int at = (int)t + r.shift, tv = at / G - tid, tk = at % G;
     const int tu = tv >= 0 && tv < F::kVecs && tv % NT == 0 ? tv / NT : -1;
     Sums sum{-kInf, 0.f, 0.f};
 #pragma unroll
@@ -132,20 +130,6 @@ __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_held(const __g
             sum = lane < kWarps ? part[lane] : Sums{-kInf, 0.f, 0.f};
             warp_merge<kKind>(sum);
         }
-        if (C > 1) {
-            cluster_wait();                                          // every peer runs
-            if (warp == 0 && lane < C) st_peer(peer_addr(&slot[rank], lane), make_float4(sum.m, sum.s, sum.w, 0.f));
-            cluster_arrive();
-            cluster_wait();
-            if (warp == 0) {
-                sum = Sums{-kInf, 0.f, 0.f};
-                if (lane < C) {
-                    const float4 o = slot[lane];
-                    sum = Sums{o.x, o.y, o.z};
-                }
-                warp_merge<kKind>(sum);                               // the same order in every block
-            }
-        }
     }
 
     // the row's scalars: one warp works them out
@@ -160,7 +144,7 @@ __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_held(const __g
         const float4 st = row_result(a, res, in, kGrad ? go : 1.f, loss);
         cf = RowCoefs{Coefs{st.y, st.z, st.w}, res.m, res.dead};
         if (kGrad && kWarps > 1 && lane == 0) coefs_of_row = cf;
-        if (rank == 0 && lane == 0) write_result(a, row, res, st, loss);
+        if (lane == 0) write_result(a, row, res, st, loss);
     } else if (kGrad && a.red == VCE_RED_MEAN) {
         wait_previous();
     }
@@ -176,13 +160,30 @@ __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_held(const __g
         fill_grads<S, O>(r, sl, grow, vec, tid, NT);
         return;
     }
-    const int v0 = sl.v0, v1 = sl.v0 + sl.n;
-    const bool fast = vec && v0 >= r.iv0 && v0 + F::kVecs <= min(r.iv1, v1);
+    const bool fast = vec && inside && F::kVecs <= r.nv;
     if (kEnt && cf.c.c1 != 0.f)
-        write_grads<S, O, U, NT, true>(x, r, v0 + tid, v1, fast, grow, vec, cf.c, cf.bias, a.k2);
+        write_grads<S, O, U, NT, true>(x, r, tid, r.nv, fast, grow, vec, cf.c, cf.bias, a.k2);
     else
-        write_grads<S, O, U, NT, false>(x, r, v0 + tid, v1, fast, grow, vec, cf.c, cf.bias, a.k2);
-    if (tu >= 0 && sl.v0 + tid + tu * NT < v1) Elt<O>::store1(grow + t, cf.c.gt);   // over what this thread wrote there
+        write_grads<S, O, U, NT, false>(x, r, tid, r.nv, fast, grow, vec, cf.c, cf.bias, a.k2);
+    if (tu >= 0 && tid + tu * NT < r.nv) Elt<O>::store1(grow + t, cf.c.gt);   // over what this thread wrote there
+}
+
+// early: the kernel may start before the one ahead of it has ended (the count of a mean's rows).
+template <typename S, typename O, bool kGrad, bool kEnt, typename F>
+cudaError_t launch(Args& a, cudaStream_t s, bool early) {
+    const int64_t blocks = (a.T + F::kPer - 1) / F::kPer;
+    return launch_clusters<k_loss_held<S, O, kGrad, kEnt, F>>(blocks, 1, F::kThreads, 0, s, a, early);
+}
+
+// By the smallest form that holds a row of nv vectors (the largest is for one pass alone).
+template <typename S, typename O, bool kGrad, bool kEnt>
+cudaError_t run(Args& a, int64_t nv, cudaStream_t s, bool early = false) {
+    if (nv <= Warp::kVecs) return launch<S, O, kGrad, kEnt, Warp>(a, s, early);
+    if (nv <= Block8::kVecs) return launch<S, O, kGrad, kEnt, Block8>(a, s, early);
+    if constexpr (kGrad) {
+        if (nv > Block16::kVecs) return launch<S, O, kGrad, kEnt, Block32>(a, s, early);
+    }
+    return launch<S, O, kGrad, kEnt, Block16>(a, s, early);
 }
 
 }  // namespace held

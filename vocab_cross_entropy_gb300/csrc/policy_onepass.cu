@@ -13,25 +13,26 @@ namespace lp {
 
 using namespace rs;
 
-// Short rows are held in registers, rows of at most 4 KB by a warp, of at most 16 KB by a block of 128 threads; longer
-// ones in the ring's stages.
-using Warp = held::Form<32, 8, 4>;
-using Block = held::Form<128, 8, 8>;
-// Rows (or a cluster's slices of one) of up to 64 KB: two blocks an SM, four consumer warps each, so that what a row
-// costs beside its columns runs under the other block's columns; longer ones have a whole SM.
+// The forms (us a call, bf16 to bf16):
+//  - Rows of at most 32 KB, a row for every SM at least, are held in registers (8192 x 4000: 34 in a graph, and 62 in
+//    the ring; 8192 x 8000: 53 and 78; 8192 x 16000: 96 and 115; at 64 KB 100 and 101, but 2048 x 32001 to fp32 99 and
+//    83).  Rows of at most 4 KB are held however few they are.
+//  - Rows below 64 KB take two blocks an SM, four consumer warps each, so that what a row costs beside its columns runs
+//    under the other block's columns (4096 x 32000: 101 in a graph; 128 with one block of 14 warps).
+//  - Longer rows have a whole SM, or a cluster of them: 14 consumer warps, so that with the two others four are on each
+//    scheduler and have 128 registers (16 had 96 and spilled); 15 stages of 14 KB, ten of which a row may take, so
+//    that the next row's first stages are summed while this row's statistics are exchanged and finished (2048 x
+//    64000: 115, and 122 with two blocks; 4096 x 128256: 387 and 435).
+// What bounds the last: 16384 x 128256 with an entropy and a KL term 1597 us, 5.3 TB/s, 0.79 of the measured copy.  A
+// column takes two exponentials and about 17 instructions a thread where the copy's time leaves 25; the
+// schedulers have a warp to issue from 60% of the time, and the row's statistics (2 us from the last sum to the first
+// gradient) are hidden but for about 1 us.
 using Pair = ring::Form<4, 2, 8, 6, 4>;
 using Whole = ring::Form<14, 1, 2, 15, 10>;
 constexpr int64_t kLongRow = 65536;
 
 template <typename S>
 int64_t vectors(int64_t V) { return (V + 2 * Elt<S>::kGroup - 2) / Elt<S>::kGroup; }
-
-template <typename S, typename O, bool kEnt, typename F>
-cudaError_t run_held(Args& a, cudaStream_t s) {
-    a.cluster = 1;
-    const int64_t blocks = (a.T + F::kPer - 1) / F::kPer;
-    return launch_clusters<held::k_loss_held<S, O, true, kEnt, F>>(blocks, 1, F::kThreads, 0, s, a, a.red == VCE_RED_MEAN);
-}
 
 template <typename F>
 int stages(int64_t nv, int C) { return (int)(((nv + C - 1) / C + F::kVecs - 1) / F::kVecs); }
@@ -55,8 +56,8 @@ cudaError_t run_ring(Args& a, cudaStream_t s) {
 template <typename S, typename O, bool kEnt>
 cudaError_t run_rows(Args& a, cudaStream_t s) {
     const int64_t nv = vectors<S>(a.V);
-    if (!a.withhold && nv <= Warp::kVecs) return run_held<S, O, kEnt, Warp>(a, s);
-    if (!a.withhold && nv <= Block::kVecs && a.T >= device_sm_count()) return run_held<S, O, kEnt, Block>(a, s);
+    if (!a.withhold && (nv <= held::Warp::kVecs || (nv <= held::Block32::kVecs && a.T >= device_sm_count())))
+        return held::run<S, O, true, kEnt>(a, nv, s, a.red == VCE_RED_MEAN);
     return a.V * (int64_t)sizeof(S) > kLongRow ? run_ring<S, O, kEnt, Whole>(a, s) : run_ring<S, O, kEnt, Pair>(a, s);
 }
 

@@ -56,6 +56,7 @@ struct GradArgs {
     const float4* row_stats;
     const float* go;             // kPolicy, kPreference
     int go_each;                 // one for each row (pair), else one
+    int64_t P;                   // kPreference: pairs
     float scale;                 // on go
     const float *ga, *gb;        // kLogprobs
     void* grad;
