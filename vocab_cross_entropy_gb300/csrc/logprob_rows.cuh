@@ -157,6 +157,7 @@ __device__ __forceinline__ void push(const float (&v)[U][G], Sums& x, float k2) 
 // What a row's sums and its token's logit say.  dead: nothing but masks (everything NaN, no gradient).
 struct Row {
     float m, f, lp, lp_lo, ent;   // lp + lp_lo: log p_t to about twice the digits
+    float pt, pnt, lnf;           // p_t, 1 - p_t, ln f
     bool dead;
 };
 
@@ -184,12 +185,14 @@ __device__ __forceinline__ Row finish(const Sums& x, float zt, Scale k) {
     const bool rest = x.s > 0.f, tok = zt * k2 > -kInf;
     if (!(x.s >= 0.f && x.s < kInf && zt * k2 < kInf)) {   // a NaN or +inf somewhere
         r.m = 0.f;
-        r.f = r.lp = r.ent = nan_f();
+        r.f = r.lp = r.ent = r.pt = r.pnt = r.lnf = nan_f();
         return r;
     }
     if (!rest) {                                     // p_t = 1, or nothing at all
         r.dead = !tok;
-        r.m = r.f = 0.f;
+        r.m = r.f = r.pnt = 0.f;
+        r.pt = 1.f;
+        r.lnf = -kInf;
         r.lp = r.ent = tok ? 0.f : nan_f();
         return r;
     }
@@ -202,8 +205,12 @@ __device__ __forceinline__ Row finish(const Sums& x, float zt, Scale k) {
     if (kKind != kSum && fabsf(mean) < kInf) near += kLn2 * k.lo * mean;
     const float hrest = kKind == kEntropy ? fmaxf(0.f, fmaf(e - ratio, kLn2, near)) : 0.f;
     r.m = x.m;
+    const float lns = fmaf(e, kLn2, near);
     if (!tok) {
         r.f = 1.f / x.s;
+        r.pt = 0.f;
+        r.pnt = 1.f;
+        r.lnf = -lns;
         r.lp = -kInf;
         r.ent = hrest;
         return r;
@@ -232,24 +239,31 @@ __device__ __forceinline__ Row finish(const Sums& x, float zt, Scale k) {
     }
     r.ent = (pt > 0.f ? pt * sp : 0.f) + (pnt > 0.f ? pnt * (spn + hrest) : 0.f);
     r.f = pnt / x.s;
+    r.pt = pt;
+    r.pnt = pnt;
+    r.lnf = -spn - lns;
     return r;
 }
 
-// The gradient's coefficients (see above).
+// The gradient's coefficients (see above), lnf being ln f.
 struct Coefs {
     float c0, c1, gt;
 };
-__device__ __forceinline__ Coefs coefs(float f, float lp, float ent, float a, float b, float inv_tau) {
-    const float pt = expf(lp), pnt = -expm1f(lp);
+__device__ __forceinline__ Coefs coefs_of(float f, float lnf, float pt, float pnt, float lp, float ent, float a, float b,
+                                          float inv_tau) {
     Coefs c;
     c.gt = inv_tau * (a * pnt - (b != 0.f && pt > 0.f ? b * pt * (lp + ent) : 0.f));
     c.c0 = c.c1 = 0.f;
     if (f != 0.f) {
-        c.c0 = inv_tau * f * (b != 0.f ? -a - b * (logf(f) + ent) : -a);
+        c.c0 = inv_tau * f * (b != 0.f ? -a - b * (lnf + ent) : -a);
         c.c1 = b != 0.f ? -inv_tau * f * b * kLn2 : 0.f;
     }
     if (f != f || lp != lp) c.c0 = c.gt = nan_f();
     return c;
+}
+// From what is saved of a row.
+__device__ __forceinline__ Coefs coefs(float f, float lp, float ent, float a, float b, float inv_tau) {
+    return coefs_of(f, b != 0.f ? logf(f) : 0.f, expf(lp), -expm1f(lp), lp, ent, a, b, inv_tau);
 }
 
 }  // namespace lp

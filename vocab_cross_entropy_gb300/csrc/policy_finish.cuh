@@ -26,20 +26,17 @@ __device__ __forceinline__ RowIn row_in(const Args& a, int64_t row, int token) {
     return in;
 }
 
-// e^d - 1 - d >= 0: its power series near 0 (to d^9 / 9!, 2e-9 relative at 0.5), else as it stands.
+// e^d - 1 - d >= 0 for |d| < 1/2 by its power series (to d^9 / 9!, 2e-9 relative at 0.5).
 __device__ __forceinline__ float exp_minus_line(float d) {
-    if (fabsf(d) < 0.5f) {
-        float c = 1.f / 362880.f;
-        c = fmaf(c, d, 1.f / 40320.f);
-        c = fmaf(c, d, 1.f / 5040.f);
-        c = fmaf(c, d, 1.f / 720.f);
-        c = fmaf(c, d, 1.f / 120.f);
-        c = fmaf(c, d, 1.f / 24.f);
-        c = fmaf(c, d, 1.f / 6.f);
-        c = fmaf(c, d, 0.5f);
-        return d * d * c;
-    }
-    return expm1f(d) - d;
+    float c = 1.f / 362880.f;
+    c = fmaf(c, d, 1.f / 40320.f);
+    c = fmaf(c, d, 1.f / 5040.f);
+    c = fmaf(c, d, 1.f / 720.f);
+    c = fmaf(c, d, 1.f / 120.f);
+    c = fmaf(c, d, 1.f / 24.f);
+    c = fmaf(c, d, 1.f / 6.f);
+    c = fmaf(c, d, 0.5f);
+    return d * d * c;
 }
 
 // What a row that is left out (code 0), or one with an error, returns.
@@ -69,14 +66,15 @@ __device__ __forceinline__ float4 row_result(const Args& a, const Row& r, const 
         if (ratio != ratio || A != A || r.lp != r.lp) got = da = nan_f();
         loss = -got;
         if (a.kl != 0.f) {
-            const float d = (in.ref - r.lp) - r.lp_lo;
-            loss += a.kl * exp_minus_line(d);
-            da -= a.kl * expm1f(d);
+            // e^d - 1 - d from e^d - 1 where that keeps its digits, else by its power series
+            const float d = (in.ref - r.lp) - r.lp_lo, e = expm1f(d);
+            loss += a.kl * (fabsf(d) < 0.5f ? exp_minus_line(d) : e - d);
+            da -= a.kl * e;
         }
         if (a.ent != 0.f) loss -= a.ent * r.ent;
         loss *= in.w;
         const float w = in.w * scale;
-        const Coefs c = coefs(r.f, r.lp, r.ent, w * da, -w * a.ent, a.inv_tau);
+        const Coefs c = coefs_of(r.f, r.lnf, r.pt, r.pnt, r.lp, r.ent, w * da, -w * a.ent, a.inv_tau);
         st = make_float4(r.m, c.c0, c.c1, c.gt);
     }
     if (r.dead) st = make_float4(kInf, 0.f, 0.f, 1.f);

@@ -22,11 +22,11 @@ using namespace rs;
 //  - Longer rows have a whole SM, or a cluster of them: 14 consumer warps, so that with the two others four are on each
 //    scheduler and have 128 registers (16 had 96 and spilled); 15 stages of 14 KB, ten of which a row may take, so
 //    that the next row's first stages are summed while this row's statistics are exchanged and finished (2048 x
-//    64000: 115, and 122 with two blocks; 4096 x 128256: 387 and 435).
-// What bounds the last: 16384 x 128256 with an entropy and a KL term 1597 us, 5.3 TB/s, 0.79 of the measured copy.  A
-// column takes two exponentials and about 17 instructions a thread where the copy's time leaves 25; the
-// schedulers have a warp to issue from 60% of the time, and the row's statistics (2 us from the last sum to the first
-// gradient) are hidden but for about 1 us.
+//    64000: 107, and 122 with two blocks; 4096 x 128256: 368 and 435).
+// What bounds the last: 16384 x 128256 1421 us, 5.9 TB/s, 0.89 of the measured copy, a column's two exponentials and the
+// instructions around them; with an entropy term 1589 us, 0.79, where a column takes two maxima and two products more.
+// The row's statistics take about 1.5 us from the last sum to the first gradient, of which the next row's first stages
+// hide most (a release at cluster scope and functions worked out twice there cost 20 us of 387 at 4096 rows).
 using Pair = ring::Form<4, 2, 8, 6, 4>;
 using Whole = ring::Form<14, 1, 2, 15, 10>;
 constexpr int64_t kLongRow = 65536;

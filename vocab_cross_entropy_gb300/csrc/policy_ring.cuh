@@ -158,8 +158,12 @@ __device__ __forceinline__ int64_t walk_next(Walk& w, const Args& a, int& token)
     return walk_next(w, a, token, [](int64_t, int) {});
 }
 
-__device__ __forceinline__ void arrive_peer(uint32_t bar_addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_addr) : "memory");
+// Four floats into a peer's shared memory, counted as 16 bytes on its barrier: no release that would wait for this
+// warp's stores to global memory.
+__device__ __forceinline__ void send_peer(uint32_t addr, float4 v, uint32_t bar_addr) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
+                 "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar_addr)
+                 : "memory");
 }
 __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
     uint32_t ok;
@@ -197,7 +201,7 @@ __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_ring(const __g
         }
         for (int p = 0; p < 2; ++p) {
             tc::mbar_init(&ctl.paired[p], kWarps);
-            tc::mbar_init(&ctl.exchanged[p], C);
+            tc::mbar_init(&ctl.exchanged[p], 1);
             tc::mbar_init(&ctl.finished[p], 1);
         }
         ctl.abort = ctl.err = 0;
@@ -316,10 +320,10 @@ __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_ring(const __g
                 if (lane == 0) tc::mbar_arrive(&ctl.finished[par]);
             }
             if (C > 1) {
-                if (lane < C) {                        // C <= kSpan: these lanes have the sums
-                    st_peer(peer_addr(&ctl.slot[par][rank], lane), make_float4(x.m, x.s, x.w, 0.f));
-                    arrive_peer(peer_addr(&ctl.exchanged[par], lane));
-                }
+                if (lane == 0) tc::mbar_arrive_expect_tx(&ctl.exchanged[par], 16 * C);
+                if (lane < C)                          // C <= kSpan: these lanes have the sums
+                    send_peer(peer_addr(&ctl.slot[par][rank], lane), make_float4(x.m, x.s, x.w, 0.f),
+                              peer_addr(&ctl.exchanged[par], lane));
                 __syncwarp();
                 const uint64_t t0 = tc::globaltimer();
                 bool ok = true;
@@ -492,7 +496,14 @@ __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_ring(const __g
     // after an abort: no row of this block is known to be right, nor of its cluster, whose first block has
     // written its results by then
     __syncthreads();
-    if (C > 1) cluster_arrive(), cluster_wait();       // and no block leaves while a peer may write into it
+    if (C > 1) {                                       // and no block leaves while a peer may write into it
+        cluster_arrive(), cluster_wait();
+        if (ctl.abort) {                               // nobody waited for what a peer has sent since: time to land
+            const uint64_t t0 = tc::globaltimer();
+            while (tc::globaltimer() - t0 < 1000000ull) {
+            }
+        }
+    }
     if (ctl.abort)
         for (int64_t row = cid + (int64_t)tid * ncl; row < a.T; row += (int64_t)F::kThreads * ncl)
             write_none(a, row, ctl.err ? ctl.err : kErrRow);
