@@ -12,14 +12,16 @@
 //                  its N (16, 32 or 64 wide), so a stage is w's 16 KB and the few rows of x.  Where w has fewer tiles
 //                  than there are SMs, a cluster's CTAs each take a part of K and the first adds the others' sums
 //                  in order.
-// What bounds them.  8192 x 4096 by 128256 to bf16: 4.0 ms, 2140 TFLOP/s (1.25 of the bf16 product's measured
-// sustained rate, 0.57 of twice its burst rate).  With neither the scaling nor the hand-over of accumulators the
-// pipeline of loads and MMAs itself takes 2630 TFLOP/s at the clock that the power limit leaves; the hand-over (a block's
-// MMAs are done, the sums are read, the accumulator is free: two blocks' time at most) takes 12% of that and the
-// reading and scaling 11%.  N = 128 accumulators, four of them, would hide the hand-over but read x's tile twice as often
-// from shared memory, which is then the limit (4.9 ms).  16 epilogue warps of 64 columns spill at 104 registers (8.2
-// ms).  A row for T = 1: 88 us, 6.0 TB/s of w (0.90 of the measured copy: 1002 tiles on 152 SMs leave 6% idle in
-// the seventh round); T = 64: 110 us, and 144 on CTA pairs at T = 100.
+// What bounds them.  8192 x 4096 by 128256 to bf16: 3.9-4.1 ms, 2180 TFLOP/s (0.58 of twice the bf16 product's
+// measured burst rate), the tensor pipe 45% active at 1.91 GHz.  At 2048 x 4096 by 32768, 263 us: the copies out of
+// L2 with a quarter of the MMAs take 168 us (15 TB/s), copies and MMAs with nobody waiting for an accumulator 209, with
+// the accumulators handed over but not read 236.  The hand-over (a block's MMAs done, both CTAs told, the sums read,
+// the even CTA told: some 1300 cycles, of which the other accumulator's block hides 500) is what keeps the
+// tensor pipe waiting.  N = 128 accumulators, four of them, would hide it but read x's tile twice as often from shared
+// memory, which is then the limit (319 us).  16 epilogue warps of 64 columns spill at 104 registers (548 us).
+// T = 1: 86 us in a graph, 6.1 TB/s of w (0.92 of the measured copy: 1002 tiles on 152 SMs leave 6% idle in the
+// seventh round); T = 64: 109 us, of which broadcasting the scales by shuffles 10 and reading the sums 5 (on CTA pairs
+// T = 100 takes 144-153).
 // Every wait is bounded (2 s); where one gives up, the CTA's tiles become NaN.
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -96,8 +98,8 @@ __device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {   // ties r to 
 }
 
 // Arrive on a barrier of either CTA of a pair.  What it orders is tensor memory (its loads have been waited for, and
-// tcgen05.fence stands before), nothing that a release at cluster scope would have to flush: that one, 32 of them a K
-// block, held the epilogue warps for two fifths of their time (2670 cycles a K block).
+// tcgen05.fence stands before), nothing that a release at cluster scope would have to flush: that one held the
+// epilogue warps for two fifths of their time (2670 cycles a K block, 1375 without it).
 __device__ __forceinline__ void arrive_either(uint32_t addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
