@@ -119,6 +119,15 @@ __device__ __forceinline__ float4 four_scales(const float* s, int k, int nd) {
                        k + 3 < nd ? __ldg(s + k + 3) : 0.f);
 }
 
+// (c0, c1) += (a[0] b0, a[1] b1), in one packed instruction.
+__device__ __forceinline__ void fma_scaled(const uint32_t* a, uint32_t b0, uint32_t b1, float& c0, float& c1) {
+    asm("{\n\t.reg .b64 pa, pb, pc;\n\t"
+        "mov.b64 pa, {%2, %3};\n\tmov.b64 pb, {%4, %5};\n\tmov.b64 pc, {%0, %1};\n\t"
+        "fma.rn.f32x2 pc, pa, pb, pc;\n\tmov.b64 {%0, %1}, pc;\n\t}"
+        : "+f"(c0), "+f"(c1)
+        : "r"(a[0]), "r"(a[1]), "r"(b0), "r"(b1));
+}
+
 // (c0, c1) += (a0, a1) * b, in one packed instruction.
 __device__ __forceinline__ void fma_pair(uint32_t a0, uint32_t a1, float b, float& c0, float& c1) {
     asm("{\n\t.reg .b64 pa, pb, pc;\n\t"
@@ -354,15 +363,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 
 // ---- few rows of x --------------------------------------------------------------------------------------
 
+constexpr int kScales = 8;                           // K blocks' scales in flight
 constexpr int kAccs = 4;                             // accumulators: an MMA waits for what an epilogue three blocks before freed
 template <int N>
 struct Few {
     static constexpr int kEach = N > 32 ? N / 2 : N;                 // rows of x of an epilogue warp
     static constexpr int kEpi = 4 * (N / kEach);                     // epilogue warps
-    static constexpr int kProducer = kEpi, kIssuer = kEpi + 1, kThreads = (kEpi + 2) * 32;
+    static constexpr int kProducer = kEpi, kIssuer = kEpi + 1, kScaler = kEpi + 2, kThreads = (kEpi + 3) * 32;
     static constexpr int kStage = kTileBytes + N * kBlock;
-    static constexpr int kBufs = (kMaxSmem - 2048) / kStage < 12 ? (kMaxSmem - 2048) / kStage : 12;
-    static constexpr int kSmem = kBufs * kStage + 1024 + 512;
+    static constexpr int kBufs = (kMaxSmem - 1536 - kScales * N * 4) / kStage < 12 ? (kMaxSmem - 1536 - kScales * N * 4) / kStage : 12;
+    static constexpr int kSmem = kBufs * kStage + 1024 + 512 + kScales * N * 4;
     static constexpr int kCols = kAccs * N;                          // of tensor memory
     // the other CTAs' sums lie in the first's stages
     static constexpr int kSplit = kBufs * kStage >= 3 * N * kM * 4 ? 4 : 2;
@@ -377,11 +387,14 @@ __global__ void __launch_bounds__(Few<N>::kThreads, 1)
     constexpr int S = F::kBufs;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * F::kStage);
+    float* scales = reinterpret_cast<float*>(smem + S * F::kStage);   // [kScales][N]
+    uint64_t* full = reinterpret_cast<uint64_t*>(scales + kScales * N);
     uint64_t* empty = full + S;
     uint64_t* acc_full = empty + S;
     uint64_t* acc_free = acc_full + kAccs;
-    uint64_t* drain = acc_free + kAccs;
+    uint64_t* sc_full = acc_free + kAccs;
+    uint64_t* sc_free = sc_full + kScales;
+    uint64_t* drain = sc_free + kScales;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -394,6 +407,10 @@ __global__ void __launch_bounds__(Few<N>::kThreads, 1)
         for (int i = 0; i < kAccs; ++i) {
             mbar_init(&acc_full[i], 1);
             mbar_init(&acc_free[i], F::kEpi);
+        }
+        for (int i = 0; i < kScales; ++i) {
+            mbar_init(&sc_full[i], 1);
+            mbar_init(&sc_free[i], F::kEpi);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -471,24 +488,42 @@ __global__ void __launch_bounds__(Few<N>::kThreads, 1)
             }
         }
         __syncwarp();
+    } else if (warp == F::kScaler) {
+        // the scales of a K block for every row of x, times the tile's, where the epilogue reads them four at a time (out
+        // of the lanes by shuffles they cost T = 64 a tenth of its time)
+        int slot = 0;
+        uint32_t phase = 0;
+        for (int tile = tile0; tile < ntiles && !*abort_flag; tile += tstep) {
+            const float* ws = a.ws + (int64_t)tile * a.nd;
+            for (int kb = k0; kb < k1; ++kb) {
+                float x[(N + 31) / 32];
+                const float w = __ldg(ws + kb);
+#pragma unroll
+                for (int i = 0; i < (N + 31) / 32; ++i) {
+                    const int t = i * 32 + lane;
+                    x[i] = t < a.T ? __ldg(a.xs + (int64_t)t * a.nd + kb) : 0.f;
+                }
+                if (!__all_sync(0xFFFFFFFFu, wait_bar<false>(&sc_free[slot], phase ^ 1u, abort_flag, nullptr, 0, a.wait_ns))) break;
+#pragma unroll
+                for (int i = 0; i < (N + 31) / 32; ++i)
+                    if (i * 32 + lane < N) scales[slot * N + i * 32 + lane] = x[i] * w;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sc_full[slot]);
+                if (++slot == kScales) slot = 0, phase ^= 1u;
+            }
+        }
     } else {
-        // a thread holds row v of w against NC rows of x; lane t keeps the scales of the t-th and t + 32nd of them
+        // a thread holds row v of w against NC rows of x
         const uint32_t taddr = tmem + ((uint32_t)(warp % 4 * 32) << 16) + (uint32_t)half;
-        int acc = 0;
-        uint32_t acc_phase = 0;
+        int acc = 0, slot = 0;
+        uint32_t acc_phase = 0, phase = 0;
         bool ok = true;
         for (int tile = tile0; tile < ntiles && ok; tile += tstep) {
-            const float* ws = a.ws + (int64_t)tile * a.nd;
-            const float* x0 = a.xs + (half + lane < a.T ? half + lane : 0) * (int64_t)a.nd;
-            const float* x1 = a.xs + (NC > 32 && half + lane + 32 < a.T ? half + lane + 32 : 0) * (int64_t)a.nd;
 #pragma unroll
             for (int i = 0; i < NC; ++i) c[i] = 0.f;
-            float n0 = 0.f, n1 = 0.f, wn = 0.f;
-            if (k0 < k1) n0 = __ldg(x0 + k0), n1 = __ldg(x1 + k0), wn = __ldg(ws + k0);
             for (int kb = k0; kb < k1; ++kb) {
-                const float s0 = n0 * wn, s1 = n1 * wn;
-                if (kb + 1 < k1) n0 = __ldg(x0 + kb + 1), n1 = __ldg(x1 + kb + 1), wn = __ldg(ws + kb + 1);
-                ok = __all_sync(0xFFFFFFFFu, wait_bar<false>(&acc_full[acc], acc_phase, abort_flag, nullptr, 0, a.wait_ns));
+                ok = __all_sync(0xFFFFFFFFu, wait_bar<false>(&sc_full[slot], phase, abort_flag, nullptr, 0, a.wait_ns) &&
+                                                 wait_bar<false>(&acc_full[acc], acc_phase, abort_flag, nullptr, 0, a.wait_ns));
                 if (!ok) break;
                 tc_fence_after();
                 uint32_t r[NC / 16][16];
@@ -499,10 +534,17 @@ __global__ void __launch_bounds__(Few<N>::kThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&acc_free[acc]);
+                const float* s = scales + slot * N + half;
 #pragma unroll
-                for (int i = 0; i < NC; ++i)
-                    c[i] = fmaf(__uint_as_float(r[i / 16][i % 16]), __shfl_sync(0xFFFFFFFFu, i < 32 ? s0 : s1, i % 32), c[i]);
+                for (int i = 0; i < NC; i += 4) {
+                    const uint4 f = lds16(s + i);
+                    fma_scaled(r[i / 16] + i % 16, f.x, f.y, c[i], c[i + 1]);
+                    fma_scaled(r[i / 16] + i % 16 + 2, f.z, f.w, c[i + 2], c[i + 3]);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sc_free[slot]);
                 if (++acc == kAccs) acc = 0, acc_phase ^= 1u;
+                if (++slot == kScales) slot = 0, phase ^= 1u;
             }
             const int64_t v = (int64_t)tile * kM + warp % 4 * 32 + lane;
             if (ok && a.split == 1 && v < a.V && dbg::ok(v < a.ld, dbg::kTile)) {
@@ -626,7 +668,8 @@ cudaError_t run_few(const void* x, const void* w, int64_t D, LinearArgs& a, cuda
 
 template <typename O>
 cudaError_t run(const void* x, const void* w, int64_t D, LinearArgs& a, cudaStream_t s) {
-    if (a.T > 64) return run_pair<O>(x, w, D, a, s);
+    if (a.T > 128) return run_pair<O>(x, w, D, a, s);
+    if (a.T > 64) return run_few<O, 128>(x, w, D, a, s);
     if (a.T > 32) return run_few<O, 64>(x, w, D, a, s);
     if (a.T > 16) return run_few<O, 32>(x, w, D, a, s);
     return run_few<O, 16>(x, w, D, a, s);
