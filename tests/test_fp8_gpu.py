@@ -110,6 +110,13 @@ def test_linear_sizes(vce, T, D, V, dtype):
     check_linear(vce, operands(T, D, V), dtype)
 
 
+@pytest.mark.parametrize("T", [1, 40, 100, 128])
+@pytest.mark.parametrize("D,V", [(4096, 1000), (4096, 1300), (2160, 300), (2048, 128), (1152, 2500), (400, 9000)])
+def test_linear_parts_of_k(vce, T, D, V):
+    """Few tiles of w: clusters of two, four and eight CTAs share K, some with blocks left over or none at all."""
+    check_linear(vce, operands(T, D, V), F32 if T == 40 else BF16)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("pad,left", [(0, 0), (1, 0), (3, 1), (8, 8), (12, 4)])
 @pytest.mark.parametrize("T,V", [(3, 1000), (40, 777), (300, 1024)])

@@ -5,13 +5,12 @@
 // tensor cores into a fresh accumulator of tensor memory (four MMAs of K = 32), and the block's sum is scaled and
 // added to the running sum in registers, while the tensor cores work on the next block in the other accumulator.
 //
-//   k_linear_pair  T > 64: CTA pairs (cta_group::2) on 256 x 256 tiles, 128 rows of x and half of the tile's rows
+//   k_linear_pair  T > 128: CTA pairs (cta_group::2) on 256 x 256 tiles, 128 rows of x and half of the tile's rows
 //                  of w per CTA and K block.  8 epilogue warps, each 32 rows x 128 columns in registers: per K
 //                  block and SM 32768 fma (256 cycles of the fma pipe) against the MMAs' 512 cycles.
-//   k_linear_few   T <= 64: bound by reading w.  The roles change sides: w's rows are the MMA's 128, the rows of x
-//                  its N (16, 32 or 64 wide), so a stage is w's 16 KB and the few rows of x.  Where w has fewer tiles
-//                  than there are SMs, a cluster's CTAs each take a part of K and the first adds the others' sums
-//                  in order.
+//   k_linear_few   T <= 128: bound by reading w.  The roles change sides: w's rows are the MMA's 128, the rows of x
+//                  its N (16 to 128 wide), so a stage is w's 16 KB and the few rows of x.  Where w has fewer tiles
+//                  than there are SMs, a cluster's CTAs each take a part of K and add their sums in order.
 // What bounds them.  8192 x 4096 by 128256 to bf16: 3.9-4.1 ms, 2180 TFLOP/s (0.58 of twice the bf16 product's
 // measured burst rate), the tensor pipe 45% active at 1.91 GHz.  At 2048 x 4096 by 32768, 263 us: the copies out of
 // L2 with a quarter of the MMAs take 168 us (15 TB/s), copies and MMAs with nobody waiting for an accumulator 209, with
@@ -20,8 +19,7 @@
 // tensor pipe waiting.  N = 128 accumulators, four of them, would hide it but read x's tile twice as often from shared
 // memory, which is then the limit (319 us).  16 epilogue warps of 64 columns spill at 104 registers (548 us).
 // T = 1: 86 us in a graph, 6.1 TB/s of w (0.92 of the measured copy: 1002 tiles on 152 SMs leave 6% idle in the
-// seventh round); T = 64: 109 us, of which broadcasting the scales by shuffles 10 and reading the sums 5 (on CTA pairs
-// T = 100 takes 144-153).
+// seventh round); T = 64: 96 us, T = 128: 115 (on CTA pairs 150).
 // Every wait is bounded (2 s); where one gives up, the CTA's tiles become NaN.
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -363,6 +361,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 
 // ---- few rows of x --------------------------------------------------------------------------------------
 
+constexpr int kMaxSplit = 8;                         // CTAs that share a tile's K, at most
 constexpr int kScales = 8;                           // K blocks' scales in flight
 constexpr int kAccs = 4;                             // accumulators: an MMA waits for what an epilogue three blocks before freed
 template <int N>
@@ -374,9 +373,8 @@ struct Few {
     static constexpr int kBufs = (kMaxSmem - 1536 - kScales * N * 4) / kStage < 12 ? (kMaxSmem - 1536 - kScales * N * 4) / kStage : 12;
     static constexpr int kSmem = kBufs * kStage + 1024 + 512 + kScales * N * 4;
     static constexpr int kCols = kAccs * N;                          // of tensor memory
-    // the other CTAs' sums lie in the first's stages
-    static constexpr int kSplit = kBufs * kStage >= 3 * N * kM * 4 ? 4 : 2;
-    static_assert(kBufs * kStage >= (kSplit - 1) * N * kM * 4 && kCols >= 32 && kCols <= 512, "tile");
+    static_assert(kBufs * kStage >= N * kM * 4, "a CTA's sums lie in its stages");
+    static_assert(kCols >= 32 && kCols <= 512 && N % kMaxSplit == 0, "tile");
 };
 
 template <typename O, int N>
@@ -557,31 +555,31 @@ __global__ void __launch_bounds__(Few<N>::kThreads, 1)
     tc_fence_before();
     __syncthreads();
     if (a.split > 1) {
-        // the parts of K: each CTA's sums into the first's stages (its copies have landed and been read), added
-        // there in order
-        cluster_sync_all();
-        const int place = half * kM + warp % 4 * 32 + lane;   // [rows of x][128]
-        if (warp < F::kEpi && rank > 0) {
-            const uint32_t to = cluster_addr(smem, 0) + (uint32_t)(((rank - 1) * N * kM + place) * 4);
+        // the parts of K: every CTA's sums into its own stages (its copies have landed and been read), and each CTA adds
+        // up a share of x's rows out of all of them, in the CTAs' order.  (Stored into the first CTA one value at a
+        // time they took 0.45 us each.)
+        float* own = reinterpret_cast<float*>(smem);          // [rows of x][128]
+        if (warp < F::kEpi) {
             const bool bad = *abort_flag != 0;
 #pragma unroll
-            for (int i = 0; i < NC; ++i)
-                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + i * (kM * 4)),
-                             "f"(bad ? __int_as_float(0x7FC00000) : c[i])
-                             : "memory");
+            for (int i = 0; i < NC; ++i) own[(half + i) * kM + warp % 4 * 32 + lane] = bad ? __int_as_float(0x7FC00000) : c[i];
         }
         cluster_sync_all();
-        if (warp < F::kEpi && rank == 0) {
-            const float* from = reinterpret_cast<const float*>(smem) + place;
-            const int64_t v = (int64_t)tile0 * kM + warp % 4 * 32 + lane;
+        const int share = N / a.split * kM, first = rank * share;
+        for (int e = threadIdx.x; e < share; e += F::kThreads) {
+            const int t = (first + e) / kM;
+            const int64_t v = (int64_t)tile0 * kM + e % kM;
+            if (t >= a.T || v >= a.V || !dbg::ok(v < a.ld, dbg::kTile)) continue;
+            float part[kMaxSplit];
 #pragma unroll
-            for (int i = 0; i < NC; ++i) {
-                for (int p = 1; p < a.split; ++p) c[i] += from[((p - 1) * N + i) * kM];
-                if (half + i < a.T && v < a.V && dbg::ok(v < a.ld, dbg::kTile))
-                    Elt<O>::store1(static_cast<O*>(a.out) + (half + i) * a.ld + v, c[i]);
-            }
+            for (int q = 0; q < kMaxSplit; ++q)
+                part[q] = q < a.split ? __uint_as_float(ld_cluster_u32(cluster_addr(own + first + e, q))) : 0.f;
+            float sum = part[0];
+#pragma unroll
+            for (int q = 1; q < kMaxSplit; ++q) sum += part[q];
+            Elt<O>::store1(static_cast<O*>(a.out) + t * a.ld + v, sum);
         }
-        __syncthreads();
+        cluster_sync_all();                                   // no CTA leaves while another reads its sums
     }
     if (*abort_flag && rank == 0)
         for (int tile = tile0; tile < ntiles; tile += tstep)
@@ -660,8 +658,12 @@ cudaError_t run_few(const void* x, const void* w, int64_t D, LinearArgs& a, cuda
     if (e != cudaSuccess) return e;
     const int sms = device_sm_count();
     const int64_t tiles = (a.V + kM - 1) / kM;
+    // As many CTAs to a tile as there are SMs for, with two blocks of K each at least (1 x 4096 by 4000: 13.9 us with
+    // one, 7.3 with four; 1 x 2048 by 8000, where two fit, 8.6 and 7.1; 128 x 2048 by 8000 12.4 and 13.4), but eight
+    // only where they take no more than half the SMs (1 x 4096 by 1000: 7.2 with four, 5.6 with eight; 1 x 16384 by 2048,
+    // 128 CTAs of 152: 15.2 and 18.1, the clusters of eight not all finding a place at once).
     a.split = 1;
-    while (a.split < Few<N>::kSplit && tiles * a.split * 2 <= sms && a.nd >= 4 * a.split) a.split *= 2;
+    while (a.split < kMaxSplit && tiles * a.split * (a.split < 4 ? 2 : 4) <= sms && a.nd >= 4 * a.split) a.split *= 2;
     const int blocks = a.split > 1 ? (int)tiles * a.split : (int)std::min<int64_t>(tiles, sms);
     return launch(k_linear_few<O, N>, blocks, a.split, Few<N>::kThreads, Few<N>::kSmem, s, mx, mw, a);
 }
