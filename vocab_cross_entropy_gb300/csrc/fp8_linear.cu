@@ -54,6 +54,19 @@ struct LinearArgs {
     uint64_t wait_ns;            // bound of every wait
 };
 
+// One lane of a whole warp, the same at every call.  The issuing warps stay whole and elect a lane for the MMAs and
+// commits: issued by lane 0 in a loop of its own, whose operands the compiler cannot take for the warp's, a block's
+// four MMAs and two commits cost 640 cycles (1 x 65536 by 1000 25.6 us for 20.2, 8192 x 4096 by 128256 3930 for 3868).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t is;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(is));
+    return is != 0;
+}
+
 template <bool kCta2>
 __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                          uint32_t accumulate) {
@@ -233,30 +246,36 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     }
                 }
             }
-        } else if (warp == kIssuer && lane == 0 && rank == 0) {
+        } else if (warp == kIssuer && rank == 0) {
             constexpr uint32_t idesc = idesc_e4m3_f32(2 * kM, kN);
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             const uint32_t base = smem_u32(smem);
             for (int tile = tile0; tile < ntiles && !*abort_flag; tile += tstep) {
                 for (int kb = 0; kb < a.nd; ++kb) {
-                    if (!wait_bar<false>(&full[stage], phase, abort_flag, nullptr, 0, a.wait_ns)) break;
-                    if (!wait_bar<false>(&acc_free[acc], acc_phase ^ 1u, abort_flag, nullptr, 0, a.wait_ns)) break;
+                    if (!__all_sync(0xFFFFFFFFu,
+                                    wait_bar<false>(&full[stage], phase, abort_flag, nullptr, 0, a.wait_ns) &&
+                                        wait_bar<false>(&acc_free[acc], acc_phase ^ 1u, abort_flag, nullptr, 0, a.wait_ns)))
+                        break;
                     tc_fence_after();
                     const uint64_t ad = desc_kmajor_sw128(base + stage * kStageBytes);
                     const uint64_t bd = desc_kmajor_sw128(base + stage * kStageBytes + kTileBytes);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < kBlock / 32; ++k)   // 32 bytes of K a step
-                        mma_e4m3<true>(tmem + (uint32_t)(acc * kN), ad + 2 * k, bd + 2 * k, idesc, k ? 1u : 0u);
-                    commit_both(smem_u32(&acc_full[acc]));
-                    commit_both(smem_u32(&empty[stage]));
+                        for (int k = 0; k < kBlock / 32; ++k)   // 32 bytes of K a step
+                            mma_e4m3<true>(tmem + (uint32_t)(acc * kN), ad + 2 * k, bd + 2 * k, idesc, k ? 1u : 0u);
+                        commit_both(smem_u32(&acc_full[acc]));
+                        commit_both(smem_u32(&empty[stage]));
+                    }
+                    __syncwarp();
                     if (++stage == kStages) stage = 0, phase ^= 1u;
                     acc ^= 1;
                     if (acc == 0) acc_phase ^= 1u;
                 }
             }
             // every MMA this thread issued has finished before tensor memory can be released
-            mma_commit<true>(smem_u32(drain));
+            if (elect_one()) mma_commit<true>(smem_u32(drain));
+            __syncwarp();
             const uint64_t t0 = globaltimer();
             while (!mbar_try_wait(drain, 0) && globaltimer() - t0 < a.wait_ns) {
             }
@@ -459,31 +478,35 @@ __global__ void __launch_bounds__(Few<N>::kThreads, 1)
         }
         __syncwarp();
     } else if (warp == F::kIssuer) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = idesc_e4m3_f32(kM, N);
-            int stage = 0, acc = 0;
-            uint32_t phase = 0, acc_phase = 0;
-            const uint32_t base = smem_u32(smem);
-            for (int tile = tile0; tile < ntiles && !*abort_flag; tile += tstep) {
-                for (int kb = k0; kb < k1; ++kb) {
-                    if (!wait_bar<false>(&acc_free[acc], acc_phase ^ 1u, abort_flag, nullptr, 0, a.wait_ns)) break;
-                    if (!wait_bar<false>(&full[stage], phase, abort_flag, nullptr, 0, a.wait_ns)) break;
-                    tc_fence_after();
-                    const uint64_t ad = desc_kmajor_sw128(base + stage * F::kStage);
-                    const uint64_t bd = desc_kmajor_sw128(base + stage * F::kStage + kTileBytes);
+        constexpr uint32_t idesc = idesc_e4m3_f32(kM, N);
+        int stage = 0, acc = 0;
+        uint32_t phase = 0, acc_phase = 0;
+        const uint32_t base = smem_u32(smem);
+        for (int tile = tile0; tile < ntiles && !*abort_flag; tile += tstep) {
+            for (int kb = k0; kb < k1; ++kb) {
+                if (!__all_sync(0xFFFFFFFFu,
+                                wait_bar<false>(&acc_free[acc], acc_phase ^ 1u, abort_flag, nullptr, 0, a.wait_ns) &&
+                                    wait_bar<false>(&full[stage], phase, abort_flag, nullptr, 0, a.wait_ns)))
+                    break;
+                tc_fence_after();
+                const uint64_t ad = desc_kmajor_sw128(base + stage * F::kStage);
+                const uint64_t bd = desc_kmajor_sw128(base + stage * F::kStage + kTileBytes);
+                if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < kBlock / 32; ++k)
                         mma_e4m3<false>(tmem + (uint32_t)(acc * N), ad + 2 * k, bd + 2 * k, idesc, k ? 1u : 0u);
                     mma_commit<false>(smem_u32(&empty[stage]));
                     mma_commit<false>(smem_u32(&acc_full[acc]));
-                    if (++stage == S) stage = 0, phase ^= 1u;
-                    if (++acc == kAccs) acc = 0, acc_phase ^= 1u;
                 }
+                __syncwarp();
+                if (++stage == S) stage = 0, phase ^= 1u;
+                if (++acc == kAccs) acc = 0, acc_phase ^= 1u;
             }
-            mma_commit<false>(smem_u32(drain));
-            const uint64_t t0 = globaltimer();
-            while (!mbar_try_wait(drain, 0) && globaltimer() - t0 < a.wait_ns) {
-            }
+        }
+        if (elect_one()) mma_commit<false>(smem_u32(drain));
+        __syncwarp();
+        const uint64_t t0 = globaltimer();
+        while (!mbar_try_wait(drain, 0) && globaltimer() - t0 < a.wait_ns) {
         }
         __syncwarp();
     } else if (warp == F::kScaler) {
