@@ -18,8 +18,9 @@
 // the even CTA told: some 1300 cycles, of which the other accumulator's block hides 500) is what keeps the
 // tensor pipe waiting.  N = 128 accumulators, four of them, would hide it but read x's tile twice as often from shared
 // memory, which is then the limit (319 us).  16 epilogue warps of 64 columns spill at 104 registers (548 us).
-// T = 1: 86 us in a graph, 6.1 TB/s of w (0.92 of the measured copy: 1002 tiles on 152 SMs leave 6% idle in the
-// seventh round); T = 64: 96 us, T = 128: 115 (on CTA pairs 150).
+// T = 1: 83 us in a graph, 6.3 TB/s of w (0.95 of the measured copy); T = 64: 90 us, T = 128: 109.  A block takes no less
+// than its copies, some 1.5 ns a row of 128 bytes (0.2 us for w's 128 rows), which is also what the tiles of a last,
+// unfilled round take; smaller tiles there (boxes of 32 rows) changed nothing, boxes of 8 rows cost 20%.
 // Every wait is bounded (2 s); where one gives up, the CTA's tiles become NaN.
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -49,6 +50,7 @@ struct LinearArgs {
     int64_t ld;
     int tiles_m, tiles_n;        // k_linear_pair
     int split;                   // k_linear_few: CTAs that share a tile's K
+    int x_rows;                  // k_linear_few: rows of x in a copy
     int aligned;                 // out's rows start on 16-byte boundaries
     uint32_t tx_extra;           // 0; > 0 only in the test hook (no stage ever completes)
     uint64_t wait_ns;            // bound of every wait
@@ -121,6 +123,12 @@ __device__ __forceinline__ void commit_both(uint32_t bar) {
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
         "h"((uint16_t)3)
         : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_cluster16(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
 }
 
 // Scales k .. k + 3 of a row of nd (0 behind its end).
@@ -459,7 +467,7 @@ __global__ void __launch_bounds__(Few<N>::kThreads, 1)
             for (int tile = tile0; tile < ntiles && !*abort_flag; tile += tstep) {
                 for (int kb = k0; kb < k1; ++kb) {
                     if (!wait_bar<false>(&empty[stage], phase ^ 1u, abort_flag, nullptr, 0, a.wait_ns)) break;
-                    mbar_arrive_expect_tx(&full[stage], F::kStage + a.tx_extra);
+                    mbar_arrive_expect_tx(&full[stage], kTileBytes + a.x_rows * kBlock + a.tx_extra);
                     uint8_t* at = smem + stage * F::kStage;
                     tma_load<false>(at, &mapW, smem_u32(&full[stage]), kb * kBlock, tile * kM);
                     tma_load<false>(at + kTileBytes, &mapX, smem_u32(&full[stage]), kb * kBlock, 0);
@@ -495,7 +503,6 @@ __global__ void __launch_bounds__(Few<N>::kThreads, 1)
 #pragma unroll
                     for (int k = 0; k < kBlock / 32; ++k)
                         mma_e4m3<false>(tmem + (uint32_t)(acc * N), ad + 2 * k, bd + 2 * k, idesc, k ? 1u : 0u);
-                    mma_commit<false>(smem_u32(&empty[stage]));
                     mma_commit<false>(smem_u32(&acc_full[acc]));
                 }
                 __syncwarp();
@@ -536,7 +543,7 @@ __global__ void __launch_bounds__(Few<N>::kThreads, 1)
     } else {
         // a thread holds row v of w against NC rows of x
         const uint32_t taddr = tmem + ((uint32_t)(warp % 4 * 32) << 16) + (uint32_t)half;
-        int acc = 0, slot = 0;
+        int acc = 0, slot = 0, stage = 0;
         uint32_t acc_phase = 0, phase = 0;
         bool ok = true;
         for (int tile = tile0; tile < ntiles && ok; tile += tstep) {
@@ -546,6 +553,9 @@ __global__ void __launch_bounds__(Few<N>::kThreads, 1)
                 ok = __all_sync(0xFFFFFFFFu, wait_bar<false>(&sc_full[slot], phase, abort_flag, nullptr, 0, a.wait_ns) &&
                                                  wait_bar<false>(&acc_full[acc], acc_phase, abort_flag, nullptr, 0, a.wait_ns));
                 if (!ok) break;
+                if (threadIdx.x == 0) mbar_arrive(&empty[stage]);     // the MMAs are done with the stage, too (a second
+                                                                      // commit: 20.2 us for 18.9, 1 x 65536 by 1000)
+                if (++stage == S) stage = 0;
                 tc_fence_after();
                 uint32_t r[NC / 16][16];
 #pragma unroll
@@ -579,8 +589,8 @@ __global__ void __launch_bounds__(Few<N>::kThreads, 1)
     __syncthreads();
     if (a.split > 1) {
         // the parts of K: every CTA's sums into its own stages (its copies have landed and been read), and each CTA adds
-        // up a share of x's rows out of all of them, in the CTAs' order.  (Stored into the first CTA one value at a
-        // time they took 0.45 us each.)
+        // up a share of x's rows out of all of them, in the CTAs' order, 16 bytes a load (128 x 2048 by 8000 10.0 us;
+        // 12.9 with 4 bytes, whose loads wait for one another; stored into the first CTA one at a time 39).
         float* own = reinterpret_cast<float*>(smem);          // [rows of x][128]
         if (warp < F::kEpi) {
             const bool bad = *abort_flag != 0;
@@ -589,18 +599,25 @@ __global__ void __launch_bounds__(Few<N>::kThreads, 1)
         }
         cluster_sync_all();
         const int share = N / a.split * kM, first = rank * share;
-        for (int e = threadIdx.x; e < share; e += F::kThreads) {
+        for (int e = threadIdx.x * 4; e < share; e += F::kThreads * 4) {
             const int t = (first + e) / kM;
             const int64_t v = (int64_t)tile0 * kM + e % kM;
-            if (t >= a.T || v >= a.V || !dbg::ok(v < a.ld, dbg::kTile)) continue;
-            float part[kMaxSplit];
+            if (t >= a.T || v >= a.V) continue;
+            uint4 part[kMaxSplit];
 #pragma unroll
             for (int q = 0; q < kMaxSplit; ++q)
-                part[q] = q < a.split ? __uint_as_float(ld_cluster_u32(cluster_addr(own + first + e, q))) : 0.f;
-            float sum = part[0];
+                if (q < a.split) part[q] = ld_cluster16(cluster_addr(own + first + e, q));
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int q = 1; q < kMaxSplit; ++q) sum += part[q];
-            Elt<O>::store1(static_cast<O*>(a.out) + t * a.ld + v, sum);
+            for (int q = 0; q < kMaxSplit; ++q)
+                if (q < a.split) {
+                    sum[0] += __uint_as_float(part[q].x), sum[1] += __uint_as_float(part[q].y);
+                    sum[2] += __uint_as_float(part[q].z), sum[3] += __uint_as_float(part[q].w);
+                }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (v + i < a.V && dbg::ok(v + i < a.ld, dbg::kTile))
+                    Elt<O>::store1(static_cast<O*>(a.out) + t * a.ld + v + i, sum[i]);
         }
         cluster_sync_all();                                   // no CTA leaves while another reads its sums
     }
@@ -674,19 +691,22 @@ cudaError_t run_pair(const void* x, const void* w, int64_t D, LinearArgs& a, cud
 template <typename O, int N>
 cudaError_t run_few(const void* x, const void* w, int64_t D, LinearArgs& a, cudaStream_t s) {
     CUtensorMap mx, mw;
-    if (!make_byte_map(&mx, x, D, a.T, N) || !make_byte_map(&mw, w, D, a.V, kM)) return cudaErrorInvalidValue;
+    // x's rows and no more than 7 behind them (copies cost by the row); what the MMA's other columns hold is not stored
+    a.x_rows = (int)(a.T + 7) / 8 * 8;
+    if (!make_byte_map(&mx, x, D, a.T, a.x_rows) || !make_byte_map(&mw, w, D, a.V, kM)) return cudaErrorInvalidValue;
     static std::atomic<int> ready[kMaxDevices];
     int none = 0;
     cudaError_t e = prepare_kernel(k_linear_few<O, N>, Few<N>::kSmem, false, ready, &none);
     if (e != cudaSuccess) return e;
     const int sms = device_sm_count();
     const int64_t tiles = (a.V + kM - 1) / kM;
-    // As many CTAs to a tile as there are SMs for, with two blocks of K each at least (1 x 4096 by 4000: 13.9 us with
-    // one, 7.3 with four; 1 x 2048 by 8000, where two fit, 8.6 and 7.1; 128 x 2048 by 8000 12.4 and 13.4), but eight
-    // only where they take no more than half the SMs (1 x 4096 by 1000: 7.2 with four, 5.6 with eight; 1 x 16384 by 2048,
-    // 128 CTAs of 152: 15.2 and 18.1, the clusters of eight not all finding a place at once).
+    // As many CTAs to a tile as there are SMs for, with two blocks of K each at least (1 x 4096 by 4000: 10.7 us with
+    // one, 8.0 with two, 6.4 with four; 128 x 1024 by 4000: 8.6, 8.8, 7.3), but eight only where they take no more than
+    // half the SMs (1 x 4096 by 1000: 6.3 with four, 5.5 with eight; 1 x 16384 by 2048, 128 CTAs of 152: 15.2 and 18.1 when
+    // tried, the clusters of eight not all finding a place at once).  Below eight blocks the joining costs more than it
+    // saves (1 and 64 x 512 by 4000: 4.3 and 5.4 with one, 4.7 and 6.0 with two).
     a.split = 1;
-    while (a.split < kMaxSplit && tiles * a.split * (a.split < 4 ? 2 : 4) <= sms && a.nd >= 4 * a.split) a.split *= 2;
+    while (a.split < kMaxSplit && tiles * a.split * (a.split < 4 ? 2 : 4) <= sms && a.nd >= std::max(8, 4 * a.split)) a.split *= 2;
     const int blocks = a.split > 1 ? (int)tiles * a.split : (int)std::min<int64_t>(tiles, sms);
     return launch(k_linear_few<O, N>, blocks, a.split, Few<N>::kThreads, Few<N>::kSmem, s, mx, mw, a);
 }
