@@ -11,7 +11,7 @@
 //   k_linear_few   T <= 128: bound by reading w.  The roles change sides: w's rows are the MMA's 128, the rows of x
 //                  its N (16 to 128 wide), so a stage is w's 16 KB and the few rows of x.  Where w has fewer tiles
 //                  than there are SMs, a cluster's CTAs each take a part of K and add their sums in order.
-// What bounds them.  8192 x 4096 by 128256 to bf16: 3.9-4.1 ms, 2180 TFLOP/s (0.58 of twice the bf16 product's
+// What bounds them.  8192 x 4096 by 128256 to bf16: 3.87-4.04 ms, 2220 TFLOP/s (0.59 of twice the bf16 product's
 // measured burst rate), the tensor pipe 45% active at 1.91 GHz.  At 2048 x 4096 by 32768, 263 us: the copies out of
 // L2 with a quarter of the MMAs take 168 us (15 TB/s), copies and MMAs with nobody waiting for an accumulator 209, with
 // the accumulators handed over but not read 236.  The hand-over (a block's MMAs done, both CTAs told, the sums read,
