@@ -18,7 +18,7 @@
 // the even CTA told: some 1300 cycles, of which the other accumulator's block hides 500) is what keeps the
 // tensor pipe waiting.  N = 128 accumulators, four of them, would hide it but read x's tile twice as often from shared
 // memory, which is then the limit (319 us).  16 epilogue warps of 64 columns spill at 104 registers (548 us).
-// T = 1: 83 us in a graph, 6.3 TB/s of w (0.95 of the measured copy); T = 64: 90 us, T = 128: 109.  A block takes no less
+// T = 1: 83-85 us in a graph, 6.2-6.3 TB/s of w (0.93-0.95 of the measured copy); T = 64: 90 us, T = 128: 109.  A block takes no less
 // than its copies, some 1.5 ns a row of 128 bytes (0.2 us for w's 128 rows), which is also what the tiles of a last,
 // unfilled round take; smaller tiles there (boxes of 32 rows) changed nothing, boxes of 8 rows cost 20%.
 // Every wait is bounded (2 s); where one gives up, the CTA's tiles become NaN.
