@@ -18,9 +18,10 @@
 // the even CTA told: some 1300 cycles, of which the other accumulator's block hides 500) is what keeps the
 // tensor pipe waiting.  N = 128 accumulators, four of them, would hide it but read x's tile twice as often from shared
 // memory, which is then the limit (319 us).  16 epilogue warps of 64 columns spill at 104 registers (548 us).
-// T = 1: 83-85 us in a graph, 6.2-6.3 TB/s of w (0.93-0.95 of the measured copy); T = 64: 90 us, T = 128: 109.  A block takes no less
-// than its copies, some 1.5 ns a row of 128 bytes (0.2 us for w's 128 rows), which is also what the tiles of a last,
-// unfilled round take; smaller tiles there (boxes of 32 rows) changed nothing, boxes of 8 rows cost 20%.
+// T = 1: 83-85 us in a graph, 6.2-6.3 TB/s of w (0.93-0.95 of the measured copy); T = 64: 90 us, T = 128: 109.  A block
+// takes no less than its copies, some 1.5 ns a row of 128 bytes (0.2 us for w's 128 rows), however few SMs work.  Each SM
+// the same number of rows, the last tile in copies of 32: 1 x 4096 by 128256 85.5 us to 87.7, 64 x 2064 by 32001 21.4 to
+// 20.3; in copies of 8 slower everywhere.
 // Every wait is bounded (2 s); where one gives up, the CTA's tiles become NaN.
 #include <cuda_runtime.h>
 #include <stdint.h>
