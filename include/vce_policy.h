@@ -17,9 +17,12 @@
  * the row's token.  A row whose token is ignore_index is left out: its logits are not read, what
  * it returns is +0.0 and so is its gradient.  Any other token outside [0, V) makes *status
  * VCE_ERR_LABEL, what the row returns NaN, and its gradient +0.0.  Masked logits may be -inf or
- * the type's lowest value (a logit whose product with log2(e) / temperature passes fp32 counts as
- * -inf).  Of a row of nothing but masks everything is NaN, and it has no gradient (+0.0).  A NaN
- * or +inf among a row's logits makes all that the row returns, and its whole gradient, NaN.
+ * any value far below the others, such as -1e10 or the type's lowest.  A logit whose product with
+ * log2(e) / temperature passes fp32 counts as -inf; of a row of nothing but -inf everything is NaN, and
+ * it has no gradient (+0.0).  A row of nothing but lesser masks is a row like any other (where that
+ * product of its largest logit but the token is 2^30 or more in size, logits count as equal when their
+ * products round to the same fp32 number).  A NaN or +inf among a row's logits (or one whose product passes
+ * fp32 upwards) makes all that the row returns, and its whole gradient, NaN.
  */
 #ifndef VCE_POLICY_H
 #define VCE_POLICY_H

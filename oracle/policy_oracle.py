@@ -18,6 +18,8 @@ def rows(z, ids, temperature=1.0, keep=None):
         valid = valid & keep
     for i in np.nonzero(valid)[0]:
         x = z[i] / temperature
+        if np.isfinite(x.max()):
+            x = x - x.max()   # beside logits of 1e20 the logarithm of a sum is lost in 64 bits too
         t = ids[i]
         rest = np.delete(x, t)
         m = rest.max() if rest.size else -np.inf

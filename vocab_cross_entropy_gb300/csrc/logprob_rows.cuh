@@ -12,7 +12,9 @@
 //   dl/dz_j = 2^y (c0 + c1 y), y = z_j k2 - m,   c0 = f (-a - b (ln f + H)) / T,  c1 = -b f ln 2 / T
 //   dl/dz_t = (a (1 - p_t) - b p_t (log p_t + H)) / T
 // The exponents are taken from m, not from the log-sum-exp: m is some z_j k2 (or a thread's first
-// maximum), exact, where a log-sum-exp of size 16 would be rounded by 5e-7 of every p_j.
+// maximum), exact, where a log-sum-exp of size 16 would be rounded by 5e-7 of every p_j.  Where |m| is 2^30 or more
+// the products z k2 are rounded first, in the sums and the gradient alike: logits of that size (masks such as -1e10
+// in a row of nothing larger) count as equal where the products round to the same number.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -51,6 +53,22 @@ struct Sums {
 struct Scale {
     float hi, lo;
 };
+
+// References of this size and more are large.  Below it the exponent of the reference's own logit, which is what the
+// product with k2 was rounded by, is 2^5 at most.
+constexpr float kLarge = 1073741824.f;               // 2^30
+__device__ __forceinline__ bool beyond(float m) { return fabsf(m) >= kLarge; }
+
+// How many products with k2 round to m, the largest of them (+inf: NaN).
+template <int G, int U>
+__device__ __forceinline__ float count_of(const float (&v)[U][G], float k2, float m) {
+    float n = 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int k = 0; k < G; ++k) n += v[u][k] * k2 == m ? 1.f : 0.f;
+    return m < kInf ? n : __int_as_float(0x7FC00000);
+}
 
 // (s, w) to the reference M >= m.
 template <int kKind>
@@ -133,23 +151,66 @@ __device__ __forceinline__ void sums_of(const float (&v)[U][G], float k2, float 
     w = w0[0] + w1[0];
 }
 
-// Adds a thread's vectors of a stage; the reference moves only when a term would pass 2^32.
+// A batch of a thread's vectors.
+template <int G, int U>
+struct Batch {
+    float v[U][G];
+};
+
 template <int G, int U, int kKind>
-__device__ __forceinline__ void push(const float (&v)[U][G], Sums& x, float k2) {
-    if (x.m == -kInf) {
-        x.m = rs::max_of<G>(v) * k2;
-        if (x.m == -kInf) return;
-    }
-    float s, w;
-#pragma unroll 1
-    for (int again = 0;; again = 1) {   // one copy of the sum's code, for the instruction cache
-        sums_of<G, U, kKind>(v, k2, x.m, s, w);
-        if (again || s < 4294967296.f) break;
-        rescale<kKind>(x, fmaxf(x.m, rs::max_of<G>(v) * k2));
-    }
+__device__ __forceinline__ void add(Sums& x, float s, float w, float k2) {
     x.s += s;
     if (kKind == kMean && !(fabsf(w) < kInf)) w = s * (x.m / k2);
     if (kKind != kSum) x.w += w;
+}
+
+// A batch whose reference moves, or is large: then it is the row's largest rounded product so far, and the sum counts
+// the logits whose products round to it (any other is 2^6 or more below).  The exponent of a mask of -1e10 with its
+// own rounded product for a reference would be up to 2^9 in size.
+template <int G, int U, int kKind>
+__device__ __forceinline__ Sums push_moving(const Batch<G, U>& b, Sums x, float k2) {
+    const float top = rs::max_of<G>(b.v) * k2;
+    if (!(top <= x.m)) rescale<kKind>(x, top);       // (a NaN: s is one then)
+    if (beyond(x.m)) {
+        x.s += count_of(b.v, k2, x.m);
+        return x;
+    }
+    float s, w;
+    sums_of<G, U, kKind>(b.v, k2, x.m, s, w);
+    add<G, U, kKind>(x, s, w, k2);
+    return x;
+}
+
+// The same by a call: in the loop of the sums its code costs the one pass 2.4% (16384 x 128256).
+template <int G, int U, int kKind>
+__device__ __noinline__ Sums call_moving(Batch<G, U> b, Sums x, float k2) {
+    return push_moving<G, U, kKind>(b, x, k2);
+}
+
+// Adds a thread's vectors of a stage; the reference moves only when a term would pass 2^32, or where it is large.
+template <int G, int U, int kKind, bool kCall = true>
+__device__ __forceinline__ void push(const float (&v)[U][G], Sums& x, float k2) {
+    bool moving = false;
+    if (!(fabsf(x.m) < kLarge)) {
+        const float top = rs::max_of<G>(v) * k2;
+        if (x.m == -kInf && top == -kInf) return;
+        moving = x.m != -kInf || beyond(top);
+        if (!moving) x.m = top;
+    }
+    if (!moving) {
+        float s, w;
+        sums_of<G, U, kKind>(v, k2, x.m, s, w);
+        moving = !(s < 4294967296.f);
+        if (!moving) add<G, U, kKind>(x, s, w, k2);
+    }
+    if (moving) {
+        Batch<G, U> b;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int k = 0; k < G; ++k) b.v[u][k] = v[u][k];
+        x = kCall ? call_moving<G, U, kKind>(b, x, k2) : push_moving<G, U, kKind>(b, x, k2);
+    }
 }
 
 // ---- a row's scalars ---------------------------------------------------------------------------------
@@ -201,8 +262,9 @@ __device__ __forceinline__ Row finish(const Sums& x, float zt, Scale k) {
     // what the exponentials' mean error and the scale's low part leave out
     const float ratio = kKind == kSum ? 0.f : x.w / x.s;
     const float mean = kKind == kMean ? ratio : (ratio + x.m) / k2;
-    near += kEx2Bias;
-    if (kKind != kSum && fabsf(mean) < kInf) near += kLn2 * k.lo * mean;
+    const bool large = beyond(x.m);                  // then the terms are 1 or nothing, and the scale's low part is lost
+    if (!large) near += kEx2Bias;
+    if (kKind != kSum && !large && fabsf(mean) < kInf) near += kLn2 * k.lo * mean;
     const float hrest = kKind == kEntropy ? fmaxf(0.f, fmaf(e - ratio, kLn2, near)) : 0.f;
     r.m = x.m;
     const float lns = fmaf(e, kLn2, near);
@@ -216,8 +278,9 @@ __device__ __forceinline__ Row finish(const Sums& x, float zt, Scale k) {
         return r;
     }
     float lo;
-    const float gap = minus_product(x.m, zt, k2, lo);
+    float gap = minus_product(x.m, zt, k2, lo);
     lo -= zt * k.lo;
+    if (large) gap = __fsub_rn(x.m, __fmul_rn(zt, k2)), lo = 0.f;   // as the terms of the sum
     const float g = gap + e, t = g - gap;            // TwoSum of gap and e
     lo += (gap - (g - t)) + (e - t);
     float u = g * kLn2;

@@ -83,17 +83,18 @@ __global__ void __launch_bounds__(kConsumers + 32, 3) k_row_grads(const __grid_c
     } else {
         const Coefs c = ctl.c;
         const float bias = ctl.bias;
+        const bool whole = vec && !beyond(bias);
         const int target = ctl.target;
         for (int j = 0; j < sl.nst; ++j) {
             wait_stage(bar, a.nbuf, j, a.wait_ns);
             uint4 x[kU];
             load_stage<S>(smem, a.nbuf, r, sl, j, j, tid, x);
             const int v0 = sl.v0 + j * kStageVecs, v1 = sl.v0 + sl.n;
-            const bool fast = vec && v0 >= r.iv0 && v0 + kStageVecs <= min(r.iv1, v1);
+            const bool fast = whole && v0 >= r.iv0 && v0 + kStageVecs <= min(r.iv1, v1);
             if (c.c1 != 0.f)
-                write_grads<S, O, kU, kConsumers, true>(x, r, v0 + tid, v1, fast, grow, vec, c, bias, a.k2);
+                write_grads<S, O, kU, kConsumers, true>(x, r, v0 + tid, v1, fast, grow, whole, c, bias, a.k2);
             else
-                write_grads<S, O, kU, kConsumers, false>(x, r, v0 + tid, v1, fast, grow, vec, c, bias, a.k2);
+                write_grads<S, O, kU, kConsumers, false>(x, r, v0 + tid, v1, fast, grow, whole, c, bias, a.k2);
             // the token's entry, over what its thread has just written there
             const int rel = target >= 0 ? (target + r.shift) / Elt<S>::kGroup - v0 - tid : -1;
             if (rel >= 0 && rel < kStageVecs && rel % kConsumers == 0 && v0 + tid + rel < v1)

@@ -43,6 +43,9 @@ __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_held(const __g
     constexpr int G = Elt<S>::kGroup, NT = F::kNT, U = F::kU, kWarps = NT / 32;
     static_assert(U % 2 == 0, "vectors go in pairs");
     constexpr int kKind = kEnt ? kEntropy : kGrad ? kSum : kMean;    // as the ring's
+    // a call where the registers allow it (8192 x 8000 bf16 one pass 50.0 us, 51.0 inlined; 4096 x 2000 fp32 with
+    // an entropy term 17.8, 16.6 inlined)
+    constexpr bool kCall = !(G == 4 && kGrad && kEnt);
     __shared__ Sums part[kWarps > 1 ? kWarps : 1];
     __shared__ RowCoefs coefs_of_row;
     __shared__ int64_t token_of_row;
@@ -120,7 +123,7 @@ __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_held(const __g
                 if (k == tk && tu == u + 1) v[1][k] = -kInf;
             }
         }
-        push<G, 2, kKind>(v, sum, a.k2);
+        push<G, 2, kKind, kCall>(v, sum, a.k2);
     }
     warp_merge<kKind>(sum);
     if (kWarps > 1) {
@@ -160,11 +163,12 @@ __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_held(const __g
         fill_grads<S, O>(r, sl, grow, vec, tid, NT);
         return;
     }
-    const bool fast = vec && inside && F::kVecs <= r.nv;
+    const bool whole = vec && !beyond(cf.bias);
+    const bool fast = whole && inside && F::kVecs <= r.nv;
     if (kEnt && cf.c.c1 != 0.f)
-        write_grads<S, O, U, NT, true>(x, r, tid, r.nv, fast, grow, vec, cf.c, cf.bias, a.k2);
+        write_grads<S, O, U, NT, true>(x, r, tid, r.nv, fast, grow, whole, cf.c, cf.bias, a.k2);
     else
-        write_grads<S, O, U, NT, false>(x, r, tid, r.nv, fast, grow, vec, cf.c, cf.bias, a.k2);
+        write_grads<S, O, U, NT, false>(x, r, tid, r.nv, fast, grow, whole, cf.c, cf.bias, a.k2);
     if (tu >= 0 && tid + tu * NT < r.nv) Elt<O>::store1(grow + t, cf.c.gt);   // over what this thread wrote there
 }
 

@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_ring(const __g
                 if (!wait(&ctl.finished[par], e, kErrCoefs)) continue;
                 const RowCoefs cf = ctl.coefs[par];
                 O* grow = static_cast<O*>(a.grad) + row * a.ld_g;
-                const bool vec = grads_aligned<S, O>(r, grow);
+                const bool vec = grads_aligned<S, O>(r, grow) && !beyond(cf.bias);
                 const int fast0 = vec ? r.iv0 : r.nv, fast1 = min(r.iv1, sl.v0 + sl.n);
                 for (int j = 0; j < sl.nst; ++j, back.step()) {
                     const uint4* buf = reinterpret_cast<const uint4*>(smem + back.st * F::kBytes) + tid;

@@ -66,12 +66,18 @@ __device__ __forceinline__ void grads_of(float (&g)[G], const Coefs& c, float bi
 }
 
 // A vector of the row from its first column c0 on (before the row's start where it is partial), element by
-// element: partial vectors, and gradients that are not aligned as the logits are.
+// element: partial vectors, gradients that are not aligned as the logits are, and rows with a large bias, whose
+// products with k2 are rounded first, as they were in the sums.
 template <typename S, typename O>
 __device__ __noinline__ void write_single(uint4 x, int64_t c0, int64_t V, O* grow, Coefs c, float bias, float k2) {
     constexpr int G = Elt<S>::kGroup;
     float g[G];
     Elt<S>::unpack(x, g);
+    if (beyond(bias)) {
+#pragma unroll
+        for (int k = 0; k < G; ++k) g[k] *= k2;
+        k2 = 1.f;
+    }
     grads_of<G, true>(g, c, bias, k2);
 #pragma unroll
     for (int k = 0; k < G; ++k)
@@ -79,7 +85,7 @@ __device__ __noinline__ void write_single(uint4 x, int64_t c0, int64_t V, O* gro
 }
 
 // The gradients of U vectors of a thread, vector v0 + u * NT of the row each, the slice's end at v1.  fast: all of
-// them lie wholly in the row and the slice, and are aligned in the gradient too.
+// them lie wholly in the row and the slice, and are aligned in the gradient too.  vec, fast: not with a large bias.
 template <typename S, typename O, int U, int NT, bool kEnt>
 __device__ __forceinline__ void write_grads(const uint4 (&x)[U], const rs::Row& r, int v0, int v1, bool fast, O* grow,
                                             bool vec, const Coefs& c, float bias, float k2) {
