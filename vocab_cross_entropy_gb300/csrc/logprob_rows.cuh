@@ -29,11 +29,14 @@ namespace lp {
 using rs::kLn2;
 constexpr float kLn2Lo = -1.90465431e-9f;            // ln 2 = kLn2 + kLn2Lo
 
-// The hardware's base-2 exponential comes out low on the mean, and so does a sum of many: by 4.9e-8 of itself over the
-// terms of a row (measured against exp2 in 64 bits; each is within 1.5e-7), and by about 2e-8 more where the sums of
-// threads and warps are brought to one reference (the mean error of log p_t at 2048 x 32000 and 128256: 1.5e-7 without
-// either correction, 2e-8 with both).
-constexpr float kEx2Bias = 7.0e-8f;
+// The factor 2^d, d < 0, that brings a thread's, a warp's or a block's sums to another's reference.  All of a sum is
+// multiplied by it, up to three times a row, and the hardware's base-2 exponential is low by 4.4e-8 on the mean, which
+// is added: the mean errors of log p_t over fp32 rows of 4000, 32000 and 128256 columns are 7.2e-8, 9.4e-8 and 1.3e-7
+// without it.  What a row's own terms are off by is not known beforehand: up to 4e-8 is left.
+__device__ __forceinline__ float factor(float d) {
+    const float e = ex2(d);
+    return fmaf(e, 4.4e-8f, e);
+}
 
 __device__ __forceinline__ float nan_f() { return __int_as_float(0x7FC00000); }
 
@@ -74,7 +77,7 @@ __device__ __forceinline__ float count_of(const float (&v)[U][G], float k2, floa
 template <int kKind>
 __device__ __forceinline__ void rescale(Sums& x, float M) {
     const float d = x.m - M;
-    const float e = (x.m == M) ? 1.f : ex2(d);
+    const float e = (x.m == M) ? 1.f : factor(d);
     if (kKind == kEntropy) x.w = e == 0.f ? 0.f : e * (x.m == M ? x.w : fmaf(d, x.s, x.w));
     if (kKind == kMean) x.w *= e;
     x.s *= e;
@@ -259,13 +262,12 @@ __device__ __forceinline__ Row finish(const Sums& x, float zt, Scale k) {
     }
     float near;
     const float e = split_log(x.s, near);
-    // what the exponentials' mean error and the scale's low part leave out
+    // what the scale's low part leaves out
     const float ratio = kKind == kSum ? 0.f : x.w / x.s;
     const float mean = kKind == kMean ? ratio : (ratio + x.m) / k2;
-    const bool large = beyond(x.m);                  // then the terms are 1 or nothing, and the scale's low part is lost
-    if (!large) near += kEx2Bias;
+    const float hrest = kKind == kEntropy ? fmaxf(0.f, fmaf(e - ratio, kLn2, near)) : 0.f;   // (of either side as much)
+    const bool large = beyond(x.m);                  // then the scale's low part is lost
     if (kKind != kSum && !large && fabsf(mean) < kInf) near += kLn2 * k.lo * mean;
-    const float hrest = kKind == kEntropy ? fmaxf(0.f, fmaf(e - ratio, kLn2, near)) : 0.f;
     r.m = x.m;
     const float lns = fmaf(e, kLn2, near);
     if (!tok) {
