@@ -82,3 +82,16 @@ def test_entropy_of_one_other_column(vce, V, tau, other):
         # the gap itself is exact (powers of two and their products), but for |u| roundings of 2^-24 in e^-|u|
         tol = (16 + 2 * u.abs()) * 2.0 ** -24 * want + 2.0 ** -126   # and fp32 ends there
         assert torch.all((got.double().cpu() - want).abs() <= tol)
+
+
+@pytest.mark.parametrize("T,V,tau,offset", CASES)
+def test_mean_error_of_the_one_pass(vce, T, V, tau, offset):
+    """Without an entropy term the scale is rounded on both sides, ln 2 k_lo (z_t - E z): a common offset of the logits
+    is not in it."""
+    z, ids, want, gap = rows(T, V, tau, offset)
+    k = 1.4426950408889634 / tau
+    lost = math.log(2) * abs((k - float(np.float32(k))) * float(gap.mean()))
+    lp = vce.policy_loss_forward_backward(z, ids, torch.ones(T, device="cuda"), temperature=tau, reduction="sum")[2]
+    off = float((lp.double() - want).mean())
+    print(f"{T} x {V} at {tau:.3g} + {offset}: {off:.2e} of {bound(T) + lost:.2e}")
+    assert abs(off) <= bound(T) + lost

@@ -281,7 +281,7 @@ __device__ __forceinline__ Row finish(const Sums& x, float zt, Scale k) {
     }
     float lo;
     float gap = minus_product(x.m, zt, k2, lo);
-    lo -= zt * k.lo;
+    if (kKind != kSum) lo -= zt * k.lo;              // as the sum's side: one alone is off by the logits' common offset
     if (large) gap = __fsub_rn(x.m, __fmul_rn(zt, k2)), lo = 0.f;   // as the terms of the sum
     const float g = gap + e, t = g - gap;            // TwoSum of gap and e
     lo += (gap - (g - t)) + (e - t);
