@@ -117,8 +117,8 @@ VCE_API int policy_loss_backward(const void* logits, vce_dtype dt, int64_t T, in
  * policy_loss_forward_backward -- both with one read of the logits, for callers that know grad_output
  * when the forward runs: each row is held in the shared memory of a thread-block cluster between
  * its statistics and its gradient (rows too long for that are read again).  The arguments and
- * results are the two calls'; for MEAN *loss_out holds 1/N while the work runs, and row_stats is
- * scratch.
+ * results are the two calls' (where a wait gave up, NaN over the columns of the block that waited too, in all of
+ * its rows); for MEAN *loss_out holds 1/N while the work runs, and row_stats is scratch.
  */
 VCE_API int policy_loss_forward_backward(const void* logits, vce_dtype dt, int64_t T, int64_t V, int64_t ld,
                                          const int64_t* actions, int64_t ignore_index, float temperature,

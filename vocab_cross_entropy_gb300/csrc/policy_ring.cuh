@@ -504,9 +504,16 @@ __global__ void __launch_bounds__(F::kThreads, F::kBlocks) k_loss_ring(const __g
             }
         }
     }
-    if (ctl.abort)
+    if (ctl.abort) {
         for (int64_t row = cid + (int64_t)tid * ncl; row < a.T; row += (int64_t)F::kThreads * ncl)
             write_none(a, row, ctl.err ? ctl.err : kErrRow);
+        if (kGrad)                                     // nor is any of its columns' gradients
+            for (int64_t row = cid; row < a.T; row += ncl) {
+                const rs::Row r = row_extent<S>(a, row);
+                O* g = static_cast<O*>(a.grad) + row * a.ld_g;
+                fill_grads<S, O>(r, ring_slice<F>(r, a.per, rank), g, grads_aligned<S, O>(r, g), tid, F::kThreads, nan_f());
+            }
+    }
 }
 
 }  // namespace ring
