@@ -28,7 +28,8 @@ extern "C" {
  * NaN or an infinity has the scale NaN and nothing but NaN in it.
  *   x, dt       fp32 or bf16, leading dimension ld >= D
  *   block_rows  1 (hidden states: a scale for every row) or 128 (weights)
- *   q           [R, D] bytes, leading dimension D, written;  scales  fp32, written
+ *   q           [R, D] bytes, leading dimension D, written;  scales  fp32, written; VCE_ERR_ARG if the extents of
+ *               x, q and scales share a byte
  *   D           1 .. 2^24;  R <= 2^27
  */
 VCE_API int vce_quantize_fp8(const void* x, vce_dtype dt, int64_t R, int64_t D, int64_t ld, int block_rows,
@@ -43,7 +44,8 @@ VCE_API int vce_quantize_fp8(const void* x, vce_dtype dt, int64_t R, int64_t D, 
  *   w         [V, D] e4m3, leading dimension D, 16-byte aligned
  *   w_scales  [ceil(V / 128), ceil(D / 128)] fp32
  *   T, V, D   T, V <= 2^24; D a multiple of 16, 16 .. 65536
- *   out       [T, ld] of dtype out_dt (bf16 or fp32), written; ld >= V
+ *   out       [T, ld] of dtype out_dt (bf16 or fp32), written; ld >= V; VCE_ERR_ARG if its extent shares a byte
+ *             with an operand's
  * Tiles behind a device-side wait that gave up after 2 s hold NaN.
  */
 VCE_API int vce_linear_fp8(const void* x, const float* x_scales, const void* w, const float* w_scales,

@@ -741,10 +741,14 @@ static int linear_call(const void* x, const float* x_scales, const void* w, cons
     if (!x || !x_scales || !w || !w_scales || !out) return VCE_ERR_NULL;
     if (!aligned(x, 16) || !aligned(w, 16) || !aligned(x_scales, 4) || !aligned(w_scales, 4) || !aligned(out, es))
         return VCE_ERR_ALIGN;
+    const int64_t nd = (D + 127) / 128, no = ((T - 1) * ld + V) * (int64_t)es;
+    if (overlap_bytes(out, no, x, T * D) || overlap_bytes(out, no, w, V * D) || overlap_bytes(out, no, x_scales, T * nd * 4) ||
+        overlap_bytes(out, no, w_scales, (V + 127) / 128 * nd * 4))
+        return VCE_ERR_ARG;                          // tiles are read while others are written
     int rc = require_sm100();
     if (rc) return rc;
     fp8::LinearArgs a{};
-    a.xs = x_scales, a.ws = w_scales, a.T = T, a.V = V, a.nd = (int)((D + 127) / 128), a.out = out, a.ld = ld, a.split = 1;
+    a.xs = x_scales, a.ws = w_scales, a.T = T, a.V = V, a.nd = (int)nd, a.out = out, a.ld = ld, a.split = 1;
     a.aligned = aligned(out, 16) && ld * (int64_t)es % 16 == 0;
     a.tx_extra = tx_extra, a.wait_ns = wait_ns;
     const cudaError_t e = out_dt == VCE_BF16 ? fp8::run<uint16_t>(x, w, D, a, s) : fp8::run<float>(x, w, D, a, s);

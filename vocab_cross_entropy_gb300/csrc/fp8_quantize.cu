@@ -204,6 +204,11 @@ extern "C" int vce_quantize_fp8(const void* x, vce_dtype dt, int64_t R, int64_t 
     if (R == 0) return VCE_OK;
     if (!x || !q || !scales) return VCE_ERR_NULL;
     if (!aligned(x, es) || !aligned(scales, 4)) return VCE_ERR_ALIGN;
+    // blocks read x while others write (and some read it twice)
+    const int64_t nx = ((R - 1) * ld + D) * (int64_t)es;
+    if (overlap_bytes(x, nx, q, R * D) || overlap_bytes(x, nx, scales, blocks * 4) ||
+        overlap_bytes(q, R * D, scales, blocks * 4))
+        return VCE_ERR_ARG;
     int rc = require_sm100();
     if (rc) return rc;
     const fp8::QuantArgs a{x, R, D, ld, static_cast<uint8_t*>(q), scales, nd};

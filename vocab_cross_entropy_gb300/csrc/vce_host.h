@@ -18,6 +18,12 @@ inline bool fits_bytes(int64_t rows, int64_t ld, size_t esize) {
     return ld <= lim / rows;
 }
 
+// Whether two extents share a byte.
+inline bool overlap_bytes(const void* a, int64_t na, const void* b, int64_t nb) {
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+    return a0 < b0 + (uintptr_t)nb && b0 < a0 + (uintptr_t)na;
+}
+
 // Per-device caches hold this many devices; calls on a device beyond it report an error
 // (or skip the cached fast path where one exists).
 constexpr int kMaxDevices = 64;
