@@ -159,8 +159,8 @@ typedef struct {
  *   ref_logprobs           [T] fp32 or NULL
  *   p                      host pointer
  *   pair_losses [P], rewards [2 P], logprobs [T] fp32, written;  loss_out [1] fp32, written for SUM / MEAN
- *   row_stats, status      as ce_logprobs_forward.  A pair with an error in one of its rows, or a row of
- *                          nothing but masks, has a NaN loss and no gradient.
+ *   row_stats, status      as ce_logprobs_forward.  A sequence with an error in one of its rows, or a row of
+ *                          nothing but -inf, has a NaN reward, and its pair a NaN loss and no gradient.
  */
 VCE_API int preference_loss_forward(const void* logits, vce_dtype dt, int64_t T, int64_t V, int64_t ld,
                                     const int64_t* labels, int64_t ignore_index, float temperature,

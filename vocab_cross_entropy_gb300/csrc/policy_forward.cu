@@ -132,7 +132,7 @@ constexpr int kPairThreads = 256;
 // gradient coefficients.
 __global__ void __launch_bounds__(kPairThreads) k_pairs(const __grid_constant__ PairArgs a) {
     __shared__ float sum[2][kPairThreads / 32], comp[2][kPairThreads / 32];
-    __shared__ int count[2], bad;
+    __shared__ int count[2], wrong[2];               // rows, and whether one of them has an error or nothing but masks
     __shared__ float slope[2];
     start_next();
     wait_previous();
@@ -140,8 +140,7 @@ __global__ void __launch_bounds__(kPairThreads) k_pairs(const __grid_constant__ 
     int64_t o[3];
 #pragma unroll
     for (int i = 0; i < 3; ++i) o[i] = min(max(a.offsets[2 * p + i], (int64_t)0), a.T);
-    if (threadIdx.x < 2) count[threadIdx.x] = 0;
-    if (threadIdx.x == 0) bad = 0;
+    if (threadIdx.x < 2) count[threadIdx.x] = wrong[threadIdx.x] = 0;
     __syncthreads();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -176,9 +175,10 @@ __global__ void __launch_bounds__(kPairThreads) k_pairs(const __grid_constant__ 
             comp[q][warp] = c;
             if (n) atomicAdd(&count[q], n);
         }
-        if (code) bad = 1;
+        if (code) wrong[q] = 1;
     }
     __syncthreads();
+    const bool bad = wrong[0] || wrong[1];
     if (threadIdx.x == 0) {
         float S[2], share[2];
         for (int q = 0; q < 2; ++q) {
@@ -190,9 +190,9 @@ __global__ void __launch_bounds__(kPairThreads) k_pairs(const __grid_constant__ 
             S[q] = fabsf(s) < kInf ? s + c : s;
             share[q] = a.average && count[q] > 0 ? 1.f / (float)count[q] : 1.f;
             if (a.average && count[q] > 0) S[q] = S[q] / (float)count[q];
-            S[q] *= a.beta;
+            S[q] = wrong[q] ? nan_f() : S[q] * a.beta;
         }
-        const float x = bad ? nan_f() : (S[0] - S[1]) - a.margin;
+        const float x = (S[0] - S[1]) - a.margin;
         float loss, g;
         if (a.kind == VCE_PREF_SIGMOID) {
             const float e = expf(-fabsf(x)), l = log1pf(e), d = 1.f / (1.f + e);
