@@ -220,11 +220,12 @@ __device__ __forceinline__ float minus_product(float c, float a, float b, float&
 // All arithmetic on the K entries, by one warp (lane + 32 i: entry k; col -1: none, z, t -inf there):
 // each entry's (r_k, r_k - qh_k), and the scalars of Top.
 __device__ __forceinline__ Top top_arithmetic(const Args& a, int K, int lane, const int (&col)[kPerLane],
-                                               const float (&z)[kPerLane], const float (&t)[kPerLane], Entry* entry,
+                                               float (&z)[kPerLane], const float (&t)[kPerLane], Entry* entry,
                                                float R) {
     float zm = -kInf, tm = -kInf;
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i) {
+        if (z[i] * a.k2 <= -kLarge) z[i] = -kInf;   // masks, as in the tail's pairs
         zm = fmaxf(zm, z[i]);
         tm = fmaxf(tm, t[i]);
     }
@@ -288,8 +289,7 @@ __device__ __forceinline__ Finish finish_row(const Args& a, float M, float S0, c
     f.code = code;
     // no finite teacher mass (comparisons that a NaN fails)
     if (!code && !((t.tsum > 0.f || R > -kInf) && t.tsum < kInf && R < kInf)) f.code = VCE_ERR_TEACHER;
-    // entries whose product with k2 passes fp32 hold nothing, as in the tail's pairs
-    const bool has_tail = S0 > 0.f, has_top = t.zmax * a.k2 > -kInf;
+    const bool has_tail = S0 > 0.f, has_top = t.zmax > -kInf;
     bool lost = false;                               // a NaN or +inf among the student's logits: NaN throughout
     float lo;
     const float gap = minus_product(M, t.zmax, a.k2, lo);

@@ -26,6 +26,7 @@
 namespace vce {
 namespace lp {
 
+using rs::kLarge;
 using rs::kLn2;
 constexpr float kLn2Lo = -1.90465431e-9f;            // ln 2 = kLn2 + kLn2Lo
 
@@ -57,9 +58,6 @@ struct Scale {
     float hi, lo;
 };
 
-// References of this size and more are large.  Below it the exponent of the reference's own logit, which is what the
-// product with k2 was rounded by, is 2^5 at most.
-constexpr float kLarge = 1073741824.f;               // 2^30
 __device__ __forceinline__ bool beyond(float m) { return fabsf(m) >= kLarge; }
 
 // How many products with k2 round to m, the largest of them (+inf: NaN).

@@ -250,14 +250,22 @@ __device__ __forceinline__ float max_of(const float (&v)[U][G]) {
     return m;
 }
 
+// References of this size and more are large.  Below it the exponent of the reference's own logit, which is what the
+// product with k2 was rounded by, is 2^5 at most; against a mask of -1e10 it would be 2^9, which no power of two holds.
+constexpr float kLarge = 1073741824.f;               // 2^30
+
 // Adds a stage's values to a pair whose reference moves only when a term would pass 2^32 (it is then one
-// of the values', so s is about 1 or more and nothing overflows).  Values whose product with k2 passes
-// fp32 (masks of the type's lowest value) count as -inf.  A NaN or +inf makes s NaN.
+// of the values', so s is about 1 or more and nothing overflows).  Values whose product with k2 is -2^30 or less
+// (masks) count as -inf.  A NaN, or a product of 2^30 or more, makes s NaN.
 template <int G, int U>
 __device__ __forceinline__ void pair_push(const float (&v)[U][G], float& m, float& s, float k2) {
     if (m == -kInf) {
         m = max_of<G>(v) * k2;
-        if (m == -kInf) return;
+        if (m <= -kLarge) {
+            m = -kInf;
+            return;
+        }
+        if (m >= kLarge) s = __int_as_float(0x7FC00000);
     }
     float t;
 #pragma unroll 1
@@ -265,6 +273,7 @@ __device__ __forceinline__ void pair_push(const float (&v)[U][G], float& m, floa
         t = sum_exp<G>(v, k2, m);
         if (again || t < 4294967296.f) break;
         const float vm = fmaxf(m, max_of<G>(v) * k2);   // a value far above the reference: take the new maximum
+        if (vm >= kLarge) s = __int_as_float(0x7FC00000);
         s *= ex2(m - vm);
         m = vm;
     }
