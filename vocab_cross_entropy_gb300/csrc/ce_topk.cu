@@ -134,6 +134,10 @@ __device__ __forceinline__ int block_sum(const Team<NS>& tm, int n, SelCtl& ctl,
     for (int w = 0; w < Team<NS>::kWarps; ++w) t += ctl.count[it & 1][w];
     return t;
 }
+// The exponent of a reference, a rounded product with k2, against another: not fused, so that it is 0 where they are
+// the same.
+__device__ __forceinline__ float less(float v, float k2, float ref) { return __fsub_rn(__fmul_rn(v, k2), ref); }
+
 // The columns left out: their pair, and the largest of them, which stands for their log-sum-exp where
 // its product with k2 passes fp32 (masks of the type's lowest value; such values are in no pair).
 struct Rest {
@@ -145,7 +149,7 @@ struct Rest {
     // a value, `times` over
     __device__ __forceinline__ void add(float v, float k2, float times = 1.f) {
         const float r = v * k2;
-        if (r > -kInf) pair_merge(m, s, r, times * ex2(fmaf(v, k2, -r)));
+        if (r > -kInf) pair_merge(m, s, r, beyond(r) ? times : times * ex2(fmaf(v, k2, -r)));
         top = fmaxf(top, v);
     }
     __device__ __forceinline__ float lse(float scale) const { return s > 0.f ? m * kLn2 + logf(s) : top * scale; }
@@ -180,6 +184,11 @@ __device__ __forceinline__ float2 pair_of(const float (&v)[G], float k2) {
     const float m = max_of_vector<G>(v) * k2;
     if (m == -kInf) return make_float2(-kInf, 0.f);
     float s = 0.f;
+    if (beyond(m)) {
+#pragma unroll
+        for (int k = 0; k < G; ++k) s += v[k] * k2 == m ? 1.f : 0.f;
+        return make_float2(m, s);
+    }
 #pragma unroll
     for (int k = 0; k < G; ++k) s += ex2(fmaf(v[k], k2, -m));
     return make_float2(m, s);
@@ -431,7 +440,7 @@ __device__ __forceinline__ void select(const Args& a, const Row& r, const Slice&
             float s = 0.f;
             if (ref > -kInf) {
 #pragma unroll
-                for (int u = 0; u < kU; ++u) s += part[i * kU + u].y * ex2(part[i * kU + u].x * a.k2 - ref);   // 0 * 0 for -inf
+                for (int u = 0; u < kU; ++u) s += part[i * kU + u].y * ex2(less(part[i * kU + u].x, a.k2, ref));   // 0 * 0 for -inf
             }
             gs[sel[i]] = s;
         }
@@ -441,7 +450,7 @@ __device__ __forceinline__ void select(const Args& a, const Row& r, const Slice&
         rest.m = rest.top * a.k2;
         if (rest.m > -kInf) {
 #pragma unroll 4
-            for (int g = tid; g < groups; g += NS) rest.s += gs[g] * ex2(gm[g] * a.k2 - rest.m);   // 0 * 0 for -inf
+            for (int g = tid; g < groups; g += NS) rest.s += gs[g] * ex2(less(gm[g], a.k2, rest.m));   // 0 * 0 for -inf
         }
     }
     // ---- 3. ranks ----
@@ -477,7 +486,10 @@ __device__ __forceinline__ void outputs(const Args& a, int64_t row, const uint64
         all.m = all.top * a.k2;
         if (all.m > -kInf)
             for (int k = tid; k < a.K; k += 32)
-                if (top[k]) all.s += ex2(fmaf(value_of(cand_key(top[k])), a.k2, -all.m));
+                if (top[k]) {
+                    const float v = value_of(cand_key(top[k]));
+                    all.s += ex2(beyond(all.m) ? less(v, a.k2, all.m) : fmaf(v, a.k2, -all.m));
+                }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) all.s += __shfl_xor_sync(0xFFFFFFFFu, all.s, off);
         all.merge(rest.m, rest.s, rest.top);
@@ -486,6 +498,18 @@ __device__ __forceinline__ void outputs(const Args& a, int64_t row, const uint64
             a.tail[row] = ok ? rest.lse(scale) : bad;
         }
     }
+}
+
+// The count of a group with a large reference, by a call: the loop over the groups is short of issue slots.
+template <typename S>
+__device__ __noinline__ float count_loaded(uint4 x0, uint4 x1, uint4 x2, uint4 x3, float k2, float ref) {
+    constexpr int G = Elt<S>::kGroup;
+    float v[4][G];
+    Elt<S>::unpack(x0, v[0]);
+    Elt<S>::unpack(x1, v[1]);
+    Elt<S>::unpack(x2, v[2]);
+    Elt<S>::unpack(x3, v[3]);
+    return count_of(v, k2, ref);
 }
 
 // A group's maximum and the sum of its exponentials relative to it (to its product with k2, as rounded).
@@ -498,7 +522,8 @@ __device__ __forceinline__ void group_of(const uint4 (&x)[kU], float k2, float& 
     for (int u = 0; u < kU; ++u) Elt<S>::unpack(x[u], v[u]);
     m = top;
     const float ref = top * k2;
-    s = ref == -kInf ? 0.f : sum_exp<G>(v, k2, ref);
+    if (!beyond(ref)) s = sum_exp<G>(v, k2, ref);
+    else s = ref == -kInf ? 0.f : count_loaded<S>(x[0], x[1], x[2], x[3], k2, ref);
 }
 
 // ---- one cluster per row -------------------------------------------------------------------------

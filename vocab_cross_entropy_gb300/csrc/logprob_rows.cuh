@@ -26,6 +26,8 @@
 namespace vce {
 namespace lp {
 
+using rs::beyond;
+using rs::count_of;
 using rs::kLarge;
 using rs::kLn2;
 constexpr float kLn2Lo = -1.90465431e-9f;            // ln 2 = kLn2 + kLn2Lo
@@ -57,19 +59,6 @@ struct Sums {
 struct Scale {
     float hi, lo;
 };
-
-__device__ __forceinline__ bool beyond(float m) { return fabsf(m) >= kLarge; }
-
-// How many products with k2 round to m, the largest of them (+inf: NaN).
-template <int G, int U>
-__device__ __forceinline__ float count_of(const float (&v)[U][G], float k2, float m) {
-    float n = 0.f;
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int k = 0; k < G; ++k) n += v[u][k] * k2 == m ? 1.f : 0.f;
-    return m < kInf ? n : __int_as_float(0x7FC00000);
-}
 
 // (s, w) to the reference M >= m.
 template <int kKind>

@@ -253,6 +253,18 @@ __device__ __forceinline__ float max_of(const float (&v)[U][G]) {
 // References of this size and more are large.  Below it the exponent of the reference's own logit, which is what the
 // product with k2 was rounded by, is 2^5 at most; against a mask of -1e10 it would be 2^9, which no power of two holds.
 constexpr float kLarge = 1073741824.f;               // 2^30
+__device__ __forceinline__ bool beyond(float m) { return fabsf(m) >= kLarge; }
+
+// How many products with k2 round to m, the largest of them (+inf: NaN).
+template <int G, int U>
+__device__ __forceinline__ float count_of(const float (&v)[U][G], float k2, float m) {
+    float n = 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int k = 0; k < G; ++k) n += v[u][k] * k2 == m ? 1.f : 0.f;
+    return m < kInf ? n : __int_as_float(0x7FC00000);
+}
 
 // Adds a stage's values to a pair whose reference moves only when a term would pass 2^32 (it is then one
 // of the values', so s is about 1 or more and nothing overflows).  Values whose product with k2 is -2^30 or less
