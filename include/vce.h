@@ -34,6 +34,9 @@
  *     16-byte aligned; 16-byte aligned rows take the vectorised path.
  *   - Labels are int64.  A label equal to ignore_index marks an ignored row: its
  *     loss and gradient are exactly +0.0, whatever its logits hold (even +-inf).
+ *   - Masked logits may be -inf or any value of -1.4885e9 (-2^31 / log2 e) or less, such as -1e10 or
+ *     the type's lowest: beside the target's own they have no mass.  A row whose target is such a
+ *     finite mask and that holds nothing but masks has a NaN loss and gradient.
  *     Any other label outside [0, V) is an error: the device writes VCE_ERR_LABEL
  *     into *status, that row's loss becomes NaN (and so does a reduced loss), its
  *     gradient is 0.  No call traps or asserts on the device.

@@ -173,8 +173,10 @@ __device__ __forceinline__ void fmul2(float a0, float a1, float b, float& d0, fl
 //
 // A pair (m, s) stands for the multiset sum  s * e^m = sum_k e^{v_k}, with m one of the v_k
 // (the largest, for ms_push; a running reference within ~22 of the largest, for
-// ms_push_lazy), so s >= 1 and no term overflows.  The empty set (or a set of -inf only) is
-// (-inf, 0).
+// ms_push_lazy), so s >= 1 and no term overflows.  The empty set (or a set of masks only) is
+// (-inf, 0).  Masks are -inf and every v_k <= kMask: the exponent of such a reference, which is what its
+// product with log2(e) was rounded by, could be 2^7, whose power of two no fp32 number holds.
+constexpr float kMask = -1.4885222e9f;               // -2^31 / log2(e)
 
 // Merge (m2, s2) into (m, s), rescaling both sums to the larger reference.
 __device__ __forceinline__ void ms_merge(float& m, float& s, float m2, float s2) {
@@ -191,7 +193,7 @@ __device__ __forceinline__ void ms_push(const float (&v)[G], float& m, float& s,
     float vm = v[0];
 #pragma unroll
     for (int k = 1; k < G; ++k) vm = fmaxf(vm, v[k]);
-    if (vm > m) {   // a new running maximum: rare after the first few groups of a row
+    if (vm > m && vm > kMask) {   // a new running maximum: rare after the first few groups of a row
         s *= ex2((m - vm) * kLog2e);
         m = vm;
         mb = m * kLog2e;
@@ -219,8 +221,10 @@ __device__ __forceinline__ void ms_push_lazy(const float (&v)[G], float& m, floa
 #pragma unroll
         for (int k = 1; k < G; ++k) vm = fmaxf(vm, v[k]);
         if (vm == -kInf) return;
-        m = vm;
-        mb = m * kLog2e;
+        if (vm > kMask) {
+            m = vm;
+            mb = m * kLog2e;
+        }
     }
     float e[G];
 #pragma unroll
@@ -247,8 +251,10 @@ __device__ __forceinline__ void ms_push_lazy_batch(const float (&v)[U][G], float
 #pragma unroll
             for (int k = 0; k < G; ++k) vm = fmaxf(vm, v[u][k]);
         if (vm == -kInf) return;
-        m = vm;
-        mb = m * kLog2e;
+        if (vm > kMask) {
+            m = vm;
+            mb = m * kLog2e;
+        }
     }
     float t[U];
 #pragma unroll
@@ -275,7 +281,7 @@ __device__ __forceinline__ void ms_push_lazy_batch(const float (&v)[U][G], float
 }
 
 __device__ __forceinline__ void ms_push1(float v, float& m, float& s, float& mb) {
-    if (v > m) {
+    if (v > m && v > kMask) {
         s *= ex2((m - v) * kLog2e);
         m = v;
         mb = m * kLog2e;
@@ -312,9 +318,9 @@ __device__ __forceinline__ float4 ce_row_finish(float M, float S, float zt, floa
         const float lnS = logf(S);
         lse = M + lnS;
         x = (M - zt) + lnS;   // M - z_t is exact for bf16 inputs of similar size
-    } else {                   // no finite non-target logit: p_t = 1
+    } else {                   // nothing but masks beside the target: p_t = 1, or nothing is left
         lse = -kInf;
-        x = -kInf;
+        x = zt <= kMask && zt > -kInf ? __int_as_float(0x7FC00000) : -kInf;
     }
     const float e = expf(-fabsf(x));
     const float d = 1.f + e;
