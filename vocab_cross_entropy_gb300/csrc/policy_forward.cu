@@ -74,8 +74,8 @@ __global__ void __launch_bounds__(kFinishThreads) k_loss_count(const __grid_cons
 __global__ void __launch_bounds__(kFinishThreads) k_loss_finish(const __grid_constant__ FinishArgs a) {
     __shared__ long long sm[kFinishThreads / 32];
     __shared__ float sum[kFinishThreads / 32], comp[kFinishThreads / 32];
-    __shared__ int code;
-    if (threadIdx.x == 0) code = 0;
+    __shared__ int code, stray;                      // the rows' largest code; offsets that bound no sequences
+    if (threadIdx.x == 0) code = stray = 0;
     __syncthreads();
     long long n = 0;
     if (a.mode == kPolicy && a.red == VCE_RED_MEAN)
@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kFinishThreads) k_loss_finish(const __grid_con
     int mine = 0;
     if (a.mode == kPreference)
         for (int64_t i = threadIdx.x; i < 2 * a.P; i += kFinishThreads)
-            if (!(a.offsets[i] >= 0 && a.offsets[i] <= a.offsets[i + 1] && a.offsets[i + 1] <= a.T)) mine = VCE_ERR_OFFSETS;
+            if (!(a.offsets[i] >= 0 && a.offsets[i] <= a.offsets[i + 1] && a.offsets[i + 1] <= a.T)) stray = 1;
     wait_previous();
 #pragma unroll 4
     for (int64_t i = threadIdx.x; i < a.T; i += kFinishThreads) {
@@ -92,8 +92,7 @@ __global__ void __launch_bounds__(kFinishThreads) k_loss_finish(const __grid_con
     }
     if (mine) atomicMax(&code, mine);
     n = block_count(n, sm);                          // (and the code is known)
-    const bool wrong = code == VCE_ERR_OFFSETS;
-    if (wrong) {                                     // sequences that are none: no loss and no gradient
+    if (stray) {                                     // sequences that are none: no loss and no gradient
         for (int64_t i = threadIdx.x; i < a.T; i += kFinishThreads) a.row_stats[i] = make_float4(kInf, 0.f, 0.f, 0.f);
         for (int64_t i = threadIdx.x; i < a.P; i += kFinishThreads) {
             a.pair_losses[i] = a.rewards[2 * i] = a.rewards[2 * i + 1] = nan_f();
@@ -110,7 +109,7 @@ __global__ void __launch_bounds__(kFinishThreads) k_loss_finish(const __grid_con
     }
     if (a.mode != kLogprobs && a.red != VCE_RED_NONE)
         fold::sum_losses<kFinishThreads>(a.losses, a.n_losses, a.mode == kPolicy ? n : a.P, a.red, a.loss_out, sum, comp);
-    if (threadIdx.x == 0) *a.status = code;
+    if (threadIdx.x == 0) *a.status = stray ? max(code, (int)VCE_ERR_OFFSETS) : code;
 }
 
 // ---- pairs of sequences ------------------------------------------------------------------------------
