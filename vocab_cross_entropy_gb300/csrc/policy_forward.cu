@@ -115,9 +115,8 @@ __global__ void __launch_bounds__(kFinishThreads) k_loss_finish(const __grid_con
 // ---- pairs of sequences ------------------------------------------------------------------------------
 
 struct PairArgs {
-    const int64_t* ids;
     const int64_t* offsets;
-    int64_t P, T;
+    int64_t T;
     const float* ref;
     float4* row_stats;
     int kind, average;
@@ -435,7 +434,7 @@ extern "C" int preference_loss_forward(const void* logits, vce_dtype dt, int64_t
     if ((rc = require_sm100())) return rc;
     cudaError_t e = run(dt, a, s);
     if (e == cudaSuccess && P) {
-        const lp::PairArgs b{labels, offsets, P, T, ref_logprobs, a.row_stats, (int)p->kind, p->average, p->beta,
+        const lp::PairArgs b{offsets, T, ref_logprobs, a.row_stats, (int)p->kind, p->average, p->beta,
                              p->label_smoothing, p->margin, a.inv_tau, pair_losses, rewards};
         e = rs::launch_clusters<lp::k_pairs>(P, 1, lp::kPairThreads, 0, s, b, T > 0);
     }

@@ -39,13 +39,6 @@ __device__ __forceinline__ bool grads_aligned(const rs::Row& r, const O* grow) {
     return (reinterpret_cast<uintptr_t>(grow - r.shift) % (GroupStore<O, G>::kAlign)) == 0;
 }
 
-// +0.0 over a thread's U vectors of stage j of the slice.
-template <typename S, typename O, int U, int NT>
-__device__ __forceinline__ void write_zeros(const rs::Row& r, const Slice& s, int j, int tid, O* grow, bool vec) {
-    Slice part{s.v0 + j * U * NT, min(s.n - j * U * NT, U * NT), 1};
-    fill_grads<S, O>(r, part, grow, vec, tid, NT);
-}
-
 // The gradients of a vector's G logits, in their place.  kEnt: c.c1 is not 0.  A mask's exponent of -inf is
 // held at -200 there, as in the sums.
 template <int G, bool kEnt>
