@@ -38,7 +38,8 @@ VCE_API int vce_quantize_fp8(const void* x, vce_dtype dt, int64_t R, int64_t D, 
 /*
  * vce_linear_fp8 -- out[t][v] = sum_b x_scales[t][b] w_scales[v / 128][b] sum_{k in block b} x[t][k] w[v][k]
  * over the blocks b of 128 columns, on the tensor cores: a block's products are summed in fp32 there,
- * and the scaled blocks in fp32 beside them.  The scales may be any fp32 numbers.
+ * and the scaled blocks in fp32 beside them.  The scales may be any fp32 numbers; a row's and a block's are
+ * multiplied first, so their product has to be one too.
  *   x         [T, D] e4m3, leading dimension D, 16-byte aligned
  *   x_scales  [T, ceil(D / 128)] fp32
  *   w         [V, D] e4m3, leading dimension D, 16-byte aligned

@@ -43,8 +43,8 @@ extern "C" {
  *   logprobs[i] = log p_it,   entropy[i] = -sum_j p_ij log p_ij
  * The logarithm is -softplus(L' - x_t) with L' the log-sum-exp of the other columns, and the
  * entropy a sum of terms >= 0 that splits off the token's own probability, so a row that is sure of
- * its token keeps its digits (of one that is sure of another column, the entropy is within about 3e-7
- * of itself or of 1).  A token on a masked column has log-probability -inf.
+ * its token keeps its digits (where it is sure of another column, the entropy of the rest among itself is
+ * off by up to about 3e-7).  A token on a column of -inf has log-probability -inf.
  *   logits, dt, T, V, ld   as ce_forward; V <= VCE_MAX_POLICY_V
  *   ids, ignore_index      [T] int64
  *   temperature            finite, > 0, with a finite reciprocal

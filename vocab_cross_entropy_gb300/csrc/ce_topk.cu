@@ -20,7 +20,7 @@
 // equal to it are taken in column order.
 //
 // What bounds it: many rows (k_topk_rows) the stream, with the selection of a row beside the next
-// one's copies (8192 x 128256 bf16, K 64: 394 us, 5.4 TB/s, 0.79 of the measured copy); few rows (k_topk)
+// one's copies (8192 x 128256 bf16, K 64: 398 us, 5.3 TB/s, 0.79 of the measured copy); few rows (k_topk)
 // the chain of a launch: copies, maxima, search, read again, rank, merge (one row of 128256: 11 us;
 // 64 x 32001 fp32: 13.8 us, 0.6 TB/s).
 #include <cuda_runtime.h>

@@ -13,15 +13,19 @@
 //                  than there are SMs, a cluster's CTAs each take a part of K and add their sums in order.
 // What bounds them.  8192 x 4096 by 128256 to bf16: 3.87-4.04 ms, 2220 TFLOP/s (0.59 of twice the bf16 product's
 // measured burst rate), the tensor pipe 45% active at 1.91 GHz.  At 2048 x 4096 by 32768, 263 us: the copies out of
-// L2 with a quarter of the MMAs take 168 us (15 TB/s), copies and MMAs with nobody waiting for an accumulator 209, with
-// the accumulators handed over but not read 236.  The hand-over (a block's MMAs done, both CTAs told, the sums read,
-// the even CTA told: some 1300 cycles, of which the other accumulator's block hides 500) is what keeps the
-// tensor pipe waiting.  N = 128 accumulators, four of them, would hide it but read x's tile twice as often from shared
-// memory, which is then the limit (319 us).  16 epilogue warps of 64 columns spill at 104 registers (548 us).
+// L2 with a quarter of the MMAs take 168 us (1024 tiles of 32 blocks of 64 KB, 12.8 TB/s), copies and MMAs with nobody
+// waiting for an accumulator 209, with the accumulators handed over but not read 236.  The hand-over (a block's MMAs
+// done, both CTAs told, the sums read, the even CTA told: some 1300 cycles, of which the other accumulator's block hides
+// 500) is what keeps the tensor pipe waiting.  N = 128 accumulators, four of them, would hide it but read x's tile twice
+// as often from shared memory, which is then the limit (319 us).  16 epilogue warps of 64 columns spill at 104 registers
+// (548 us).
+// All this is for scales of any value.  Powers of two, as quantize_fp8 makes them, could be handed to the block-scaled
+// form of the MMA as bytes, which would add up all of K in one accumulator; that needs operands of a type of their own
+// and is not built.
 // T = 1: 83-85 us in a graph, 6.2-6.3 TB/s of w (0.93-0.95 of the measured copy); T = 64: 90 us, T = 128: 109.  A block
-// takes no less than its copies, some 1.5 ns a row of 128 bytes (0.2 us for w's 128 rows), however few SMs work.  Each SM
-// the same number of rows, the last tile in copies of 32: 1 x 4096 by 128256 85.5 us to 87.7, 64 x 2064 by 32001 21.4 to
-// 20.3; in copies of 8 slower everywhere.
+// takes no less than its copies, some 1.5 ns a row of 128 bytes (0.2 us for w's 128 rows), however few SMs work, and
+// 0.38 us where all do, which is the memory's rate.  Each SM the same number of rows, the last tile in copies of 32:
+// 1 x 4096 by 128256 85.5 us to 87.7, 64 x 2064 by 32001 21.4 to 20.3; in copies of 8 slower everywhere.
 // Every wait is bounded (2 s); where one gives up, the CTA's tiles become NaN.
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -5,9 +5,9 @@
 // order, writes the status word and, for a mean, scales the saved coefficients; each starts while the one ahead of it
 // runs (programmatic dependent launch).  Nothing is shared between calls.
 //
-// What bounds them, bf16: the forward reads the logits once (16384 x 128256: 608 us, 6.8 TB/s, 1.02 of the measured
-// copy; with entropies 4096 x 128256: 181 us, 5.8 TB/s, one fma and one maximum more a column); short rows cost about
-// 1 us beside their columns (4096 x 32000: 53 us, 4.9 TB/s).  Few rows are latency: one of 128256 takes 8.1 us.
+// What bounds them, bf16: the forward reads the logits once (16384 x 128256: 606 us, 6.9 TB/s, 1.02 of the measured
+// copy; with entropies 635 us, and 4096 x 128256 169 us, 6.2 TB/s, one fma and one maximum more a column); short rows
+// cost about 1 us beside their columns (4096 x 32000: 53 us, 4.9 TB/s).  Few rows are latency: one of 128256 takes 7.2 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
 

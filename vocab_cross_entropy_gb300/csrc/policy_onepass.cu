@@ -23,8 +23,8 @@ using namespace rs;
 //    scheduler and have 128 registers (16 had 96 and spilled); 15 stages of 14 KB, ten of which a row may take, so
 //    that the next row's first stages are summed while this row's statistics are exchanged and finished (2048 x
 //    64000: 107, and 122 with two blocks; 4096 x 128256: 368 and 435).
-// What bounds the last: 16384 x 128256 1421 us, 5.9 TB/s, 0.89 of the measured copy, a column's two exponentials and the
-// instructions around them; with an entropy term 1589 us, 0.79, where a column takes two maxima and two products more.
+// What bounds the last: 16384 x 128256 1402 us, 6.0 TB/s, 0.90 of the measured copy, a column's two exponentials and the
+// instructions around them; with an entropy term 1577 us, 0.80, where a column takes two maxima and two products more.
 // The row's statistics take about 1.5 us from the last sum to the first gradient, of which the next row's first stages
 // hide most (a release at cluster scope and functions worked out twice there cost 20 us of 387 at 4096 rows).
 using Pair = ring::Form<4, 2, 8, 6, 4>;
