@@ -163,3 +163,41 @@ def test_great_logits(vce, V, dtype, tau, size):
                      (one[4], -grad), (two[4], -grad)):
         # 16 roundings of factors of size log V, and the output's
         G.near(host(got), g64, 16 * G.E24 * (1 + np.log(V)) * (p + hot) / tau + eps / 2 * np.abs(g64) * 1.01, "gradient")
+
+
+@pytest.mark.parametrize("V,dtype", [(600, F32), (20001, BF16), (128256, BF16), (300001, F32)])
+@pytest.mark.parametrize("tau", [1e-30, 1e-12, 1e-9, 1e-7, 1e-4, 1e6, 1e20, 1e37])
+def test_temperatures_of_every_size(vce, V, dtype, tau):
+    """The largest logits share all of the mass, or all columns do.  What a log-probability is off by: the products'
+    roundings, as above, and an even row's handful."""
+    tau = float(np.float32(tau))
+    g = torch.Generator().manual_seed(V)
+    z = (2 * torch.randn(5, V, generator=g)).to(dtype).cuda()
+    ids = torch.randint(0, V, (5,), generator=g).cuda()
+    ids[0] = z[0].argmax()
+    z[1, 7] = z[1, int(ids[1])] = 12.0
+    z[2, int(ids[2])] = 11.0
+    z[3] = -3.0
+    x = host(z) / tau
+    x = x - x.max(1, keepdims=True)
+    e = np.exp(x)
+    p = e / e.sum(1, keepdims=True)
+    t = ids.cpu().numpy()
+    want = x[np.arange(5), t] - np.log(e.sum(1))
+    size = np.abs(host(z) / tau).max(1)
+    tol = 5 * G.E24 * np.maximum(np.abs(want), size * (p[np.arange(5), t] < 0.999)) + 16 * G.E24 * (1 + np.log(V))
+    lp, H, stats, status = vce.ce_logprobs_forward(z, ids, tau)
+    assert vce.vce_get_status(status) == 0
+    one = vce.policy_loss_forward_backward(z, ids, torch.ones(5, device="cuda"), temperature=tau, reduction="none",
+                                           grad_dtype=F32)
+    hot = np.zeros(p.shape)
+    hot[np.arange(5), t] = 1.0
+    for l in (lp, one[2]):
+        G.near(host(l), want, tol, "log-probabilities")
+    # exponents up to 110 matter, each off by what z / tau rounds by
+    rel = 5 * G.E24 * np.minimum(size, 110.0)[:, None] + 64 * G.E24 * (1 + np.log(V))
+    got = vce.ce_logprobs_backward(z, ids, stats, torch.ones(5, device="cuda"), None, tau, grad_dtype=F32)
+    for g64, sign in ((got, 1.0), (one[4], -1.0)):
+        G.near(sign * host(g64) * tau, hot - p, rel * np.where(hot > 0, 1 - p + 1e-30, p) * 2 + 1e-37 * max(tau, 1.0) + 1e-30,
+               "gradient")
+    assert np.all(np.isfinite(host(H))) and np.all(host(H) >= 0) and np.all(host(H) <= np.log(V) * 1.000001)
