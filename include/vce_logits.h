@@ -87,10 +87,10 @@ VCE_API int ce_topk(const void* logits, vce_dtype dt, int64_t T, int64_t V, int6
  *   status                 [1] int32: 0, VCE_ERR_TEACHER, or 105 .. 109 when a bounded device-side
  *                          wait gave up (the largest of the rows' codes).  A row with an error has a
  *                          NaN loss and no gradient (the one pass's of 105 .. 109: unspecified).
- * A student's logit whose product with log2(e) / temperature is -2^30 or less (a mask: -1e10, the type's
+ * A student's logit whose product with log2(e) / temperature is -2^31 or less (a mask: -1e10, the type's
  * lowest value) counts as -inf.  A student row of nothing else has a NaN loss and no gradient; an entry with
  * q_k > 0 on a logit of -inf, and a teacher's tail on nothing but such, make the loss +inf.  A NaN or +inf among a
- * student's logits, or a logit but an entry's whose product is 2^30 or more, makes its loss and its whole gradient
+ * student's logits, or a logit but an entry's whose product is 2^31 or more, makes its loss and its whole gradient
  * NaN (not the status).
  */
 VCE_API int ce_distill_forward(const void* logits, vce_dtype dt, int64_t T, int64_t V, int64_t ld,

@@ -20,7 +20,7 @@
  * any value far below the others, such as -1e10 or the type's lowest.  A logit whose product with
  * log2(e) / temperature passes fp32 counts as -inf; of a row of nothing but -inf everything is NaN, and
  * it has no gradient (+0.0).  A row of nothing but lesser masks is a row like any other (where that
- * product of its largest logit but the token is 2^30 or more in size, logits count as equal when their
+ * product of its largest logit but the token is 2^31 or more in size, logits count as equal when their
  * products round to the same fp32 number).  A NaN or +inf among a row's logits (or one whose product passes
  * fp32 upwards) makes all that the row returns, and its whole gradient, NaN.
  */

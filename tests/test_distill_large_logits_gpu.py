@@ -35,7 +35,7 @@ def student(T, V, K, dtype, seed):
 def check(vce, z, ids, values, tail, tau, zmax, lost=()):
     """Masks count as -inf; rows of nothing else have no gradient; the rows `lost` are NaN throughout."""
     z64 = host(z)
-    z64[z64 * 1.4426950408889634 / tau <= -2.0 ** 30] = -np.inf
+    z64[z64 * 1.4426950408889634 / tau <= -2.0 ** 31] = -np.inf
     dead = np.isneginf(z64).all(1)
     live = ~dead
     live[list(lost)] = False
@@ -96,3 +96,25 @@ def test_great_logits(vce, V, dtype, size):
     z[3, 0] = size
     values[1, 2] = 500.0                    # which the teacher is sure of, too: else the loss is of that size
     check(vce, z, ids, values, tail, 1.0, 10.0, lost=(0, 2, 3))
+
+
+@pytest.mark.parametrize("V,dtype", [(700, F32), (20000, BF16), (70001, F32)])
+def test_products_below_the_border(vce, V, dtype):
+    """A temperature whose products stay below 2^31: losses of the size of the logits' differences times it, off by 64
+    roundings of the largest logit."""
+    tau = float(np.float32(6e-9))
+    g = torch.Generator().manual_seed(V)
+    z = (2 * torch.randn(5, V, generator=g)).clamp(-8, 8).to(dtype).cuda()
+    z[:, 1] = torch.tensor([7.75, -7.75, 7.5, 3.0, 8.0])
+    z[1] -= 8 + z[1].max()
+    z[1].clamp_(min=-8)
+    ids = torch.stack([torch.randperm(V, generator=g)[:4] for _ in range(5)]).cuda()
+    values = torch.randn(5, 4, generator=g).cuda()
+    ref = L.distill(host(z), ids.cpu().numpy(), host(values), None, tau, None, "sum", 1.0)
+    _, rows, stats, tops, status = vce.ce_distill_forward(z, ids, values, None, tau, reduction="sum")
+    _, r1, one, s1 = vce.ce_distill_forward_backward(z, ids, values, None, tau, reduction="sum",
+                                                    grad_output=torch.ones(1, device="cuda"))
+    for r, s in ((rows, status), (r1, s1)):
+        assert vce.vce_get_status(s) == 0
+        assert np.all(np.abs(host(r) - ref["loss_rows"]) <= 64 * G.E24 * 8 * tau)
+    assert torch.isfinite(one).all()

@@ -12,7 +12,7 @@
 //   dl/dz_j = 2^y (c0 + c1 y), y = z_j k2 - m,   c0 = f (-a - b (ln f + H)) / T,  c1 = -b f ln 2 / T
 //   dl/dz_t = (a (1 - p_t) - b p_t (log p_t + H)) / T
 // The exponents are taken from m, not from the log-sum-exp: m is some z_j k2 (or a thread's first
-// maximum), exact, where a log-sum-exp of size 16 would be rounded by 5e-7 of every p_j.  Where |m| is 2^30 or more
+// maximum), exact, where a log-sum-exp of size 16 would be rounded by 5e-7 of every p_j.  Where |m| is 2^31 or more
 // the products z k2 are rounded first, in the sums and the gradient alike: logits of that size (masks such as -1e10
 // in a row of nothing larger) count as equal where the products round to the same number.
 #pragma once
@@ -155,7 +155,7 @@ __device__ __forceinline__ void add(Sums& x, float s, float w, float k2) {
 }
 
 // A batch whose reference moves, or is large: then it is the row's largest rounded product so far, and the sum counts
-// the logits whose products round to it (any other is 2^6 or more below).  The exponent of a mask of -1e10 with its
+// the logits whose products round to it (any other is 2^7 or more below).  The exponent of a mask of -1e10 with its
 // own rounded product for a reference would be up to 2^9 in size.
 template <int G, int U, int kKind>
 __device__ __forceinline__ Sums push_moving(const Batch<G, U>& b, Sums x, float k2) {

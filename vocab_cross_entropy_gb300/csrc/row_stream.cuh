@@ -251,8 +251,8 @@ __device__ __forceinline__ float max_of(const float (&v)[U][G]) {
 }
 
 // References of this size and more are large.  Below it the exponent of the reference's own logit, which is what the
-// product with k2 was rounded by, is 2^5 at most; against a mask of -1e10 it would be 2^9, which no power of two holds.
-constexpr float kLarge = 1073741824.f;               // 2^30
+// product with k2 was rounded by, is 2^6 at most; against a mask of -1e10 it would be 2^9, which no power of two holds.
+constexpr float kLarge = 2147483648.f;               // 2^31
 __device__ __forceinline__ bool beyond(float m) { return fabsf(m) >= kLarge; }
 
 // How many products with k2 round to m, the largest of them (+inf: NaN).
@@ -267,8 +267,8 @@ __device__ __forceinline__ float count_of(const float (&v)[U][G], float k2, floa
 }
 
 // Adds a stage's values to a pair whose reference moves only when a term would pass 2^32 (it is then one
-// of the values', so s is about 1 or more and nothing overflows).  Values whose product with k2 is -2^30 or less
-// (masks) count as -inf.  A NaN, or a product of 2^30 or more, makes s NaN.
+// of the values', so s is about 1 or more and nothing overflows).  Values whose product with k2 is -2^31 or less
+// (masks) count as -inf.  A NaN, or a product of 2^31 or more, makes s NaN.
 template <int G, int U>
 __device__ __forceinline__ void pair_push(const float (&v)[U][G], float& m, float& s, float k2) {
     if (m == -kInf) {
